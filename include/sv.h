@@ -64,7 +64,8 @@ typedef enum {
   SV_ERR_TIMEOUT = 4      /* reserved: no call of this build waits on the device */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+/* SV_F16 is taken by sv_paged_attention only. */
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype;
 
 /* Bits of the per-sequence out_status word. */
 #define SV_ROW_NAN 1u        /* a used logit row holds NaN or +inf, or is all -inf */
@@ -74,6 +75,9 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_ROW_BAD_TREE 16u  /* parent/score arrays do not describe a tree */
 #define SV_ROW_BAD_BASE 32u  /* sv_tree_attention: base < 0 or base + T > S */
 #define SV_ROW_TIMEOUT 64u   /* a bounded wait on the device ran out (row pass, sampling, attention) */
+#define SV_ROW_BAD_RAND 128u /* sv_verify_chain_probs: a used random number outside [0, 1) */
+#define SV_ROW_BAD_LEN 256u  /* a length outside its range (n_draft, seq_len) */
+#define SV_ROW_BAD_PAGE 512u /* a used page table entry outside [0, num_pages) */
 
 /* Build limits. */
 #define SV_MAX_VOCAB (1 << 22)  /* fixed-point sampling sums stay below 2^63 */
@@ -415,6 +419,49 @@ sv_status sv_tree_attention_ex(const void *q, const void *kv, const int32_t *bas
                                const uint64_t *mask, int B, int T, int Hq, int Hkv,
                                int D, int S, float scale, void *out, float *out_lse,
                                uint32_t *out_status, uint64_t wait_ns, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_verify_chain_probs -- sv_verify_chain from probabilities and given random
+ * numbers: for callers whose distributions are probabilities already (top-k /
+ * top-p filtered, mixed, tempered elsewhere), whose drafts have no distribution
+ * (copied from the prompt: pprobs NULL), or whose random numbers come from
+ * their own generator.  [Lesson] "O invariante", Passo 1-3, as sv_verify_chain.
+ *
+ * For sequence b and position i = 0..n-1, n = n_draft[b], the draft token
+ * d = draft_tokens[b][i] is accepted iff u p(d) < q(d) in exact arithmetic
+ * (or p(d) = 0), u = u_accept[b][i], q = qprobs[b][i], p = pprobs[b][i]; with
+ * pprobs NULL, p is 1 at d and 0 elsewhere.  At the first rejection a < n the
+ * correction is drawn with weights w_v = max(0, fl32(q_v - p_v)) (w = q if all
+ * are 0, SV_ROW_RESID_ZERO), and if all n pass the bonus with w = row n of
+ * qprobs: the first token k whose sum of floor(w_v 2^62), v <= k, exceeds
+ * u_sample[b] times the total, in integers (the result does not depend on how
+ * the sum is split; equal inputs give equal tokens).  Rows need not be
+ * normalised: only the weights' proportions count.
+ *
+ *   qprobs       [B][N+1][ldq] target probabilities, the first V of each row;
+ *                ldq >= V elements between rows (N+1 rows a sequence, packed)
+ *   pprobs       [B][N][ldp] draft probabilities, ldp >= V, or NULL
+ *   dt           SV_F32 or SV_BF16, of both
+ *   draft_tokens [B][N] int32 (may be NULL when N == 0)
+ *   n_draft      [B] int32 drafted tokens of each sequence, 0..N, or NULL: N
+ *   u_accept     [B][N] fp32 in [0, 1) (may be NULL when N == 0)
+ *   u_sample     [B] fp32 in [0, 1)
+ * Outputs: out_tokens [B][N+1], out_accept_len [B] as sv_verify_chain;
+ * out_status [B], written in full.  Only what the walk reaches is read: the
+ * tested tokens' probabilities and the row (or pair of rows) sampled from.  A
+ * fault there -- an entry that is NaN, negative or at least 2, weights that
+ * sum to 2 or more (an fp32 sum) or to 0 (SV_ROW_NAN), a tested token outside
+ * [0, V) (SV_ROW_BAD_TOKEN), a used random number outside [0, 1)
+ * (SV_ROW_BAD_RAND) or n_draft outside [0, N] (SV_ROW_BAD_LEN) -- makes the
+ * sequence emit nothing: accept_len 0, tokens all -1.  V <= SV_MAX_VOCAB,
+ * N <= SV_MAX_POSITIONS.  One launch, no workspace; capturable.
+ * --------------------------------------------------------------------------- */
+sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, const void *pprobs, int64_t ldp,
+                                sv_dtype dt, const int32_t *draft_tokens,
+                                const int32_t *n_draft, const float *u_accept,
+                                const float *u_sample, int B, int N, int V,
+                                int32_t *out_tokens, int32_t *out_accept_len,
+                                uint32_t *out_status, void *stream);
 
 /* Thread-local message for the last non-OK status returned on this thread. */
 const char *sv_last_error(void);

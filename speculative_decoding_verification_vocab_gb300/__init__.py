@@ -9,6 +9,7 @@ is no CPU fallback: if the shared library is missing, loading fails loudly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -18,9 +19,10 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsv.so")
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_TIMEOUT = 0, 1, 2, 3, 4
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_ROW_NAN, SV_ROW_BAD_TOKEN, SV_ROW_RESID_ZERO, SV_ROW_P_ZERO, SV_ROW_BAD_TREE = 1, 2, 4, 8, 16
 SV_ROW_BAD_BASE, SV_ROW_TIMEOUT = 32, 64
+SV_ROW_BAD_RAND, SV_ROW_BAD_LEN, SV_ROW_BAD_PAGE = 128, 256, 512
 SV_MAX_VOCAB, SV_MAX_POSITIONS, SV_MAX_TREE_NODES = 1 << 22, 1024, 1024
 
 EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_verify_chain",
@@ -29,7 +31,7 @@ EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_ve
            "sv_verify_chain_noalloc_max_bytes", "sv_verify_tree_workspace",
            "sv_verify_tree", "sv_tree_build_mask", "sv_kv_compact", "sv_tree_attention", "sv_tree_attention_ex", "sv_last_error",
            "sv_launch_count", "sv_trace_enable", "sv_trace_collect", "sv_tree_expand",
-           "sv_tree_select", "sv_tree_finalize", "sv_tree_level")
+           "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs")
 
 
 class SvError(RuntimeError):
@@ -96,6 +98,10 @@ def load_library(path: str = LIB_PATH):
     L.sv_tree_attention_ex.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp,
                                        vp, u64, vp]
     L.sv_tree_attention_ex.restype = i32
+    i64 = C.c_int64
+    L.sv_verify_chain_probs.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
+                                        vp, vp, vp, vp]
+    L.sv_verify_chain_probs.restype = i32
     L.sv_last_error.argtypes = []
     L.sv_last_error.restype = C.c_char_p
     L.sv_launch_count.argtypes = []
@@ -303,6 +309,52 @@ def sv_tree_level(dlogits, K, level, n0, frontier, cand_parent, cand_token, cand
         _p(cand_score), _p(cand_level), _stream(stream)))
 
 
+def _want(name, t, dtype, shape):
+    """A packed tensor of this type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _row_stride(name, t, dtype, shape):
+    """Elements between the rows of t [B][R][V]: rows may be padded (a view of
+    the first V columns), sequences follow each other row by row."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: need a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    B, R, V = shape
+    sb, sr, sv = t.stride()
+    ld = sr if R > 1 else sb if B > 1 else V
+    if (V > 1 and sv != 1) or (B > 1 and R > 0 and sb != R * ld):
+        raise ValueError(f"{name}: rows need unit stride and one row stride, got strides "
+                         f"{t.stride()}")
+    return max(ld, V)
+
+
+def sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample, out_tokens,
+                          out_accept_len, out_status, stream=None):
+    """qprobs [B][N+1][V], pprobs [B][N][V] or None (one-hot drafts); rows may be padded."""
+    B, R, V = qprobs.shape
+    N = R - 1
+    i32, f32 = torch.int32, torch.float32
+    ldq = _row_stride("qprobs", qprobs, qprobs.dtype, (B, R, V))
+    ldp = _row_stride("pprobs", pprobs, qprobs.dtype, (B, N, V)) if pprobs is not None else V
+    if N > 0:
+        _want("draft_tokens", draft_tokens, i32, (B, N))
+        _want("u_accept", u_accept, f32, (B, N))
+    if n_draft is not None:
+        _want("n_draft", n_draft, i32, (B,))
+    _want("u_sample", u_sample, f32, (B,))
+    _want("out_tokens", out_tokens, i32, (B, R))
+    _want("out_accept_len", out_accept_len, i32, (B,))
+    _want("out_status", out_status, i32, (B,))
+    return _check(load_library().sv_verify_chain_probs(
+        _p(qprobs), ldq, _p(pprobs) if N > 0 else None, ldp, _dtype(qprobs),
+        _p(draft_tokens) if N > 0 else None, _p(n_draft), _p(u_accept) if N > 0 else None,
+        _p(u_sample), B, N, V, _p(out_tokens), _p(out_accept_len), _p(out_status),
+        _stream(stream)))
+
+
 def sv_last_error():
     return load_library().sv_last_error().decode()
 
@@ -377,6 +429,31 @@ def verify_tree(vlogits, dlogits, parent, token, score, max_depth, temperature=1
     sv_verify_tree(vlogits, dlogits, parent, token, score, max_depth, temperature, seed, step,
                    out["path"], out["tokens"], out["accept_len"], out["q_prob"], out["p_prob"],
                    out["margin"], out["status"], workspace, stream, accept_event)
+    return out
+
+
+def _allocating(stream):
+    """Outputs and scratch of a call on ``stream`` come from that stream's
+    memory pool, so no earlier work of another stream can still be using them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def verify_chain_probs(qprobs, pprobs, draft_tokens, u_accept, u_sample, n_draft=None,
+                       stream=None):
+    """Verify a chain from probabilities and given random numbers (see
+    sv_verify_chain_probs): qprobs [B][N+1][V] and pprobs [B][N][V] (or None:
+    drafts without a distribution) in fp32 or bf16, rows possibly padded;
+    draft_tokens int32 [B][N]; u_accept fp32 [B][N] and u_sample fp32 [B] in
+    [0, 1); n_draft int32 [B] (None: N drafts everywhere).  Returns a dict of
+    tensors: tokens [B][N+1], accept_len [B], status [B]."""
+    B, R, _ = qprobs.shape
+    dev = _out_dev(qprobs)
+    with _allocating(stream):
+        out = dict(tokens=torch.empty(B, R, dtype=torch.int32, device=dev),
+                   accept_len=torch.empty(B, dtype=torch.int32, device=dev),
+                   status=torch.empty(B, dtype=torch.int32, device=dev))
+    sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample,
+                          out["tokens"], out["accept_len"], out["status"], stream)
     return out
 
 
