@@ -463,6 +463,53 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, const void *ppr
                                 int32_t *out_tokens, int32_t *out_accept_len,
                                 uint32_t *out_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * sv_paged_attention -- attention of one new token per sequence over a paged
+ * KV cache, one layer: the step in which a draft (or target) model produces
+ * the next token.  [Lesson] Passo 3, [Blog] section 4 (the drafting loop); the
+ * pages leave the cache's layout open.  Grouped-query heads: query head h
+ * reads KV head h / G, G = Hq / Hkv.
+ *
+ * Slot j of sequence b is row j % page of page block_table[b][j / page].  With
+ * n = seq_len[b] (the new token's own row included), slot j is visible iff
+ * j < n and (window == 0 or j >= n - window or j < sinks): the whole sequence,
+ * or a sliding window and a few first tokens.
+ *
+ *   q     [B][Hq][D], dt SV_BF16 or SV_F16
+ *   kv    K rows at kv + id page_stride + r Hkv D + h D, V rows kv_stride
+ *         further (elements of dt; page id, row r, KV head h): [2][num_pages]
+ *         [page][Hkv][D] and [num_pages][2][page][Hkv][D] alike.  Both strides
+ *         multiples of 8, page_stride >= page Hkv D
+ *   block_table int32 [B][max_pages]; seq_len int32 [B], 0..max_pages page
+ *   scale > 0, finite; D 64, 128 or 256; any G
+ *   weight_sum fp32 [B][Hkv][S] or NULL, S >= max_pages page: at every visible
+ *         slot the weights of the G query heads exp(scale q.k - lse) are added
+ *         (what sv_kv_evict evicts by); other slots are left as they are
+ *   out   [B][Hq][D] of dt; out_lse fp32 [B][Hq] or NULL, natural log
+ *   out_status uint32 [B] or NULL, written in full
+ * A sequence with no visible slot (seq_len 0), or a row whose scores are all
+ * -inf, gives 0 and lse -inf.  Slots that are not visible, and pages that hold
+ * none that is, are never read (they may hold anything, their table entries
+ * too).  seq_len out of range (SV_ROW_BAD_LEN) or a needed page outside
+ * [0, num_pages) (SV_ROW_BAD_PAGE) gives NaN rows and leaves weight_sum.
+ * Pages may be shared between sequences.  q, kv, out 16-byte aligned.
+ *
+ * Work is split over the slots by the lengths found on the device, so that one
+ * captured launch serves growing sequences.  The workspace (bytes from the
+ * query, `weights` nonzero when weight_sum is given; 0: none needed, or bad
+ * sizes) is written before it is read; calls that may overlap need one each.
+ * Results do not depend on scheduling.
+ * --------------------------------------------------------------------------- */
+size_t sv_paged_attention_workspace(int B, int Hq, int Hkv, int D, int page, int max_pages,
+                                    int window, int sinks, int weights);
+sv_status sv_paged_attention(const void *q, const void *kv, int64_t kv_stride,
+                             int64_t page_stride, sv_dtype dt, const int32_t *block_table,
+                             const int32_t *seq_len, int B, int Hq, int Hkv, int D, int page,
+                             int max_pages, int num_pages, int window, int sinks, float scale,
+                             float *weight_sum, int S, void *out, float *out_lse,
+                             uint32_t *out_status, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
 /* Thread-local message for the last non-OK status returned on this thread. */
 const char *sv_last_error(void);
 

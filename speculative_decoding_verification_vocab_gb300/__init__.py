@@ -31,7 +31,8 @@ EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_ve
            "sv_verify_chain_noalloc_max_bytes", "sv_verify_tree_workspace",
            "sv_verify_tree", "sv_tree_build_mask", "sv_kv_compact", "sv_tree_attention", "sv_tree_attention_ex", "sv_last_error",
            "sv_launch_count", "sv_trace_enable", "sv_trace_collect", "sv_tree_expand",
-           "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs")
+           "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs",
+           "sv_paged_attention_workspace", "sv_paged_attention")
 
 
 class SvError(RuntimeError):
@@ -102,6 +103,11 @@ def load_library(path: str = LIB_PATH):
     L.sv_verify_chain_probs.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
                                         vp, vp, vp, vp]
     L.sv_verify_chain_probs.restype = i32
+    L.sv_paged_attention_workspace.argtypes = [i32] * 9
+    L.sv_paged_attention_workspace.restype = sz
+    L.sv_paged_attention.argtypes = ([vp, vp, i64, i64, i32, vp, vp] + [i32] * 9 +
+                                     [f32, vp, i32, vp, vp, vp, vp, sz, vp])
+    L.sv_paged_attention.restype = i32
     L.sv_last_error.argtypes = []
     L.sv_last_error.restype = C.c_char_p
     L.sv_launch_count.argtypes = []
@@ -355,6 +361,58 @@ def sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sam
         _stream(stream)))
 
 
+def _pages(kv, lead):
+    """Strides in elements from K to V and from page to page of a cache
+    [..., 2][P][page][Hkv][D] with ``lead`` dimensions before the 2."""
+    if kv.dim() != lead + 5 or kv.shape[lead] != 2:
+        raise ValueError(f"kv: need [{'L, ' * lead}2, pages, page, Hkv, D], got {tuple(kv.shape)}")
+    P, page, H, D = kv.shape[lead + 1:]
+    sk, sp, sr, sh, sd = kv.stride()[lead:]
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (page > 1 and sr != H * D):
+        raise ValueError(f"kv: the rows of a page must be packed, got strides {kv.stride()}")
+    return sk, (sp if P > 1 else page * H * D)
+
+
+def sv_paged_attention_workspace(B, Hq, Hkv, D, page, max_pages, window=0, sinks=0, weights=False):
+    return int(load_library().sv_paged_attention_workspace(B, Hq, Hkv, D, page, max_pages, window,
+                                                           sinks, 1 if weights else 0))
+
+
+def sv_paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_sum, out,
+                       out_lse=None, out_status=None, workspace=None, stream=None):
+    """q [B][Hq][D]; kv [2][pages][page][Hkv][D], the first two dimensions in
+    any order of strides; weight_sum [B][Hkv][S] or None."""
+    B, Hq, D = q.shape
+    kv_stride, page_stride = _pages(kv, 0)
+    P, page, Hkv, Dk = kv.shape[1:]
+    if kv.dtype != q.dtype or Dk != D:
+        raise ValueError(f"kv: {kv.dtype} rows of {Dk}, q has {q.dtype} rows of {D}")
+    dt = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported cache dtype {q.dtype}")
+    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    _want("q", q, q.dtype, (B, Hq, D))
+    _want("block_table", block_table, torch.int32, (B, max_pages))
+    _want("seq_len", seq_len, torch.int32, (B,))
+    _want("out", out, q.dtype, (B, Hq, D))
+    S = 0
+    if weight_sum is not None:
+        S = weight_sum.shape[-1]
+        _want("weight_sum", weight_sum, torch.float32, (B, Hkv, S))
+    if out_lse is not None:
+        _want("out_lse", out_lse, torch.float32, (B, Hq))
+    if out_status is not None:
+        _want("out_status", out_status, torch.int32, (B,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor")
+    return _check(load_library().sv_paged_attention(
+        _p(q), _p(kv), kv_stride, page_stride, dt, _p(block_table), _p(seq_len), B, Hq, Hkv, D,
+        page, max_pages, P, int(window), int(sinks), float(scale), _p(weight_sum), S, _p(out),
+        _p(out_lse), _p(out_status), _p(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
 def sv_last_error():
     return load_library().sv_last_error().decode()
 
@@ -455,6 +513,30 @@ def verify_chain_probs(qprobs, pprobs, draft_tokens, u_accept, u_sample, n_draft
     sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample,
                           out["tokens"], out["accept_len"], out["status"], stream)
     return out
+
+
+def paged_attention(q, kv, block_table, seq_len, scale=None, window=0, sinks=0, weight_sum=None,
+                    return_lse=False, workspace=None, stream=None):
+    """One new token's attention over a paged cache (see sv_paged_attention):
+    q [B][Hq][D], kv [2][pages][page][Hkv][D] (one layer), block_table int32
+    [B][max_pages], seq_len int32 [B]; scale defaults to 1/sqrt(D); window and
+    sinks narrow the visible slots; weight_sum fp32 [B][Hkv][S] gets the
+    attention weights added.  Returns out (like q), and with return_lse the
+    log-sum-exp [B][Hq] and the status words [B]."""
+    B, Hq, D = q.shape
+    dev = _out_dev(q)
+    with _allocating(stream):
+        out = torch.empty(B, Hq, D, dtype=q.dtype, device=dev)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
+        status = torch.empty(B, dtype=torch.int32, device=dev) if return_lse else None
+        if workspace is None and kv.dim() == 5 and block_table.dim() == 2:
+            workspace = _ws(sv_paged_attention_workspace(
+                B, Hq, kv.shape[3], D, kv.shape[2], block_table.shape[1], window, sinks,
+                weight_sum is not None), dev)
+    sv_paged_attention(q, kv, block_table, seq_len, window, sinks,
+                       D ** -0.5 if scale is None else scale, weight_sum, out, lse, status,
+                       workspace, stream)
+    return (out, lse, status) if return_lse else out
 
 
 def tree_expand(dlogits, frontier_score, K, temperature=1.0, stream=None):

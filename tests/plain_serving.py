@@ -104,3 +104,38 @@ def verify_probs(q, p, d, ua, us, n=None):
         tokens[b, :len(t)] = t
         alen[b], status[b] = a, s
     return tokens, alen, status
+
+
+# ------------------------------------------------------- paged decode attention
+def visible_slots(n, window, sinks):
+    j = np.arange(n)
+    return j[(j >= n - window) | (j < sinks)] if window else j
+
+
+def paged_attention(q, kv, table, lens, scale, window=0, sinks=0):
+    """q [B][Hq][D], kv [2][P][page][Hkv][D], both float64; returns out, lse,
+    the weight each slot received [B][Hkv][cap], and per (b, h) the bound
+    max_j scale sum_d |q_d k_d| that error bounds are made of."""
+    B, Hq, D = q.shape
+    page, Hkv = kv.shape[2], kv.shape[3]
+    G = Hq // Hkv
+    cap = table.shape[1] * page
+    out, lse = np.zeros((B, Hq, D)), np.full((B, Hq), -np.inf)
+    got, size = np.zeros((B, Hkv, cap)), np.zeros((B, Hq))
+    for b in range(B):
+        j = visible_slots(int(lens[b]), window, sinks)
+        if not len(j):
+            continue
+        k, v = kv[0][table[b, j // page], j % page], kv[1][table[b, j // page], j % page]
+        for h in range(Hq):
+            s = scale * (k[:, h // G] @ q[b, h])
+            size[b, h] = scale * (np.abs(k[:, h // G]) @ np.abs(q[b, h])).max()
+            m = s.max()
+            if m == -np.inf:
+                continue
+            e = np.exp(s - m)
+            l = e.sum()
+            lse[b, h] = m + np.log(l)
+            out[b, h] = (e / l) @ v[:, h // G]
+            got[b, h // G, j] += e / l
+    return out, lse, got, size

@@ -1,0 +1,307 @@
+"""sv_paged_attention against the plain definition in 64 bits
+(tests/plain_serving.py).
+
+Tolerances, from the arithmetic (u = 2^-24, d = relative error of a weight):
+a score is an fp32 sum of D exact products, off by at most D u A with
+A = scale sum |q_d k_d|, and two more roundings of |s| <= A; the base-2
+exponential adds 2^-22; the weights' sum over n slots n u.  So
+d <= (D + 4) u A + 2^-22 + n u for a weight relative to its row's largest, and
+the same bounds ln l.  The weights enter the product with the values as two
+parts of the cache's type, off by eps^2 / 4 <= 2^-18 at most.  An output is a
+weighted mean of values: off by 2 d max|v| + 2^-17 max|v|, and by half a unit
+of its own type, 2^-8 (bf16) or 2^-11 (fp16) of its value (fp16: 2^-25 near
+zero)."""
+import numpy as np
+import pytest
+import torch
+
+import plain_serving as plain
+
+pytestmark = pytest.mark.gpu
+
+sv = pytest.importorskip("speculative_decoding_verification_vocab_gb300")
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load_library()
+
+
+def make(lens, Hq, Hkv, D, page, dtype=torch.bfloat16, seed=0, window=0, sinks=0, spare=2,
+         extra_pages=1, sigma=1.5):
+    """CPU inputs; NaN in every slot that is not visible, -1 for every table
+    entry without one."""
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    per = max(1, -(-max(lens) // page)) + extra_pages
+    P = B * per + spare
+    q = (torch.randn(B, Hq, D, generator=g) * sigma).to(dtype)
+    full = torch.randn(2, P, page, Hkv, D, generator=g).to(dtype)
+    kv = torch.full_like(full, float("nan"))
+    table = torch.full((B, per), -1, dtype=torch.int32)
+    ids = torch.randperm(P, generator=g)
+    for b, n in enumerate(lens):
+        j = torch.from_numpy(plain.visible_slots(n, window, sinks))
+        own = ids[b * per:(b + 1) * per]
+        table[b, j // page] = own[j // page].int()
+        kv[:, own[j // page], j % page] = full[:, own[j // page], j % page]
+    return q, kv, table, torch.tensor(lens, dtype=torch.int32)
+
+
+def reference(q, kv, table, lens, scale, window=0, sinks=0):
+    return plain.paged_attention(q.double().numpy(), kv.double().numpy(), table.numpy(),
+                                 lens.numpy(), scale, window, sinks)
+
+
+def check(q, kv, table, lens, scale=None, window=0, sinks=0, weights=False, **kw):
+    B, Hq, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    page, Hkv = kv.shape[2], kv.shape[3]
+    sums = None
+    if weights:
+        sums = torch.rand(B, Hkv, table.shape[1] * page + 3, generator=torch.Generator().manual_seed(3))
+    dev_sums = None if sums is None else sums.to(DEV)
+    out, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table.to(DEV), lens.to(DEV), scale,
+                                      window, sinks, dev_sums, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert not st.any()
+    ref, rlse, got, size = reference(q, kv, table, lens, scale, window, sinks)
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(l), np.isneginf(rlse))
+    n = np.maximum(lens.numpy().astype(np.float64), 1)[:, None]
+    d = (D + 4) * U * size + 2.0 ** -22 + n * U
+    fin = np.isfinite(rlse)
+    lerr = np.abs(np.where(fin, l, 0) - np.where(fin, rlse, 0))
+    assert (lerr <= d + 4 * U * np.abs(np.where(fin, rlse, 0))).all(), lerr.max()
+    vmax = np.nan_to_num(kv[1].double().abs().numpy(), nan=0.0).max()
+    half = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -11
+    tol = half * np.abs(ref) + (2 * d + 2.0 ** -17)[..., None] * vmax + 2.0 ** -25
+    err = np.abs(o - ref)
+    assert (err <= tol).all(), (err - tol).max()
+    if weights:
+        s, before = dev_sums.double().cpu().numpy(), sums.double().numpy()
+        cap = table.shape[1] * page
+        G = Hq // Hkv
+        dk = d.reshape(B, Hkv, G).max(-1)[..., None]
+        lmax = np.abs(np.where(fin, rlse, 0)).reshape(B, Hkv, G).max(-1)[..., None]
+        bound = got * (2 * dk + 8 * U * lmax + G * U) + U * (before[..., :cap] + got)
+        assert (np.abs(s[..., :cap] - before[..., :cap] - got) <= bound).all()
+        untouched = got == 0
+        assert np.array_equal(s[..., :cap][untouched], before[..., :cap][untouched])
+        assert np.array_equal(s[..., cap:], before[..., cap:])
+    return out, lse, dev_sums
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,Hq,Hkv,page", [
+    ([1], 1, 1, 16),                         # one slot: the value itself
+    ([5, 0, 64, 65, 17], 8, 2, 16),          # an empty sequence; tile edges; G = 4
+    ([130, 1, 63], 3, 3, 1),                 # G = 1, pages of one slot
+    ([200, 333], 14, 2, 24),                 # G = 7, pages that end inside a tile
+    ([129, 700], 32, 2, 128),                # G = 16
+    ([77, 300], 20, 1, 33),                  # G = 20: two groups of query heads
+])
+def test_matches_the_definition(lens, Hq, Hkv, page, D, dtype):
+    check(*make(lens, Hq, Hkv, D, page, dtype, seed=D + page))
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (64, 4), (100, 1), (63, 70), (5000, 4), (1, 1)])
+def test_window_and_first_tokens(window, sinks):
+    lens = [0, 1, 2, 64, 65, 103, 104, 105, 500, 1111]
+    check(*make(lens, 8, 2, 64, 16, seed=window, window=window, sinks=sinks), window=window,
+          sinks=sinks)
+    check(*make(lens, 4, 4, 128, 7, torch.float16, seed=window, window=window, sinks=sinks),
+          window=window, sinks=sinks, weights=True)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page", [
+    ([40000], 8, 1, 128, 64),                # one long sequence: split and joined
+    ([9001, 3], 16, 8, 64, 16),
+    ([12000, 1, 5000], 6, 2, 256, 20),
+    ([3000] * 9, 4, 4, 128, 32),
+])
+def test_split_over_the_length(lens, Hq, Hkv, D, page):
+    check(*make(lens, Hq, Hkv, D, page, seed=7), weights=True)
+
+
+@pytest.mark.parametrize("B", [130, 700])
+def test_many_sequences(B):
+    """More sequences than threads; ragged, with empty ones."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    lens[B // 2] = 3000
+    check(*make(lens, 2, 1, 64, 16, seed=B), weights=B == 130)
+
+
+def test_more_sequences_than_are_split():
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 5, 2100)]
+    lens[2099] = 400
+    check(*make(lens, 2, 1, 64, 16, seed=5, extra_pages=0))
+
+
+def test_sharp_scores_and_growing_maxima():
+    """Scores that grow along the slots (every tile raises the maximum), and
+    one slot that takes all the weight."""
+    q, kv, table, lens = make([1500], 4, 1, 128, 16, seed=3)
+    base = q[0, 0].float()
+    for j in range(1500):
+        kv[0, table[0, j // 16], j % 16, 0] = (base * (j / 1500) * 0.2).to(q.dtype)
+    q[0] = base.to(q.dtype)
+    check(q, kv, table, lens, weights=True)
+    check(q, kv, table, lens, scale=2.0)
+    kv[0, table[0, 40], 3, 0] = (base * 2).to(q.dtype)
+    check(q, kv, table, lens, scale=1.0, weights=True)
+
+
+def test_infinities_and_nan_in_the_data():
+    q, kv, table, lens = make([100, 100, 100, 700], 4, 2, 64, 16, seed=4)
+    q = q.abs() + 0.1
+    inf = float("inf")
+    kv[0, table[0, 2], 5, 0] = -inf            # a score of -inf: weight 0
+    kv[0, table[1, :7].long(), :, 1] = -inf    # a head with no finite score
+    kv[0, table[2, 0], 0, 0] = float("nan")    # NaN: that head's rows are NaN
+    kv[0, table[3, 43], 5, 1] = inf
+    sums = torch.zeros(4, 2, table.shape[1] * 16, device=DEV)
+    out, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table.to(DEV), lens.to(DEV),
+                                      weight_sum=sums, return_lse=True)
+    assert not st.any()
+    ref, rlse, got, _ = reference(q[:2], kv, table[:2], lens[:2], 64 ** -0.5)
+    o = out.double().cpu().numpy()
+    assert np.abs(o[:2] - ref).max() < 0.05
+    assert (o[1, 2:] == 0).all() and torch.isneginf(lse[1, 2:]).all() and (sums[1, 1] == 0).all()
+    assert float(sums[0, 0, 2 * 16 + 5]) == 0.0
+    assert np.isnan(o[2, :2]).all() and np.isfinite(o[2, 2:]).all()
+    assert np.isnan(o[3, 2:]).all() and np.isfinite(o[3, :2]).all()
+    assert torch.isnan(lse[2, :2]).all() and torch.isnan(lse[3, 2:]).all()
+    assert torch.isnan(sums[2, 0, :100]).all() and (sums[2, 0, 100:] == 0).all()
+
+
+@pytest.mark.parametrize("n", [40, 5000])
+def test_bad_lengths_and_pages(n):
+    """Refused per sequence: NaN rows and a status bit, weight_sum untouched,
+    the other sequences as if alone."""
+    q, kv, table, lens = make([n] * 6, 4, 2, 128, 16, seed=6)
+    cap = table.shape[1] * 16
+    want, wlse = [t.clone() for t in sv.paged_attention(
+        q.to(DEV), kv.to(DEV), table.to(DEV), lens.to(DEV), return_lse=True)[:2]]
+    P = kv.shape[1]
+    lens[0], lens[1] = -1, cap + 1
+    table[2, 0], table[3, (n - 1) // 16] = P, -1
+    table[4, (n - 1) // 16] = 2 ** 31 - 1
+    table[5, -1] = -7                          # not needed: anything may stand there
+    sums = torch.rand(6, 2, cap, device=DEV)
+    before = sums.clone()
+    out, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table.to(DEV), lens.to(DEV),
+                                      weight_sum=sums, return_lse=True)
+    L, G = sv.SV_ROW_BAD_LEN, sv.SV_ROW_BAD_PAGE
+    assert st.tolist() == [L, L, G, G, G, 0]
+    assert torch.isnan(out[:5]).all() and torch.isnan(lse[:5]).all()
+    assert torch.equal(sums[:5], before[:5]) and not torch.equal(sums[5], before[5])
+    if n == 40:
+        assert torch.equal(out[5], want[5]) and torch.equal(lse[5], wlse[5])
+    else:                                      # split otherwise: equal within the output's half unit
+        assert torch.allclose(out[5].float(), want[5].float(), rtol=2.0 ** -7, atol=1e-4)
+
+
+def test_layouts_agree_bit_for_bit():
+    """[2][P] and [P][2] orders, a pool inside a larger one, other page ids."""
+    q, kv, table, lens = make([300, 777], 8, 2, 128, 16, seed=8)
+    d = [t.to(DEV) for t in (q, kv, table, lens)]
+    want = sv.paged_attention(*d).clone()
+    by_page = d[1].transpose(0, 1).contiguous().transpose(0, 1)
+    assert by_page.stride(1) > by_page.stride(0)
+    assert torch.equal(sv.paged_attention(d[0], by_page, d[2], d[3]), want)
+    wide = torch.full((2, 2 * kv.shape[1], 16, 2, 128), float("nan"), dtype=q.dtype, device=DEV)
+    wide[:, ::2] = d[1]
+    assert torch.equal(sv.paged_attention(d[0], wide[:, ::2], d[2], d[3]), want)
+    layers = torch.zeros(3, *kv.shape, dtype=q.dtype, device=DEV)
+    layers[1] = d[1]
+    assert torch.equal(sv.paged_attention(d[0], layers[1], d[2], d[3]), want)
+    table[1, :10] = table[0, :10]              # shared pages: a common prefix
+    check(q, kv, table, lens)
+
+
+def test_rows_of_the_output_alone_are_written():
+    q, kv, table, lens = make([100, 50], 8, 2, 64, 16, seed=9)
+    d = [t.to(DEV) for t in (q, kv, table, lens)]
+    ws = torch.empty(sv.sv_paged_attention_workspace(2, 8, 2, 64, 16, table.shape[1]),
+                     dtype=torch.uint8, device=DEV)
+    out = torch.full((4, 8, 64), 7.0, dtype=q.dtype, device=DEV)
+    lse = torch.full((4, 8), 7.0, device=DEV)
+    st = torch.full((4,), 7, dtype=torch.int32, device=DEV)
+    sv.sv_paged_attention(*d, 0, 0, 0.125, None, out[1:3], lse[1:3], st[1:3], ws)
+    want, wl, _ = sv.paged_attention(*d, scale=0.125, return_lse=True)
+    assert torch.equal(out[1:3], want) and torch.equal(lse[1:3], wl) and st.tolist() == [7, 0, 0, 7]
+    for t in (out, lse):
+        assert (t[0] == 7).all() and (t[3] == 7).all()
+
+
+def test_repeats_streams_and_graphs():
+    """The same bits from run to run, on two streams at once with a workspace
+    each, and from a captured graph whose lengths grow between replays."""
+    q, kv, table, lens = make([4000, 9, 2500], 16, 2, 128, 16, seed=10)
+    d = [t.to(DEV) for t in (q, kv, table, lens)]
+    kv2 = torch.nan_to_num(d[1], nan=0.5)
+    table2 = torch.arange(3 * table.shape[1], dtype=torch.int32, device=DEV).view(3, -1)
+    args = (d[0], kv2, table2, d[3])
+    want = sv.paged_attention(*args).clone()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        a, b = sv.paged_attention(*args, stream=s1), sv.paged_attention(*args, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want)
+    ln = d[3].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = sv.paged_attention(d[0], kv2, table2, ln)
+    for step in (0, 1, 16):
+        ln.copy_(d[3] + step)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, sv.paged_attention(d[0], kv2, table2, ln)), step
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 elements whose last pages are the ones used."""
+    page, Hkv, D = 64, 8, 128
+    P = (1 << 32) // (page * Hkv * D) + 40
+    kv = torch.empty(2, P, page, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q, small, table, lens = make([900, 1300], 8, 8, D, page, seed=11)
+    n = small.shape[1]
+    kv[:, P - n:] = small.to(DEV)
+    want = sv.paged_attention(q.to(DEV), small.to(DEV), table.to(DEV), lens.to(DEV))
+    moved = torch.where(table >= 0, table + (P - n), table)
+    got = sv.paged_attention(q.to(DEV), kv, moved.to(DEV), lens.to(DEV))
+    assert torch.equal(got, want)
+
+
+def test_the_layer_of_the_dynamic_tree_workload():
+    """64 query heads on 8 KV heads of 128 over about 4096 tokens, 128
+    sequences; a few of them replayed."""
+    B, page = 128, 16
+    g = torch.Generator(device=DEV).manual_seed(2)
+    lens = torch.randint(3585, 4097, (B,), generator=g, device=DEV, dtype=torch.int32)
+    kv = torch.empty(2, B * 256, page, 8, 128, dtype=torch.bfloat16, device=DEV)
+    kv.normal_(generator=g)
+    table = torch.randperm(B * 256, generator=g, device=DEV).to(torch.int32).view(B, 256)
+    q = torch.randn(B, 64, 128, generator=g, device=DEV).to(torch.bfloat16)
+    sums = torch.zeros(B, 8, 4096, device=DEV)
+    out, lse, st = sv.paged_attention(q, kv, table, lens, weight_sum=sums, return_lse=True)
+    assert not st.any()
+    assert torch.allclose(sums.sum(-1), torch.full((B, 8), 8.0, device=DEV), atol=1e-4)
+    for b in (0, 63, 127):
+        own = table[b].long()
+        small = kv[:, own].cpu()
+        t = torch.arange(256, dtype=torch.int32)[None]
+        ref, rlse, got, size = reference(q[b:b + 1].cpu(), small, t, lens[b:b + 1].cpu(), 128 ** -0.5)
+        d = (128 + 4) * U * size.max() + 2.0 ** -22 + 4096 * U
+        tol = 2.0 ** -8 * np.abs(ref) + (2 * d + 2.0 ** -17) * 6
+        assert (np.abs(out[b:b + 1].double().cpu().numpy() - ref) <= tol).all()
+        assert np.abs(lse[b:b + 1].double().cpu().numpy() - rlse).max() <= d + 60 * U

@@ -98,3 +98,71 @@ def test_verify_probs_binding_refusals(sv):
     call(n=torch.zeros(3, dtype=torch.int32))
     call(d=torch.zeros(2, 4, dtype=torch.int32)[:, ::2])
     call()                                                 # pageable host memory
+
+
+def test_paged_attention_plain_equals_dense_attention():
+    """The plain paged form against torch's dense attention on gathered rows,
+    with and without a window."""
+    g = torch.Generator().manual_seed(0)
+    q = torch.randn(2, 6, 32, generator=g, dtype=torch.float64)
+    kv = torch.randn(2, 9, 5, 2, 32, generator=g, dtype=torch.float64)
+    table = torch.randperm(9, generator=g)[:8].view(2, 4)
+    for window, sinks, lens in ((0, 0, [17, 3]), (6, 2, [20, 7])):
+        out, lse, got, _ = plain.paged_attention(q.numpy(), kv.numpy(), table.numpy(),
+                                                 np.array(lens), 0.2, window, sinks)
+        for b in range(2):
+            n = lens[b]
+            rows = kv[:, table[b]].reshape(2, 20, 2, 32)[:, :n].repeat_interleave(3, 2)
+            seen = torch.tensor([window == 0 or j >= n - window or j < sinks for j in range(n)])
+            want = torch.nn.functional.scaled_dot_product_attention(
+                q[b][:, None], rows[0].transpose(0, 1), rows[1].transpose(0, 1),
+                attn_mask=seen[None, None], scale=0.2)[:, 0]
+            assert np.allclose(out[b], want.numpy(), atol=1e-12)
+            assert np.allclose(got[b].sum(-1), 3) and not got[b][:, :n][:, ~seen.numpy()].any()
+
+
+def test_paged_attention_host_checks(sv):
+    lib = sv.load_library()
+    f, x = lib.sv_paged_attention, 4096
+
+    def call(q=x, kv=x, ks=1 << 20, ps=16 * 2 * 128, dt=1, table=x, lens=x, B=1, Hq=8, Hkv=2, D=128,
+             page=16, mp=4, P=8, window=0, sinks=0, scale=1.0, w=None, S=0, out=x, lse=None, st=None,
+             ws=x, wb=1 << 30):
+        return f(q, kv, ks, ps, dt, table, lens, B, Hq, Hkv, D, page, mp, P, window, sinks, scale, w, S,
+                 out, lse, st, ws, wb, None)
+    assert call(B=-1) == 1 and call(Hq=9) == 1 and call(page=0) == 1 and call(mp=0) == 1
+    assert call(P=0) == 1 and call(window=-1) == 1 and call(sinks=-1) == 1 and call(Hkv=0) == 1
+    assert call(dt=0) == 1 and call(D=96) == 2 and b"head dimension" in lib.sv_last_error()
+    assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
+    assert call(page=1 << 20, mp=1 << 11, ps=1 << 40) == 2
+    assert call(ps=16 * 2 * 128 - 8) == 1 and call(ps=16 * 2 * 128 + 4) == 1 and call(ks=-8) == 1
+    assert call(w=x, S=63) == 1 and b"weight_sum" in lib.sv_last_error()
+    assert call(q=None) == 1 and call(kv=None) == 1 and call(table=None) == 1
+    assert call(lens=None) == 1 and call(out=None) == 1
+    assert call(q=x + 8) == 1 and call(out=x + 2) == 1 and call(lens=x + 2) == 1
+    assert call(mp=400, P=800, wb=16) == 1 and b"workspace" in lib.sv_last_error()
+    assert call(B=0, q=None, kv=None) == 0
+    ws = sv.sv_paged_attention_workspace
+    assert ws(1, 8, 2, 128, 16, 4) == 0 or ws(1, 8, 2, 128, 16, 4) > 0
+    assert ws(4, 8, 2, 128, 16, 400, weights=True) > ws(4, 8, 2, 128, 16, 400) > 0
+    assert ws(4, 9, 2, 128, 16, 400) == 0 and ws(4, 8, 2, 128, 1 << 20, 1 << 11) == 0
+    # a window bounds what is kept aside
+    assert ws(4, 8, 2, 128, 16, 4000, 64, 4, True) < ws(4, 8, 2, 128, 16, 4000, 0, 0, True)
+
+
+def test_paged_attention_binding_refusals(sv):
+    bf = torch.bfloat16
+    q, kv = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, 6, 16, 2, 64, dtype=bf)
+    t, n = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+
+    def call(q=q, kv=kv, t=t, n=n, w=None, out=None, lse=None, st=None):
+        with pytest.raises(ValueError):
+            sv.sv_paged_attention(q, kv, t, n, 0, 0, 1.0, w, torch.empty_like(q) if out is None else out,
+                                  lse, st)
+    call(q=q.half()), call(q=q.float(), kv=kv.float()), call(kv=kv[..., :32])
+    call(kv=kv.transpose(2, 3)), call(kv=kv[0]), call(kv=kv[:1])
+    call(q=torch.zeros(2, 64, 8, dtype=bf).transpose(1, 2))
+    call(t=t.long()), call(t=t[0]), call(n=n[:1]), call(n=n.long())
+    call(w=torch.zeros(2, 8, 48)), call(w=torch.zeros(2, 2, 48, dtype=torch.float64))
+    call(out=torch.zeros(2, 8, 64)), call(lse=torch.zeros(8, 2)), call(st=torch.zeros(2))
+    call()                                                 # pageable host memory
