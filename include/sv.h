@@ -510,6 +510,46 @@ sv_status sv_paged_attention(const void *q, const void *kv, int64_t kv_stride,
                              uint32_t *out_status, void *workspace, size_t workspace_bytes,
                              void *stream);
 
+/* ---------------------------------------------------------------------------
+ * sv_kv_evict -- bring a paged KV cache back under a budget by the attention
+ * its slots received.  [Lesson] "Reversão de KV cache" (a physical cache with a
+ * logical length); the pages leave the choice of the rows open.
+ *
+ * For every layer l, sequence b and KV head h on its own, with n = seq_len[b]:
+ * if n > budget, the slots kept are the first `sinks`, the last `recent`, and
+ * of those between the budget - sinks - recent with the largest weight_sum
+ * (equal ones: the lower slot; -0 equals 0; NaN below everything).  In
+ * ascending order kept[0] < kept[1] < ..., slot k takes the K and V row and
+ * the weight of slot kept[k], k < budget, in place; weights of slots
+ * [budget, n) become 0, the rows there stay as they are.  n <= budget moves
+ * nothing (kept[k] = k).
+ *
+ *   kv    the cache of sv_paged_attention with a layer dimension in front:
+ *         layer l starts layer_stride elements further; elem_bytes per
+ *         element, D elem_bytes a multiple of 4 (of 16, with 16-byte-aligned
+ *         kv and strides, is faster).  Every page a sequence uses belongs to
+ *         it alone and appears once in its table: a page that does not ends
+ *         with one of the rows that were to move there
+ *   weight_sum fp32 [L][B][Hkv][S], S >= max_pages page (what
+ *         sv_paged_attention adds up); out_weight_sum the same, or weight_sum
+ *         itself: its first n slots are written, the others left
+ *   out_kept   int32 [L][B][Hkv][budget]: the slots kept, then -1
+ *   out_kv_len int32 [B]: min(n, budget)
+ *   out_status uint32 [B] or NULL, written in full
+ * A length outside [0, max_pages page] (SV_ROW_BAD_LEN) or a page of the
+ * sequence outside [0, num_pages) (SV_ROW_BAD_PAGE) moves nothing: kept -1,
+ * out_kv_len -1, weights untouched.  budget >= 1, sinks + recent <= budget.
+ * The workspace is written before it is read; overlapping calls need one each.
+ * --------------------------------------------------------------------------- */
+size_t sv_kv_evict_workspace(int L, int B, int Hkv, int budget);
+sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stride, int64_t page_stride,
+                      int elem_bytes, const int32_t *block_table, const int32_t *seq_len,
+                      const float *weight_sum, float *out_weight_sum, int L, int B, int Hkv,
+                      int D, int page, int max_pages, int num_pages, int S, int budget,
+                      int sinks, int recent, int32_t *out_kept, int32_t *out_kv_len,
+                      uint32_t *out_status, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /* Thread-local message for the last non-OK status returned on this thread. */
 const char *sv_last_error(void);
 

@@ -32,7 +32,8 @@ EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_ve
            "sv_verify_tree", "sv_tree_build_mask", "sv_kv_compact", "sv_tree_attention", "sv_tree_attention_ex", "sv_last_error",
            "sv_launch_count", "sv_trace_enable", "sv_trace_collect", "sv_tree_expand",
            "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs",
-           "sv_paged_attention_workspace", "sv_paged_attention")
+           "sv_paged_attention_workspace", "sv_paged_attention", "sv_kv_evict_workspace",
+           "sv_kv_evict")
 
 
 class SvError(RuntimeError):
@@ -108,6 +109,11 @@ def load_library(path: str = LIB_PATH):
     L.sv_paged_attention.argtypes = ([vp, vp, i64, i64, i32, vp, vp] + [i32] * 9 +
                                      [f32, vp, i32, vp, vp, vp, vp, sz, vp])
     L.sv_paged_attention.restype = i32
+    L.sv_kv_evict_workspace.argtypes = [i32] * 4
+    L.sv_kv_evict_workspace.restype = sz
+    L.sv_kv_evict.argtypes = ([vp, i64, i64, i64, i32, vp, vp, vp, vp] + [i32] * 11 +
+                              [vp, vp, vp, vp, sz, vp])
+    L.sv_kv_evict.restype = i32
     L.sv_last_error.argtypes = []
     L.sv_last_error.restype = C.c_char_p
     L.sv_launch_count.argtypes = []
@@ -413,6 +419,37 @@ def sv_paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight
         _stream(stream)))
 
 
+def sv_kv_evict_workspace(L, B, Hkv, budget):
+    return int(load_library().sv_kv_evict_workspace(L, B, Hkv, budget))
+
+
+def sv_kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sinks, recent,
+                out_kept, out_kv_len, out_status=None, workspace=None, stream=None):
+    """kv [L][2][pages][page][Hkv][D], moved in place; weight_sum and
+    out_weight_sum [L][B][Hkv][S] (may be the same tensor)."""
+    kv_stride, page_stride = _pages(kv, 1)
+    L, _, P, page, Hkv, D = kv.shape
+    B, max_pages = block_table.shape if block_table.dim() == 2 else (seq_len.shape[0], 0)
+    S = weight_sum.shape[-1]
+    _want("block_table", block_table, torch.int32, (B, max_pages))
+    _want("seq_len", seq_len, torch.int32, (B,))
+    _want("weight_sum", weight_sum, torch.float32, (L, B, Hkv, S))
+    _want("out_weight_sum", out_weight_sum, torch.float32, (L, B, Hkv, S))
+    _want("out_kept", out_kept, torch.int32, (L, B, Hkv, int(budget)))
+    _want("out_kv_len", out_kv_len, torch.int32, (B,))
+    if out_status is not None:
+        _want("out_status", out_status, torch.int32, (B,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor")
+    return _check(load_library().sv_kv_evict(
+        _p(kv), kv.stride(0) if L > 1 else 0, kv_stride, page_stride, kv.element_size(),
+        _p(block_table), _p(seq_len), _p(weight_sum), _p(out_weight_sum), L, B, Hkv, D, page,
+        max_pages, P, S, int(budget), int(sinks), int(recent), _p(out_kept), _p(out_kv_len),
+        _p(out_status), _p(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
 def sv_last_error():
     return load_library().sv_last_error().decode()
 
@@ -537,6 +574,29 @@ def paged_attention(q, kv, block_table, seq_len, scale=None, window=0, sinks=0, 
                        D ** -0.5 if scale is None else scale, weight_sum, out, lse, status,
                        workspace, stream)
     return (out, lse, status) if return_lse else out
+
+
+def kv_evict(kv, block_table, seq_len, weight_sum, budget, sinks=0, recent=0, out_weight_sum=None,
+             workspace=None, stream=None):
+    """Bring a paged cache kv [L][2][pages][page][Hkv][D] under ``budget`` slots
+    per sequence (see sv_kv_evict), in place: the first ``sinks``, the last
+    ``recent`` and the most attended slots between stay.  weight_sum fp32
+    [L][B][Hkv][S] follows its slots, into out_weight_sum (None: in place).
+    Returns the kept slots [L][B][Hkv][budget], the new lengths [B] and the
+    status words [B]."""
+    L, Hkv, B = kv.shape[0], kv.shape[-2], seq_len.shape[0]
+    budget = int(budget)
+    dev = _out_dev(kv)
+    with _allocating(stream):
+        kept = torch.empty(L, B, Hkv, max(budget, 0), dtype=torch.int32, device=dev)
+        kv_len = torch.empty(B, dtype=torch.int32, device=dev)
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = _ws(sv_kv_evict_workspace(L, B, Hkv, budget), dev)
+    sv_kv_evict(kv, block_table, seq_len, weight_sum,
+                weight_sum if out_weight_sum is None else out_weight_sum, budget, sinks, recent,
+                kept, kv_len, status, workspace, stream)
+    return kept, kv_len, status
 
 
 def tree_expand(dlogits, frontier_score, K, temperature=1.0, stream=None):

@@ -139,3 +139,37 @@ def paged_attention(q, kv, table, lens, scale, window=0, sinks=0):
             out[b, h] = (e / l) @ v[:, h // G]
             got[b, h // G, j] += e / l
     return out, lse, got, size
+
+
+# -------------------------------------------------------------------- eviction
+def kept_slots(w, n, budget, sinks, recent):
+    """The slots kept of one (layer, sequence, head): w its weights."""
+    if n <= budget:
+        return list(range(n))
+    def place(j):
+        x = w[j]
+        return (1, 0.0, j) if x != x else (0, -float(x), j)
+    mid = sorted(range(sinks, n - recent), key=place)[:budget - sinks - recent]
+    return list(range(sinks)) + sorted(mid) + list(range(n - recent, n))
+
+
+def kv_evict(kv, table, lens, w, budget, sinks, recent):
+    """kv [L][2][P][page][H][D] (any dtype), w [L][B][H][S]: copies of both
+    after the eviction, the kept slots and the new lengths."""
+    kv, w = kv.copy(), w.copy()
+    L, B, H, _ = w.shape
+    page = kv.shape[3]
+    kept = np.full((L, B, H, budget), -1, np.int32)
+    for b in range(B):
+        n = int(lens[b])
+        for l in range(L):
+            for h in range(H):
+                k = np.array(kept_slots(w[l, b, h], n, budget, sinks, recent), np.int64)
+                kept[l, b, h, :len(k)] = k
+                if n > budget:
+                    to = np.arange(budget)
+                    rows = kv[l][:, table[b, k // page], k % page, h].copy()
+                    kv[l][:, table[b, to // page], to % page, h] = rows
+                    w[l, b, h, :budget] = w[l, b, h, k]
+                    w[l, b, h, budget:n] = 0
+    return kv, w, kept, np.minimum(lens, budget).astype(np.int32)

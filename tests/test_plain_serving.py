@@ -166,3 +166,56 @@ def test_paged_attention_binding_refusals(sv):
     call(w=torch.zeros(2, 8, 48)), call(w=torch.zeros(2, 2, 48, dtype=torch.float64))
     call(out=torch.zeros(2, 8, 64)), call(lse=torch.zeros(8, 2)), call(st=torch.zeros(2))
     call()                                                 # pageable host memory
+
+
+def test_kept_slots_by_hand():
+    w = np.array([5, 0, 3, 3, 9, 1, 3, 2], np.float32)
+    assert plain.kept_slots(w, 8, 8, 1, 1) == list(range(8))
+    assert plain.kept_slots(w, 8, 5, 1, 1) == [0, 2, 3, 4, 7]      # the tie at 3: the lower slots
+    assert plain.kept_slots(w, 8, 2, 1, 1) == [0, 7]
+    assert plain.kept_slots(w, 8, 3, 0, 0) == [0, 2, 4]
+    w[4] = np.nan
+    assert plain.kept_slots(w, 8, 4, 0, 0) == [0, 2, 3, 6]
+    assert plain.kept_slots(w, 8, 8, 0, 0) == list(range(8)) and 4 not in plain.kept_slots(w, 8, 7, 0, 0)
+
+
+def test_kv_evict_host_checks(sv):
+    lib = sv.load_library()
+    f, x = lib.sv_kv_evict, 4096
+
+    def call(kv=x, ls=1 << 22, ks=1 << 20, ps=16 * 2 * 64, e=2, t=x, n=x, w=x, ow=x, L=2, B=1, H=2, D=64,
+             page=16, mp=4, P=8, S=64, budget=32, sinks=2, recent=4, kept=x, kl=x, st=None, ws=x,
+             wb=1 << 30):
+        return f(kv, ls, ks, ps, e, t, n, w, ow, L, B, H, D, page, mp, P, S, budget, sinks, recent, kept,
+                 kl, st, ws, wb, None)
+    assert call(L=0) == 1 and call(B=-1) == 1 and call(H=0) == 1 and call(D=0) == 1 and call(e=0) == 1
+    assert call(page=0) == 1 and call(mp=0) == 1 and call(P=0) == 1
+    assert call(budget=0) == 1 and call(sinks=-1) == 1 and call(recent=-1) == 1
+    assert call(sinks=30, recent=3) == 1 and b"budget" in lib.sv_last_error()
+    assert call(sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == 1
+    assert call(page=1 << 20, mp=1 << 11, S=2 ** 31 - 1) == 2
+    assert call(S=63) == 1 and call(D=3, e=1, ps=1 << 12) == 2
+    assert call(ps=16 * 2 * 64 - 1) == 1 and call(ks=0) == 1 and call(ls=0) == 1 and call(ls=-4) == 1
+    assert call(ps=2 ** 62) == 1 and call(ls=2 ** 62) == 1
+    for name in ("kv", "t", "n", "w", "ow", "kept", "kl", "ws"):
+        assert call(**{name: None}) == 1 and b"null" in lib.sv_last_error(), name
+    assert call(kv=x + 2) == 1 and call(w=x + 2) == 1 and call(ws=x + 64) == 1
+    assert call(ps=16 * 2 * 64 + 1) == 1 and b"misaligned" in lib.sv_last_error()
+    assert call(wb=100) == 1 and b"workspace" in lib.sv_last_error()
+    assert call(B=0, kv=None, w=None) == 0
+    assert sv.sv_kv_evict_workspace(2, 3, 4, 100) >= 2 * 3 * 4 * 404
+    assert sv.sv_kv_evict_workspace(0, 3, 4, 100) == 0 and sv.sv_kv_evict_workspace(1 << 20, 1 << 10, 8, 9) == 0
+
+
+def test_kv_evict_binding_refusals(sv):
+    kv = torch.zeros(1, 2, 6, 16, 2, 64, dtype=torch.bfloat16)
+    t, n, w = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.zeros(1, 2, 2, 48)
+    kept, kl = torch.zeros(1, 2, 2, 8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+
+    def call(kv=kv, t=t, n=n, w=w, ow=w, budget=8, kept=kept, kl=kl, st=None):
+        with pytest.raises(ValueError):
+            sv.sv_kv_evict(kv, t, n, w, ow, budget, 1, 1, kept, kl, st)
+    call(kv=kv[0]), call(kv=kv.transpose(3, 4)), call(t=t.long()), call(t=t[:1]), call(n=n.float())
+    call(w=w.double()), call(w=w[..., ::2], ow=w), call(ow=w[..., :40]), call(budget=9)
+    call(kept=kept.long()), call(kl=kl[:1]), call(st=torch.zeros(3, dtype=torch.int32))
+    call()                                                 # pageable host memory
