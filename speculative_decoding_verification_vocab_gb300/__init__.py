@@ -131,13 +131,13 @@ def _p(t):
         return None
     if not (t.is_cuda or t.is_pinned()):
         raise ValueError("sv: tensors must be in device memory or page-locked host memory")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    if stream is None:  # the current stream's handle, without a torch.cuda.Stream around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _event(ev):

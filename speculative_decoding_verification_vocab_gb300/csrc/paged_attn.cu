@@ -11,20 +11,25 @@
 //
 // Bound: every visible K and V row is read once (4 D bytes a slot and KV
 // head), 4 D G operations on it: memory, for any G a model has.  The matrix
-// products therefore only have to keep up with HBM (45 GB/s per SM): m16n8k16
-// tensor instructions on registers, with the 16 rows holding the query heads
-// of one KV head, need no staging of S, P or O and no exchange between warps,
-// and take a tenth of what the SM could do.
+// products only have to keep up with HBM (45 GB/s per SM), so they run as
+// m16n8k16 tensor instructions on registers, transposed: S^T = K Q^T with 16
+// keys as rows and 8 (or 16) query heads as columns, O^T = V^T P^T with 16
+// dimensions as rows.  With the keys on the long side no row of an instruction
+// is spent on heads a model does not have (G = 1 to 8 costs the same), and S,
+// P and O never leave a warp's registers.
 //
-// Work: a unit is a run of 64-key tiles of one (sequence, KV head, 16 query
-// heads); KV heads of the same tiles are neighbouring CTAs, so that the D-wide
-// slices of one token's row are read at about the same time.  Each CTA finds
-// its unit from the lengths alone (a sum and a scan over the batch), so the
-// host never sees them and a captured graph follows them.  Within a unit each
-// of the 4 warps owns 16 keys of every tile: it loads them (cp.async, one
-// 16-byte piece per lane, rows found through the page table one tile ahead;
-// slots past the end are zero-filled, never read), multiplies, and keeps its
-// own m, l and O; nothing but the last merge crosses warps.
+// Work: a unit is a run of 64-key tiles of one (sequence, KV head, up to 16
+// query heads); KV heads of the same tiles are neighbouring CTAs, so that the
+// D-wide slices of one token's row are read at about the same time.  Each CTA
+// finds its unit from the lengths alone (a sum and a scan over the batch), so
+// the host never sees them and a captured graph follows them.  Within a unit
+// each of the 4 warps owns 16 keys of every tile: it loads them (cp.async, 16
+// bytes a lane), multiplies, and keeps its own m, l and O; nothing but the last
+// merge crosses warps, and no CTA barrier stands in the loop.
+//
+// Groups of 16 keys start at multiples of 16 slots, so with pages of a multiple
+// of 16 slots one table entry serves a group; other page sizes look up every
+// row.  Rows that are not visible are zero-filled in shared memory, not read.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -36,15 +41,21 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kWarpKeys = 16;
-constexpr int kTile = kWarps * kWarpKeys;  // keys of a CTA tile
-constexpr int kRows = 16;                  // query heads of a unit
-// Units aimed at, and the fewest tiles of one (below that a unit's fixed cost
-// shows).  Batches of kWhole sequences and more are not split.
-constexpr int kUnits = 1216;
-constexpr int kMinTiles = 2;
+constexpr int kGroup = 16;                // keys of a warp in a tile
+constexpr int kTile = kWarps * kGroup;    // keys of a CTA tile
+constexpr int kRows = 16;                 // query heads of a unit, at most
+// CTAs that are resident at once on 152 SMs (2 per SM at D = 128), and the
+// fewest tiles of a unit (below that a unit's fixed cost shows).  Batches of
+// kWhole sequences and more are not split.
+template <int D> constexpr int kSlots = D == 64 ? 608 : D == 128 ? 304 : 152;
+constexpr int kMinTiles = 8;
 constexpr int kWhole = 2048;
 constexpr int kMaxSlots = 1 << 30;
+// The reference the exponentials are taken against follows the maximum only
+// when a score is above it by 2^8: weights stay below 2^8, sums and products
+// are in 32 bits, and most tiles need no maximum over the warp.
+constexpr float kSlack = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
 
 struct PagedArgs {
   const void *q, *kv;
@@ -53,6 +64,7 @@ struct PagedArgs {
   int B, Hq, Hkv, G, gt, NH;  // gt groups of 16 query heads per KV head, NH = Hkv gt
   int page, page_shift, max_pages, num_pages;
   int window, sinks, cap;
+  int units;  // aimed at
   float scale_log2;
   int rows;  // query heads of a unit: min(G, 16)
   int vis_max;
@@ -63,16 +75,18 @@ struct PagedArgs {
   uint32_t *status;
   // workspace
   float *w_o;        // [units][rows][D]
-  float2 *w_ml;      // [units][rows]
+  float2 *w_ml;      // [units][rows]: reference (log2 units) and sum
   uint32_t *w_flag;  // [units]
-  uint32_t *w_status;  // [B]
-  float *w_lse;      // [B][Hq], log2 units
-  float *w_score;    // [B][Hkv][vis_max][G], log2 units
+  float *w_score;    // [B][Hkv][vis_max][G], q.k
 };
 
-// the visible slots of a sequence, in order: [0, first), then [lo, len)
+// The visible slots of a sequence: [0, first) and [lo, len), laid out one after
+// the other from multiples of 16 slots, so that positions v, v + 1, ... of a
+// group are slots of one aligned run of 16 (some of them not visible).
 struct Visible {
-  int len, lo, first, n;
+  int len, lo, first;
+  int split, shift;  // position v is slot v below split, v + shift from there
+  int n;             // positions
   bool bad;
 };
 __device__ __forceinline__ Visible visible(const PagedArgs &a, int len) {
@@ -80,9 +94,18 @@ __device__ __forceinline__ Visible visible(const PagedArgs &a, int len) {
   v.bad = len < 0 || len > a.cap;
   v.len = v.bad ? 0 : len;
   v.lo = a.window > 0 ? max(0, v.len - a.window) : 0;
-  v.first = min(a.sinks, v.lo);
-  v.n = v.first + v.len - v.lo;
+  v.first = a.sinks;
+  if (v.lo <= a.sinks) v.lo = v.first = 0;  // they meet: [0, len)
+  v.split = (v.first + kGroup - 1) / kGroup * kGroup;
+  v.shift = v.lo / kGroup * kGroup - v.split;
+  v.n = v.len - v.shift;
   return v;
+}
+__device__ __forceinline__ int slot_of(const Visible &v, int pos) {
+  return pos < v.split ? pos : pos + v.shift;
+}
+__device__ __forceinline__ bool seen(const Visible &v, int pos) {
+  return pos < v.split ? pos < v.first : pos + v.shift >= v.lo && pos < v.n;
 }
 __device__ __forceinline__ int tiles_of(const Visible &v) { return (v.n + kTile - 1) / kTile; }
 
@@ -91,16 +114,28 @@ struct Plan {
   int first;     // group index of the sequence's first unit
 };
 
+// One sequence splits evenly: as many units as are resident at once.  Several
+// of different lengths leave units of different sizes: twice as many, so that
+// the early ones make room.  Rounding up adds half a unit to each (sequence,
+// head); a batch of more of those than units is left whole.
+int units_for(int D, int B) { return (D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>) * (B == 1 ? 1 : 2); }
+// tiles that a unit may have at most, for a batch of that many tiles in all
+__device__ __forceinline__ long long unit_tiles(const PagedArgs &a, long long tiles) {
+  const long long room = max((long long)a.units / 2, a.B == 1 ? (long long)a.units : a.units - (long long)a.B * a.NH / 2);
+  return min(max((long long)kMinTiles, (tiles * a.NH + room - 1) / room), (long long)kMaxSlots);
+}
 // units of a sequence of t tiles when a unit may have `most`
 __device__ __forceinline__ int units_of(const PagedArgs &a, int t, long long most) {
-  if (a.B >= kWhole || t == 0) return 1;
-  return (int)((t + most - 1) / most);
+  if (a.B >= kWhole || t <= kMinTiles) return 1;
+  return ((unsigned)t + (unsigned)most - 1) / (unsigned)most;
 }
 
 // The sequence and part that group g is (by_group), or the units of sequence g.
 // Every thread of the CTA calls it; b = -1 when there is no such group.
+template <int THREADS>
 __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
-  __shared__ long long s_red[kWarps];
+  constexpr int W = THREADS / 32;
+  __shared__ long long s_red[W];
   __shared__ Plan s_plan;
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -114,14 +149,14 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   }
   if (a.B == 1) {
     const int t = tiles_of(visible(a, a.seq_len[0]));
-    const long long most = max((long long)kMinTiles, ((long long)t * a.NH + kUnits - 1) / kUnits);
-    p.n = units_of(a, t, most);
+    p.n = units_of(a, t, unit_tiles(a, t));
     p.first = 0;
     p.b = by_group && g >= p.n ? -1 : 0;
     p.i = by_group ? g : 0;
     return p;
   }
-  const int k = (a.B + kThreads - 1) / kThreads;
+  // a run of k sequences to each thread
+  const int k = (a.B + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * k, a.B), b1 = min(b0 + k, a.B);
   long long tiles = 0;
   for (int b = b0; b < b1; ++b) tiles += tiles_of(visible(a, a.seq_len[b]));
@@ -132,9 +167,9 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   __syncthreads();
   tiles = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) tiles += s_red[w];
+  for (int w = 0; w < W; ++w) tiles += s_red[w];
   __syncthreads();
-  const long long most = max((long long)kMinTiles, (tiles * a.NH + kUnits - 1) / kUnits);
+  const long long most = unit_tiles(a, tiles);
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += units_of(a, tiles_of(visible(a, a.seq_len[b])), most);
   int incl = mine;
@@ -207,7 +242,17 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// 16 bytes to shared memory, zeros (nothing read) when `bytes` is 0
+// an 8 x 8 matrix of 16-bit elements, a row's pair per lane, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// 16 bytes to shared memory; the second form writes zeros (and reads nothing)
+// when `bytes` is 0
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
@@ -217,28 +262,36 @@ template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D> struct Shape {
+template <int D, int NT> struct Shape {
   static constexpr int kRowBytes = 2 * D;
-  static constexpr int kPart = kWarpKeys * kRowBytes;     // a warp's K (or V) rows of a tile
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kPart = kGroup * kRowBytes;  // a group's K (or V) rows
+  static constexpr int kStages = 3;
   static constexpr int kWarpBytes = kStages * 2 * kPart;
-  static constexpr bool kQRegs = D <= 128;                // the query tile stays in registers
-  static constexpr int kQBytes = kQRegs ? 0 : kRows * kRowBytes;
-  static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + kQBytes;
-  static_assert((size_t)kWarps * kRows * D * 4 <= (size_t)kWarps * kWarpBytes, "merge buffer");
+  static constexpr int kHeads = 8 * NT;
+  // the query tile stays in registers but where the accumulators fill them
+  static constexpr bool kQRegs = D * NT < 512;
+  static constexpr int kQBytes = kQRegs ? 0 : kHeads * kRowBytes;
+  static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + kQBytes + 512;  // + alignment
+  // O of the warps for the last merge: rows 4 floats longer than D, so that the
+  // 8 x 4 lanes of a store meet in no bank
+  static constexpr int kMergeRow = D + 4;
+  static_assert((size_t)kWarps * kHeads * kMergeRow * 4 <= (size_t)kWarps * kWarpBytes, "merge");
 };
 
-template <typename T, int D, bool WEIGHTS>
+template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   grid_dep_sync();
-  using Sh = Shape<D>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  using Sh = Shape<D, NT>;
+  // the operands' rows are addressed by exclusive or: they start at 512 bytes
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t sm0 = ((uint32_t)__cvta_generic_to_shared(smem_raw) + 511) & ~511u;
+  unsigned char *smem = smem_raw + (sm0 - (uint32_t)__cvta_generic_to_shared(smem_raw));
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g4 = lane >> 2, t4 = lane & 3;
   const int unit = blockIdx.x;
   const int h = unit % a.NH;
-  const Plan plan = find_plan(a, unit / a.NH, true);
+  const Plan plan = find_plan<kThreads>(a, unit / a.NH, true);
   if (plan.b < 0) return;
   const int b = plan.b;
   const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
@@ -247,28 +300,27 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   const int tiles = tiles_of(vis);
   const int t0 = (int)((long long)tiles * plan.i / plan.n);
   const int t1 = (int)((long long)tiles * (plan.i + 1) / plan.n);
-  const int v_end = min(t1 * kTile, vis.n);
 
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ uint32_t s_bad[kWarps];
+  __shared__ long long s_row[kWarps][32];  // offsets of two groups' rows (pages not of 16)
 
-  // ------------------------------------------------------------ query tile
+  // query heads as the right-hand operand: head g4 (+ 8), dimensions 2 t4 ...
   const T *q = (const T *)a.q + ((size_t)b * a.Hq + head0) * D;
-  uint32_t qf[Sh::kQRegs ? D / 16 : 1][4];
-  const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(smem);
+  uint32_t qf[Sh::kQRegs ? D / 16 : 1][NT][2];
   const uint32_t sm_q = sm0 + kWarps * Sh::kWarpBytes;
   if (Sh::kQRegs) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t *r0 = (const uint32_t *)(q + (size_t)g4 * D + k * 16 + t4 * 2);
-      const uint32_t *r1 = (const uint32_t *)(q + (size_t)(g4 + 8) * D + k * 16 + t4 * 2);
-      qf[k][0] = g4 < rows ? r0[0] : 0;
-      qf[k][1] = g4 + 8 < rows ? r1[0] : 0;
-      qf[k][2] = g4 < rows ? r0[4] : 0;
-      qf[k][3] = g4 + 8 < rows ? r1[4] : 0;
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t *r = (const uint32_t *)(q + (size_t)(g4 + 8 * n) * D + 2 * t4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[k][n][0] = g4 + 8 * n < rows ? r[8 * k] : 0;
+        qf[k][n][1] = g4 + 8 * n < rows ? r[8 * k + 4] : 0;
+      }
     }
   } else {
-    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+    for (int i = threadIdx.x; i < Sh::kHeads * (D / 8); i += kThreads) {
       const int r = i / (D / 8), c = i % (D / 8);
       const uint4 v = r < rows ? *(const uint4 *)(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
       *(uint4 *)(smem + kWarps * Sh::kWarpBytes + r * Sh::kRowBytes + ((c ^ (r & 7)) * 16)) = v;
@@ -277,165 +329,239 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   }
 
   // ------------------------------------------------------------ the loads
+  // This warp's group i is the 16 positions from (t0 + i) kTile + 16 warp.
+  const int groups = t1 - t0;
+  auto pos_of = [&](int i) { return (t0 + i) * kTile + warp * kGroup; };
   const uint32_t sm_w = sm0 + warp * Sh::kWarpBytes;
   const int32_t *table = a.table + (size_t)b * a.max_pages;
-  const T *kv = (const T *)a.kv;
-  const int64_t head_off = (int64_t)hkv * D;
+  const T *kv = (const T *)a.kv + (int64_t)hkv * D;
   const int64_t row_elems = (int64_t)a.Hkv * D;
-  uint32_t bad = 0;
-  // lane r (and r + 16) looks up row r of this warp's part of a tile
-  int n_id = 0, n_slot = -1;
-  auto look_up = [&](int t) {
-    const int v = t * kTile + warp * kWarpKeys + (lane & 15);
-    n_slot = -1;
-    if (t < t1 && v < v_end) {
-      const int key = v < vis.first ? v : v - vis.first + vis.lo;
-      const int pg = a.page_shift >= 0 ? key >> a.page_shift : key / a.page;
-      n_slot = key - pg * a.page;
-      n_id = table[pg];
+  constexpr int CPR = D / 8;     // 16-byte pieces of a row
+  constexpr int RPI = 32 / CPR;  // rows of one round of the warp's copies
+  const int lr = lane / CPR, lc = lane % CPR;
+  const bool by_row = a.page % kGroup != 0;
+  bool bad = false;
+  // Lanes look rows up in parallel: lane l the first row of group i0 + l
+  // (`ids` of 32 groups), or by_row the row l % 16 of group i0 + l / 16 (of 2).
+  // The table entries are loaded a batch ahead; an offset is -1 where nothing
+  // is visible, and odd where not all of the group's 16 slots are.
+  const int batch = by_row ? 2 : 32;
+  int next_id = 0;
+  auto position = [&](int i0) { return by_row ? pos_of(i0 + (lane >> 4)) + (lane & 15) : pos_of(i0 + lane); };
+  auto wanted = [&](int i0) {  // whether the lane's row or group has a slot to load
+    const int i = i0 + (by_row ? lane >> 4 : lane), p = position(i0);
+    return i < groups && (by_row ? seen(vis, p) : p < vis.n);
+  };
+  auto fetch_ids = [&](int i0) {
+    if (wanted(i0)) {
+      const int slot = slot_of(vis, position(i0));
+      next_id = table[a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page];
     }
   };
-  constexpr int CPR = D / 8;         // 16-byte pieces of a row
-  constexpr int RPI = 32 / CPR;      // rows of one round of the warp's copies
-  auto load_tile = [&](int stage) {  // the rows looked up last
-    int64_t off = -1;
-    if (n_slot >= 0) {
-      if ((unsigned)n_id < (unsigned)a.num_pages)
-        off = (int64_t)n_id * a.page_stride + (int64_t)n_slot * row_elems + head_off;
-      else
-        bad = 1;
+  auto offsets = [&](int i0) -> long long {
+    if (!wanted(i0)) return -1;
+    if ((unsigned)next_id >= (unsigned)a.num_pages) {
+      bad = true;
+      return -1;
     }
-    const uint32_t dst0 = sm_w + stage * 2 * Sh::kPart;
+    const int p = position(i0), slot = slot_of(vis, p);
+    const int in_page = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
+    const long long off = next_id * (long long)a.page_stride + in_page * (long long)row_elems;
+    return by_row || (seen(vis, p) && seen(vis, p + kGroup - 1)) ? off : off | 1;
+  };
+  long long offs = -1;
+  auto load_group = [&](int i, int stage) {
+    if ((i & (batch - 1)) == 0) {
+      offs = offsets(i);
+      fetch_ids(i + batch);
+      if (by_row) {
+        __syncwarp();
+        s_row[warp][lane] = offs;
+        __syncwarp();
+      }
+    }
+    const uint32_t dst = (sm_w + stage * 2 * Sh::kPart) + lr * Sh::kRowBytes + ((lc ^ lr) * 16);
+    if (by_row) {
 #pragma unroll
-    for (int i = 0; i < kWarpKeys / RPI; ++i) {
-      const int r = i * RPI + lane / CPR, c = lane % CPR;
-      const int64_t o = __shfl_sync(FULL, off, r);
-      const T *src = o >= 0 ? kv + o + c * 8 : kv;
-      const uint32_t n = o >= 0 ? 16u : 0u;
-      const uint32_t dst = dst0 + r * Sh::kRowBytes + ((c ^ (r & 7)) * 16);
-      cp16(dst, src, n);
-      cp16(dst + Sh::kPart, o >= 0 ? src + a.kv_stride : kv, n);
+      for (int j = 0; j < kGroup / RPI; ++j) {
+        const long long off = s_row[warp][(i & 1) * kGroup + j * RPI + lr];
+        const uint32_t n = off >= 0 ? 16u : 0u;
+        const T *src = kv + (off >= 0 ? off : 0) + lc * 8;
+        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+        cp16(d, src, n);
+        cp16(d + Sh::kPart, src + a.kv_stride, n);
+      }
+      return;
+    }
+    const long long off = __shfl_sync(FULL, offs, i & 31);
+    if (!(off & 1)) {  // all 16 rows
+      const T *k = kv + off + lr * row_elems + lc * 8, *v = k + a.kv_stride;
+#pragma unroll
+      for (int j = 0; j < kGroup / RPI; ++j) {
+        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+        cp16(d, k);
+        cp16(d + Sh::kPart, v);
+        k += RPI * row_elems;
+        v += RPI * row_elems;
+      }
+    } else {  // some, or none
+      const int p = pos_of(i);
+#pragma unroll 1
+      for (int j = 0; j < kGroup / RPI; ++j) {
+        const int r = j * RPI + lr;
+        const uint32_t n = off >= 0 && seen(vis, p + r) ? 16u : 0u;
+        const T *src = kv + (n ? (off ^ 1) + r * row_elems : 0) + lc * 8;
+        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+        cp16(d, src, n);
+        cp16(d + Sh::kPart, src + a.kv_stride, n);
+      }
     }
   };
 
-  float o[D / 8][4];
+  float o[D / 16][NT][4];
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+  // per head 2 t4 + e (+ 8 n): the reference m (log2 units), l, and the z that
+  // is subtracted (m, or 0 while there is no finite score)
+  float m[NT][2], z[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[n][e] = -INFINITY;
+      z[n][e] = l[n][e] = 0.0f;
+    }
+  const float sc = a.scale_log2;
+  float *scores = a.w_score ? a.w_score + ((size_t)b * a.Hkv + hkv) * a.vis_max * a.G + (h % a.gt) * kRows
+                            : nullptr;
 
-  look_up(t0);
+  fetch_ids(0);
 #pragma unroll
-  for (int s = 0; s < Sh::kStages - 1; ++s) {
-    load_tile(s);
+  for (int i = 0; i < Sh::kStages - 1; ++i) {
+    load_group(i, i);
     cp_commit();
-    look_up(t0 + s + 1);
   }
+  // addresses of this lane's rows of the operands: K's row (key) and V's
+  const int ka = (((lane >> 3) & 1) << 3) + (lane & 7), kh = lane >> 4;
+  const int va = ((lane >> 4) << 3) + (lane & 7), vh = (lane >> 3) & 1;
+  const uint32_t k_lane = sm_w + ka * Sh::kRowBytes + ((kh ^ (ka & 7)) * 16);
+  const uint32_t v_lane = sm_w + Sh::kPart + va * Sh::kRowBytes + ((vh ^ (va & 7)) * 16);
   int st_load = Sh::kStages - 1, st = 0;
-  for (int t = t0; t < t1; ++t) {
+  uint32_t partial = 0;  // of the 32 groups from i & ~31: those with slots that are not visible
+  for (int i = 0; i < groups; ++i) {
     cp_wait<Sh::kStages - 2>();
     __syncwarp();
-    load_tile(st_load);  // tile t + kStages - 1, into the stage read last round
+    load_group(i + Sh::kStages - 1, st_load);  // into the stage read last round
     cp_commit();
-    look_up(t + Sh::kStages);
-    const uint32_t sm_k = sm_w + st * 2 * Sh::kPart, sm_v = sm_k + Sh::kPart;
+    const uint32_t k_at = k_lane + st * 2 * Sh::kPart, v_at = v_lane + st * 2 * Sh::kPart;
     st = st + 1 == Sh::kStages ? 0 : st + 1;
     st_load = st_load + 1 == Sh::kStages ? 0 : st_load + 1;
+    if ((i & 31) == 0) {
+      const int p = pos_of(i + lane);
+      partial = __ballot_sync(FULL, !(seen(vis, p) && seen(vis, p + kGroup - 1)));
+    }
+    const int pos0 = pos_of(i);
+    if (pos0 >= vis.n) continue;  // the last tile's groups past the end
 
-    // S = Q K^T: 16 query rows x 16 keys
-    float s[2][4] = {};
-    {
-      const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-      const uint32_t base = sm_k + key * Sh::kRowBytes;
-      const int qr = (lane & 7) + ((lane >> 3) & 1) * 8, qh = lane >> 4;
+    // S^T = K Q^T: 16 keys x 8 NT heads, even and odd steps apart
+    float s[NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t bk[4];
-        ldsm4(bk, base + (((2 * k + half) ^ (key & 7)) * 16));
-        if (Sh::kQRegs) {
-          Pair<T>::mma(s[0], qf[k], bk[0], bk[1]);
-          Pair<T>::mma(s[1], qf[k], bk[2], bk[3]);
-        } else {
-          uint32_t aq[4];
-          ldsm4(aq, sm_q + qr * Sh::kRowBytes + (((2 * k + qh) ^ (qr & 7)) * 16));
-          Pair<T>::mma(s[0], aq, bk[0], bk[1]);
-          Pair<T>::mma(s[1], aq, bk[2], bk[3]);
-        }
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t ak[4];
+      ldsm4(ak, k_at ^ (k * 32));
+      if (Sh::kQRegs) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, qf[k][n][0], qf[k][n][1]);
+      } else {
+        uint32_t bq[4];  // heads 0-7 and 8-15, 16 dimensions
+        const int qr = (lane & 7) + ((lane >> 4) << 3), qh = (lane >> 3) & 1;
+        ldsm4(bq, sm_q + qr * Sh::kRowBytes + (((2 * k + qh) ^ (qr & 7)) * 16));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, bq[2 * n], bq[2 * n + 1]);
       }
     }
-    const int v0 = t * kTile + warp * kWarpKeys + 2 * t4;  // keys v0, v0+1, v0+8, v0+9
-    float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool in = v0 + 8 * n + e < v_end;
-        s[n][e] = in ? s[n][e] * a.scale_log2 : -INFINITY;
-        s[n][2 + e] = in ? s[n][2 + e] * a.scale_log2 : -INFINITY;
-        if (WEIGHTS && in) {
-          float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + v0 + 8 * n + e) * a.G +
-                      (h % a.gt) * kRows;
-          if (g4 < rows) sc[g4] = s[n][e];
-          if (g4 + 8 < rows) sc[g4 + 8] = s[n][2 + e];
+      for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+    // keys pos0 + g4 and pos0 + g4 + 8 of this lane; whole groups need no test
+    if (partial >> (i & 31) & 1) {
+      const bool in0 = seen(vis, pos0 + g4), in1 = seen(vis, pos0 + g4 + 8);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][e] = in0 ? s[n][e] : -INFINITY;
+          s[n][2 + e] = in1 ? s[n][2 + e] : -INFINITY;
         }
-        mx0 = fmaxf(mx0, s[n][e]);
-        mx1 = fmaxf(mx1, s[n][2 + e]);
-      }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(FULL, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(FULL, mx1, 2));
-    if (__any_sync(FULL, mx0 > m0 || mx1 > m1)) {
-      const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-      // a row without a finite score yet: nothing to rescale
-      const float f0 = n0 == -INFINITY ? 1.0f : ex2_approx(m0 - n0);
-      const float f1 = n1 == -INFINITY ? 1.0f : ex2_approx(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= f0;
-      l1 *= f1;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        o[j][0] *= f0;
-        o[j][1] *= f0;
-        o[j][2] *= f1;
-        o[j][3] *= f1;
-      }
     }
-    const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+    if (scores) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[n][e] = ex2_approx(s[n][e] - z0);
-        s[n][2 + e] = ex2_approx(s[n][2 + e] - z1);
-        l0 += s[n][e];
-        l1 += s[n][2 + e];
-      }
-    // P as the sum of two 16-bit parts: the weights keep twice the type's bits
-    // (one part alone would add a rounding as large as the output's own)
-    uint32_t ph[4], pl[4];
+        for (int r = 0; r < 2; ++r) {
+          float *w = scores + (size_t)(pos0 + g4 + 8 * r) * a.G;
+          const int c = 2 * t4 + 8 * n;
+          if (pos0 + g4 + 8 * r < vis.n) {
+            if (c < rows) w[c] = s[n][2 * r];
+            if (c + 1 < rows) w[c + 1] = s[n][2 * r + 1];
+          }
+        }
+    }
+    // a score above the reference by more than the slack moves it
+    bool up = false;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][2 + e]) * sc > m[n][e] + kSlack;
+    if (__any_sync(FULL, up)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[n][e], s[n][2 + e]) * sc;
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, w));
+          x = fmaxf(x, m[n][e]);
+          // a head without a finite score yet has nothing to rescale
+          const float f = x == -INFINITY ? 1.0f : ex2_approx(m[n][e] - x);
+          m[n][e] = x;
+          z[n][e] = x == -INFINITY ? 0.0f : x;
+          l[n][e] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[j][n][e] *= f;
+            o[j][n][2 + e] *= f;
+          }
+        }
+    }
+    // P^T as the sum of two 16-bit parts: the weights keep twice the type's
+    // bits (one part alone would add a rounding as large as the output's own)
+    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float x = s[n][2 * r], y = s[n][2 * r + 1];
+        const float x = ex2_approx(fmaf(s[n][2 * r], sc, -z[n][0]));
+        const float y = ex2_approx(fmaf(s[n][2 * r + 1], sc, -z[n][1]));
+        l[n][0] += x;
+        l[n][1] += y;
         const uint32_t hi = Pair<T>::pack(x, y);
         const float2 back = Pair<T>::unpack(hi);
-        ph[2 * n + r] = hi;
-        pl[2 * n + r] = Pair<T>::pack(x - back.x, y - back.y);
+        ph[n][r] = transpose8(hi);
+        pl[n][r] = transpose8(Pair<T>::pack(x - back.x, y - back.y));
       }
-    // O += P V
-    {
-      const int key = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
-      const uint32_t base = sm_v + key * Sh::kRowBytes;
+    // O^T += V^T P^T
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t bv[4];
-        ldsm4t(bv, base + (((2 * j + half) ^ (key & 7)) * 16));
-        Pair<T>::mma(o[2 * j], ph, bv[0], bv[1]);
-        Pair<T>::mma(o[2 * j + 1], ph, bv[2], bv[3]);
-        Pair<T>::mma(o[2 * j], pl, bv[0], bv[1]);
-        Pair<T>::mma(o[2 * j + 1], pl, bv[2], bv[3]);
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t av[4];
+      ldsm4t(av, v_at ^ (j * 32));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        Pair<T>::mma(o[j][n], av, ph[n][0], ph[n][1]);
+        Pair<T>::mma(o[j][n], av, pl[n][0], pl[n][1]);
       }
     }
     __syncwarp();  // every lane is done with this stage before it is filled again
@@ -443,175 +569,206 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   cp_wait<0>();
 
   // ------------------------------------------------------------ merge the warps
-  l0 += __shfl_xor_sync(FULL, l0, 1);
-  l1 += __shfl_xor_sync(FULL, l1, 1);
-  l0 += __shfl_xor_sync(FULL, l0, 2);
-  l1 += __shfl_xor_sync(FULL, l1, 2);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], w);
+      if (g4 == 0) {
+        s_m[warp][8 * n + 2 * t4 + e] = m[n][e];
+        s_l[warp][8 * n + 2 * t4 + e] = l[n][e];
+      }
+    }
   bad = __any_sync(FULL, bad);
-  if (t4 == 0) {
-    s_m[warp][g4] = m0;
-    s_m[warp][g4 + 8] = m1;
-    s_l[warp][g4] = l0;
-    s_l[warp][g4 + 8] = l1;
-  }
-  if (lane == 0) s_bad[warp] = bad;
-  __syncthreads();
-  float M0 = -INFINITY, M1 = -INFINITY;
+  if (lane == 0) s_bad[warp] = bad ? 1 : 0;
+  __syncthreads();  // the ring is free too: O goes there
+  float *mo = (float *)smem + (size_t)warp * Sh::kHeads * Sh::kMergeRow;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = 8 * n + 2 * t4 + e;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][c]);
+      const float f = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - M);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        mo[c * Sh::kMergeRow + 16 * j + g4] = o[j][n][e] * f;
+        mo[c * Sh::kMergeRow + 16 * j + 8 + g4] = o[j][n][2 + e] * f;
+      }
+    }
   uint32_t flag = vis.bad ? SV_ROW_BAD_LEN : 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    M0 = fmaxf(M0, s_m[w][g4]);
-    M1 = fmaxf(M1, s_m[w][g4 + 8]);
+  for (int w = 0; w < kWarps; ++w)
     if (s_bad[w]) flag |= SV_ROW_BAD_PAGE;
-  }
-  const float f0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M0);
-  const float f1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M1);
-  float *mo = (float *)smem + (size_t)warp * kRows * D;
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    *(float2 *)(mo + g4 * D + j * 8 + t4 * 2) = make_float2(o[j][0] * f0, o[j][1] * f0);
-    *(float2 *)(mo + (g4 + 8) * D + j * 8 + t4 * 2) = make_float2(o[j][2] * f1, o[j][3] * f1);
-  }
   __syncthreads();
   const float *mr = (const float *)smem;
   const bool whole = plan.n == 1;
   for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    float x = 0.0f, y = 0.0f, l = 0.0f, M = -INFINITY;
+    float x = 0.0f, y = 0.0f, sum = 0.0f, M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 p = *(const float2 *)(mr + ((size_t)w * kRows + r) * D + c);
+      const float2 p = *(const float2 *)(mr + ((size_t)w * Sh::kHeads + r) * Sh::kMergeRow + c);
       x += p.x;
       y += p.y;
       M = fmaxf(M, s_m[w][r]);
     }
+    // (a sum without a finite reference is 0, or NaN from the data: it stays)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      l += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2_approx(s_m[w][r] - M);
+      sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2_approx(s_m[w][r] - M);
     if (whole) {
       const float nan = __int_as_float(0x7fffffff);
-      const float inv = 1.0f / l;
-      x = flag ? nan : l == 0.0f ? 0.0f : x * inv;
-      y = flag ? nan : l == 0.0f ? 0.0f : y * inv;
+      const float inv = 1.0f / sum;
+      x = flag ? nan : sum == 0.0f ? 0.0f : x * inv;
+      y = flag ? nan : sum == 0.0f ? 0.0f : y * inv;
       *(uint32_t *)((T *)a.out + ((size_t)b * a.Hq + head0 + r) * D + c) = Pair<T>::pack(x, y);
-      if (c == 0) {
-        const float lse2 = flag ? nan : l == 0.0f ? -INFINITY : M + log2f(l);
-        if (a.lse) a.lse[(size_t)b * a.Hq + head0 + r] = lse2 * 0.693147180559945309f;
-        if (WEIGHTS) a.w_lse[(size_t)b * a.Hq + head0 + r] = lse2;
-      }
+      if (c == 0 && a.lse)
+        a.lse[(size_t)b * a.Hq + head0 + r] =
+            flag ? nan : sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
     } else {
       *(float2 *)(a.w_o + ((size_t)unit * a.rows + r) * D + c) = make_float2(x, y);
-      if (c == 0) a.w_ml[(size_t)unit * a.rows + r] = make_float2(M, l);
     }
+    if (c == 0 && a.w_ml) a.w_ml[(size_t)unit * a.rows + r] = make_float2(M, sum);
   }
   if (threadIdx.x == 0) {
-    if (whole) {
-      if (h == 0) {
-        if (a.status) a.status[b] = flag;
-        if (WEIGHTS) a.w_status[b] = flag;
-      }
-    } else {
-      a.w_flag[unit] = flag;
-    }
+    if (a.w_flag) a.w_flag[unit] = flag;
+    if (whole && h == 0 && a.status) a.status[b] = flag;
   }
 }
 
 // ---------------------------------------------------------------------------
-// The join: one CTA per (sequence, KV head group, query row) merges the units'
-// m, l and O; a sequence that was one unit is written already.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(PagedArgs a, int with_weights) {
-  grid_dep_sync();
+// The end of a call that was split or sums weights.  CTAs below `joins`: the
+// join, one query row of a (sequence, head group) with its units spread over
+// the warps (wide), or a warp to each row (many sequences, few units each).
+// The others: weight_sum += sum over the G query heads of exp(s - lse), one
+// thread per visible slot, so no two add to one place.
+constexpr int kEndThreads = 256;
+constexpr int kEndWarps = kEndThreads / 32;
+constexpr int kSumKeys = 512;  // positions of a CTA
+
+// reference and sum of a row's units; every lane of the warp calls it
+__device__ __forceinline__ float2 join_ml(const PagedArgs &a, const Plan &p, int h, int r, uint32_t &flag) {
   const unsigned FULL = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % a.NH, b = blockIdx.x / a.NH, r = blockIdx.y;
-  const Plan plan = find_plan(a, b, false);
-  if (plan.n == 1) return;
-  const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
-  if (r >= min(kRows, a.G - (h % a.gt) * kRows)) return;
-  __shared__ float s_red[kWarps];
-  __shared__ uint32_t s_flag[kWarps];
-  __shared__ float s_l[kWarps];
-  __shared__ float s_o[kWarps][D];
-  float M = -INFINITY;
-  uint32_t flag = 0;
-  for (int i = threadIdx.x; i < plan.n; i += kThreads) {
-    const size_t u = (size_t)(plan.first + i) * a.NH + h;
-    M = fmaxf(M, a.w_ml[u * a.rows + r].x);
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY, sum = 0.0f;
+  flag = 0;
+  for (int i = lane; i < p.n; i += 32) {
+    const size_t u = (size_t)(p.first + i) * a.NH + h;
+    const float2 ml = a.w_ml[u * a.rows + r];
+    const float x = fmaxf(M, ml.x);
+    sum = (M == -INFINITY ? sum : sum * ex2_approx(M - x)) + (ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - x));
+    M = x;
     flag |= a.w_flag[u];
   }
-  M = warp_max(M);
   flag = __reduce_or_sync(FULL, flag);
-  if (lane == 0) {
-    s_red[warp] = M;
-    s_flag[warp] = flag;
-  }
-  __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  flag = s_flag[0] | s_flag[1] | s_flag[2] | s_flag[3];
-  constexpr int E = D / 32;
-  float acc[E] = {}, l = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < plan.n; i += kWarps) {
-    const size_t u = (size_t)(plan.first + i) * a.NH + h;
-    const float2 ml = a.w_ml[u * a.rows + r];
-    const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - M);
-    // an l of NaN without a finite m comes from the data and stays
-    l += ml.x == -INFINITY ? ml.y : ml.y * f;
-    const float *src = a.w_o + (u * a.rows + r) * D;
+  const float top = warp_max(M);
+  sum = M == -INFINITY ? sum : sum * ex2_approx(M - top);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = *(const float2 *)(src + (e / 2) * 64 + lane * 2);
-      acc[e] += x.x * f;
-      acc[e + 1] += x.y * f;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *(float2 *)&s_o[warp][(e / 2) * 64 + lane * 2] = make_float2(acc[e], acc[e + 1]);
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const float nan = __int_as_float(0x7fffffff);
-  const float inv = 1.0f / l;
-  const size_t row = (size_t)b * a.Hq + head0 + r;
-  for (int c = threadIdx.x * 2; c < D; c += kThreads * 2) {
-    float x = s_o[0][c] + s_o[1][c] + s_o[2][c] + s_o[3][c];
-    float y = s_o[0][c + 1] + s_o[1][c + 1] + s_o[2][c + 1] + s_o[3][c + 1];
-    x = flag ? nan : l == 0.0f ? 0.0f : x * inv;
-    y = flag ? nan : l == 0.0f ? 0.0f : y * inv;
-    *(uint32_t *)((T *)a.out + row * D + c) = Pair<T>::pack(x, y);
-  }
-  if (threadIdx.x == 0) {
-    const float lse2 = flag ? nan : l == 0.0f ? -INFINITY : M + log2f(l);
-    if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
-    if (with_weights) a.w_lse[row] = lse2;
-    if (h == 0 && r == 0) {
-      if (a.status) a.status[b] = flag;
-      if (with_weights) a.w_status[b] = flag;
-    }
-  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  return make_float2(top, sum);
 }
 
-// ---------------------------------------------------------------------------
-// weight_sum += sum over the G query heads of exp(s - lse), from the scores
-// the attention left: one thread per visible slot, so no two add to one place.
-constexpr int kSumKeys = 256;
-__global__ void __launch_bounds__(kSumKeys) paged_weights_kernel(PagedArgs a) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, int joins, int wide, int key_ctas) {
   grid_dep_sync();
-  const int b = blockIdx.x / a.Hkv, hkv = blockIdx.x % a.Hkv;
-  if (a.w_status[b]) return;
-  const Visible vis = visible(a, a.seq_len[b]);
-  const float *lse = a.w_lse + (size_t)b * a.Hq + (size_t)hkv * a.G;
-  for (int v = blockIdx.y * kSumKeys + threadIdx.x; v < vis.n; v += gridDim.y * kSumKeys) {
-    const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + v) * a.G;
-    float w = 0.0f;
-    for (int g = 0; g < a.G; ++g) {
-      const float z = lse[g];
-      w += z == -INFINITY ? 0.0f : ex2_approx(sc[g] - z);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float nan = __int_as_float(0x7fffffff);
+  if ((int)blockIdx.x < joins) {
+    const int at = wide ? blockIdx.x / a.rows : blockIdx.x;
+    const int h = at % a.NH, b = at / a.NH;
+    const Plan plan = find_plan<kEndThreads>(a, b, false);
+    if (plan.n == 1) return;  // written already
+    const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
+    const int rows = min(kRows, a.G - (h % a.gt) * kRows);
+    __shared__ __align__(16) float s_o[kEndWarps][D];  // written in pairs
+    constexpr int E = D / 32;
+    for (int r = wide ? blockIdx.x % a.rows : warp; r < rows; r += wide ? kRows : kEndWarps) {
+      uint32_t flag;
+      const float2 ml = join_ml(a, plan, h, r, flag);
+      float acc[E] = {};
+#pragma unroll 4
+      for (int i = wide ? warp : 0; i < plan.n; i += wide ? kEndWarps : 1) {
+        const size_t u = (size_t)(plan.first + i) * a.NH + h;
+        const float m = a.w_ml[u * a.rows + r].x;
+        const float f = m == -INFINITY ? 0.0f : ex2_approx(m - ml.x);
+        const float *src = a.w_o + (u * a.rows + r) * D + lane * 2;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *(const float2 *)(src + e * 32);
+          acc[e] += x.x * f;
+          acc[e + 1] += x.y * f;
+        }
+      }
+      const size_t row = (size_t)b * a.Hq + head0 + r;
+      const float inv = 1.0f / ml.y;
+      auto put = [&](int c, float x, float y) {
+        x = flag ? nan : ml.y == 0.0f ? 0.0f : x * inv;
+        y = flag ? nan : ml.y == 0.0f ? 0.0f : y * inv;
+        *(uint32_t *)((T *)a.out + row * D + c) = Pair<T>::pack(x, y);
+      };
+      if (wide) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          *(float2 *)&s_o[warp][e * 32 + lane * 2] = make_float2(acc[e], acc[e + 1]);
+        __syncthreads();
+        for (int c = threadIdx.x * 2; c < D; c += kEndThreads * 2) {
+          float x = 0.0f, y = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kEndWarps; ++w) {
+            x += s_o[w][c];
+            y += s_o[w][c + 1];
+          }
+          put(c, x, y);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) put(e * 32 + lane * 2, acc[e], acc[e + 1]);
+      }
+      if (lane == 0 && (!wide || warp == 0)) {
+        if (a.lse) a.lse[row] = flag ? nan : ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+        if (h == 0 && r == 0 && a.status) a.status[b] = flag;
+      }
     }
-    const int key = v < vis.first ? v : v - vis.first + vis.lo;
-    a.weight_sum[((size_t)b * a.Hkv + hkv) * a.S + key] += w;
+    return;
+  }
+  const int at = blockIdx.x - joins;
+  const int item = at / key_ctas, b = item / a.Hkv, hkv = item % a.Hkv;
+  const Visible vis = visible(a, a.seq_len[b]);
+  const int p0 = at % key_ctas * kSumKeys;
+  if (vis.bad || p0 >= vis.n) return;
+  const Plan plan = find_plan<kEndThreads>(a, b, false);
+  extern __shared__ float s_lse[];  // [G]: log2 of the row's sum of exponentials
+  __shared__ uint32_t s_flag;
+  if (threadIdx.x == 0) s_flag = 0;
+  __syncthreads();
+  for (int g = warp; g < a.G; g += kEndWarps) {
+    uint32_t flag;
+    const float2 ml = join_ml(a, plan, hkv * a.gt + g / kRows, g % kRows, flag);
+    if (lane == 0) {
+      s_lse[g] = ml.y == 0.0f ? INFINITY : ml.x + log2f(ml.y);  // no weight at all: exp2(-inf)
+      if (flag) s_flag = 1;
+    }
+  }
+  __syncthreads();
+  if (s_flag) return;
+  for (int p = p0 + threadIdx.x; p < min(p0 + kSumKeys, vis.n); p += kEndThreads) {
+    if (!seen(vis, p)) continue;
+    const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + p) * a.G;
+    float w = 0.0f;
+    if (a.G % 4 == 0) {
+      for (int g = 0; g < a.G; g += 4) {
+        const float4 x = *(const float4 *)(sc + g);
+        w += ex2_approx(fmaf(x.x, a.scale_log2, -s_lse[g])) + ex2_approx(fmaf(x.y, a.scale_log2, -s_lse[g + 1])) +
+             ex2_approx(fmaf(x.z, a.scale_log2, -s_lse[g + 2])) + ex2_approx(fmaf(x.w, a.scale_log2, -s_lse[g + 3]));
+      }
+    } else {
+      for (int g = 0; g < a.G; ++g) w += ex2_approx(fmaf(sc[g], a.scale_log2, -s_lse[g]));
+    }
+    a.weight_sum[((size_t)b * a.Hkv + hkv) * a.S + slot_of(vis, p)] += w;
   }
 }
 
@@ -619,10 +776,10 @@ __global__ void __launch_bounds__(kSumKeys) paged_weights_kernel(PagedArgs a) {
 struct Sizes {
   int G, gt, NH, rows, cap, vis_max;
   long long groups, units;
-  size_t o, ml, flag, status, lse, score, total;
+  size_t o, ml, flag, score, total;
 };
 
-// 0 when the shape is beyond what the kernels index
+// false when the shape is beyond what the kernels index
 bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, int window,
               int sinks, int weights) {
   z.G = Hq / Hkv;
@@ -632,19 +789,25 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
   const long long cap = (long long)page * max_pages;
   if (cap > kMaxSlots) return false;
   z.cap = (int)cap;
-  z.vis_max = z.cap;
-  if (window > 0 && (long long)window + sinks < cap) z.vis_max = window + sinks;
+  // positions: a window and the first tokens start at multiples of 16 each
+  long long most = cap;
+  if (window > 0) {
+    const long long w = ((long long)sinks + 2 * kGroup - 1) / kGroup * kGroup + window + kGroup;
+    most = w < cap + 2 * kGroup ? w : cap + 2 * kGroup;
+  }
+  z.vis_max = (int)most;
   const long long tiles = (z.vis_max + kTile - 1) / kTile;
   if (B >= kWhole) {
     z.groups = B;
   } else {
     const long long by_len = (long long)B * ((tiles + kMinTiles - 1) / kMinTiles);
-    const long long by_units = (long long)B + kUnits / z.NH;
+    const long long by_units = (long long)B + units_for(D, B) / z.NH;
     z.groups = by_len < by_units ? by_len : by_units;
     if (z.groups < B) z.groups = B;
   }
   z.units = z.groups * z.NH;
-  if (z.units > 0x7fffffffLL || (long long)B * z.NH > 0x7fffffffLL) return false;
+  const long long rows = (long long)B * z.NH * kRows;  // CTAs of the join, at most
+  if (z.units > 0x3fffffffLL || rows > 0x3fffffffLL || z.G > 8192) return false;
   const bool split = z.groups > B;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -653,54 +816,48 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
     return r;
   };
   z.o = take(split ? (size_t)z.units * z.rows * D * 4 : 0);
-  z.ml = take(split ? (size_t)z.units * z.rows * 8 : 0);
-  z.flag = take(split ? (size_t)z.units * 4 : 0);
-  z.status = take(weights ? (size_t)B * 4 : 0);
-  z.lse = take(weights ? (size_t)B * Hq * 4 : 0);
+  z.ml = take(split || weights ? (size_t)z.units * z.rows * 8 : 0);
+  z.flag = take(split || weights ? (size_t)z.units * 4 : 0);
   z.score = take(weights ? (size_t)B * Hq * z.vis_max * 4 : 0);
   z.total = at;
   return true;
 }
 
-template <typename T, int D, bool W>
-cudaError_t allow_smem() {
+template <typename T, int D, int NT>
+sv_status attend(const PagedArgs &a, const Sizes &z, cudaStream_t st) {
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev == set_dev) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(
-      paged_attn_kernel<T, D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
-  if (e == cudaSuccess) set_dev = dev;
-  return e;
+  if (dev != set_dev) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Shape<D, NT>::kSmem);
+    if (e != cudaSuccess) return check_launch("paged_attention", e);
+    set_dev = dev;
+  }
+  LaunchScope ls("paged_attention", st);
+  return check_launch("paged_attention",
+                      launch_pdl(paged_attn_kernel<T, D, NT>, dim3((unsigned)z.units), dim3(kThreads),
+                                 Shape<D, NT>::kSmem, st, a));
 }
 
 template <typename T, int D>
 sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st) {
-  sv_status s;
-  cudaError_t e = weights ? allow_smem<T, D, true>() : allow_smem<T, D, false>();
-  if (e != cudaSuccess) return check_launch("paged_attention", e);
-  {
-    LaunchScope ls("paged_attention", st);
-    e = weights ? launch_pdl(paged_attn_kernel<T, D, true>, dim3((unsigned)z.units), dim3(kThreads),
-                             Shape<D>::kSmem, st, a)
-                : launch_pdl(paged_attn_kernel<T, D, false>, dim3((unsigned)z.units), dim3(kThreads),
-                             Shape<D>::kSmem, st, a);
-    if ((s = check_launch("paged_attention", e)) != SV_OK) return s;
-  }
-  if (z.groups > a.B) {
-    LaunchScope ls("paged_join", st);
-    e = launch_pdl(paged_join_kernel<T, D>, dim3((unsigned)(a.B * a.NH), (unsigned)a.rows),
-                   dim3(kThreads), 0, st, a, weights ? 1 : 0);
-    if ((s = check_launch("paged_join", e)) != SV_OK) return s;
-  }
-  if (weights) {
-    const int want = (z.vis_max + kSumKeys - 1) / kSumKeys;
-    LaunchScope ls("paged_weights", st);
-    e = launch_pdl(paged_weights_kernel, dim3((unsigned)(a.B * a.Hkv), (unsigned)(want < 65535 ? want : 65535)),
-                   dim3(kSumKeys), 0, st, a);
-    if ((s = check_launch("paged_weights", e)) != SV_OK) return s;
-  }
-  return SV_OK;
+  const sv_status s = z.rows <= 8 ? attend<T, D, 1>(a, z, st) : attend<T, D, 2>(a, z, st);
+  if (s != SV_OK) return s;
+  const bool split = z.groups > a.B;
+  if (!split && !weights) return SV_OK;
+  // a CTA to each row while the rows are few (a long sequence's many units are
+  // spread over its warps), a warp to each row otherwise
+  const int wide = (long long)a.B * a.NH < 256;
+  const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
+  const int key_ctas = weights ? (z.vis_max + kSumKeys - 1) / kSumKeys : 0;
+  const long long ctas = joins + (long long)key_ctas * a.B * a.Hkv;
+  if (ctas > 0x7fffffffLL) return set_error(SV_ERR_UNSUPPORTED, "too many work units");
+  LaunchScope ls("paged_finish", st);
+  return check_launch("paged_finish",
+                      launch_pdl(paged_finish_kernel<T, D>, dim3((unsigned)ctas), dim3(kEndThreads),
+                                 weights ? (size_t)a.G * 4 : 0, st, a, joins, wide, key_ctas ? key_ctas : 1));
 }
 
 bool bad_shape(int B, int Hq, int Hkv, int D, int page, int max_pages, int window, int sinks) {
@@ -791,6 +948,7 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.window = window;
   a.sinks = sinks;
   a.cap = z.cap;
+  a.units = units_for(D, B);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.rows = z.rows;
   a.vis_max = z.vis_max;
@@ -800,14 +958,12 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.lse = out_lse;
   a.status = out_status;
   char *w = (char *)workspace;
-  a.w_o = (float *)(w + z.o);
-  a.w_ml = (float2 *)(w + z.ml);
-  a.w_flag = (uint32_t *)(w + z.flag);
-  a.w_status = (uint32_t *)(w + z.status);
-  a.w_lse = (float *)(w + z.lse);
-  a.w_score = (float *)(w + z.score);
+  const bool split = z.groups > B, wt = weight_sum != nullptr;
+  a.w_o = split ? (float *)(w + z.o) : nullptr;
+  a.w_ml = split || wt ? (float2 *)(w + z.ml) : nullptr;
+  a.w_flag = split || wt ? (uint32_t *)(w + z.flag) : nullptr;
+  a.w_score = wt ? (float *)(w + z.score) : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool wt = weight_sum != nullptr;
   if (dt == SV_BF16)
     return D == 64    ? run<__nv_bfloat16, 64>(a, z, wt, st)
            : D == 128 ? run<__nv_bfloat16, 128>(a, z, wt, st)
