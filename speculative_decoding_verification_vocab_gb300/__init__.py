@@ -346,6 +346,16 @@ def _row_stride(name, t, dtype, shape):
 def sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample, out_tokens,
                           out_accept_len, out_status, stream=None):
     """qprobs [B][N+1][V], pprobs [B][N][V] or None (one-hot drafts); rows may be padded."""
+    B, R, _ = qprobs.shape
+    _want("out_tokens", out_tokens, torch.int32, (B, R))
+    _want("out_accept_len", out_accept_len, torch.int32, (B,))
+    _want("out_status", out_status, torch.int32, (B,))
+    return _verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample,
+                               out_tokens, out_accept_len, out_status, stream)
+
+
+def _verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample, out_tokens,
+                        out_accept_len, out_status, stream):
     B, R, V = qprobs.shape
     N = R - 1
     i32, f32 = torch.int32, torch.float32
@@ -357,14 +367,14 @@ def sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sam
     if n_draft is not None:
         _want("n_draft", n_draft, i32, (B,))
     _want("u_sample", u_sample, f32, (B,))
-    _want("out_tokens", out_tokens, i32, (B, R))
-    _want("out_accept_len", out_accept_len, i32, (B,))
-    _want("out_status", out_status, i32, (B,))
     return _check(load_library().sv_verify_chain_probs(
         _p(qprobs), ldq, _p(pprobs) if N > 0 else None, ldp, _dtype(qprobs),
         _p(draft_tokens) if N > 0 else None, _p(n_draft), _p(u_accept) if N > 0 else None,
         _p(u_sample), B, N, V, _p(out_tokens), _p(out_accept_len), _p(out_status),
         _stream(stream)))
+
+
+_CACHE_DTYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 
 
 def _pages(kv, lead):
@@ -389,26 +399,33 @@ def sv_paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight
     """q [B][Hq][D]; kv [2][pages][page][Hkv][D], the first two dimensions in
     any order of strides; weight_sum [B][Hkv][S] or None."""
     B, Hq, D = q.shape
+    _want("out", out, q.dtype, (B, Hq, D))
+    if out_lse is not None:
+        _want("out_lse", out_lse, torch.float32, (B, Hq))
+    if out_status is not None:
+        _want("out_status", out_status, torch.int32, (B,))
+    return _paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_sum, out,
+                            out_lse, out_status, workspace, stream)
+
+
+def _paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_sum, out, out_lse,
+                     out_status, workspace, stream):
+    B, Hq, D = q.shape
     kv_stride, page_stride = _pages(kv, 0)
     P, page, Hkv, Dk = kv.shape[1:]
     if kv.dtype != q.dtype or Dk != D:
         raise ValueError(f"kv: {kv.dtype} rows of {Dk}, q has {q.dtype} rows of {D}")
-    dt = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}.get(q.dtype)
+    dt = _CACHE_DTYPES.get(q.dtype)
     if dt is None:
         raise ValueError(f"unsupported cache dtype {q.dtype}")
     max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
     _want("q", q, q.dtype, (B, Hq, D))
     _want("block_table", block_table, torch.int32, (B, max_pages))
     _want("seq_len", seq_len, torch.int32, (B,))
-    _want("out", out, q.dtype, (B, Hq, D))
     S = 0
     if weight_sum is not None:
         S = weight_sum.shape[-1]
         _want("weight_sum", weight_sum, torch.float32, (B, Hkv, S))
-    if out_lse is not None:
-        _want("out_lse", out_lse, torch.float32, (B, Hq))
-    if out_status is not None:
-        _want("out_status", out_status, torch.int32, (B,))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: need a contiguous tensor")
     return _check(load_library().sv_paged_attention(
@@ -427,6 +444,17 @@ def sv_kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, si
                 out_kept, out_kv_len, out_status=None, workspace=None, stream=None):
     """kv [L][2][pages][page][Hkv][D], moved in place; weight_sum and
     out_weight_sum [L][B][Hkv][S] (may be the same tensor)."""
+    B = seq_len.shape[0]
+    _want("out_kept", out_kept, torch.int32, (kv.shape[0], B, kv.shape[-2], int(budget)))
+    _want("out_kv_len", out_kv_len, torch.int32, (B,))
+    if out_status is not None:
+        _want("out_status", out_status, torch.int32, (B,))
+    return _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sinks, recent,
+                     out_kept, out_kv_len, out_status, workspace, stream)
+
+
+def _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sinks, recent,
+              out_kept, out_kv_len, out_status, workspace, stream):
     kv_stride, page_stride = _pages(kv, 1)
     L, _, P, page, Hkv, D = kv.shape
     B, max_pages = block_table.shape if block_table.dim() == 2 else (seq_len.shape[0], 0)
@@ -434,11 +462,8 @@ def sv_kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, si
     _want("block_table", block_table, torch.int32, (B, max_pages))
     _want("seq_len", seq_len, torch.int32, (B,))
     _want("weight_sum", weight_sum, torch.float32, (L, B, Hkv, S))
-    _want("out_weight_sum", out_weight_sum, torch.float32, (L, B, Hkv, S))
-    _want("out_kept", out_kept, torch.int32, (L, B, Hkv, int(budget)))
-    _want("out_kv_len", out_kv_len, torch.int32, (B,))
-    if out_status is not None:
-        _want("out_status", out_status, torch.int32, (B,))
+    if out_weight_sum is not weight_sum:
+        _want("out_weight_sum", out_weight_sum, torch.float32, (L, B, Hkv, S))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: need a contiguous tensor")
     return _check(load_library().sv_kv_evict(
@@ -547,8 +572,8 @@ def verify_chain_probs(qprobs, pprobs, draft_tokens, u_accept, u_sample, n_draft
         out = dict(tokens=torch.empty(B, R, dtype=torch.int32, device=dev),
                    accept_len=torch.empty(B, dtype=torch.int32, device=dev),
                    status=torch.empty(B, dtype=torch.int32, device=dev))
-    sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample,
-                          out["tokens"], out["accept_len"], out["status"], stream)
+    _verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample, out["tokens"],
+                        out["accept_len"], out["status"], stream)
     return out
 
 
@@ -570,9 +595,9 @@ def paged_attention(q, kv, block_table, seq_len, scale=None, window=0, sinks=0, 
             workspace = _ws(sv_paged_attention_workspace(
                 B, Hq, kv.shape[3], D, kv.shape[2], block_table.shape[1], window, sinks,
                 weight_sum is not None), dev)
-    sv_paged_attention(q, kv, block_table, seq_len, window, sinks,
-                       D ** -0.5 if scale is None else scale, weight_sum, out, lse, status,
-                       workspace, stream)
+    _paged_attention(q, kv, block_table, seq_len, window, sinks,
+                     D ** -0.5 if scale is None else scale, weight_sum, out, lse, status,
+                     workspace, stream)
     return (out, lse, status) if return_lse else out
 
 
@@ -593,9 +618,9 @@ def kv_evict(kv, block_table, seq_len, weight_sum, budget, sinks=0, recent=0, ou
         status = torch.empty(B, dtype=torch.int32, device=dev)
         if workspace is None:
             workspace = _ws(sv_kv_evict_workspace(L, B, Hkv, budget), dev)
-    sv_kv_evict(kv, block_table, seq_len, weight_sum,
-                weight_sum if out_weight_sum is None else out_weight_sum, budget, sinks, recent,
-                kept, kv_len, status, workspace, stream)
+    _kv_evict(kv, block_table, seq_len, weight_sum,
+              weight_sum if out_weight_sum is None else out_weight_sum, budget, sinks, recent,
+              kept, kv_len, status, workspace, stream)
     return kept, kv_len, status
 
 

@@ -8,16 +8,20 @@
 // kept, `budget` in all, in their order; slot k of the shorter cache is slot
 // kept[k] of the longer.
 //
-// Two launches.  evict_select: a cluster of C CTAs per (layer, sequence, KV
-// head) finds the weight of the last slot kept by a radix selection (four
-// rounds of 8 bits, histograms added over the cluster's shared memory), then
-// ranks the kept slots by a scan and writes their list and their weights.
-// evict_move moves the rows in place: kept[k] >= k and strictly increasing, so
-// in increasing k no write reaches a slot whose read is still to come; a CTA
-// owns a column range of one (layer, K or V, sequence, KV head) and goes
-// through the list in batches, all reads of a batch before its writes.
-//
-// Bound: the rows that move, read and written once: memory.
+// One launch: a cluster of C CTAs per (layer, sequence, KV head), or one CTA
+// while there are many, goes through
+//   selection  the weight of the last slot kept, by a radix selection (rounds
+//              of 11, 11 and 10 bits over keys kept in shared memory, counts
+//              added over the cluster's shared memory);
+//   ranks      the kept slots in their order, by a scan: their list, weights
+//              and where their rows lie;
+//   moves      the rows in place, K and V together.  kept[k] >= k and strictly
+//              increasing, so in increasing k no write reaches a slot whose
+//              read is still to come: a ring of asynchronous copies runs ahead
+//              of the stores, and a barrier per stage stands between a stage's
+//              reads and its writes.
+// Bound: the rows that move, read and written once: memory.  With many CTAs
+// the selections of some run under the moves of others.
 #include <math.h>
 
 #include "common.cuh"
@@ -25,10 +29,12 @@
 namespace sv {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kAhead = 8;  // loads of a thread in flight
 constexpr unsigned kMaxCluster = 8;
-constexpr int kMoveThreads = 256;
+constexpr int kWordsEach = 4;     // words of a thread in a stage of the ring
+constexpr int kStages = 3;
+constexpr int kMaxRowBytes = 2048;
 constexpr int kMaxSlots = 1 << 30;
 
 struct EvictArgs {
@@ -37,16 +43,17 @@ struct EvictArgs {
   const int32_t *table, *seq_len;
   const float *w;
   float *out_w;
-  int L, B, H, page, max_pages, num_pages, cap, S;
-  int row_bytes;  // of one head
+  int L, B, H, page, page_shift, max_pages, num_pages, cap, S;
+  int row_bytes;      // of one head
   int64_t tok_bytes;  // from slot to slot in a page
   int budget, sinks, recent;
   int32_t *kept, *kv_len;
   uint32_t *status;
+  int C;       // CTAs of a cluster
+  int cached;  // keys of a CTA that fit its shared memory; longer parts are read again
   // workspace
-  float *w_stage;   // [L B H][budget]: the kept slots' weights
-  int32_t *w_todo;  // [L B H]: slots to move (0: none), -1 on a fault
-  int col_bytes, ncol;  // a move CTA's columns of a row, and how many such ranges
+  float *w_stage;    // [L B H][budget]: the kept slots' weights
+  long long *w_src;  // [L B H][budget]: where their rows lie, in bytes from head 0
 };
 
 // A weight as an unsigned number in the order of eviction: larger is kept
@@ -57,118 +64,193 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, unsigned C) {
+template <typename V>
+__device__ __forceinline__ void cp_word(uint32_t dst, const void *src) {
+  if constexpr (sizeof(V) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Shared memory: the ring; before the moves, two histograms and the keys.
+template <typename V, int T> struct Layout {
+  static constexpr int kStageWords = T * kWordsEach;
+  static constexpr int kRing = kStages * kStageWords * (int)sizeof(V);
+  static constexpr int kKeysAt = 2 * kBins * 4;
+  // keys that make the block no larger than its ring, but not fewer than this
+  static constexpr int kMostKeys = T == 1024 ? 32768 : 8192;
+  static constexpr int kPer = T / 4;  // rows of a stage, at most
+  static int bytes(int cached) {
+    const int select = kKeysAt + cached * 4;
+    return select > kRing ? select : kRing;
+  }
+  static_assert(2 * kMaxRowBytes <= kStageWords * (int)sizeof(V), "a stage holds a row's K and V");
+};
+
+// T = 256: C = 1, many items; T = 1024: few items or long ones.
+template <typename V, int T>
+__global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a) {
   grid_dep_sync();
+  using Lay = Layout<V, T>;
+  constexpr int W = T / 32;
+  constexpr int PB = kBins / T;  // bins of a thread
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ long long s_from[kStages + 1][Lay::kPer], s_to[kStages + 1][Lay::kPer];
+  __shared__ uint32_t s_part[W], s_pick[2];
+  __shared__ uint32_t s_cnt[2];  // this CTA's slots above the limit, and at it
+  __shared__ uint32_t s_scan[W][2];
+  __shared__ int s_first, s_range[2];
+  uint32_t *s_hist = (uint32_t *)smem;  // [2][kBins], used in turn
+  uint32_t *s_keys = (uint32_t *)(smem + Lay::kKeysAt);
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = T == 256 ? 1 : a.C;
   const int item = blockIdx.x / C;  // (layer, sequence, head)
   const int rank = C > 1 ? (int)cluster_rank() : 0;
-  const int b = item / a.H % a.B;
+  const int h = item % a.H, b = item / a.H % a.B, l = item / a.H / a.B;
   const int n = a.seq_len[b];
   const int m = a.budget;
-  __shared__ uint32_t s_hist[256 * 33];
-  __shared__ uint32_t s_sum[256];
-  __shared__ uint32_t s_pick[2];
-  __shared__ uint32_t s_cnt[2];  // this CTA's slots above the limit, and at it
-  __shared__ uint32_t s_scan[kSelWarps][2];
   int32_t *kept = a.kept + (size_t)item * m;
-  const bool writer = item < a.B * a.H && item % a.H == 0 && rank == 0;  // layer 0, head 0
+  const int32_t *table = a.table + (size_t)b * a.max_pages;
+  const float *w = a.w + (size_t)item * a.S;
+  float *out_w = a.out_w + (size_t)item * a.S;
 
   // faults: a length out of range, or a page of the sequence out of the pool
   uint32_t fault = n < 0 || n > a.cap ? SV_ROW_BAD_LEN : 0;
+  bool bad = false;
   if (!fault) {
     const int pages = (int)(((long long)n + a.page - 1) / a.page);
-    bool bad = false;
-    for (int i = threadIdx.x; i < pages; i += kSelThreads)
-      bad |= (unsigned)a.table[(size_t)b * a.max_pages + i] >= (unsigned)a.num_pages;
-    if (__syncthreads_or(bad)) fault = SV_ROW_BAD_PAGE;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < pages; i += T) bad |= (unsigned)table[i] >= (unsigned)a.num_pages;
   }
-  if (writer && threadIdx.x == 0) {
+  for (int i = threadIdx.x; i < 2 * kBins; i += T) s_hist[i] = 0;
+  if (threadIdx.x == 0) s_first = 0x7fffffff;
+  if (__syncthreads_or(bad)) fault = SV_ROW_BAD_PAGE;
+  if (l == 0 && h == 0 && rank == 0 && threadIdx.x == 0) {
     a.kv_len[b] = fault ? -1 : min(n, m);
     if (a.status) a.status[b] = fault;
   }
-  const int me = rank * kSelThreads + threadIdx.x, all = (int)C * kSelThreads;
+  const int me = rank * T + threadIdx.x, all = C * T;
   if (fault || n <= m) {  // the same for every CTA of the cluster
     for (int k = me; k < m; k += all) kept[k] = !fault && k < n ? k : -1;
-    if (me == 0) a.w_todo[item] = fault ? -1 : 0;
+    if (!fault && a.out_w != a.w)
+      for (int k = me; k < n; k += all) out_w[k] = w[k];
     return;
   }
 
+  // ------------------------------------------------------------ selection
   // the slots between the first and the last, and how many of them stay
-  const float *w = a.w + (size_t)item * a.S;
   const int mid0 = a.sinks, mid1 = n - a.recent;
   uint32_t need = (uint32_t)(m - a.sinks - a.recent);
+  const bool none = need == 0;
   const int per = (int)(((long long)(mid1 - mid0) + C - 1) / C);
   const int lo = min(mid0 + rank * per, mid1), hi = min(lo + per, mid1);
-
-  // radix selection: `limit` is the key of the need-th largest; `need` ends as
-  // the number of slots at the limit that stay
+  const bool cached = hi - lo <= a.cached;
+  // `limit` becomes the key of the need-th largest, `need` the number of slots
+  // at the limit that stay
   uint32_t limit = 0, mask = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256 * 33; i += kSelThreads) s_hist[i] = 0;
+  if (!none) {
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+      const uint32_t bins = round == 2 ? kBins / 2 : kBins;
+      uint32_t *hist = s_hist + (round & 1) * kBins;
+      if (round == 2)  // read in round 0, which every CTA has left
+        for (int i = threadIdx.x; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
-      // a column of bins per lane: no two lanes of a warp meet in one counter
-      for (int i = lo + threadIdx.x; i < hi; i += kSelThreads) {
-        const uint32_t key = order_key(w[i]);
-        if ((key & mask) == limit) atomicAdd(&s_hist[(key >> shift & 255) * 33 + lane], 1u);
-      }
-      __syncthreads();
-      if (threadIdx.x < 256) {
-        uint32_t c = 0;
+      auto count = [&](int i, uint32_t key) {
+        const bool in = i < hi && (key & mask) == limit;
+        const uint32_t bin = in ? key >> shift & (bins - 1) : 0xffffffffu;
+        if (!__all_sync(FULL, bin == __shfl_sync(FULL, bin, 0))) {
+          if (in) atomicAdd(&hist[bin], 1u);
+        } else if (in && lane == 0) {  // 32 equal digits: one addition
+          atomicAdd(&hist[bin], 32u);
+        }
+      };
+      if (round > 0 && cached) {
+#pragma unroll 4
+        for (int i = lo + threadIdx.x; i - lane < hi; i += T) count(i, i < hi ? s_keys[i - lo] : 0);
+      } else {  // kAhead loads in flight
+        for (int i0 = lo + threadIdx.x; i0 - lane < hi; i0 += T * kAhead) {
+          float x[kAhead];
 #pragma unroll
-        for (int l = 0; l < 32; ++l) c += s_hist[threadIdx.x * 33 + l];
-        s_sum[threadIdx.x] = c;
+          for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * T;
+            x[j] = i < hi ? w[i] : 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * T;
+            const uint32_t key = order_key(x[j]);
+            if (cached && i < hi) s_keys[i - lo] = key;
+            if (i - lane < hi) count(i, key);
+          }
+        }
       }
       if (C > 1)
         cluster_sync();
       else
         __syncthreads();
-      if (warp == 0) {  // lane l: the bins 255 - 8 l ... 248 - 8 l, from the top
-        uint32_t c[8], sum = 0;
+      // thread t: the bins from the top, PB t on
+      const int low = (int)bins - PB * ((int)threadIdx.x + 1);
+      uint32_t c[PB] = {}, sum = 0;
+      if (low >= 0) {
+        if constexpr (T == 256) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          c[j] = 0;
-          for (unsigned r = 0; r < C; ++r)
-            c[j] += C > 1 ? cluster_ld_u32(&s_sum[255 - 8 * lane - j], r) : s_sum[255 - 8 * lane - j];
-          sum += c[j];
-        }
-        uint32_t incl = sum;
+          for (int j = 0; j < PB; ++j) c[j] = hist[low + PB - 1 - j];
+        } else {
+          unsigned long long x[kMaxCluster];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(FULL, incl, o);
-          if (lane >= o) incl += x;
-        }
-        uint32_t before = incl - sum;
-        if (before < need && need <= incl) {
+          for (int r = 0; r < (int)kMaxCluster; ++r)
+            x[r] = r >= C ? 0 : C > 1 ? cluster_ld_u64(&hist[low], (uint32_t)r) : *(const unsigned long long *)&hist[low];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (before < need && need <= before + c[j]) {
-              s_pick[0] = 255 - 8 * lane - j;
-              s_pick[1] = need - before;
-            }
-            before += c[j];
+          for (int r = 0; r < (int)kMaxCluster; ++r) {
+            c[0] += (uint32_t)(x[r] >> 32);
+            c[1] += (uint32_t)x[r];
           }
+        }
+#pragma unroll
+        for (int j = 0; j < PB; ++j) sum += c[j];
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(FULL, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) s_part[warp] = incl;
+      __syncthreads();
+      // (the warps' sums fit a warp)
+      uint32_t before = incl - sum + __reduce_add_sync(FULL, lane < warp ? s_part[lane < W ? lane : 0] : 0);
+      if (before < need && need <= before + sum) {
+#pragma unroll
+        for (int j = 0; j < PB; ++j) {
+          if (before < need && need <= before + c[j]) {
+            s_pick[0] = (uint32_t)(low + PB - 1 - j);
+            s_pick[1] = need - before;
+          }
+          before += c[j];
         }
       }
       __syncthreads();
       limit |= s_pick[0] << shift;
       need = s_pick[1];
-      mask |= 255u << shift;
-      if (C > 1) cluster_sync();  // the counts are read: they may be written again
+      mask |= (bins - 1) << shift;
     }
   }
 
-  // ranks: slots above the limit all stay, those at it while `need` lasts
+  // ------------------------------------------------------------ ranks
+  // slots above the limit all stay, those at it while `need` lasts
   auto kind = [&](int i) -> uint32_t {
-    if (m == a.sinks + a.recent) return 0;  // none of these stays
-    const uint32_t key = order_key(w[i]);
+    if (none) return 0;
+    const uint32_t key = cached ? s_keys[i - lo] : order_key(w[i]);
     return key > limit ? 1 : key == limit ? 2 : 0;
   };
   // a warp's run of slots
-  const int run = ((hi - lo + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int run = ((hi - lo + W - 1) / W + 31) / 32 * 32;
   const int r0 = min(lo + warp * run, hi), r1 = min(r0 + run, hi);
   uint32_t above = 0, at = 0;
+#pragma unroll 4
   for (int i0 = r0; i0 < r1; i0 += 32) {
     const uint32_t k = i0 + lane < r1 ? kind(i0 + lane) : 0;
     above += __popc(__ballot_sync(FULL, k == 1));
@@ -179,137 +261,202 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     s_scan[warp][1] = at;
   }
   __syncthreads();
-  uint32_t b_above = 0, b_at = 0, t_above = 0, t_at = 0;
-  for (int j = 0; j < kSelWarps; ++j) {
-    if (j < warp) {
-      b_above += s_scan[j][0];
-      b_at += s_scan[j][1];
-    }
-    t_above += s_scan[j][0];
-    t_at += s_scan[j][1];
-  }
+  const uint32_t of_warp[2] = {lane < W ? s_scan[lane < W ? lane : 0][0] : 0, lane < W ? s_scan[lane < W ? lane : 0][1] : 0};
+  uint32_t b_above = __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
+  uint32_t b_at = __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
+  const uint32_t t_above = __reduce_add_sync(FULL, of_warp[0]), t_at = __reduce_add_sync(FULL, of_warp[1]);
   if (C > 1) {
     if (threadIdx.x == 0) {
       s_cnt[0] = t_above;
       s_cnt[1] = t_at;
     }
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      b_above += cluster_ld_u32(&s_cnt[0], (uint32_t)r);
-      b_at += cluster_ld_u32(&s_cnt[1], (uint32_t)r);
+    uint32_t x = 0, y = 0;
+    if (lane < rank) {
+      x = cluster_ld_u32(&s_cnt[0], (uint32_t)lane);
+      y = cluster_ld_u32(&s_cnt[1], (uint32_t)lane);
     }
+    b_above += __reduce_add_sync(FULL, x);
+    b_at += __reduce_add_sync(FULL, y);
   }
-  float *stage = a.w_stage + (size_t)item * m;
+  // this CTA's part of the list: positions [s_range[0], s_range[1])
+  if (threadIdx.x == 0) {  // warp 0's bases are the CTA's
+    s_range[0] = a.sinks + (int)(b_above + min(b_at, need));
+    s_range[1] = a.sinks + (int)(b_above + t_above + min(b_at + t_at, need));
+  }
+#pragma unroll 2
   for (int i0 = r0; i0 < r1; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < r1 ? kind(i) : 0;
     const uint32_t ma = __ballot_sync(FULL, k == 1), me_ = __ballot_sync(FULL, k == 2);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t ra = b_above + __popc(ma & below), re = b_at + __popc(me_ & below);
-    if (k == 1 || (k == 2 && re < need)) {
-      const int pos = a.sinks + (int)(ra + min(re, need));
-      kept[pos] = i;
-      stage[pos] = w[i];
-    }
+    if (k == 1 || (k == 2 && re < need)) kept[a.sinks + (int)(ra + min(re, need))] = i;
     b_above += __popc(ma);
     b_at += __popc(me_);
   }
-  for (int k = me; k < a.sinks; k += all) {
-    kept[k] = k;
-    stage[k] = w[k];
+  __syncthreads();  // the CTA reads its part back
+  float *stage = a.w_stage + (size_t)item * m;
+  long long *src = a.w_src + (size_t)item * m;
+  int first = 0x7fffffff;
+  // weights and rows of positions from, from + by, ..., kAhead at a time
+  auto rows_of = [&](int from, int to, int by, auto slot) {
+    for (int k0 = from; k0 < to; k0 += by * kAhead) {
+      int i[kAhead], id[kAhead];
+      float x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) i[j] = k0 + j * by < to ? slot(k0 + j * by) : 0;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        id[j] = table[a.page_shift >= 0 ? i[j] >> a.page_shift : i[j] / a.page];
+        x[j] = w[i[j]];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j * by;
+        if (k < to) {
+          const int in_page = a.page_shift >= 0 ? i[j] & (a.page - 1) : i[j] % a.page;
+          stage[k] = x[j];
+          src[k] = id[j] * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
+          if (i[j] != k) first = min(first, k);
+        }
+      }
+    }
+  };
+  rows_of(s_range[0] + (int)threadIdx.x, s_range[1], T, [&](int k) { return kept[k]; });
+  rows_of(me, a.sinks, all, [&](int k) { return kept[k] = k; });
+  rows_of(m - a.recent + me, m, all, [&](int k) { return kept[k] = n - m + k; });
+  first = __reduce_min_sync(FULL, first);
+  if (lane == 0) atomicMin(&s_first, first);
+  // The lists are the cluster's from here on, no weight is read again, and the
+  // ring takes the keys' place.
+  if (C > 1) {
+    cluster_sync();
+    first = 0x7fffffff;
+    if (lane < C) first = (int)cluster_ld_u32(&s_first, (uint32_t)lane);
+    first = __reduce_min_sync(FULL, first);
+    cluster_sync();
+  } else {
+    __syncthreads();
+    first = s_first;
   }
-  for (int k = me; k < a.recent; k += all) {
-    kept[m - a.recent + k] = n - a.recent + k;
-    stage[m - a.recent + k] = w[n - a.recent + k];
+
+  // ------------------------------------------------------------ moves
+#pragma unroll 4
+  for (int k = me; k < m; k += all) out_w[k] = stage[k];
+#pragma unroll 4
+  for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
+  first = min(first, m);
+  const int rows = m - first;  // that move
+  src += first;
+  char *base = a.kv + l * a.layer_stride + (int64_t)h * a.row_bytes;
+  const int words = a.row_bytes / (int)sizeof(V);
+  // a stage is `each` whole rows, K and V, of each CTA of the cluster; this
+  // thread moves up to kWordsEach words of it, at the same places in every
+  // stage, and looks up row threadIdx.x of it
+  const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
+  const int stages = (int)((rows + (long long)each * C - 1) / (each * C));
+  auto start = [&](int s) { return (s * C + rank) * each; };
+  int row[kWordsEach];
+  long long off[kWordsEach];
+#pragma unroll
+  for (int j = 0; j < kWordsEach; ++j) {
+    const int at = j * T + threadIdx.x, word = at % (2 * words);
+    row[j] = at / (2 * words);
+    off[j] = word < words ? word * (long long)sizeof(V) : (word - words) * (long long)sizeof(V) + a.kv_stride;
+    if (row[j] >= each) row[j] = 0x40000000;  // no word
   }
-  if (me == 0) a.w_todo[item] = m;
-  if (C > 1) cluster_sync();  // no CTA leaves while its counts may still be read
+  V *mine = (V *)smem + threadIdx.x;
+  const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
+  long long next_from = 0;
+  int next_id = 0;
+  auto fetch = [&](int s) {  // what the look-up of stage s needs from memory
+    const int k = start(s) + (int)threadIdx.x;
+    if ((int)threadIdx.x < each && k < rows) {
+      next_from = src[k];
+      next_id = table[a.page_shift >= 0 ? (first + k) >> a.page_shift : (first + k) / a.page];
+    }
+  };
+  auto look_up = [&](int s, int at) {
+    if ((int)threadIdx.x >= each) return;
+    const int k = first + start(s) + (int)threadIdx.x;
+    const int in_page = a.page_shift >= 0 ? k & (a.page - 1) : k % a.page;
+    s_from[at][threadIdx.x] = next_from;
+    s_to[at][threadIdx.x] = next_id * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
+  };
+  auto load = [&](int s, int slot, int at) {
+    const int left = rows - start(s);
+#pragma unroll
+    for (int j = 0; j < kWordsEach; ++j)
+      if (row[j] < left)
+        cp_word<V>(mine_at + (slot * Lay::kStageWords + j * T) * (int)sizeof(V),
+                   base + s_from[at][row[j]] + off[j]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(0);
+  for (int s = 0; s < kStages; ++s) {
+    look_up(s, s);
+    fetch(s + 1);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(s, s, s);
+  int slot = 0, place = 0;  // of stage s: s mod kStages, s mod (kStages + 1)
+  for (int s = 0; s < stages; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    // This stage's reads are done and its successors' rows looked up, by all
+    // threads.  Over the cluster nothing has to be made visible: the copies
+    // have arrived, and only then may the others write where they read from.
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    __syncthreads();
+    const int before = place == 0 ? kStages : place - 1;
+    load(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1, place >= 2 ? place - 2 : place + kStages - 1);
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    const int left = rows - start(s);
+    V v[kWordsEach];
+#pragma unroll
+    for (int j = 0; j < kWordsEach; ++j)
+      if (row[j] < left) v[j] = mine[slot * Lay::kStageWords + j * T];
+#pragma unroll
+    for (int j = 0; j < kWordsEach; ++j)
+      if (row[j] < left) *(V *)(base + s_to[place][row[j]] + off[j]) = v[j];
+    look_up(s + kStages, before);  // in the place of stage s - 1
+    fetch(s + kStages + 1);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    place = place == kStages ? 0 : place + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// ---------------------------------------------------------------------------
-// Moves: blockIdx.x = ((item, K or V), column range).  The CTAs of an item also
-// put its weights in place.
-constexpr int kBatchRows = 128;
-template <typename V>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
-  grid_dep_sync();
-  const int col = blockIdx.x % a.ncol;
-  const int rest = blockIdx.x / a.ncol;
-  const int which = rest & 1, item = rest >> 1;
-  const int b = item / a.H % a.B, h = item % a.H, l = item / a.H / a.B;
-  const int todo = a.w_todo[item];
-  if (todo < 0) return;
-  const int n = a.seq_len[b];
-  {  // the weights, spread over the item's CTAs
-    const float *w = a.w + (size_t)item * a.S;
-    float *__restrict__ out = a.out_w + (size_t)item * a.S;
-    const float *__restrict__ stage = a.w_stage + (size_t)item * a.budget;
-    const int k0 = (which * a.ncol + col) * kMoveThreads + threadIdx.x, step = 2 * a.ncol * kMoveThreads;
-    if (todo > 0) {
-#pragma unroll 8
-      for (int k = k0; k < todo; k += step) out[k] = stage[k];
-#pragma unroll 8
-      for (int k = todo + k0; k < n; k += step) out[k] = 0.0f;
-    } else if (a.out_w != a.w) {
-      for (int k = k0; k < n; k += step) out[k] = w[k];
-    }
+template <typename V, int T>
+sv_status launch(EvictArgs &a, int items, cudaStream_t st) {
+  using Lay = Layout<V, T>;
+  static thread_local int set_dev = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != set_dev) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        evict_kernel<V, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::bytes(Lay::kMostKeys));
+    if (e != cudaSuccess) return check_launch("kv_evict", e);
+    set_dev = dev;
   }
-  if (todo == 0) return;
-  const int32_t *kept = a.kept + (size_t)item * a.budget;
-  // the first slot that moves: kept[k] - k never falls
-  int k0 = 0, k1 = todo;
-  while (k0 < k1) {
-    const int k = (k0 + k1) >> 1;
-    if (kept[k] == k)
-      k0 = k + 1;
-    else
-      k1 = k;
-  }
-  __shared__ long long s_src[kBatchRows], s_dst[kBatchRows];
-  const int32_t *table = a.table + (size_t)b * a.max_pages;
-  char *base = a.kv + l * a.layer_stride + which * a.kv_stride + (int64_t)h * a.row_bytes +
-               (int64_t)col * a.col_bytes;
-  const int words = min(a.col_bytes, a.row_bytes - col * a.col_bytes) / (int)sizeof(V);
-  constexpr int U = 8;
-  for (; k0 < todo; k0 += kBatchRows) {
-    const int cnt = min(kBatchRows, todo - k0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * cnt; i += kMoveThreads) {
-      const int r = i >> 1;
-      const int slot = i & 1 ? kept[k0 + r] : k0 + r;
-      const int pg = slot / a.page;
-      const long long off = (long long)table[pg] * a.page_stride + (long long)(slot - pg * a.page) * a.tok_bytes;
-      (i & 1 ? s_src : s_dst)[r] = off;
-    }
-    __syncthreads();
-    const int total = cnt * words;
-    for (int i0 = 0; i0 < total; i0 += kMoveThreads * U) {
-      V v[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int i = i0 + j * kMoveThreads + threadIdx.x;
-        if (i < total) v[j] = *(const V *)(base + s_src[i / words] + (size_t)(i % words) * sizeof(V));
-      }
-      __syncthreads();  // every read of these rows before their writes
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int i = i0 + j * kMoveThreads + threadIdx.x;
-        if (i < total) *(V *)(base + s_dst[i / words] + (size_t)(i % words) * sizeof(V)) = v[j];
-      }
-    }
-  }
+  const long long part = ((long long)a.cap + a.C - 1) / a.C;
+  a.cached = (int)(part < Lay::kMostKeys ? part : Lay::kMostKeys);
+  LaunchScope ls("kv_evict", st);
+  return check_launch("kv_evict", launch_pdl_cluster(evict_kernel<V, T>, dim3((unsigned)(items * a.C)), dim3(T),
+                                                     (unsigned)a.C, (size_t)Lay::bytes(a.cached), st, a));
 }
 
 struct Sizes {
   long long items;
-  size_t stage, todo, total;
+  size_t stage, src, total;
 };
 bool sizes_of(Sizes &z, int L, int B, int H, int budget) {
   z.items = (long long)L * B * H;
   if (z.items > (1 << 24) || budget > kMaxSlots) return false;
   z.stage = 0;
-  z.todo = align_up((size_t)z.items * budget * 4, 256);
-  z.total = align_up(z.todo + (size_t)z.items * 4, 256);
+  z.src = align_up((size_t)z.items * budget * 4, 256);
+  z.total = align_up(z.src + (size_t)z.items * budget * 8, 256);
   return true;
 }
 
@@ -338,9 +485,10 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
     return set_error(SV_ERR_INVALID_ARG, "need budget >= 1, sinks, recent >= 0 and sinks + recent <= budget");
   const long long cap = (long long)page * max_pages;
   Sizes z;
-  if (cap > kMaxSlots || !sizes_of(z, L, B, Hkv, budget) || (long long)D * elem_bytes > (1 << 20))
+  if (cap > kMaxSlots || !sizes_of(z, L, B, Hkv, budget) || (long long)D * elem_bytes > kMaxRowBytes)
     return set_error(SV_ERR_UNSUPPORTED,
-                     "more than 2^30 slots a sequence, 2^24 (layer, sequence, head)s or 1 MiB a row");
+                     "more than 2^30 slots a sequence, 2^24 (layer, sequence, head)s or %d bytes a row",
+                     kMaxRowBytes);
   if (S < cap) return set_error(SV_ERR_INVALID_ARG, "weight sums have %d slots a head, the page table %lld", S, cap);
   const int row = D * elem_bytes;
   if (row % 4) return set_error(SV_ERR_UNSUPPORTED, "rows of %d bytes (a multiple of 4 is needed)", row);
@@ -357,6 +505,8 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
       (uintptr_t)weight_sum % 4 || (uintptr_t)out_weight_sum % 4 || (uintptr_t)out_kept % 4 ||
       (uintptr_t)out_kv_len % 4 || (uintptr_t)out_status % 4 || (uintptr_t)workspace % 256)
     return set_error(SV_ERR_INVALID_ARG, "misaligned pointer or stride (4 bytes; the workspace 256)");
+  const bool vec = row % 16 == 0 && (uintptr_t)kv % 16 == 0 && page_stride * elem_bytes % 16 == 0 &&
+                   kv_stride * elem_bytes % 16 == 0 && layer_stride * elem_bytes % 16 == 0;
   if (workspace_bytes < z.total)
     return set_error(SV_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes, z.total);
   sv_status s;
@@ -379,6 +529,9 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   a.B = B;
   a.H = Hkv;
   a.page = page;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page == 1 << i) a.page_shift = i;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
   a.cap = (int)cap;
@@ -391,28 +544,17 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   a.kept = out_kept;
   a.kv_len = out_kv_len;
   a.status = out_status;
-  a.w_stage = (float *)((char *)workspace + z.stage);
-  a.w_todo = (int32_t *)((char *)workspace + z.todo);
+  char *ws = (char *)workspace;
+  a.w_stage = (float *)(ws + z.stage);
+  a.w_src = (long long *)(ws + z.src);
+  // A cluster to each item while that leaves SMs free; large CTAs for few
+  // items and for long sequences, small ones (4 on an SM, selecting under each
+  // other's moves) for many.
   const int items = (int)z.items;
-  // CTAs of an item: one per 8192 slots, while the card has room for them
-  unsigned C = 1;
-  while (C < kMaxCluster && cap > (long long)C * 8192 && (long long)items * C * 2 <= 1216) C *= 2;
+  a.C = 1;
+  while (a.C < (int)kMaxCluster && items * a.C * 2 <= 152) a.C *= 2;
   cudaStream_t st = (cudaStream_t)stream;
-  {
-    LaunchScope ls("evict_select", st);
-    s = check_launch("evict_select", launch_pdl_cluster(evict_select_kernel, dim3((unsigned)items * C),
-                                                        dim3(kSelThreads), C, 0, st, a, C));
-    if (s != SV_OK) return s;
-  }
-  const bool vec = row % 16 == 0 && (uintptr_t)kv % 16 == 0 && a.page_stride % 16 == 0 &&
-                   a.kv_stride % 16 == 0 && a.layer_stride % 16 == 0;
-  // columns of a row apart while the streams are few; 64 bytes keep whole sectors
-  a.col_bytes = row;
-  while (a.col_bytes > 64 && a.col_bytes % 128 == 0 && (long long)items * 2 * (row / a.col_bytes) < 608)
-    a.col_bytes /= 2;
-  a.ncol = row / a.col_bytes;
-  const dim3 grid((unsigned)items * 2 * a.ncol);
-  LaunchScope ls("evict_move", st);
-  return check_launch("evict_move", vec ? launch_pdl(evict_move_kernel<uint4>, grid, dim3(kMoveThreads), 0, st, a)
-                                        : launch_pdl(evict_move_kernel<uint32_t>, grid, dim3(kMoveThreads), 0, st, a));
+  if (items <= 152 || cap > 16384)
+    return vec ? launch<uint4, 1024>(a, items, st) : launch<uint32_t, 1024>(a, items, st);
+  return vec ? launch<uint4, 256>(a, items, st) : launch<uint32_t, 256>(a, items, st);
 }

@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   };
   long long offs = -1;
   auto load_group = [&](int i, int stage) {
+    if (i >= groups || pos_of(i) >= vis.n) return;  // nothing, and nothing after it
     if ((i & (batch - 1)) == 0) {
       offs = offsets(i);
       fetch_ids(i + batch);
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
 // thread per visible slot, so no two add to one place.
 constexpr int kEndThreads = 256;
 constexpr int kEndWarps = kEndThreads / 32;
-constexpr int kSumKeys = 512;  // positions of a CTA
+constexpr int kSumKeys = 1024;  // positions of a CTA
 
 // reference and sum of a row's units; every lane of the warp calls it
 __device__ __forceinline__ float2 join_ml(const PagedArgs &a, const Plan &p, int h, int r, uint32_t &flag) {
@@ -849,7 +850,7 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   if (!split && !weights) return SV_OK;
   // a CTA to each row while the rows are few (a long sequence's many units are
   // spread over its warps), a warp to each row otherwise
-  const int wide = (long long)a.B * a.NH < 256;
+  const int wide = (long long)a.B * a.NH < 64;
   const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
   const int key_ctas = weights ? (z.vis_max + kSumKeys - 1) / kSumKeys : 0;
   const long long ctas = joins + (long long)key_ctas * a.B * a.Hkv;
