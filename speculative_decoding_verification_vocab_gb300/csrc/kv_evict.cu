@@ -11,8 +11,10 @@
 // One launch: a cluster of C CTAs per (layer, sequence, KV head), or one CTA
 // while there are many, goes through
 //   selection  the weight of the last slot kept, by a radix selection (rounds
-//              of 11, 11 and 10 bits over keys kept in shared memory, counts
-//              added over the cluster's shared memory);
+//              of 11, 11 and 10 bits over keys kept in shared memory).  Up to
+//              kLocal slots every CTA of the cluster selects by itself (an
+//              exchange costs 2.5 us a round), beyond that each a part, the
+//              counts added over the cluster's shared memory;
 //   ranks      the kept slots in their order, by a scan: their list, weights
 //              and where their rows lie;
 //   moves      the rows in place, K and V together.  kept[k] >= k and strictly
@@ -30,10 +32,10 @@ namespace sv {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kAhead = 8;  // loads of a thread in flight
+constexpr int kAhead = 4;  // loads of a thread in flight
 constexpr unsigned kMaxCluster = 8;
 constexpr int kWordsEach = 4;     // words of a thread in a stage of the ring
-constexpr int kStages = 3;
+constexpr int kLocal = 8192;
 constexpr int kMaxRowBytes = 2048;
 constexpr int kMaxSlots = 1 << 30;
 
@@ -64,6 +66,14 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ uint4 cluster_ld_v4(const void *p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
 template <typename V>
 __device__ __forceinline__ void cp_word(uint32_t dst, const void *src) {
   if constexpr (sizeof(V) == 16)
@@ -75,11 +85,16 @@ __device__ __forceinline__ void cp_word(uint32_t dst, const void *src) {
 // Shared memory: the ring; before the moves, two histograms and the keys.
 template <typename V, int T> struct Layout {
   static constexpr int kStageWords = T * kWordsEach;
+  // Stages of the ring, and how many of them the arrival at the cluster's
+  // barrier goes ahead of the stores (a barrier a stage costs 0.5 us).
+  static constexpr int kStages = T == 512 ? 5 : 3;
+  static constexpr int kLead = T == 512 ? 1 : 0;
   static constexpr int kRing = kStages * kStageWords * (int)sizeof(V);
   static constexpr int kKeysAt = 2 * kBins * 4;
   // keys that make the block no larger than its ring, but not fewer than this
-  static constexpr int kMostKeys = T == 1024 ? 32768 : 8192;
+  static constexpr int kMostKeys = T == 512 ? 47104 : 8192;
   static constexpr int kPer = T / 4;  // rows of a stage, at most
+  static constexpr int kOnePerSm = 200 * 1024;
   static int bytes(int cached) {
     const int select = kKeysAt + cached * 4;
     return select > kRing ? select : kRing;
@@ -87,19 +102,20 @@ template <typename V, int T> struct Layout {
   static_assert(2 * kMaxRowBytes <= kStageWords * (int)sizeof(V), "a stage holds a row's K and V");
 };
 
-// T = 256: C = 1, many items; T = 1024: few items or long ones.
+// T = 256: C = 1, many items; T = 512: few items or long ones.
 template <typename V, int T>
 __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a) {
   grid_dep_sync();
   using Lay = Layout<V, T>;
   constexpr int W = T / 32;
+  constexpr int kStages = Lay::kStages;
   constexpr int PB = kBins / T;  // bins of a thread
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ long long s_from[kStages + 1][Lay::kPer], s_to[kStages + 1][Lay::kPer];
   __shared__ uint32_t s_part[W], s_pick[2];
   __shared__ uint32_t s_cnt[2];  // this CTA's slots above the limit, and at it
   __shared__ uint32_t s_scan[W][2];
-  __shared__ int s_first, s_range[2];
+  __shared__ int s_first;
   uint32_t *s_hist = (uint32_t *)smem;  // [2][kBins], used in turn
   uint32_t *s_keys = (uint32_t *)(smem + Lay::kKeysAt);
   const unsigned FULL = 0xffffffffu;
@@ -143,8 +159,10 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   const int mid0 = a.sinks, mid1 = n - a.recent;
   uint32_t need = (uint32_t)(m - a.sinks - a.recent);
   const bool none = need == 0;
-  const int per = (int)(((long long)(mid1 - mid0) + C - 1) / C);
-  const int lo = min(mid0 + rank * per, mid1), hi = min(lo + per, mid1);
+  const int P = mid1 - mid0 > kLocal ? C : 1;  // CTAs that select together
+  const int part = P > 1 ? rank : 0;
+  const int per = (int)(((long long)(mid1 - mid0) + P - 1) / P);
+  const int lo = min(mid0 + part * per, mid1), hi = min(lo + per, mid1);
   const bool cached = hi - lo <= a.cached;
   // `limit` becomes the key of the need-th largest, `need` the number of slots
   // at the limit that stay
@@ -159,19 +177,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
         for (int i = threadIdx.x; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
       auto count = [&](int i, uint32_t key) {
-        const bool in = i < hi && (key & mask) == limit;
-        const uint32_t bin = in ? key >> shift & (bins - 1) : 0xffffffffu;
-        if (!__all_sync(FULL, bin == __shfl_sync(FULL, bin, 0))) {
-          if (in) atomicAdd(&hist[bin], 1u);
-        } else if (in && lane == 0) {  // 32 equal digits: one addition
-          atomicAdd(&hist[bin], 32u);
-        }
+        // (equal digits of a warp cost no more than different ones)
+        if (i < hi && (key & mask) == limit) atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
       };
       if (round > 0 && cached) {
 #pragma unroll 4
-        for (int i = lo + threadIdx.x; i - lane < hi; i += T) count(i, i < hi ? s_keys[i - lo] : 0);
+        for (int i = lo + threadIdx.x; i < hi; i += T) count(i, s_keys[i - lo]);
       } else {  // kAhead loads in flight
-        for (int i0 = lo + threadIdx.x; i0 - lane < hi; i0 += T * kAhead) {
+        for (int i0 = lo + threadIdx.x; i0 < hi; i0 += T * kAhead) {
           float x[kAhead];
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) {
@@ -183,11 +196,11 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
             const int i = i0 + j * T;
             const uint32_t key = order_key(x[j]);
             if (cached && i < hi) s_keys[i - lo] = key;
-            if (i - lane < hi) count(i, key);
+            count(i, key);
           }
         }
       }
-      if (C > 1)
+      if (P > 1)
         cluster_sync();
       else
         __syncthreads();
@@ -195,18 +208,20 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
       const int low = (int)bins - PB * ((int)threadIdx.x + 1);
       uint32_t c[PB] = {}, sum = 0;
       if (low >= 0) {
-        if constexpr (T == 256) {
+        if (T == 256 || P == 1) {
 #pragma unroll
           for (int j = 0; j < PB; ++j) c[j] = hist[low + PB - 1 - j];
-        } else {
-          unsigned long long x[kMaxCluster];
+        } else if constexpr (T == 512) {
+          uint4 x[kMaxCluster];
 #pragma unroll
           for (int r = 0; r < (int)kMaxCluster; ++r)
-            x[r] = r >= C ? 0 : C > 1 ? cluster_ld_u64(&hist[low], (uint32_t)r) : *(const unsigned long long *)&hist[low];
+            x[r] = r < P ? cluster_ld_v4(&hist[low], (uint32_t)r) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int r = 0; r < (int)kMaxCluster; ++r) {
-            c[0] += (uint32_t)(x[r] >> 32);
-            c[1] += (uint32_t)x[r];
+            c[0] += x[r].w;
+            c[1] += x[r].z;
+            c[2] += x[r].y;
+            c[3] += x[r].x;
           }
         }
 #pragma unroll
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   uint32_t b_above = __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
   uint32_t b_at = __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
   const uint32_t t_above = __reduce_add_sync(FULL, of_warp[0]), t_at = __reduce_add_sync(FULL, of_warp[1]);
-  if (C > 1) {
+  if (P > 1) {
     if (threadIdx.x == 0) {
       s_cnt[0] = t_above;
       s_cnt[1] = t_at;
@@ -279,63 +294,70 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     b_above += __reduce_add_sync(FULL, x);
     b_at += __reduce_add_sync(FULL, y);
   }
-  // this CTA's part of the list: positions [s_range[0], s_range[1])
-  if (threadIdx.x == 0) {  // warp 0's bases are the CTA's
-    s_range[0] = a.sinks + (int)(b_above + min(b_at, need));
-    s_range[1] = a.sinks + (int)(b_above + t_above + min(b_at + t_at, need));
-  }
-#pragma unroll 2
+  // Positions of the list go round the cluster's CTAs, `each` at a time: a
+  // stage of the ring, K and V of whole rows.  Where all select, each writes
+  // its own.
+  const int words = a.row_bytes / (int)sizeof(V);
+  const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
+  auto mine_at_all = [&](int k) { return P == C || k / each % C == rank; };
+#pragma unroll 4
   for (int i0 = r0; i0 < r1; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < r1 ? kind(i) : 0;
     const uint32_t ma = __ballot_sync(FULL, k == 1), me_ = __ballot_sync(FULL, k == 2);
     const uint32_t below = (1u << lane) - 1u;
     const uint32_t ra = b_above + __popc(ma & below), re = b_at + __popc(me_ & below);
-    if (k == 1 || (k == 2 && re < need)) kept[a.sinks + (int)(ra + min(re, need))] = i;
+    if (k == 1 || (k == 2 && re < need)) {
+      const int pos = a.sinks + (int)(ra + min(re, need));
+      if (mine_at_all(pos)) kept[pos] = i;
+    }
     b_above += __popc(ma);
     b_at += __popc(me_);
   }
-  __syncthreads();  // the CTA reads its part back
+  if (P > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // weights and rows of this CTA's positions, kAhead of a thread at a time;
+  // turn j of the CTA's rows is position j / each * each * C + ...
   float *stage = a.w_stage + (size_t)item * m;
   long long *src = a.w_src + (size_t)item * m;
   int first = 0x7fffffff;
-  // weights and rows of positions from, from + by, ..., kAhead at a time
-  auto rows_of = [&](int from, int to, int by, auto slot) {
-    for (int k0 = from; k0 < to; k0 += by * kAhead) {
-      int i[kAhead], id[kAhead];
-      float x[kAhead];
+  auto position = [&](int j) { return C == 1 ? j : (j / each * C + rank) * each + j % each; };
+  for (int j0 = threadIdx.x; position(j0) < m; j0 += T * kAhead) {
+    int i[kAhead], id[kAhead];
+    float x[kAhead];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) i[j] = k0 + j * by < to ? slot(k0 + j * by) : 0;
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = position(j0 + j * T);
+      i[j] = k >= m ? 0 : k < a.sinks ? k : k >= m - a.recent ? n - m + k : kept[k];
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        id[j] = table[a.page_shift >= 0 ? i[j] >> a.page_shift : i[j] / a.page];
-        x[j] = w[i[j]];
-      }
+    for (int j = 0; j < kAhead; ++j) {
+      id[j] = table[a.page_shift >= 0 ? i[j] >> a.page_shift : i[j] / a.page];
+      x[j] = w[i[j]];
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int k = k0 + j * by;
-        if (k < to) {
-          const int in_page = a.page_shift >= 0 ? i[j] & (a.page - 1) : i[j] % a.page;
-          stage[k] = x[j];
-          src[k] = id[j] * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
-          if (i[j] != k) first = min(first, k);
-        }
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = position(j0 + j * T);
+      if (k < m) {
+        const int in_page = a.page_shift >= 0 ? i[j] & (a.page - 1) : i[j] % a.page;
+        stage[k] = x[j];
+        src[k] = id[j] * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
+        if (k < a.sinks || k >= m - a.recent) kept[k] = i[j];
+        if (i[j] != k) first = min(first, k);
       }
     }
-  };
-  rows_of(s_range[0] + (int)threadIdx.x, s_range[1], T, [&](int k) { return kept[k]; });
-  rows_of(me, a.sinks, all, [&](int k) { return kept[k] = k; });
-  rows_of(m - a.recent + me, m, all, [&](int k) { return kept[k] = n - m + k; });
+  }
   first = __reduce_min_sync(FULL, first);
   if (lane == 0) atomicMin(&s_first, first);
-  // The lists are the cluster's from here on, no weight is read again, and the
-  // ring takes the keys' place.
+  // No weight is read again, and the ring takes the keys' place.
   if (C > 1) {
     cluster_sync();
     first = 0x7fffffff;
     if (lane < C) first = (int)cluster_ld_u32(&s_first, (uint32_t)lane);
     first = __reduce_min_sync(FULL, first);
-    cluster_sync();
+    cluster_sync();  // read by all: a CTA may leave
   } else {
     __syncthreads();
     first = s_first;
@@ -343,19 +365,15 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
 
   // ------------------------------------------------------------ moves
 #pragma unroll 4
-  for (int k = me; k < m; k += all) out_w[k] = stage[k];
+  for (int j = threadIdx.x; position(j) < m; j += T) out_w[position(j)] = stage[position(j)];
 #pragma unroll 4
   for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
-  first = min(first, m);
-  const int rows = m - first;  // that move
-  src += first;
   char *base = a.kv + l * a.layer_stride + (int64_t)h * a.row_bytes;
-  const int words = a.row_bytes / (int)sizeof(V);
-  // a stage is `each` whole rows, K and V, of each CTA of the cluster; this
-  // thread moves up to kWordsEach words of it, at the same places in every
-  // stage, and looks up row threadIdx.x of it
-  const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
-  const int stages = (int)((rows + (long long)each * C - 1) / (each * C));
+  // Stage s: positions (s C + rank) each + 0 ... each - 1 of this CTA, from the
+  // first stage with a row that moves.  This thread moves up to kWordsEach
+  // words of it, at the same places in every stage, and looks up one row.
+  const int stages = (int)((m + (long long)each * C - 1) / (each * C));
+  const int s0 = min(first / (each * C), stages);
   auto start = [&](int s) { return (s * C + rank) * each; };
   int row[kWordsEach];
   long long off[kWordsEach];
@@ -372,20 +390,20 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   int next_id = 0;
   auto fetch = [&](int s) {  // what the look-up of stage s needs from memory
     const int k = start(s) + (int)threadIdx.x;
-    if ((int)threadIdx.x < each && k < rows) {
+    if ((int)threadIdx.x < each && k < m) {
       next_from = src[k];
-      next_id = table[a.page_shift >= 0 ? (first + k) >> a.page_shift : (first + k) / a.page];
+      next_id = table[a.page_shift >= 0 ? k >> a.page_shift : k / a.page];
     }
   };
   auto look_up = [&](int s, int at) {
     if ((int)threadIdx.x >= each) return;
-    const int k = first + start(s) + (int)threadIdx.x;
+    const int k = start(s) + (int)threadIdx.x;
     const int in_page = a.page_shift >= 0 ? k & (a.page - 1) : k % a.page;
     s_from[at][threadIdx.x] = next_from;
     s_to[at][threadIdx.x] = next_id * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
   };
   auto load = [&](int s, int slot, int at) {
-    const int left = rows - start(s);
+    const int left = m - start(s);
 #pragma unroll
     for (int j = 0; j < kWordsEach; ++j)
       if (row[j] < left)
@@ -393,26 +411,48 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
                    base + s_from[at][row[j]] + off[j]);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(0);
-  for (int s = 0; s < kStages; ++s) {
-    look_up(s, s);
-    fetch(s + 1);
+  {  // the first look-ups side by side
+    long long from[kStages];
+    int id[kStages];
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      fetch(s0 + s);
+      from[s] = next_from;
+      id[s] = next_id;
+    }
+    fetch(s0 + kStages);
+    const long long keep_from = next_from;
+    const int keep_id = next_id;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      next_from = from[s];
+      next_id = id[s];
+      look_up(s0 + s, s);
+    }
+    next_from = keep_from;
+    next_id = keep_id;
   }
   __syncthreads();
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) load(s, s, s);
-  int slot = 0, place = 0;  // of stage s: s mod kStages, s mod (kStages + 1)
-  for (int s = 0; s < stages; ++s) {
+  for (int s = 0; s < kStages - 1; ++s) load(s0 + s, s, s);
+  if (C > 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  }
+  int slot = 0, place = 0;  // of stage s: (s - s0) mod kStages, mod (kStages + 1)
+  for (int s = s0; s < stages; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2 - Lay::kLead) : "memory");
     // This stage's reads are done and its successors' rows looked up, by all
     // threads.  Over the cluster nothing has to be made visible: the copies
     // have arrived, and only then may the others write where they read from.
-    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (C > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");            // for stage s
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // for stage s + 1
+    }
     __syncthreads();
     const int before = place == 0 ? kStages : place - 1;
     load(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1, place >= 2 ? place - 2 : place + kStages - 1);
-    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    const int left = rows - start(s);
+    const int left = m - start(s);
     V v[kWordsEach];
 #pragma unroll
     for (int j = 0; j < kWordsEach; ++j)
@@ -426,21 +466,55 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     place = place == kStages ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the last arrival's
+}
+
+// How many clusters of C CTAs, one CTA to an SM, the device runs at once: GPCs
+// of different sizes leave 15 clusters of 8, 23 of 6, 36 of 4 on 152 SMs.
+int cluster_room(int C) {
+  static thread_local int dev_of = -1, room[kMaxCluster + 1];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != dev_of) {
+    for (int c = 1; c <= (int)kMaxCluster; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)c * 256);
+      cfg.blockDim = dim3(512);
+      cfg.dynamicSmemBytes = Layout<uint4, 512>::kOnePerSm;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)c;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&room[c], evict_kernel<uint4, 512>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        room[c] = c == 1 ? num_sms() : 0;
+      }
+    }
+    dev_of = dev;
+  }
+  return room[C];
+}
+
+template <typename V, int T>
+sv_status allow_smem() {
+  static thread_local int set_dev = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev == set_dev) return SV_OK;
+  const cudaError_t e = cudaFuncSetAttribute(
+      evict_kernel<V, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<V, T>::kOnePerSm);
+  if (e != cudaSuccess) return check_launch("kv_evict", e);
+  set_dev = dev;
+  return SV_OK;
 }
 
 template <typename V, int T>
 sv_status launch(EvictArgs &a, int items, cudaStream_t st) {
   using Lay = Layout<V, T>;
-  static thread_local int set_dev = -1;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev != set_dev) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        evict_kernel<V, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::bytes(Lay::kMostKeys));
-    if (e != cudaSuccess) return check_launch("kv_evict", e);
-    set_dev = dev;
-  }
-  const long long part = ((long long)a.cap + a.C - 1) / a.C;
+  // (up to kLocal slots a CTA holds them all)
+  const long long part = a.cap > kLocal ? max(((long long)a.cap + a.C - 1) / a.C, (long long)kLocal) : a.cap;
   a.cached = (int)(part < Lay::kMostKeys ? part : Lay::kMostKeys);
   LaunchScope ls("kv_evict", st);
   return check_launch("kv_evict", launch_pdl_cluster(evict_kernel<V, T>, dim3((unsigned)(items * a.C)), dim3(T),
@@ -547,14 +621,19 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   char *ws = (char *)workspace;
   a.w_stage = (float *)(ws + z.stage);
   a.w_src = (long long *)(ws + z.src);
-  // A cluster to each item while that leaves SMs free; large CTAs for few
-  // items and for long sequences, small ones (4 on an SM, selecting under each
-  // other's moves) for many.
+  // Few items, or long sequences: large CTAs, and for each item the largest
+  // cluster with which all run at once (two clusters on the same SMs end last:
+  // 16 items in clusters of 8 took 175 us where 6 take 144).  Many: small CTAs,
+  // 4 on an SM, which select under each other's moves.
   const int items = (int)z.items;
   a.C = 1;
-  while (a.C < (int)kMaxCluster && items * a.C * 2 <= 152) a.C *= 2;
   cudaStream_t st = (cudaStream_t)stream;
-  if (items <= 152 || cap > 16384)
-    return vec ? launch<uint4, 1024>(a, items, st) : launch<uint32_t, 1024>(a, items, st);
+  if (items <= 304 || cap > 16384) {
+    if ((s = allow_smem<uint4, 512>()) != SV_OK || (s = allow_smem<uint32_t, 512>()) != SV_OK) return s;
+    for (int c = (int)kMaxCluster; c > 1 && a.C == 1; --c)
+      if (items <= cluster_room(c)) a.C = c;
+    return vec ? launch<uint4, 512>(a, items, st) : launch<uint32_t, 512>(a, items, st);
+  }
+  if ((s = allow_smem<uint4, 256>()) != SV_OK || (s = allow_smem<uint32_t, 256>()) != SV_OK) return s;
   return vec ? launch<uint4, 256>(a, items, st) : launch<uint32_t, 256>(a, items, st);
 }
