@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kMaxCluster = 8;
+constexpr int kDepth = 4;  // pieces of a lane in flight
 constexpr uint32_t kTwo = 0x40000000u;  // bits of 2.0f: from here on, and below 0, an entry is bad
 
 struct ProbArgs {
@@ -99,52 +100,68 @@ __device__ __forceinline__ void add_vec(Sums &s, const uint4 &q, const uint4 &p,
   add<PAIR>(s, bf16_hi(q.w), bf16_hi(p.w));
 }
 
-// this lane's share of the weights of [lo, hi) of a row (pair)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// This lane's share of the weights of [lo, hi) of a row (pair).  The lane's
+// 16-byte pieces go through its own places in shared memory, kDepth of them in
+// flight: registers enough for those would halve the CTAs on an SM, which are
+// what hides the walk and the pick of one behind the rows of the others.
 template <typename T, bool PAIR>
-__device__ __forceinline__ Sums part_sums(const T *q, const T *p, int lo, int hi, int lane) {
+__device__ __forceinline__ Sums part_sums(const T *q, const T *p, int lo, int hi, int lane, uint4 *ring) {
   constexpr int VEC = 16 / sizeof(T);
-  constexpr int U = 4;
   Sums s{0, 0.0f, 0};
   int i = lo;
   if (((uintptr_t)q | (PAIR ? (uintptr_t)p : 0)) % 16 == 0) {
     const int full = lo + (hi - lo) / VEC * VEC;  // lo is a multiple of 8
-    for (; i < full; i += 32 * VEC * U) {
-      uint4 qv[U], pv[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int at = i + (j * 32 + lane) * VEC;
-        qv[j] = pv[j] = make_uint4(0, 0, 0, 0);
-        if (at < full) {
-          qv[j] = ld_stream_v4(q + at);
-          if (PAIR) pv[j] = ld_stream_v4(p + at);
-        }
+    const uint4 *mine = ring + threadIdx.x;
+    const uint32_t at0 = (uint32_t)__cvta_generic_to_shared(mine);
+    auto load = [&](int at, int slot) {
+      if (at < full) {
+        cp16(at0 + (2 * slot) * kThreads * 16, q + at);
+        if (PAIR) cp16(at0 + (2 * slot + 1) * kThreads * 16, p + at);
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int at = lo + lane * VEC;
 #pragma unroll
-      for (int j = 0; j < U; ++j) add_vec<PAIR>(s, qv[j], pv[j], T());
+    for (int j = 0; j < kDepth - 1; ++j) load(at + j * 32 * VEC, j);
+    int slot = 0;
+    for (; at < full; at += 32 * VEC) {
+      load(at + (kDepth - 1) * 32 * VEC, slot == 0 ? kDepth - 1 : slot - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      const uint4 qv = mine[(2 * slot) * kThreads];
+      const uint4 pv = PAIR ? mine[(2 * slot + 1) * kThreads] : make_uint4(0, 0, 0, 0);
+      add_vec<PAIR>(s, qv, pv, T());
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     i = full;
   }
-  for (; i < hi; i += 32 * 2 * U) {
-    float qv[2 * U], pv[2 * U];
+  constexpr int U = 4;
+  for (; i < hi; i += 32 * U) {
+    float qv[U], pv[U];
 #pragma unroll
-    for (int j = 0; j < 2 * U; ++j) {
+    for (int j = 0; j < U; ++j) {
       const int at = i + j * 32 + lane;
       qv[j] = at < hi ? load_elem(q + at) : 0.0f;
       pv[j] = PAIR && at < hi ? load_elem(p + at) : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 2 * U; ++j) add<PAIR>(s, qv[j], pv[j]);
+    for (int j = 0; j < U; ++j) add<PAIR>(s, qv[j], pv[j]);
   }
   return s;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) verify_probs_kernel(ProbArgs a, unsigned C) {
+__global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, unsigned C) {
   grid_dep_sync();
   const unsigned FULL = 0xffffffffu;
   const int b = blockIdx.x / C;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ uint4 ring[2 * kDepth * kThreads];
   __shared__ unsigned long long s_w[kWarps];   // this CTA's warps' sums, read by the cluster
   __shared__ unsigned long long s_ft[kWarps];  // fp32 sum (low word) and largest entry (high)
   __shared__ int s_a, s_n;                     // accepted tokens; drafted tokens
@@ -212,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_probs_kernel(ProbArgs a, u
     const int part = (int)rank * kWarps + warp;
     const long long lo64 = (long long)part * a.per;
     const int lo = (int)min(lo64, (long long)a.V), hi = (int)min(lo64 + a.per, (long long)a.V);
-    Sums s = p ? part_sums<T, true>(q, p, lo, hi, lane) : part_sums<T, false>(q, nullptr, lo, hi, lane);
+    Sums s = p ? part_sums<T, true>(q, p, lo, hi, lane, ring) : part_sums<T, false>(q, nullptr, lo, hi, lane, ring);
     if (hot >= lo && hot < hi && lane == 0) {
       const float x = load_elem(q + hot);
       const float over = fmaxf(__fsub_rn(x, 1.0f), 0.0f);
