@@ -148,7 +148,7 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
     return p;
   }
   if (a.B == 1) {
-    const int t = tiles_of(visible(a, a.seq_len[0]));
+    const int t = tiles_of(visible(a, __ldcg(a.seq_len)));
     p.n = units_of(a, t, unit_tiles(a, t));
     p.first = 0;
     p.b = by_group && g >= p.n ? -1 : 0;
@@ -159,7 +159,7 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   const int k = (a.B + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * k, a.B), b1 = min(b0 + k, a.B);
   long long tiles = 0;
-  for (int b = b0; b < b1; ++b) tiles += tiles_of(visible(a, a.seq_len[b]));
+  for (int b = b0; b < b1; ++b) tiles += tiles_of(visible(a, __ldcg(a.seq_len + b)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(FULL, tiles, o);
   if (lane == 0) s_red[warp] = tiles;
@@ -171,7 +171,7 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   __syncthreads();
   const long long most = unit_tiles(a, tiles);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(a, tiles_of(visible(a, a.seq_len[b])), most);
+  for (int b = b0; b < b1; ++b) mine += units_of(a, tiles_of(visible(a, __ldcg(a.seq_len + b))), most);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +184,7 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   for (int w = 0; w < warp; ++w) at += (int)s_red[w];
   if (by_group ? g >= at && g < at + mine : g >= b0 && g < b1) {
     for (int b = b0; b < b1; ++b) {
-      const int n = units_of(a, tiles_of(visible(a, a.seq_len[b])), most);
+      const int n = units_of(a, tiles_of(visible(a, __ldcg(a.seq_len + b))), most);
       if (by_group ? g < at + n : b == g) {
         s_plan.b = b;
         s_plan.i = by_group ? g - at : 0;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   const int b = plan.b;
   const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
   const int rows = min(kRows, a.G - (h % a.gt) * kRows);
-  const Visible vis = visible(a, a.seq_len[b]);
+  const Visible vis = visible(a, __ldcg(a.seq_len + b));
   const int tiles = tiles_of(vis);
   const int t0 = (int)((long long)tiles * plan.i / plan.n);
   const int t1 = (int)((long long)tiles * (plan.i + 1) / plan.n);
@@ -646,7 +646,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
 // join, one query row of a (sequence, head group) with its units spread over
 // the warps (wide), or a warp to each row (many sequences, few units each).
 // The others: weight_sum += sum over the G query heads of exp(s - lse), one
-// thread per visible slot, so no two add to one place.
+// thread per visible slot, so no two add to one place.  Both find their units
+// from the lengths (read past L1) before they wait for the attention: it
+// started after whatever wrote those had ended.
 constexpr int kEndThreads = 256;
 constexpr int kEndWarps = kEndThreads / 32;
 constexpr int kSumKeys = 1024;  // positions of a CTA
@@ -675,13 +677,13 @@ __device__ __forceinline__ float2 join_ml(const PagedArgs &a, const Plan &p, int
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, int joins, int wide, int key_ctas) {
-  grid_dep_sync();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float nan = __int_as_float(0x7fffffff);
   if ((int)blockIdx.x < joins) {
     const int at = wide ? blockIdx.x / a.rows : blockIdx.x;
     const int h = at % a.NH, b = at / a.NH;
     const Plan plan = find_plan<kEndThreads>(a, b, false);
+    grid_dep_sync();
     if (plan.n == 1) return;  // written already
     const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
     const int rows = min(kRows, a.G - (h % a.gt) * kRows);
@@ -738,10 +740,14 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   }
   const int at = blockIdx.x - joins;
   const int item = at / key_ctas, b = item / a.Hkv, hkv = item % a.Hkv;
-  const Visible vis = visible(a, a.seq_len[b]);
+  const Visible vis = visible(a, __ldcg(a.seq_len + b));
   const int p0 = at % key_ctas * kSumKeys;
-  if (vis.bad || p0 >= vis.n) return;
+  if (vis.bad || p0 >= vis.n) {
+    grid_dep_sync();
+    return;
+  }
   const Plan plan = find_plan<kEndThreads>(a, b, false);
+  grid_dep_sync();
   extern __shared__ float s_lse[];  // [G]: log2 of the row's sum of exponentials
   __shared__ uint32_t s_flag;
   if (threadIdx.x == 0) s_flag = 0;
