@@ -180,24 +180,26 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
         // (equal digits of a warp cost no more than different ones)
         if (i < hi && (key & mask) == limit) atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
       };
-      if (round > 0 && cached) {
+      if (cached) {  // a thread's keys stay its own until the ranks
+        if (round == 0) {
+          const uint32_t at = (uint32_t)__cvta_generic_to_shared(s_keys) - 4 * (uint32_t)lo;
+          for (int i = lo + threadIdx.x; i < hi; i += T)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4 * (uint32_t)i), "l"(w + i) : "memory");
+          asm volatile("cp.async.wait_all;" ::: "memory");
+        }
 #pragma unroll 4
-        for (int i = lo + threadIdx.x; i < hi; i += T) count(i, s_keys[i - lo]);
+        for (int i = lo + threadIdx.x; i < hi; i += T) {
+          uint32_t key = s_keys[i - lo];
+          if (round == 0) s_keys[i - lo] = key = order_key(__uint_as_float(key));
+          count(i, key);
+        }
       } else {  // kAhead loads in flight
         for (int i0 = lo + threadIdx.x; i0 < hi; i0 += T * kAhead) {
           float x[kAhead];
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j * T;
-            x[j] = i < hi ? w[i] : 0.0f;
-          }
+          for (int j = 0; j < kAhead; ++j) x[j] = i0 + j * T < hi ? w[i0 + j * T] : 0.0f;
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j * T;
-            const uint32_t key = order_key(x[j]);
-            if (cached && i < hi) s_keys[i - lo] = key;
-            count(i, key);
-          }
+          for (int j = 0; j < kAhead; ++j) count(i0 + j * T, order_key(x[j]));
         }
       }
       if (P > 1)
@@ -255,30 +257,38 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   }
 
   // ------------------------------------------------------------ ranks
-  // slots above the limit all stay, those at it while `need` lasts
-  auto kind = [&](int i) -> uint32_t {
-    if (none) return 0;
-    const uint32_t key = cached ? s_keys[i - lo] : order_key(w[i]);
-    return key > limit ? 1 : key == limit ? 2 : 0;
-  };
-  // a warp's run of slots
-  const int run = ((hi - lo + W - 1) / W + 31) / 32 * 32;
-  const int r0 = min(lo + warp * run, hi), r1 = min(r0 + run, hi);
-  uint32_t above = 0, at = 0;
+  // Slots above the limit all stay, those at it while `need` lasts.  A thread
+  // takes a run of slots, an odd number, so that the lanes meet in no bank.
+  __syncthreads();
+  auto key_at = [&](int i) { return cached ? s_keys[i - lo] : order_key(w[i]); };
+  const int run = ((hi - lo + T - 1) / T) | 1;
+  const int r0 = min(lo + (int)threadIdx.x * run, hi), r1 = none ? r0 : min(r0 + run, hi);
+  uint32_t b_above = 0, b_at = 0;  // in this thread's run, then before it
 #pragma unroll 4
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const uint32_t k = i0 + lane < r1 ? kind(i0 + lane) : 0;
-    above += __popc(__ballot_sync(FULL, k == 1));
-    at += __popc(__ballot_sync(FULL, k == 2));
+  for (int i = r0; i < r1; ++i) {
+    const uint32_t key = key_at(i);
+    b_above += key > limit;
+    b_at += key == limit;
   }
-  if (lane == 0) {
-    s_scan[warp][0] = above;
-    s_scan[warp][1] = at;
+  uint32_t i_above = b_above, i_at = b_at;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(FULL, i_above, o), y = __shfl_up_sync(FULL, i_at, o);
+    if (lane >= o) {
+      i_above += x;
+      i_at += y;
+    }
+  }
+  b_above = i_above - b_above;
+  b_at = i_at - b_at;
+  if (lane == 31) {
+    s_scan[warp][0] = i_above;
+    s_scan[warp][1] = i_at;
   }
   __syncthreads();
   const uint32_t of_warp[2] = {lane < W ? s_scan[lane < W ? lane : 0][0] : 0, lane < W ? s_scan[lane < W ? lane : 0][1] : 0};
-  uint32_t b_above = __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
-  uint32_t b_at = __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
+  b_above += __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
+  b_at += __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
   const uint32_t t_above = __reduce_add_sync(FULL, of_warp[0]), t_at = __reduce_add_sync(FULL, of_warp[1]);
   if (P > 1) {
     if (threadIdx.x == 0) {
@@ -301,18 +311,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
   auto mine_at_all = [&](int k) { return P == C || k / each % C == rank; };
 #pragma unroll 4
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < r1 ? kind(i) : 0;
-    const uint32_t ma = __ballot_sync(FULL, k == 1), me_ = __ballot_sync(FULL, k == 2);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t ra = b_above + __popc(ma & below), re = b_at + __popc(me_ & below);
-    if (k == 1 || (k == 2 && re < need)) {
-      const int pos = a.sinks + (int)(ra + min(re, need));
+  for (int i = r0; i < r1; ++i) {
+    const uint32_t key = key_at(i);
+    if (key > limit || (key == limit && b_at < need)) {
+      const int pos = a.sinks + (int)(b_above + min(b_at, need));
       if (mine_at_all(pos)) kept[pos] = i;
     }
-    b_above += __popc(ma);
-    b_at += __popc(me_);
+    b_above += key > limit;
+    b_at += key == limit;
   }
   if (P > 1)
     cluster_sync();
@@ -364,10 +370,6 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   }
 
   // ------------------------------------------------------------ moves
-#pragma unroll 4
-  for (int j = threadIdx.x; position(j) < m; j += T) out_w[position(j)] = stage[position(j)];
-#pragma unroll 4
-  for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
   char *base = a.kv + l * a.layer_stride + (int64_t)h * a.row_bytes;
   // Stage s: positions (s C + rank) each + 0 ... each - 1 of this CTA, from the
   // first stage with a row that moves.  This thread moves up to kWordsEach
@@ -435,6 +437,11 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   __syncthreads();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(s0 + s, s, s);
+  // the weights, while the first rows are on their way
+#pragma unroll 4
+  for (int j = threadIdx.x; position(j) < m; j += T) out_w[position(j)] = stage[position(j)];
+#pragma unroll 4
+  for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
   if (C > 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
