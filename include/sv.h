@@ -438,9 +438,10 @@ sv_status sv_tree_attention_ex(const void *q, const void *kv, const int32_t *bas
  * the sum is split; equal inputs give equal tokens).  Rows need not be
  * normalised: only the weights' proportions count.
  *
- *   qprobs       [B][N+1][ldq] target probabilities, the first V of each row;
- *                ldq >= V elements between rows (N+1 rows a sequence, packed)
- *   pprobs       [B][N][ldp] draft probabilities, ldp >= V, or NULL
+ *   qprobs       [B][N+1][V] target probabilities: row i of sequence b starts
+ *                b q_seq + i q_row elements in (strides >= 0: padded, sliced
+ *                or broadcast rows are read where they are)
+ *   pprobs       [B][N][V] draft probabilities, strides p_seq, p_row, or NULL
  *   dt           SV_F32 or SV_BF16, of both
  *   draft_tokens [B][N] int32 (may be NULL when N == 0)
  *   n_draft      [B] int32 drafted tokens of each sequence, 0..N, or NULL: N
@@ -456,7 +457,8 @@ sv_status sv_tree_attention_ex(const void *q, const void *kv, const int32_t *bas
  * sequence emit nothing: accept_len 0, tokens all -1.  V <= SV_MAX_VOCAB,
  * N <= SV_MAX_POSITIONS.  One launch, no workspace; capturable.
  * --------------------------------------------------------------------------- */
-sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, const void *pprobs, int64_t ldp,
+sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row,
+                                const void *pprobs, int64_t p_seq, int64_t p_row,
                                 sv_dtype dt, const int32_t *draft_tokens,
                                 const int32_t *n_draft, const float *u_accept,
                                 const float *u_sample, int B, int N, int V,
@@ -492,7 +494,9 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, const void *ppr
  * none that is, are never read (they may hold anything, their table entries
  * too).  seq_len out of range (SV_ROW_BAD_LEN) or a needed page outside
  * [0, num_pages) (SV_ROW_BAD_PAGE) gives NaN rows and leaves weight_sum.
- * Pages may be shared between sequences.  q, kv, out 16-byte aligned.
+ * Pages may be shared between sequences.  q, kv, out 16-byte aligned.  The
+ * outputs overlap no input.  Sums are held unnormalised in 32 bits: n slots of
+ * values beyond 2^120 / n can overflow.
  *
  * Work is split over the slots by the lengths found on the device, so that one
  * captured launch serves growing sequences.  The workspace (bytes from the
@@ -527,14 +531,15 @@ sv_status sv_paged_attention(const void *q, const void *kv, int64_t kv_stride,
  *   kv    the cache of sv_paged_attention with a layer dimension in front:
  *         layer l starts layer_stride elements further; elem_bytes per
  *         element, D elem_bytes a multiple of 4 (of 16, with 16-byte-aligned
- *         kv and strides, is faster).  Every page a sequence uses belongs to
- *         it alone and appears once in its table: a page that does not ends
- *         with one of the rows that were to move there
+ *         kv and strides, is faster), at most 2048.  Every page a sequence
+ *         uses belongs to it alone and appears once in its table (a page that
+ *         does not ends with words of any of the rows that move there)
  *   weight_sum fp32 [L][B][Hkv][S], S >= max_pages page (what
  *         sv_paged_attention adds up); out_weight_sum the same, or weight_sum
- *         itself: its first n slots are written, the others left
+ *         itself (not a shifted part of it): its first n slots are written,
+ *         the others left
  *   out_kept   int32 [L][B][Hkv][budget]: the slots kept, then -1
- *   out_kv_len int32 [B]: min(n, budget)
+ *   out_kv_len int32 [B]: min(n, budget); not seq_len itself
  *   out_status uint32 [B] or NULL, written in full
  * A length outside [0, max_pages page] (SV_ROW_BAD_LEN) or a page of the
  * sequence outside [0, num_pages) (SV_ROW_BAD_PAGE) moves nothing: kept -1,

@@ -101,8 +101,8 @@ def load_library(path: str = LIB_PATH):
                                        vp, u64, vp]
     L.sv_tree_attention_ex.restype = i32
     i64 = C.c_int64
-    L.sv_verify_chain_probs.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
-                                        vp, vp, vp, vp]
+    L.sv_verify_chain_probs.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32,
+                                        i32, vp, vp, vp, vp]
     L.sv_verify_chain_probs.restype = i32
     L.sv_paged_attention_workspace.argtypes = [i32] * 9
     L.sv_paged_attention_workspace.restype = sz
@@ -328,24 +328,21 @@ def _want(name, t, dtype, shape):
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _row_stride(name, t, dtype, shape):
-    """Elements between the rows of t [B][R][V]: rows may be padded (a view of
-    the first V columns), sequences follow each other row by row."""
+def _row_strides(name, t, dtype, shape):
+    """Elements between the sequences and between the rows of t [B][R][V]."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: need a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    B, R, V = shape
-    sb, sr, sv = t.stride()
-    ld = sr if R > 1 else sb if B > 1 else V
-    if (V > 1 and sv != 1) or (B > 1 and R > 0 and sb != R * ld):
-        raise ValueError(f"{name}: rows need unit stride and one row stride, got strides "
-                         f"{t.stride()}")
-    return max(ld, V)
+    seq, row, col = t.stride()
+    if col != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: rows need unit stride, got strides {t.stride()}")
+    return seq, row
 
 
 def sv_verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sample, out_tokens,
                           out_accept_len, out_status, stream=None):
-    """qprobs [B][N+1][V], pprobs [B][N][V] or None (one-hot drafts); rows may be padded."""
+    """qprobs [B][N+1][V], pprobs [B][N][V] or None (one-hot drafts); only a row's
+    own elements have to be packed."""
     B, R, _ = qprobs.shape
     _want("out_tokens", out_tokens, torch.int32, (B, R))
     _want("out_accept_len", out_accept_len, torch.int32, (B,))
@@ -359,8 +356,10 @@ def _verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sampl
     B, R, V = qprobs.shape
     N = R - 1
     i32, f32 = torch.int32, torch.float32
-    ldq = _row_stride("qprobs", qprobs, qprobs.dtype, (B, R, V))
-    ldp = _row_stride("pprobs", pprobs, qprobs.dtype, (B, N, V)) if pprobs is not None else V
+    q_seq, q_row = _row_strides("qprobs", qprobs, qprobs.dtype, (B, R, V))
+    p_seq = p_row = 0
+    if pprobs is not None:
+        p_seq, p_row = _row_strides("pprobs", pprobs, qprobs.dtype, (B, N, V))
     if N > 0:
         _want("draft_tokens", draft_tokens, i32, (B, N))
         _want("u_accept", u_accept, f32, (B, N))
@@ -368,7 +367,7 @@ def _verify_chain_probs(qprobs, pprobs, draft_tokens, n_draft, u_accept, u_sampl
         _want("n_draft", n_draft, i32, (B,))
     _want("u_sample", u_sample, f32, (B,))
     return _check(load_library().sv_verify_chain_probs(
-        _p(qprobs), ldq, _p(pprobs) if N > 0 else None, ldp, _dtype(qprobs),
+        _p(qprobs), q_seq, q_row, _p(pprobs) if N > 0 else None, p_seq, p_row, _dtype(qprobs),
         _p(draft_tokens) if N > 0 else None, _p(n_draft), _p(u_accept) if N > 0 else None,
         _p(u_sample), B, N, V, _p(out_tokens), _p(out_accept_len), _p(out_status),
         _stream(stream)))
@@ -562,8 +561,8 @@ def verify_chain_probs(qprobs, pprobs, draft_tokens, u_accept, u_sample, n_draft
                        stream=None):
     """Verify a chain from probabilities and given random numbers (see
     sv_verify_chain_probs): qprobs [B][N+1][V] and pprobs [B][N][V] (or None:
-    drafts without a distribution) in fp32 or bf16, rows possibly padded;
-    draft_tokens int32 [B][N]; u_accept fp32 [B][N] and u_sample fp32 [B] in
+    drafts without a distribution) in fp32 or bf16, rows padded, sliced or
+    broadcast as they come; draft_tokens int32 [B][N]; u_accept fp32 [B][N] and u_sample fp32 [B] in
     [0, 1); n_draft int32 [B] (None: N drafts everywhere).  Returns a dict of
     tensors: tokens [B][N+1], accept_len [B], status [B]."""
     B, R, _ = qprobs.shape

@@ -26,7 +26,7 @@
 // the selections of some run under the moves of others.
 #include <math.h>
 
-#include "common.cuh"
+#include "cluster.cuh"
 
 namespace sv {
 namespace {
@@ -66,14 +66,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint4 cluster_ld_v4(const void *p, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(cluster_addr(p, rank))
-               : "memory");
-  return v;
-}
 template <typename V>
 __device__ __forceinline__ void cp_word(uint32_t dst, const void *src) {
   if constexpr (sizeof(V) == 16)
@@ -444,7 +436,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
   if (C > 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   }
   int slot = 0, place = 0;  // of stage s: (s - s0) mod kStages, mod (kStages + 1)
   for (int s = s0; s < stages; ++s) {
@@ -453,8 +445,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     // threads.  Over the cluster nothing has to be made visible: the copies
     // have arrived, and only then may the others write where they read from.
     if (C > 1) {
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");            // for stage s
-      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // for stage s + 1
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");            // for stage s
+      asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // for stage s + 1
     }
     __syncthreads();
     const int before = place == 0 ? kStages : place - 1;
@@ -473,7 +465,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     place = place == kStages ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // the last arrival's
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // the last arrival's
 }
 
 // How many clusters of C CTAs, one CTA to an SM, the device runs at once: GPCs
@@ -590,6 +582,15 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
                    kv_stride * elem_bytes % 16 == 0 && layer_stride * elem_bytes % 16 == 0;
   if (workspace_bytes < z.total)
     return set_error(SV_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes, z.total);
+  // other CTAs still read what one writes
+  auto overlap = [](const void *x, size_t nx, const void *y, size_t ny) {
+    return (uintptr_t)x < (uintptr_t)y + ny && (uintptr_t)y < (uintptr_t)x + nx;
+  };
+  const size_t sums = (size_t)z.items * S * 4;
+  if (out_weight_sum != weight_sum && overlap(weight_sum, sums, out_weight_sum, sums))
+    return set_error(SV_ERR_INVALID_ARG, "out_weight_sum overlaps weight_sum (it may be the same)");
+  if (overlap(out_kv_len, (size_t)B * 4, seq_len, (size_t)B * 4))
+    return set_error(SV_ERR_INVALID_ARG, "out_kv_len overlaps seq_len");
   sv_status s;
   if ((s = map_arg(kv, "kv")) != SV_OK || (s = map_arg(block_table, "block_table")) != SV_OK ||
       (s = map_arg(seq_len, "seq_len")) != SV_OK || (s = map_arg(weight_sum, "weight_sum")) != SV_OK ||

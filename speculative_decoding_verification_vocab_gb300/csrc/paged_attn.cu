@@ -55,7 +55,7 @@ constexpr int kMaxSlots = 1 << 30;
 // when a score is above it by 2^8: weights stay below 2^8, sums and products
 // are in 32 bits, and most tiles need no maximum over the warp.
 constexpr float kSlack = 8.0f;
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.4426950408889634f;
 
 struct PagedArgs {
   const void *q, *kv;
@@ -901,7 +901,8 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
     return set_error(SV_ERR_INVALID_ARG, "the cache is SV_BF16 or SV_F16, not dtype %d", (int)dt);
   if (D != 64 && D != 128 && D != 256)
     return set_error(SV_ERR_UNSUPPORTED, "head dimension %d (64, 128 or 256)", D);
-  if (!(scale > 0.0f) || !isfinite(scale)) return set_error(SV_ERR_INVALID_ARG, "scale must be > 0");
+  if (!(scale > 0.0f) || !isfinite(scale * kLog2e))
+    return set_error(SV_ERR_INVALID_ARG, "scale must be > 0 and finite");
   Sizes z;
   if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, window, sinks, weight_sum != nullptr))
     return set_error(SV_ERR_UNSUPPORTED, "more than 2^30 slots a sequence, or too many work units");
@@ -956,7 +957,7 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.sinks = sinks;
   a.cap = z.cap;
   a.units = units_for(D, B);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale * kLog2e;
   a.rows = z.rows;
   a.vis_max = z.vis_max;
   a.weight_sum = weight_sum;

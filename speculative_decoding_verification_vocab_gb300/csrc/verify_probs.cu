@@ -16,7 +16,7 @@
 //
 // The sum is exact: floor(w 2^62) of a w in [0, 2) is its 24-bit mantissa
 // shifted into 63 bits, so the order of the additions cannot change the token.
-#include "common.cuh"
+#include "cluster.cuh"
 
 namespace sv {
 namespace {
@@ -29,7 +29,7 @@ constexpr uint32_t kTwo = 0x40000000u;  // bits of 2.0f: from here on, and below
 
 struct ProbArgs {
   const void *q, *p;  // p NULL: one-hot drafts
-  int64_t ldq, ldp;
+  int64_t q_seq, q_row, p_seq, p_row;  // elements between sequences and between rows
   const int32_t *draft, *n_draft;
   const float *ua, *us;
   int N, V;
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
   __shared__ int s_part, s_again, s_token;
   __shared__ unsigned long long s_scan[kWarps];
   constexpr uint32_t kFault = 1u << 31;
-  const T *qrows = (const T *)a.q + (size_t)b * (a.N + 1) * a.ldq;
-  const T *prows = a.p ? (const T *)a.p + (size_t)b * a.N * a.ldp : nullptr;
+  const T *qrows = (const T *)a.q + b * a.q_seq;
+  const T *prows = a.p ? (const T *)a.p + b * a.p_seq : nullptr;
   const float us = a.us[b];
 
   if (warp == 0) {  // the walk, 32 positions at a time
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
         if (d < 0 || d >= a.V) {
           f = kFault | SV_ROW_BAD_TOKEN;
         } else {
-          const float qd = load_elem(qrows + (size_t)i * a.ldq + d);
-          const float pd = prows ? load_elem(prows + (size_t)i * a.ldp + d) : 1.0f;
+          const float qd = load_elem(qrows + i * a.q_row + d);
+          const float pd = prows ? load_elem(prows + i * a.p_row + d) : 1.0f;
           if (bad_entry(qd) || bad_entry(pd)) f |= kFault | SV_ROW_NAN;
           if (pd == 0.0f) f |= SV_ROW_P_ZERO;
           // 24-bit mantissas: the product is exact in 64 bits
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
   const int n_acc = s_a;
   const bool rejected = n_acc < s_n;
   uint32_t flags = s_flags;
-  const T *q = qrows + (size_t)n_acc * a.ldq;
-  const T *p = rejected && prows ? prows + (size_t)n_acc * a.ldp : nullptr;
+  const T *q = qrows + n_acc * a.q_row;
+  const T *p = rejected && prows ? prows + n_acc * a.p_row : nullptr;
   // one-hot: the weight of the rejected token is what q has above 1
   int hot = rejected && !prows && !(flags & kFault) ? a.draft[(size_t)b * a.N + n_acc] : -1;
   const int parts = (int)C * kWarps;
@@ -381,8 +381,8 @@ cudaError_t launch(const ProbArgs &a, int B, unsigned C, cudaStream_t st) {
 
 using namespace sv;
 
-extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, const void *pprobs,
-                                           int64_t ldp, sv_dtype dt, const int32_t *draft_tokens,
+extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row,
+                                           const void *pprobs, int64_t p_seq, int64_t p_row, sv_dtype dt, const int32_t *draft_tokens,
                                            const int32_t *n_draft, const float *u_accept,
                                            const float *u_sample, int B, int N, int V,
                                            int32_t *out_tokens, int32_t *out_accept_len,
@@ -390,14 +390,13 @@ extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, cons
   if (B < 0 || N < 0 || V < 1) return set_error(SV_ERR_INVALID_ARG, "need B >= 0, N >= 0, V >= 1");
   if (dt != SV_F32 && dt != SV_BF16)
     return set_error(SV_ERR_INVALID_ARG, "probabilities are SV_F32 or SV_BF16, not dtype %d", (int)dt);
-  if (ldq < V || (pprobs && ldp < V))
-    return set_error(SV_ERR_INVALID_ARG, "row strides ldq, ldp must be at least V");
   if (V > SV_MAX_VOCAB) return set_error(SV_ERR_UNSUPPORTED, "V > %d", SV_MAX_VOCAB);
   if (N > SV_MAX_POSITIONS) return set_error(SV_ERR_UNSUPPORTED, "N > %d", SV_MAX_POSITIONS);
   if (B > (1 << 24)) return set_error(SV_ERR_UNSUPPORTED, "B > %d", 1 << 24);
-  const int64_t ld_max = INT64_MAX / ((int64_t)(N + 1) * (B > 0 ? B : 1) * 8);
-  if (ldq > ld_max || (pprobs && ldp > ld_max))
-    return set_error(SV_ERR_INVALID_ARG, "row stride too large");
+  const int64_t most = INT64_MAX / 16;  // of any offset, in elements
+  auto bad_stride = [most](int64_t x, int64_t n) { return x < 0 || (n > 0 && x > most / n); };
+  if (bad_stride(q_seq, B) || bad_stride(q_row, N) || (pprobs && (bad_stride(p_seq, B) || bad_stride(p_row, N))))
+    return set_error(SV_ERR_INVALID_ARG, "negative or too large stride");
   if (B == 0) return SV_OK;
   if (!qprobs || !u_sample || !out_tokens || !out_accept_len || !out_status ||
       (N > 0 && (!draft_tokens || !u_accept)))
@@ -423,8 +422,10 @@ extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t ldq, cons
   ProbArgs a;
   a.q = qprobs;
   a.p = pprobs;
-  a.ldq = ldq;
-  a.ldp = ldp;
+  a.q_seq = q_seq;
+  a.q_row = q_row;
+  a.p_seq = p_seq;
+  a.p_row = p_row;
   a.draft = draft_tokens;
   a.n_draft = n_draft;
   a.ua = u_accept;

@@ -24,11 +24,13 @@ def make(L, lens, Hkv, D, page, dtype=torch.bfloat16, seed=0, zeros=0.2, coarse=
     g = torch.Generator().manual_seed(seed)
     B = len(lens)
     per = max(1, -(-max(lens) // page)) + 1
-    P = B * per + 3
+    need = [-(-n // page) for n in lens]
+    P = sum(need) + 3
     kv = torch.randint(-100, 100, (L, 2, P, page, Hkv, D), generator=g).to(dtype)
-    table = torch.randperm(P, generator=g)[:B * per].view(B, per).to(torch.int32)
-    for b, n in enumerate(lens):
-        table[b, -(-n // page):] = -9              # entries nothing needs
+    ids = torch.randperm(P, generator=g).to(torch.int32)
+    table = torch.full((B, per), -9, dtype=torch.int32)   # entries nothing needs
+    for b, k in enumerate(need):
+        table[b, :k] = ids[sum(need[:b]):sum(need[:b]) + k]
     w = torch.randn(L, B, Hkv, per * page + 5, generator=g).exp()
     if coarse:
         w = torch.round(w * 2) / 2                 # many equal weights
@@ -84,6 +86,18 @@ def test_matches_the_definition(L, lens, Hkv, D, page, dtype, budget, sinks, rec
 def test_one_long_sequence(budget, recent):
     """Several CTAs choose together; column ranges move apart."""
     check(*make(1, [30011], 2, 64, 64, seed=budget), budget, 4, recent)
+
+
+@pytest.mark.parametrize("L,lens,Hkv,page,budget", [
+    (1, [20000, 9000, 3, 12000, 9001], 4, 64, 5000),     # 20 heads: clusters of 6 that choose together
+    (5, [10000], 5, 33, 1000),                           # 25: clusters of 5
+    (1, [9500, 200], 17, 16, 333),                       # 34: of 4
+    (2, [8300] + [40] * 24, 3, 16, 33),                  # 150: single CTAs
+    (4, [9000, 700] + [60] * 18, 4, 32, 50),             # 320: small CTAs, keys read again
+    (1, [50000] + [30] * 39, 4, 64, 7),                  # 160, long: large CTAs, keys read again
+])
+def test_every_arrangement_of_the_work(L, lens, Hkv, page, budget):
+    check(*make(L, lens, Hkv, 8, page, seed=budget, coarse=budget % 2 == 1), budget, 1, 3)
 
 
 def test_equal_weights_keep_the_lower_slots():
@@ -178,6 +192,35 @@ def test_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert np.array_equal(as_bytes(k.cpu()), want[0]) and np.array_equal(ws.cpu().numpy(), want[1])
+
+
+def test_empty_batch_and_host_memory():
+    kv, table, lens, w = make(1, [150, 90], 2, 64, 16, seed=12)
+    d = [t.to(DEV) for t in (kv, table, lens, w)]
+    kept, n, st = sv.kv_evict(d[0], d[1][:0], d[2][:0], d[3][:, :0], 8)
+    assert kept.shape == (1, 0, 2, 8) and n.shape == (0,) and torch.equal(d[0].cpu(), kv)
+    want = plain.kv_evict(as_bytes(kv), table.numpy(), lens.numpy(), w.numpy(), 64, 4, 8)
+    h = [t.pin_memory() for t in (kv, table, lens, w)]
+    kept, n, _ = sv.kv_evict(*h, 64, 4, 8)
+    torch.cuda.synchronize()
+    assert np.array_equal(as_bytes(h[0]), want[0]) and np.array_equal(h[3].numpy(), want[1])
+    assert np.array_equal(kept.cpu().numpy(), want[2])
+
+
+def test_refusals_leave_everything():
+    kv, table, lens, w = [t.to(DEV) for t in make(1, [100], 2, 64, 16, seed=13)]
+    before = kv.clone(), w.clone()
+    n0 = sv.sv_launch_count()
+    for kw in (dict(budget=0), dict(budget=20, sinks=15, recent=6), dict(budget=20, sinks=-1)):
+        with pytest.raises(sv.SvError):
+            sv.kv_evict(kv, table, lens, w, **kw)
+    flat = torch.zeros(w.numel() + 4, device=DEV)
+    with pytest.raises(sv.SvError):          # a shifted part of the weights themselves
+        sv.kv_evict(kv, table, lens, flat[:-4].view(w.shape), 20, out_weight_sum=flat[4:].view(w.shape))
+    with pytest.raises(sv.SvError):
+        sv.kv_evict(kv, table, lens, w, 20, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+    assert sv.sv_launch_count() == n0
+    assert torch.equal(kv, before[0]) and torch.equal(w, before[1])
 
 
 def test_offsets_past_32_bits():

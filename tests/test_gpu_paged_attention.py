@@ -129,6 +129,18 @@ def test_split_over_the_length(lens, Hq, Hkv, D, page):
     check(*make(lens, Hq, Hkv, D, page, seed=7), weights=True)
 
 
+@pytest.mark.parametrize("Hq,Hkv,page,window,sinks", [
+    (20, 1, 24, 0, 0),       # two groups of heads, rows looked up one by one
+    (33, 1, 16, 0, 0),       # three, the last of one head
+    (24, 2, 16, 3000, 20),   # G = 12; a window from the middle of a group of 16
+    (6, 2, 7, 2500, 37),
+])
+def test_split_with_groups_and_windows(Hq, Hkv, page, window, sinks):
+    lens = [7001, 100, 2530, 4096]
+    check(*make(lens, Hq, Hkv, 64, page, torch.float16, seed=Hq, window=window, sinks=sinks),
+          window=window, sinks=sinks, weights=True)
+
+
 @pytest.mark.parametrize("B", [130, 700])
 def test_many_sequences(B):
     """More sequences than threads; ragged, with empty ones."""
@@ -266,6 +278,52 @@ def test_repeats_streams_and_graphs():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, sv.paged_attention(d[0], kv2, table2, ln)), step
+
+
+def test_empty_batch_host_memory_and_refusals():
+    q, kv, table, lens = make([150, 90], 8, 2, 64, 16, seed=12)
+    d = [t.to(DEV) for t in (q, kv, table, lens)]
+    out, lse, st = sv.paged_attention(d[0][:0], d[1], d[2][:0], d[3][:0], return_lse=True)
+    assert out.shape == (0, 8, 64) and lse.shape == (0, 8) and st.shape == (0,)
+    want = sv.paged_attention(*d)
+    got = sv.paged_attention(*[t.pin_memory() for t in (q, kv, table, lens)])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    n0 = sv.sv_launch_count()
+    sums = torch.zeros(2, 2, 40, device=DEV)
+    for kw in (dict(scale=0.0), dict(window=-1), dict(weight_sum=sums),
+               dict(weight_sum=torch.zeros(2, 2, 400, device=DEV),
+                    workspace=torch.empty(8, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(sv.SvError):
+            sv.paged_attention(*d, **kw)
+    flat = torch.zeros(2 * 8 * 64 + 1, dtype=q.dtype, device=DEV)
+    with pytest.raises(sv.SvError):                # q off the 16-byte grid
+        sv.paged_attention(flat[1:].view(2, 8, 64), *d[1:])
+    assert sv.sv_launch_count() == n0
+
+
+def test_two_host_threads():
+    """Calls of two threads at once, each on a stream of its own."""
+    import threading
+    jobs, results = [], {}
+    for i in range(2):
+        q, kv, table, lens = make([3000 + 700 * i, 40], 8, 2, 128, 16, seed=30 + i)
+        jobs.append([t.to(DEV) for t in (q, kv, table, lens)])
+    want = [sv.paged_attention(*j) for j in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        s = torch.cuda.Stream()
+        r = [sv.paged_attention(*jobs[i], stream=s) for _ in range(20)]
+        s.synchronize()
+        results[i] = r
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in results[i])
 
 
 def test_offsets_past_32_bits():

@@ -208,6 +208,21 @@ def test_same_sums_whatever_the_alignment():
     assert np.array_equal(r["tokens"].cpu().numpy(), want[0])
 
 
+def test_sliced_and_broadcast_rows():
+    """Rows where they are: a part of a longer draft, every other sequence, one
+    row for all sequences, one for all positions."""
+    q, p, d, ua, us = [t.to(DEV) for t in make(8, 5, 3001, seed=6)]
+    want = [run(*[t[::2].contiguous().cpu() for t in (q[:, :4], p[:, :3], d[:, :3], ua[:, :3], us)])]
+    r = sv.verify_chain_probs(q[::2, :4], p[::2, :3], *[t[::2].contiguous() for t in (d[:, :3], ua[:, :3], us)])
+    assert np.array_equal(r["tokens"].cpu().numpy(), want[0][0])
+    for a, b in ((q[:1].expand(8, -1, -1), p[:1].expand(8, -1, -1)),
+                 (q[:, :1].expand(-1, 6, -1), p[:, 2:3].expand(-1, 5, -1))):
+        r = sv.verify_chain_probs(a, b, d, ua, us)
+        want = run(a.contiguous().cpu(), b.contiguous().cpu(), d.cpu(), ua.cpu(), us.cpu())
+        for k, x in zip(("tokens", "accept_len", "status"), want):
+            assert np.array_equal(r[k].cpu().numpy(), x), k
+
+
 def test_empty_batch_and_host_memory():
     r = sv.verify_chain_probs(torch.zeros(0, 3, 10, device=DEV), torch.zeros(0, 2, 10, device=DEV),
                               torch.zeros(0, 2, dtype=torch.int32, device=DEV),

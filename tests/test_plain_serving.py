@@ -64,15 +64,15 @@ def test_verify_probs_host_checks(sv):
     f = sv.load_library().sv_verify_chain_probs
     x = 4096  # never looked at: the refusals below come first
 
-    def call(ldq=10, p=None, ldp=10, dt=0, d=x, n=None, ua=x, us=x, B=1, N=2, V=10, t=x, a=x, s=x,
-             q=x):
-        return f(q, ldq, p, ldp, dt, d, n, ua, us, B, N, V, t, a, s, None)
+    def call(qs=30, qr=10, p=None, ps=20, pr=10, dt=0, d=x, n=None, ua=x, us=x, B=1, N=2, V=10, t=x,
+             a=x, s=x, q=x):
+        return f(q, qs, qr, p, ps, pr, dt, d, n, ua, us, B, N, V, t, a, s, None)
     assert call(B=-1) == 1 and call(N=-1) == 1 and call(V=0) == 1
     assert call(dt=2) == 1 and b"SV_F32" in sv.load_library().sv_last_error()
-    assert call(ldq=9) == 1 and call(p=x, ldp=9) == 1
+    assert call(qs=-1) == 1 and call(qr=-1) == 1 and call(p=x, pr=-8) == 1
     assert b"stride" in sv.load_library().sv_last_error()
-    assert call(ldq=2 ** 61) == 1
-    assert call(V=(1 << 22) + 1, ldq=1 << 23) == 2 and call(N=1025) == 2
+    assert call(qr=2 ** 61) == 1 and call(p=x, ps=2 ** 62) == 1
+    assert call(V=(1 << 22) + 1) == 2 and call(N=1025) == 2
     assert call(q=None) == 1 and call(us=None) == 1 and call(d=None) == 1 and call(ua=None) == 1
     assert call(t=None) == 1 and call(a=None) == 1 and call(s=None) == 1
     assert b"null" in sv.load_library().sv_last_error()
@@ -93,7 +93,6 @@ def test_verify_probs_binding_refusals(sv):
     call(p=p.bfloat16())                                   # another type than q
     call(p=torch.zeros(2, 3, 8))                           # another shape
     call(q=torch.zeros(2, 8, 3).transpose(1, 2))           # columns apart
-    call(q=torch.zeros(4, 3, 8)[::2])                      # sequences apart
     call(d=d.long()), call(ua=ua.double()), call(us=us[:1])
     call(n=torch.zeros(3, dtype=torch.int32))
     call(d=torch.zeros(2, 4, dtype=torch.int32)[:, ::2])
@@ -134,6 +133,7 @@ def test_paged_attention_host_checks(sv):
     assert call(P=0) == 1 and call(window=-1) == 1 and call(sinks=-1) == 1 and call(Hkv=0) == 1
     assert call(dt=0) == 1 and call(D=96) == 2 and b"head dimension" in lib.sv_last_error()
     assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1 and call(scale=float("inf")) == 1
+    assert call(scale=3e38) == 1 and call(scale=-1.0) == 1
     assert call(page=1 << 20, mp=1 << 11, ps=1 << 40) == 2
     assert call(ps=16 * 2 * 128 - 8) == 1 and call(ps=16 * 2 * 128 + 4) == 1 and call(ks=-8) == 1
     assert call(w=x, S=63) == 1 and b"weight_sum" in lib.sv_last_error()
@@ -202,6 +202,10 @@ def test_kv_evict_host_checks(sv):
     assert call(kv=x + 2) == 1 and call(w=x + 2) == 1 and call(ws=x + 64) == 1
     assert call(ps=16 * 2 * 64 + 1) == 1 and b"misaligned" in lib.sv_last_error()
     assert call(wb=100) == 1 and b"workspace" in lib.sv_last_error()
+    y = 1 << 20
+    assert call(ow=x + 64, kl=y) == 1 and b"out_weight_sum overlaps" in lib.sv_last_error()
+    assert call(ow=x, kl=x) == 1 and b"out_kv_len overlaps" in lib.sv_last_error()
+    assert call(D=1025, e=2, ps=1 << 24) == 2 and b"2048" in lib.sv_last_error()
     assert call(B=0, kv=None, w=None) == 0
     assert sv.sv_kv_evict_workspace(2, 3, 4, 100) >= 2 * 3 * 4 * 404
     assert sv.sv_kv_evict_workspace(0, 3, 4, 100) == 0 and sv.sv_kv_evict_workspace(1 << 20, 1 << 10, 8, 9) == 0
