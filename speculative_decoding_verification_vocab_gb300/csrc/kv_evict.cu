@@ -23,7 +23,11 @@
 //              of the stores, and a barrier per stage stands between a stage's
 //              reads and its writes.
 // Bound: the rows that move, read and written once: memory.  With many CTAs
-// the selections of some run under the moves of others.
+// the selections of some run under the moves of others.  Measured (of the copy
+// rate, 6788 GB/s): 2048 items of about 2100 slots to 1024, 349 us for 2.18 GB
+// (0.92); 16 items of 131001 to 32768, 127 us for 0.56 GB (0.64: 33 us of
+// selection with idle memory, then 92); 8 items of 1101 to 1024, 15 us, of
+// which 3.5 select, 4 rank and list, 4 move.
 #include <math.h>
 
 #include "cluster.cuh"
@@ -34,7 +38,6 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kAhead = 4;  // loads of a thread in flight
 constexpr unsigned kMaxCluster = 8;
-constexpr int kWordsEach = 4;     // words of a thread in a stage of the ring
 constexpr int kLocal = 8192;
 constexpr int kMaxRowBytes = 2048;
 constexpr int kMaxSlots = 1 << 30;
@@ -76,21 +79,23 @@ __device__ __forceinline__ void cp_word(uint32_t dst, const void *src) {
 
 // Shared memory: the ring; before the moves, two histograms and the keys.
 template <typename V, int T> struct Layout {
+  // Words of a thread in a stage: 64 KB stages where a cluster's barrier stands
+  // between them (16 items of 131001 slots: 127 us; 136 with 32 KB ones and the
+  // barrier's arrival a stage ahead), 16 KB ones where four CTAs share an SM.
+  static constexpr int kWordsEach = T == 512 ? 8 : 4;
   static constexpr int kStageWords = T * kWordsEach;
-  // Stages of the ring, and how many of them the arrival at the cluster's
-  // barrier goes ahead of the stores (a barrier a stage costs 0.5 us).
-  static constexpr int kStages = T == 512 ? 5 : 3;
-  static constexpr int kLead = T == 512 ? 1 : 0;
+  static constexpr int kStages = 3;
   static constexpr int kRing = kStages * kStageWords * (int)sizeof(V);
   static constexpr int kKeysAt = 2 * kBins * 4;
   // keys that make the block no larger than its ring, but not fewer than this
   static constexpr int kMostKeys = T == 512 ? 47104 : 8192;
   static constexpr int kPer = T / 4;  // rows of a stage, at most
-  static constexpr int kOnePerSm = 200 * 1024;
+  static constexpr int kOnePerSm = 208 * 1024;
   static int bytes(int cached) {
     const int select = kKeysAt + cached * 4;
     return select > kRing ? select : kRing;
   }
+  static_assert(kRing <= kOnePerSm && kKeysAt + kMostKeys * 4 <= kOnePerSm, "one CTA to an SM");
   static_assert(2 * kMaxRowBytes <= kStageWords * (int)sizeof(V), "a stage holds a row's K and V");
 };
 
@@ -100,7 +105,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   grid_dep_sync();
   using Lay = Layout<V, T>;
   constexpr int W = T / 32;
-  constexpr int kStages = Lay::kStages;
+  constexpr int kStages = Lay::kStages, kWordsEach = Lay::kWordsEach;
   constexpr int PB = kBins / T;  // bins of a thread
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ long long s_from[kStages + 1][Lay::kPer], s_to[kStages + 1][Lay::kPer];
@@ -434,23 +439,17 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   for (int j = threadIdx.x; position(j) < m; j += T) out_w[position(j)] = stage[position(j)];
 #pragma unroll 4
   for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
-  if (C > 1) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-  }
   int slot = 0, place = 0;  // of stage s: (s - s0) mod kStages, mod (kStages + 1)
   for (int s = s0; s < stages; ++s) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2 - Lay::kLead) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     // This stage's reads are done and its successors' rows looked up, by all
     // threads.  Over the cluster nothing has to be made visible: the copies
     // have arrived, and only then may the others write where they read from.
-    if (C > 1) {
-      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");            // for stage s
-      asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // for stage s + 1
-    }
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     __syncthreads();
     const int before = place == 0 ? kStages : place - 1;
     load(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1, place >= 2 ? place - 2 : place + kStages - 1);
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     const int left = m - start(s);
     V v[kWordsEach];
 #pragma unroll
@@ -465,7 +464,6 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     place = place == kStages ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // the last arrival's
 }
 
 // How many clusters of C CTAs, one CTA to an SM, the device runs at once: GPCs
@@ -630,9 +628,10 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   a.w_stage = (float *)(ws + z.stage);
   a.w_src = (long long *)(ws + z.src);
   // Few items, or long sequences: large CTAs, and for each item the largest
-  // cluster with which all run at once (two clusters on the same SMs end last:
-  // 16 items in clusters of 8 took 175 us where 6 take 144).  Many: small CTAs,
-  // 4 on an SM, which select under each other's moves.
+  // cluster with which all run at once (16 items in clusters of 8, two of them
+  // on the same SMs, took 175 us where clusters of 6 took 144).  Many: small
+  // CTAs, 4 on an SM, which select under each other's moves (2048 items: 349 us;
+  // in two launches, selection and moves, 400).
   const int items = (int)z.items;
   a.C = 1;
   cudaStream_t st = (cudaStream_t)stream;

@@ -30,6 +30,14 @@
 // Groups of 16 keys start at multiples of 16 slots, so with pages of a multiple
 // of 16 slots one table entry serves a group; other page sizes look up every
 // row.  Rows that are not visible are zero-filled in shared memory, not read.
+//
+// Measured (of the copy rate, 6788 GB/s): 128 sequences of 3585-4096 tokens, 64
+// query heads on 8 KV heads of 128, 302 us for 2.02 GB (0.98; pages of 20 or of
+// 1 slot: 330 us); one of 131001 tokens, 84 us (0.94); windows of 2048 at D =
+// 64, 64 x 16 heads, 89 us (0.89); 24 ragged sequences with weight sums, 56 us
+// (0.62: units of unequal size, the scores' way to memory and back, two
+// launches).  With queries on the long side of the products (heads padded to
+// 16 rows) the same took 342, 109, 106 and 83 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
