@@ -1,4 +1,4 @@
-// cluster.cuh -- thread-block clusters: the launch, the barrier and loads from
+// cluster.cuh -- thread-block clusters: the launch, the barrier and access to
 // another CTA's shared memory.
 #pragma once
 
@@ -28,8 +28,8 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 }
 
 // This CTA's rank, the barrier of all threads of the cluster (its shared and
-// global memory writes before it are visible after it), and loads from the
-// shared memory of the cluster's CTA `rank` at this CTA's address `p`.
+// global memory writes before it are visible after it), and stores to and loads
+// from the shared memory of the cluster's CTA `rank` at this CTA's address `p`.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -46,14 +46,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
                : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void cluster_st_u64(const void *p, uint32_t rank, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(p, rank)), "l"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_ld_u32(const void *p, uint32_t rank) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ unsigned long long cluster_ld_u64(const void *p, uint32_t rank) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
 }
 __device__ __forceinline__ uint4 cluster_ld_v4(const void *p, uint32_t rank) {

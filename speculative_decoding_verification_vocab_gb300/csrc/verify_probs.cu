@@ -8,14 +8,17 @@
 // With probabilities given there is no row pass: the walk reads two numbers a
 // position, and the draw needs one row (bonus) or one row pair (residual) per
 // sequence, read once.  A cluster of C CTAs takes a sequence: every CTA walks
-// (the same few loads), sums the integer weights of its part of the row, warp
-// by warp, and after one cluster barrier reads all warps' sums from the
-// cluster's shared memory; the CTA that holds the threshold re-reads the one
-// warp's part it lies in (1 / (8 C) of the row, still in L2) and picks the
-// token.  No workspace, no counters, one launch.
+// (the same few loads) and sums the integer weights of its part of the row,
+// warp by warp; each warp stores its sum to every CTA of the cluster, and after
+// one cluster barrier every CTA finds the part that holds the threshold from
+// its own shared memory.  The CTA whose part it is re-reads it (1 / (8 C) of
+// the row, still in L2) and picks the token; the others are done.  No
+// workspace, no counters, one launch.  (With the sums loaded from the other
+// CTAs instead, which then have to stay until all have read, a CTA lived 19 us
+// at V = 128256, 8 of them reading its rows.)
 //
 // Bound: one row pair per sequence, memory, where there are many sequences: 256
-// at V = 128256 fp32, 45 us for 263 MB (0.86 of the copy rate; the rest is the
+// at V = 128256 fp32, 43 us for 263 MB (0.90 of the copy rate; the rest is the
 // first walk and the last pick, with idle memory).  Few: the chain of latencies
 // (walk, row, barrier, pick), 6 us of GPU time for one sequence at V = 1000.
 //
@@ -167,14 +170,18 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ uint4 ring[2 * kDepth * kThreads];
-  __shared__ unsigned long long s_w[kWarps];   // this CTA's warps' sums, read by the cluster
-  __shared__ unsigned long long s_ft[kWarps];  // fp32 sum (low word) and largest entry (high)
+  // all parts' sums, written by the cluster's warps: weights; fp32 sum (low
+  // word) and largest entry (high).  A second round has places of its own.
+  __shared__ unsigned long long s_w[2][kMaxCluster * kWarps], s_ft[2][kMaxCluster * kWarps];
   __shared__ int s_a, s_n;                     // accepted tokens; drafted tokens
   __shared__ uint32_t s_flags;                 // bits of the walk; kFault with them on a fault
   __shared__ unsigned long long s_left;        // the threshold within the part found
   __shared__ int s_part, s_again, s_token;
   __shared__ unsigned long long s_scan[kWarps];
   constexpr uint32_t kFault = 1u << 31;
+  // every CTA has started before another stores to its shared memory: waited
+  // for after the walk
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const T *qrows = (const T *)a.q + b * a.q_seq;
   const T *prows = a.p ? (const T *)a.p + b * a.p_seq : nullptr;
   const float us = a.us[b];
@@ -220,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
     }
   }
   __syncthreads();
+  if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   const int n_acc = s_a;
   const bool rejected = n_acc < s_n;
   uint32_t flags = s_flags;
@@ -245,16 +253,22 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
 #pragma unroll
     for (int o = 16; o; o >>= 1) s.f += __shfl_xor_sync(FULL, s.f, o);
     const uint32_t top = __reduce_max_sync(FULL, s.top);
-    if (lane == 0) {
-      s_w[warp] = w;
-      s_ft[warp] = (unsigned long long)top << 32 | __float_as_uint(s.f);
-    }
-    if (C > 1)
+    const unsigned long long ft = (unsigned long long)top << 32 | __float_as_uint(s.f);
+    if (C > 1) {
+      if (lane < (int)C) {
+        cluster_st_u64(&s_w[round][part], (uint32_t)lane, w);
+        cluster_st_u64(&s_ft[round][part], (uint32_t)lane, ft);
+      }
       cluster_sync();
-    else
+    } else {
+      if (lane == 0) {
+        s_w[round][part] = w;
+        s_ft[round][part] = ft;
+      }
       __syncthreads();
+    }
     if (warp == 0) {
-      // every CTA reads all parts' sums: lane l the parts [l k, (l + 1) k)
+      // lane l: the parts [l k, (l + 1) k)
       constexpr int K = (int)kMaxCluster * kWarps / 32;
       unsigned long long v[K], sum = 0;
       float f = 0.0f;
@@ -265,14 +279,8 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
         const int e = lane * k + j;
         v[j] = 0;
         if (j < k && e < parts) {
-          unsigned long long ft;
-          if (C > 1) {
-            v[j] = cluster_ld_u64(&s_w[e % kWarps], (uint32_t)(e / kWarps));
-            ft = cluster_ld_u64(&s_ft[e % kWarps], (uint32_t)(e / kWarps));
-          } else {
-            v[j] = s_w[e];
-            ft = s_ft[e];
-          }
+          v[j] = s_w[round][e];
+          const unsigned long long ft = s_ft[round][e];
           f += __uint_as_float((uint32_t)ft);
           tp = max(tp, (uint32_t)(ft >> 32));
         }
@@ -316,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
     flags = s_flags;
     const int found = s_part;
     const bool again = s_again;
-    if (C > 1 && again) cluster_sync();  // the sums are read: they may be written again
-    if (C == 1) __syncthreads();
+    __syncthreads();  // read by all before another round writes them
     if (!again) {
       if (!(flags & kFault) && found / kWarps == (int)rank) {
         // this CTA's part `found`: thread t takes k elements in a row
@@ -372,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
       a.status[b] = flags & ~kFault;
     }
   }
-  if (C > 1) cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
 template <typename T>
@@ -421,8 +427,8 @@ extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, in
       (s = map_arg(out_accept_len, "out_accept_len")) != SV_OK ||
       (s = map_arg(out_status, "out_status")) != SV_OK)
     return s;
-  // CTAs of a sequence: one per 32 KB of a row, up to 8 (4 at most: 52 us where
-  // 8 take 45; twice as many for short rows: no change)
+  // CTAs of a sequence: one per 32 KB of a row, up to 8 (4 at most: 49 us where
+  // 8 take 44; twice as many for short rows: no change)
   unsigned C = 1;
   while (C < kMaxCluster && (size_t)V * es > C * (size_t)32768) C *= 2;
   ProbArgs a;
