@@ -455,7 +455,8 @@ sv_status sv_tree_attention_ex(const void *q, const void *kv, const int32_t *bas
  * [0, V) (SV_ROW_BAD_TOKEN), a used random number outside [0, 1)
  * (SV_ROW_BAD_RAND) or n_draft outside [0, N] (SV_ROW_BAD_LEN) -- makes the
  * sequence emit nothing: accept_len 0, tokens all -1.  V <= SV_MAX_VOCAB,
- * N <= SV_MAX_POSITIONS.  One launch, no workspace; capturable.
+ * N <= SV_MAX_POSITIONS.  One launch, no workspace; capturable.  The outputs
+ * overlap no input.
  * --------------------------------------------------------------------------- */
 sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row,
                                 const void *pprobs, int64_t p_seq, int64_t p_row,
@@ -480,8 +481,9 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row
  *   q     [B][Hq][D], dt SV_BF16 or SV_F16
  *   kv    K rows at kv + id page_stride + r Hkv D + h D, V rows kv_stride
  *         further (elements of dt; page id, row r, KV head h): [2][num_pages]
- *         [page][Hkv][D] and [num_pages][2][page][Hkv][D] alike.  Both strides
- *         multiples of 8, page_stride >= page Hkv D
+ *         [page][Hkv][D] and [num_pages][2][page][Hkv][D] alike, and a
+ *         contiguous cache [2][B][S][Hkv][D] with page = S, block_table[b] =
+ *         b.  Both strides multiples of 8, page_stride >= page Hkv D
  *   block_table int32 [B][max_pages]; seq_len int32 [B], 0..max_pages page
  *   scale > 0, finite; D 64, 128 or 256; any G
  *   weight_sum fp32 [B][Hkv][S] or NULL, S >= max_pages page: at every visible
@@ -496,7 +498,7 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row
  * [0, num_pages) (SV_ROW_BAD_PAGE) gives NaN rows and leaves weight_sum.
  * Pages may be shared between sequences.  q, kv, out 16-byte aligned.  The
  * outputs overlap no input.  Sums are held unnormalised in 32 bits: n slots of
- * values beyond 2^120 / n can overflow.
+ * values beyond 2^120 / n can overflow, and infinite values give NaN.
  *
  * Work is split over the slots by the lengths found on the device, so that one
  * captured launch serves growing sequences.  The workspace (bytes from the

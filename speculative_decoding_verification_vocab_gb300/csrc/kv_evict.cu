@@ -99,7 +99,7 @@ template <typename V, int T> struct Layout {
   static_assert(2 * kMaxRowBytes <= kStageWords * (int)sizeof(V), "a stage holds a row's K and V");
 };
 
-// T = 256: C = 1, many items; T = 512: few items or long ones.
+// T = 256: C = 1, many items; T = 512: few.
 template <typename V, int T>
 __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a) {
   grid_dep_sync();
@@ -190,13 +190,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
           if (round == 0) s_keys[i - lo] = key = order_key(__uint_as_float(key));
           count(i, key);
         }
-      } else {  // kAhead loads in flight
-        for (int i0 = lo + threadIdx.x; i0 < hi; i0 += T * kAhead) {
-          float x[kAhead];
+      } else {  // too many to keep: read again each round
+        constexpr int kMany = 16;  // loads of a thread in flight
+        for (int i0 = lo + threadIdx.x; i0 < hi; i0 += T * kMany) {
+          float x[kMany];
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) x[j] = i0 + j * T < hi ? w[i0 + j * T] : 0.0f;
+          for (int j = 0; j < kMany; ++j) x[j] = i0 + j * T < hi ? w[i0 + j * T] : 0.0f;
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) count(i0 + j * T, order_key(x[j]));
+          for (int j = 0; j < kMany; ++j) count(i0 + j * T, order_key(x[j]));
         }
       }
       if (P > 1)
@@ -627,15 +628,15 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   char *ws = (char *)workspace;
   a.w_stage = (float *)(ws + z.stage);
   a.w_src = (long long *)(ws + z.src);
-  // Few items, or long sequences: large CTAs, and for each item the largest
-  // cluster with which all run at once (16 items in clusters of 8, two of them
+  // Few items: large CTAs, one to an SM, and for each item the largest cluster
+  // with which all run at once (16 items in clusters of 8, two of them
   // on the same SMs, took 175 us where clusters of 6 took 144).  Many: small
   // CTAs, 4 on an SM, which select under each other's moves (2048 items: 349 us;
   // in two launches, selection and moves, 400).
   const int items = (int)z.items;
   a.C = 1;
   cudaStream_t st = (cudaStream_t)stream;
-  if (items <= 304 || cap > 16384) {
+  if (items <= 152) {
     if ((s = allow_smem<uint4, 512>()) != SV_OK || (s = allow_smem<uint32_t, 512>()) != SV_OK) return s;
     for (int c = (int)kMaxCluster; c > 1 && a.C == 1; --c)
       if (items <= cluster_room(c)) a.C = c;

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   const int at = blockIdx.x - joins;
   const int item = at / key_ctas, b = item / a.Hkv, hkv = item % a.Hkv;
   const Visible vis = visible(a, __ldcg(a.seq_len + b));
-  const int p0 = at % key_ctas * kSumKeys;
+  int p0 = at % key_ctas * kSumKeys;
   if (vis.bad || p0 >= vis.n) {
     grid_dep_sync();
     return;
@@ -770,21 +770,22 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   }
   __syncthreads();
   if (s_flag) return;
-  for (int p = p0 + threadIdx.x; p < min(p0 + kSumKeys, vis.n); p += kEndThreads) {
-    if (!seen(vis, p)) continue;
-    const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + p) * a.G;
-    float w = 0.0f;
-    if (a.G % 4 == 0) {
-      for (int g = 0; g < a.G; g += 4) {
-        const float4 x = *(const float4 *)(sc + g);
-        w += ex2_approx(fmaf(x.x, a.scale_log2, -s_lse[g])) + ex2_approx(fmaf(x.y, a.scale_log2, -s_lse[g + 1])) +
-             ex2_approx(fmaf(x.z, a.scale_log2, -s_lse[g + 2])) + ex2_approx(fmaf(x.w, a.scale_log2, -s_lse[g + 3]));
+  for (; p0 < vis.n; p0 += key_ctas * kSumKeys)
+    for (int p = p0 + threadIdx.x; p < min(p0 + kSumKeys, vis.n); p += kEndThreads) {
+      if (!seen(vis, p)) continue;
+      const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + p) * a.G;
+      float w = 0.0f;
+      if (a.G % 4 == 0) {
+        for (int g = 0; g < a.G; g += 4) {
+          const float4 x = *(const float4 *)(sc + g);
+          w += ex2_approx(fmaf(x.x, a.scale_log2, -s_lse[g])) + ex2_approx(fmaf(x.y, a.scale_log2, -s_lse[g + 1])) +
+               ex2_approx(fmaf(x.z, a.scale_log2, -s_lse[g + 2])) + ex2_approx(fmaf(x.w, a.scale_log2, -s_lse[g + 3]));
+        }
+      } else {
+        for (int g = 0; g < a.G; ++g) w += ex2_approx(fmaf(sc[g], a.scale_log2, -s_lse[g]));
       }
-    } else {
-      for (int g = 0; g < a.G; ++g) w += ex2_approx(fmaf(sc[g], a.scale_log2, -s_lse[g]));
+      a.weight_sum[((size_t)b * a.Hkv + hkv) * a.S + slot_of(vis, p)] += w;
     }
-    a.weight_sum[((size_t)b * a.Hkv + hkv) * a.S + slot_of(vis, p)] += w;
-  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -822,7 +823,7 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
   }
   z.units = z.groups * z.NH;
   const long long rows = (long long)B * z.NH * kRows;  // CTAs of the join, at most
-  if (z.units > 0x3fffffffLL || rows > 0x3fffffffLL || z.G > 8192) return false;
+  if (z.units > 0x3fffffffLL || rows > 0x1fffffffLL || z.G > 8192) return false;
   const bool split = z.groups > B;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -866,9 +867,13 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   // spread over its warps), a warp to each row otherwise
   const int wide = (long long)a.B * a.NH < 64;
   const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
-  const int key_ctas = weights ? (z.vis_max + kSumKeys - 1) / kSumKeys : 0;
-  const long long ctas = joins + (long long)key_ctas * a.B * a.Hkv;
-  if (ctas > 0x7fffffffLL) return set_error(SV_ERR_UNSUPPORTED, "too many work units");
+  // CTAs for a head's slots: as the table has room for, but no more in all than
+  // the card runs a few times over (a table far longer than its sequences would
+  // cost an empty CTA for each of its parts)
+  const long long heads = (long long)a.B * a.Hkv, room = (4864 + heads - 1) / heads;
+  const long long want = (z.vis_max + kSumKeys - 1) / kSumKeys;
+  const int key_ctas = weights ? (int)(want < room ? want : room) : 0;
+  const long long ctas = joins + key_ctas * heads;
   LaunchScope ls("paged_finish", st);
   return check_launch("paged_finish",
                       launch_pdl(paged_finish_kernel<T, D>, dim3((unsigned)ctas), dim3(kEndThreads),

@@ -393,7 +393,8 @@ cudaError_t launch(const ProbArgs &a, int B, unsigned C, cudaStream_t st) {
 using namespace sv;
 
 extern "C" sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row,
-                                           const void *pprobs, int64_t p_seq, int64_t p_row, sv_dtype dt, const int32_t *draft_tokens,
+                                           const void *pprobs, int64_t p_seq, int64_t p_row,
+                                           sv_dtype dt, const int32_t *draft_tokens,
                                            const int32_t *n_draft, const float *u_accept,
                                            const float *u_sample, int B, int N, int V,
                                            int32_t *out_tokens, int32_t *out_accept_len,

@@ -93,8 +93,8 @@ def test_one_long_sequence(budget, recent):
     (5, [10000], 5, 33, 1000),                           # 25: clusters of 5
     (1, [9500, 200], 17, 16, 333),                       # 34: of 4
     (2, [8300] + [40] * 24, 3, 16, 33),                  # 150: single CTAs
-    (4, [9000, 700] + [60] * 18, 4, 32, 50),             # 320: small CTAs, keys read again
-    (1, [50000] + [30] * 39, 4, 64, 7),                  # 160, long: large CTAs, keys read again
+    (2, [9000, 700] + [60] * 18, 4, 32, 50),             # 160: small CTAs, keys read again
+    (1, [50000] + [30] * 24, 4, 64, 7),                  # 100, long: large CTAs, keys read again
 ])
 def test_every_arrangement_of_the_work(L, lens, Hkv, page, budget):
     check(*make(L, lens, Hkv, 8, page, seed=budget, coarse=budget % 2 == 1), budget, 1, 3)

@@ -239,6 +239,29 @@ def test_layouts_agree_bit_for_bit():
     check(q, kv, table, lens)
 
 
+def test_a_contiguous_cache_is_one_page_a_sequence():
+    """The library's own cache layout [2][B][S][Hkv][D], any S, slots past the
+    sequences holding anything."""
+    for S in (256, 300, 7):
+        q, kv, table, lens = make([S, S // 2], 8, 2, 64, S, seed=S, spare=0, extra_pages=0)
+        check(q, kv, table, lens, weights=True)
+
+
+def test_a_table_far_longer_than_its_sequences():
+    """Room for a million slots a sequence, a few used: the sums too."""
+    q, kv, table, lens = make([700, 20, 3001], 8, 2, 64, 16, seed=21, extra_pages=0)
+    long = torch.full((3, 60000), -1, dtype=torch.int32)
+    long[:, :table.shape[1]] = table
+    d = [t.to(DEV) for t in (q, kv)]
+    sums = torch.zeros(3, 2, 960000, device=DEV)
+    out, lse, st = sv.paged_attention(*d, long.to(DEV), lens.to(DEV), weight_sum=sums, return_lse=True)
+    assert not st.any()
+    small = torch.zeros(3, 2, table.shape[1] * 16, device=DEV)
+    want, wlse, _ = sv.paged_attention(*d, table.to(DEV), lens.to(DEV), weight_sum=small, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    assert torch.equal(sums[..., :small.shape[2]], small) and not sums[..., small.shape[2]:].any()
+
+
 def test_rows_of_the_output_alone_are_written():
     q, kv, table, lens = make([100, 50], 8, 2, 64, 16, seed=9)
     d = [t.to(DEV) for t in (q, kv, table, lens)]
