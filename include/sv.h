@@ -3,7 +3,8 @@
  * speculative decoding: Leviathan rejection sampling along a draft chain or
  * the best-scored path of an EAGLE-style draft tree, residual / bonus
  * sampling, the tree's ancestor attention mask, and KV-cache rollback /
- * compaction.
+ * compaction; beside them verification from given probabilities and random
+ * numbers, decode attention over a paged KV cache, and eviction from it.
  *
  * Sources (web pages; cited by title and section):
  *   [Lesson] "Decodificação Especulativa e EAGLE-3" (ai-engineering.academy,

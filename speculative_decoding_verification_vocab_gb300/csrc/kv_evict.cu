@@ -25,7 +25,7 @@
 // Bound: the rows that move, read and written once: memory.  With many CTAs
 // the selections of some run under the moves of others.  Measured (of the copy
 // rate, 6788 GB/s): 2048 items of about 2100 slots to 1024, 349 us for 2.18 GB
-// (0.92); 16 items of 131001 to 32768, 127 us for 0.56 GB (0.64: 33 us of
+// (0.92); 16 items of 131001 to 32768, 126 us for 0.56 GB (0.65: 33 us of
 // selection with idle memory, then 92); 8 items of 1101 to 1024, 15 us, of
 // which 3.5 select, 4 rank and list, 4 move.
 #include <math.h>
@@ -307,7 +307,9 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   // its own.
   const int words = a.row_bytes / (int)sizeof(V);
   const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
-  auto mine_at_all = [&](int k) { return P == C || k / each % C == rank; };
+  const int each_shift = (each & (each - 1)) ? -1 : __ffs(each) - 1;
+  auto turn_of = [&](int k) { return each_shift >= 0 ? k >> each_shift : k / each; };
+  auto mine_at_all = [&](int k) { return P == C || turn_of(k) % C == rank; };
 #pragma unroll 4
   for (int i = r0; i < r1; ++i) {
     const uint32_t key = key_at(i);
@@ -323,11 +325,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   else
     __syncthreads();
   // weights and rows of this CTA's positions, kAhead of a thread at a time;
-  // turn j of the CTA's rows is position j / each * each * C + ...
+  // its j-th position is the list's (j / each C + rank) each + j mod each
   float *stage = a.w_stage + (size_t)item * m;
   long long *src = a.w_src + (size_t)item * m;
   int first = 0x7fffffff;
-  auto position = [&](int j) { return C == 1 ? j : (j / each * C + rank) * each + j % each; };
+  auto position = [&](int j) {
+    const int turn = turn_of(j);
+    return j + (turn * (C - 1) + rank) * each;
+  };
   for (int j0 = threadIdx.x; position(j0) < m; j0 += T * kAhead) {
     int i[kAhead], id[kAhead];
     float x[kAhead];
@@ -436,8 +441,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(s0 + s, s, s);
   // the weights, while the first rows are on their way
-#pragma unroll 4
-  for (int j = threadIdx.x; position(j) < m; j += T) out_w[position(j)] = stage[position(j)];
+  for (int j0 = threadIdx.x; position(j0) < m; j0 += T * kAhead) {
+    float x[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) x[j] = position(j0 + j * T) < m ? stage[position(j0 + j * T)] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (position(j0 + j * T) < m) out_w[position(j0 + j * T)] = x[j];
+  }
 #pragma unroll 4
   for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
   int slot = 0, place = 0;  // of stage s: (s - s0) mod kStages, mod (kStages + 1)
