@@ -641,7 +641,7 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   a.w_src = (long long *)(ws + z.src);
   // Few items: large CTAs, one to an SM, and for each item the largest cluster
   // with which all run at once (16 items in clusters of 8, two of them
-  // on the same SMs, took 175 us where clusters of 6 took 144).  Many: small
+  // on the same SMs, took 175 us where clusters of 6 took 166).  Many: small
   // CTAs, 4 on an SM, which select under each other's moves (2048 items: 349 us;
   // in two launches, selection and moves, 400).
   const int items = (int)z.items;

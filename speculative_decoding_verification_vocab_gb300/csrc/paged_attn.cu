@@ -547,7 +547,8 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
         }
     }
     // P^T as the sum of two 16-bit parts: the weights keep twice the type's
-    // bits (one part alone would add a rounding as large as the output's own)
+    // bits (one part alone would add a rounding as large as the output's own:
+    // 2.2e-3 from 64 bits where bf16 rounds by 1.7e-3; it costs 1 % of the time)
     uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
