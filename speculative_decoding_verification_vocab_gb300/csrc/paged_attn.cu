@@ -122,11 +122,17 @@ struct Plan {
   int first;     // group index of the sequence's first unit
 };
 
-// One sequence splits evenly: as many units as are resident at once.  Several
-// of different lengths leave units of different sizes: twice as many, so that
-// the early ones make room.  Rounding up adds half a unit to each (sequence,
-// head); a batch of more of those than units is left whole.
-int units_for(int D, int B) { return (D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>) * (B == 1 ? 1 : 2); }
+// Units aimed at.  Where each (sequence, KV head) is cut into 8 and more, their
+// sizes are nearly equal, and one wave of as many as are resident is best (one
+// of 131001 tokens: 84 us, in two waves 93; two of 20000: 36 and 40).  Fewer
+// units each leave them unequal: twice as many, so that the early ones make
+// room (24 ragged sequences: 56 us, in one wave 61; 8 of 8000: 55 and 56).
+// Rounding up adds half a unit to each (sequence, head); a batch of more of
+// those than units is left whole.
+int units_for(int D, int B, int NH) {
+  const int slots = D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>;
+  return 8LL * B * NH <= slots ? slots : 2 * slots;
+}
 // tiles that a unit may have at most, for a batch of that many tiles in all
 __device__ __forceinline__ long long unit_tiles(const PagedArgs &a, long long tiles) {
   const long long room = max((long long)a.units / 2, a.B == 1 ? (long long)a.units : a.units - (long long)a.B * a.NH / 2);
@@ -818,7 +824,7 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
     z.groups = B;
   } else {
     const long long by_len = (long long)B * ((tiles + kMinTiles - 1) / kMinTiles);
-    const long long by_units = (long long)B + units_for(D, B) / z.NH;
+    const long long by_units = (long long)B + units_for(D, B, z.NH) / z.NH;
     z.groups = by_len < by_units ? by_len : by_units;
     if (z.groups < B) z.groups = B;
   }
@@ -970,7 +976,7 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.window = window;
   a.sinks = sinks;
   a.cap = z.cap;
-  a.units = units_for(D, B);
+  a.units = units_for(D, B, z.NH);
   a.scale_log2 = scale * kLog2e;
   a.rows = z.rows;
   a.vis_max = z.vis_max;
