@@ -129,9 +129,9 @@ struct Plan {
 // room (24 ragged sequences: 56 us, in one wave 61; 8 of 8000: 55 and 56).
 // Rounding up adds half a unit to each (sequence, head); a batch of more of
 // those than units is left whole.
+int slots_of(int D) { return D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>; }
 int units_for(int D, int B, int NH) {
-  const int slots = D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>;
-  return 8LL * B * NH <= slots ? slots : 2 * slots;
+  return 8LL * B * NH <= slots_of(D) ? slots_of(D) : 2 * slots_of(D);
 }
 // tiles that a unit may have at most, for a batch of that many tiles in all
 __device__ __forceinline__ long long unit_tiles(const PagedArgs &a, long long tiles) {
@@ -870,9 +870,9 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   if (s != SV_OK) return s;
   const bool split = z.groups > a.B;
   if (!split && !weights) return SV_OK;
-  // a CTA to each row while the rows are few (a long sequence's many units are
-  // spread over its warps), a warp to each row otherwise
-  const int wide = (long long)a.B * a.NH < 64;
+  // a CTA to each row where a head has 8 units and more, spread over its warps;
+  // a warp to each row otherwise
+  const int wide = 4LL * a.B * a.NH <= slots_of(D);
   const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
   // CTAs for a head's slots: as the table has room for, but no more in all than
   // the card runs a few times over (a table far longer than its sequences would
