@@ -20,9 +20,9 @@
 //
 // Work: a unit is a run of 64-key tiles of one (sequence, KV head, up to 16
 // query heads); KV heads of the same tiles are neighbouring CTAs, so that the
-// D-wide slices of one token's row are read at about the same time.  Each CTA
-// finds its unit from the lengths alone (a sum and a scan over the batch), so
-// the host never sees them and a captured graph follows them.  Within a unit
+// D-wide slices of one token's row are read at about the same time.  Units are
+// cut from the lengths on the device (a sum and a scan over the batch), so the
+// host never sees them and a captured graph follows them.  Within a unit
 // each of the 4 warps owns 16 keys of every tile: it loads them (cp.async, 16
 // bytes a lane), multiplies, and keeps its own m, l and O; nothing but the last
 // merge crosses warps, and no CTA barrier stands in the loop.
@@ -53,11 +53,11 @@ constexpr int kGroup = 16;                // keys of a warp in a tile
 constexpr int kTile = kWarps * kGroup;    // keys of a CTA tile
 constexpr int kRows = 16;                 // query heads of a unit, at most
 // CTAs that are resident at once on 152 SMs (2 per SM at D = 128), and the
-// fewest tiles of a unit (below that a unit's fixed cost shows).  Batches of
-// kWhole sequences and more are not split.
+// fewest tiles of a unit: below that its fixed cost shows (24 ragged sequences:
+// 56 us with 8, 59 with 16; one of 200 tokens: 8.4 us of GPU time with 8, 12.4
+// with 2 and a join).
 template <int D> constexpr int kSlots = D == 64 ? 608 : D == 128 ? 304 : 152;
 constexpr int kMinTiles = 8;
-constexpr int kWhole = 2048;
 constexpr int kMaxSlots = 1 << 30;
 // The reference the exponentials are taken against follows the maximum only
 // when a score is above it by 2^8: weights stay below 2^8, sums and products
@@ -72,7 +72,9 @@ struct PagedArgs {
   int B, Hq, Hkv, G, gt, NH;  // gt groups of 16 query heads per KV head, NH = Hkv gt
   int page, page_shift, max_pages, num_pages;
   int window, sinks, cap;
-  int units;  // aimed at
+  int units;   // aimed at
+  int groups;  // of units, one per KV head group, that the grid has room for
+  int finding;  // how a CTA finds its unit: one of the below
   float scale_log2;
   int rows;  // query heads of a unit: min(G, 16)
   int vis_max;
@@ -82,6 +84,8 @@ struct PagedArgs {
   float *lse;
   uint32_t *status;
   // workspace
+  int4 *w_map;       // [groups]: sequence (or -1), unit within it, its units, its length
+  int2 *w_first;     // [B]: index of the sequence's first group, its units
   float *w_o;        // [units][rows][D]
   float2 *w_ml;      // [units][rows]: reference (log2 units) and sum
   uint32_t *w_flag;  // [units]
@@ -121,6 +125,13 @@ struct Plan {
   int b, i, n;   // sequence, unit within it, units of it
   int first;     // group index of the sequence's first unit
 };
+// How a CTA finds its unit.  kWhole: no sequence has room for two.  kOne: a
+// single sequence.  kScan: by a scan of the lengths in every CTA.  kMap: from a
+// map that a launch of its own has written (128 sequences of 90-1110 tokens: 62
+// us either way; 256: 110 us with the map, 117 with the scan; 2000: 752 and
+// 1326; 16 of 2000-4000: 46 and 44).
+enum { kWhole, kOne, kScan, kMap };
+constexpr int kMapFrom = 160;
 
 // Units aimed at.  Where each (sequence, KV head) is cut into 8 and more, their
 // sizes are nearly equal, and one wave of as many as are resident is best (one
@@ -139,45 +150,30 @@ __device__ __forceinline__ long long unit_tiles(const PagedArgs &a, long long ti
   return min(max((long long)kMinTiles, (tiles * a.NH + room - 1) / room), (long long)kMaxSlots);
 }
 // units of a sequence of t tiles when a unit may have `most`
-__device__ __forceinline__ int units_of(const PagedArgs &a, int t, long long most) {
-  if (a.B >= kWhole || t <= kMinTiles) return 1;
+__device__ __forceinline__ int units_of(int t, long long most) {
+  if (t <= kMinTiles) return 1;
   return ((unsigned)t + (unsigned)most - 1) / (unsigned)most;
 }
 
-// The sequence and part that group g is (by_group), or the units of sequence g.
-// Every thread of the CTA calls it; b = -1 when there is no such group.
-template <int THREADS>
-__device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
+// Cuts the batch into groups of units: calls out(b, first, n) for every
+// sequence, each from one thread, and returns how many groups there are.  Every
+// thread of the CTA calls it.  Lengths are read past L1 (paged_finish_kernel).
+template <int THREADS, typename F>
+__device__ int cut_batch(const PagedArgs &a, F out) {
   constexpr int W = THREADS / 32;
   __shared__ long long s_red[W];
-  __shared__ Plan s_plan;
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Plan p;
-  if (a.B >= kWhole) {
-    p.b = g < a.B ? g : -1;
-    p.i = 0;
-    p.n = 1;
-    p.first = g;
-    return p;
-  }
-  if (a.B == 1) {
-    const int t = tiles_of(visible(a, __ldcg(a.seq_len)));
-    p.n = units_of(a, t, unit_tiles(a, t));
-    p.first = 0;
-    p.b = by_group && g >= p.n ? -1 : 0;
-    p.i = by_group ? g : 0;
-    return p;
-  }
   // a run of k sequences to each thread
   const int k = (a.B + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * k, a.B), b1 = min(b0 + k, a.B);
+  const int t0 = b0 < b1 ? tiles_of(visible(a, __ldcg(a.seq_len + b0))) : 0;  // read once where k = 1
+  auto tiles_at = [&](int b) { return b == b0 ? t0 : tiles_of(visible(a, __ldcg(a.seq_len + b))); };
   long long tiles = 0;
-  for (int b = b0; b < b1; ++b) tiles += tiles_of(visible(a, __ldcg(a.seq_len + b)));
+  for (int b = b0; b < b1; ++b) tiles += tiles_at(b);
 #pragma unroll
   for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(FULL, tiles, o);
   if (lane == 0) s_red[warp] = tiles;
-  if (threadIdx.x == 0) s_plan.b = -1;
   __syncthreads();
   tiles = 0;
 #pragma unroll
@@ -185,7 +181,7 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   __syncthreads();
   const long long most = unit_tiles(a, tiles);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units_of(a, tiles_of(visible(a, __ldcg(a.seq_len + b))), most);
+  for (int b = b0; b < b1; ++b) mine += units_of(tiles_at(b), most);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -194,23 +190,57 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
   }
   if (lane == 31) s_red[warp] = incl;
   __syncthreads();
-  int at = incl - mine;
-  for (int w = 0; w < warp; ++w) at += (int)s_red[w];
-  if (by_group ? g >= at && g < at + mine : g >= b0 && g < b1) {
-    for (int b = b0; b < b1; ++b) {
-      const int n = units_of(a, tiles_of(visible(a, __ldcg(a.seq_len + b))), most);
-      if (by_group ? g < at + n : b == g) {
-        s_plan.b = b;
-        s_plan.i = by_group ? g - at : 0;
-        s_plan.n = n;
-        s_plan.first = at;
-        break;
-      }
-      at += n;
-    }
+  int at = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) at += (int)s_red[w];
+    all += (int)s_red[w];
   }
+  for (int b = b0; b < b1; ++b) {
+    const int n = units_of(tiles_at(b), most);
+    out(b, at, n);
+    at += n;
+  }
+  return all;
+}
+
+// The sequence and part that group g is (by_group), or the units of sequence g.
+// Every thread of the CTA calls it; b = -1 when there is no such group.
+template <int THREADS>
+__device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
+  if (a.finding == kWhole) return Plan{g, 0, 1, g};
+  if (a.finding == kOne) {
+    const int t = tiles_of(visible(a, __ldcg(a.seq_len)));
+    const int n = units_of(t, unit_tiles(a, t));
+    return Plan{by_group && g >= n ? -1 : 0, by_group ? g : 0, n, 0};
+  }
+  if (a.finding == kMap) {
+    if (by_group) {
+      const int4 e = __ldcg(a.w_map + g);
+      return Plan{e.x, e.y, e.z, g - e.y};
+    }
+    const int2 e = __ldcg(a.w_first + g);
+    return Plan{g, 0, e.y, e.x};
+  }
+  __shared__ Plan s_plan;
+  if (threadIdx.x == 0) s_plan.b = -1;
+  __syncthreads();
+  cut_batch<THREADS>(a, [&](int b, int first, int n) {
+    if (by_group ? g >= first && g < first + n : b == g) s_plan = Plan{b, by_group ? g - first : 0, n, first};
+  });
   __syncthreads();
   return s_plan;
+}
+
+constexpr int kMapThreads = 1024;
+__global__ void __launch_bounds__(kMapThreads) paged_map_kernel(PagedArgs a) {
+  grid_dep_sync();
+  const int all = cut_batch<kMapThreads>(a, [&](int b, int first, int n) {
+    a.w_first[b] = make_int2(first, n);
+    const int len = a.seq_len[b];
+    for (int i = 0; i < n; ++i) a.w_map[first + i] = make_int4(b, i, n, len);
+  });
+  for (int g = all + threadIdx.x; g < a.groups; g += kMapThreads) a.w_map[g] = make_int4(-1, 0, 0, 0);
 }
 
 // ------------------------------------------------------------ element types
@@ -310,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   const int b = plan.b;
   const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
   const int rows = min(kRows, a.G - (h % a.gt) * kRows);
-  const Visible vis = visible(a, __ldcg(a.seq_len + b));
+  const Visible vis = visible(a, a.finding == kMap ? __ldcg(&a.w_map[unit / a.NH].w) : __ldcg(a.seq_len + b));
   const int tiles = tiles_of(vis);
   const int t0 = (int)((long long)tiles * plan.i / plan.n);
   const int t1 = (int)((long long)tiles * (plan.i + 1) / plan.n);
@@ -799,7 +829,8 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
 struct Sizes {
   int G, gt, NH, rows, cap, vis_max;
   long long groups, units;
-  size_t o, ml, flag, score, total;
+  int finding;
+  size_t map, first, o, ml, flag, score, total;
 };
 
 // false when the shape is beyond what the kernels index
@@ -820,14 +851,11 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
   }
   z.vis_max = (int)most;
   const long long tiles = (z.vis_max + kTile - 1) / kTile;
-  if (B >= kWhole) {
-    z.groups = B;
-  } else {
-    const long long by_len = (long long)B * ((tiles + kMinTiles - 1) / kMinTiles);
-    const long long by_units = (long long)B + units_for(D, B, z.NH) / z.NH;
-    z.groups = by_len < by_units ? by_len : by_units;
-    if (z.groups < B) z.groups = B;
-  }
+  const long long by_len = (long long)B * ((tiles + kMinTiles - 1) / kMinTiles);
+  const long long by_units = (long long)B + units_for(D, B, z.NH) / z.NH;
+  z.groups = by_len < by_units ? by_len : by_units;
+  if (z.groups < B) z.groups = B;
+  z.finding = z.groups == B ? kWhole : B == 1 ? kOne : B < kMapFrom ? kScan : kMap;
   z.units = z.groups * z.NH;
   const long long rows = (long long)B * z.NH * kRows;  // CTAs of the join, at most
   if (z.units > 0x3fffffffLL || rows > 0x1fffffffLL || z.G > 8192) return false;
@@ -838,6 +866,8 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
     at = align_up(at + n, 256);
     return r;
   };
+  z.map = take(z.finding == kMap ? (size_t)z.groups * 16 : 0);
+  z.first = take(z.finding == kMap ? (size_t)B * 8 : 0);
   z.o = take(split ? (size_t)z.units * z.rows * D * 4 : 0);
   z.ml = take(split || weights ? (size_t)z.units * z.rows * 8 : 0);
   z.flag = take(split || weights ? (size_t)z.units * 4 : 0);
@@ -866,12 +896,19 @@ sv_status attend(const PagedArgs &a, const Sizes &z, cudaStream_t st) {
 
 template <typename T, int D>
 sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st) {
-  const sv_status s = z.rows <= 8 ? attend<T, D, 1>(a, z, st) : attend<T, D, 2>(a, z, st);
+  sv_status s = SV_OK;
+  if (a.finding == kMap) {
+    LaunchScope ls("paged_map", st);
+    s = check_launch("paged_map", launch_pdl(paged_map_kernel, dim3(1), dim3(kMapThreads), 0, st, a));
+    if (s != SV_OK) return s;
+  }
+  s = z.rows <= 8 ? attend<T, D, 1>(a, z, st) : attend<T, D, 2>(a, z, st);
   if (s != SV_OK) return s;
   const bool split = z.groups > a.B;
   if (!split && !weights) return SV_OK;
-  // a CTA to each row where a head has 8 units and more, spread over its warps;
-  // a warp to each row otherwise
+  // a CTA to each row where a head has 8 units and more, spread over its warps
+  // (8 sequences of 8000: 53 us, with a warp to each 55); a warp to each row
+  // otherwise (24 ragged ones: 56 us, with a CTA to each 60)
   const int wide = 4LL * a.B * a.NH <= slots_of(D);
   const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
   // CTAs for a head's slots: as the table has room for, but no more in all than
@@ -987,6 +1024,10 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.status = out_status;
   char *w = (char *)workspace;
   const bool split = z.groups > B, wt = weight_sum != nullptr;
+  a.groups = (int)z.groups;
+  a.finding = z.finding;
+  a.w_map = z.finding == kMap ? (int4 *)(w + z.map) : nullptr;
+  a.w_first = z.finding == kMap ? (int2 *)(w + z.first) : nullptr;
   a.w_o = split ? (float *)(w + z.o) : nullptr;
   a.w_ml = split || wt ? (float2 *)(w + z.ml) : nullptr;
   a.w_flag = split || wt ? (uint32_t *)(w + z.flag) : nullptr;
