@@ -59,10 +59,17 @@ constexpr int kRows = 16;                 // query heads of a unit, at most
 template <int D> constexpr int kSlots = D == 64 ? 608 : D == 128 ? 304 : 152;
 constexpr int kMinTiles = 8;
 constexpr int kMaxSlots = 1 << 30;
-// The reference the exponentials are taken against follows the maximum only
-// when a score is above it by 2^8: weights stay below 2^8, sums and products
-// are in 32 bits, and most tiles need no maximum over the warp.
-constexpr float kSlack = 8.0f;
+// The reference the exponentials are taken against follows the maximum only when
+// a score is more than 2^kSlack above it: most tiles need no maximum over the
+// warp, and sums and products are in 32 bits.  In fp16 the reference lies 2^kBias
+// below the maximum it was set by, so that weights fill the type's range from the
+// top (2^15 at most): numbers below 2^-24 round to nothing, and 20000 weights of
+// 2^-25.5 beside one of 1 lost a quarter of their output with the reference at
+// the maximum.  Now a weight is off by 2^-36 of the largest.  bf16 reaches 2^-126.
+template <typename T> constexpr float kSlack = 8.0f;
+template <typename T> constexpr float kBias = 0.0f;
+template <> constexpr float kSlack<__half> = 4.0f;
+template <> constexpr float kBias<__half> = 11.0f;
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.4426950408889634f;
 
 struct PagedArgs {
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][2 + e]) * sc > m[n][e] + kSlack;
+      for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][2 + e]) * sc > m[n][e] + (kBias<T> + kSlack<T>);
     if (__any_sync(FULL, up)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
           float x = fmaxf(s[n][e], s[n][2 + e]) * sc;
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, w));
-          x = fmaxf(x, m[n][e]);
+          x = fmaxf(x - kBias<T>, m[n][e]);
           // a head without a finite score yet has nothing to rescale
           const float f = x == -INFINITY ? 1.0f : ex2_approx(m[n][e] - x);
           m[n][e] = x;

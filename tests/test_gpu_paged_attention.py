@@ -7,7 +7,8 @@ A = scale sum |q_d k_d|, and two more roundings of |s| <= A; the base-2
 exponential adds 2^-22; the weights' sum over n slots n u.  So
 d <= (D + 4) u A + 2^-22 + n u for a weight relative to its row's largest, and
 the same bounds ln l.  The weights enter the product with the values as two
-parts of the cache's type, off by eps^2 / 4 <= 2^-18 at most.  An output is a
+parts of the cache's type, off by eps^2 / 4 <= 2^-18 at most (and fp16 ones by
+2^-36 of the row's largest: n u has room for that).  An output is a
 weighted mean of values: off by 2 d max|v| + 2^-17 max|v|, and by half a unit
 of its own type, 2^-8 (bf16) or 2^-11 (fp16) of its value (fp16: 2^-25 near
 zero)."""
@@ -169,6 +170,40 @@ def test_sharp_scores_and_growing_maxima():
     check(q, kv, table, lens, scale=2.0)
     kv[0, table[0, 40], 3, 0] = (base * 2).to(q.dtype)
     check(q, kv, table, lens, scale=1.0, weights=True)
+
+
+@pytest.mark.parametrize("dtype,whole", [(torch.float16, True), (torch.float16, False), (torch.bfloat16, True)])
+def test_many_weights_far_below_the_largest(dtype, whole):
+    """One slot with weight 1 and value 0, all others with weight 2^-25.5 and
+    value 1, in a sequence that one unit goes through (1300 of them, on the same
+    pages) or that is cut: out = n w / (1 + n w).  Half the smallest fp16 number
+    is 2^-25, so weights held in fp16 against the largest would all be lost.
+    Tolerance: each weight of fp16 is off by 2^-36 of the largest (its two
+    parts reach down to 2^-24 / 2^11), n of them, and by d of itself; bf16 has
+    no such floor."""
+    n, D = 20001, 64
+    B = 1300 if whole else 1
+    k = torch.full((n, D), -2.208984375)  # q.k / 8 = -17.671875
+    k[0] = 0
+    v = torch.ones(n, D)
+    v[0] = 0
+    pages = -(-n // 16)
+    kv = torch.zeros(2, pages * 16, D)
+    kv[0, :n], kv[1, :n] = k, v
+    kv = kv.to(dtype).view(2, pages, 16, 1, D)
+    q = torch.ones(B, 1, D, dtype=dtype)
+    table = torch.arange(pages, dtype=torch.int32).repeat(B, 1)
+    out, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table.to(DEV),
+                                      torch.full((B,), n, dtype=torch.int32, device=DEV), return_lse=True)
+    assert not st.any()
+    s = float(kv[0, 1, 0, 0, 0].double()) * D / 8
+    w = (n - 1) * np.exp(s)
+    ref = w / (1 + w)
+    d = (D + 4) * U * abs(s) + 2.0 ** -22 + n * U
+    half, floor = (2.0 ** -11, n * 2.0 ** -36 + 2.0 ** -25) if dtype == torch.float16 else (2.0 ** -8, 0.0)
+    err = (out.double().cpu() - ref).abs().max()
+    assert err <= (half + 2 * d + 2.0 ** -17) * ref + floor, (float(err), ref)
+    assert (lse.double().cpu() - np.log1p(w)).abs().max() <= d + 4 * U
 
 
 def test_infinities_and_nan_in_the_data():
