@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kAhead = 4;  // loads of a thread in flight
+constexpr int kGather = 256;  // slots of a warp that are listed together, 8 of a lane
 constexpr unsigned kMaxCluster = 8;
 constexpr int kLocal = 8192;
 constexpr int kMaxRowBytes = 2048;
@@ -92,10 +93,11 @@ template <typename V, int T> struct Layout {
   static constexpr int kPer = T / 4;  // rows of a stage, at most
   static constexpr int kOnePerSm = 208 * 1024;
   static int bytes(int cached) {
-    const int select = kKeysAt + cached * 4;
+    const int select = kKeysAt + (cached + kGather) * 4;  // (the last lanes read past the keys)
     return select > kRing ? select : kRing;
   }
-  static_assert(kRing <= kOnePerSm && kKeysAt + kMostKeys * 4 <= kOnePerSm, "one CTA to an SM");
+  static_assert(T / 32 * kGather * 4 <= kKeysAt, "the histograms hold what the warps gather");
+  static_assert(kRing <= kOnePerSm && kKeysAt + (kMostKeys + kGather) * 4 <= kOnePerSm, "one CTA to an SM");
   static_assert(2 * kMaxRowBytes <= kStageWords * (int)sizeof(V), "a stage holds a row's K and V");
 };
 
@@ -255,38 +257,29 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   }
 
   // ------------------------------------------------------------ ranks
-  // Slots above the limit all stay, those at it while `need` lasts.  A thread
-  // takes a run of slots, an odd number, so that the lanes meet in no bank.
+  // Slots above the limit all stay, those at it while `need` lasts.  A warp
+  // takes a run of slots, 32 side by side.
   __syncthreads();
   auto key_at = [&](int i) { return cached ? s_keys[i - lo] : order_key(w[i]); };
-  const int run = ((hi - lo + T - 1) / T) | 1;
-  const int r0 = min(lo + (int)threadIdx.x * run, hi), r1 = none ? r0 : min(r0 + run, hi);
-  uint32_t b_above = 0, b_at = 0;  // in this thread's run, then before it
+  const int run = ((hi - lo + W - 1) / W + 31) & ~31;
+  const int r0 = min(lo + warp * run, hi), r1 = none ? r0 : min(r0 + run, hi);
+  uint32_t b_above = 0, b_at = 0;  // in this warp's run, then before its next slots
 #pragma unroll 4
-  for (int i = r0; i < r1; ++i) {
+  for (int i = r0 + lane; i < r1; i += 32) {
     const uint32_t key = key_at(i);
     b_above += key > limit;
     b_at += key == limit;
   }
-  uint32_t i_above = b_above, i_at = b_at;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(FULL, i_above, o), y = __shfl_up_sync(FULL, i_at, o);
-    if (lane >= o) {
-      i_above += x;
-      i_at += y;
-    }
-  }
-  b_above = i_above - b_above;
-  b_at = i_at - b_at;
-  if (lane == 31) {
-    s_scan[warp][0] = i_above;
-    s_scan[warp][1] = i_at;
+  b_above = __reduce_add_sync(FULL, b_above);
+  b_at = __reduce_add_sync(FULL, b_at);
+  if (lane == 0) {
+    s_scan[warp][0] = b_above;
+    s_scan[warp][1] = b_at;
   }
   __syncthreads();
   const uint32_t of_warp[2] = {lane < W ? s_scan[lane < W ? lane : 0][0] : 0, lane < W ? s_scan[lane < W ? lane : 0][1] : 0};
-  b_above += __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
-  b_at += __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
+  b_above = __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
+  b_at = __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
   const uint32_t t_above = __reduce_add_sync(FULL, of_warp[0]), t_at = __reduce_add_sync(FULL, of_warp[1]);
   if (P > 1) {
     if (threadIdx.x == 0) {
@@ -303,61 +296,122 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     b_at += __reduce_add_sync(FULL, y);
   }
   // Positions of the list go round the cluster's CTAs, `each` at a time: a
-  // stage of the ring, K and V of whole rows.  Where all select, each writes
-  // its own.
+  // stage of the ring, K and V of whole rows.  Where all select the same, each
+  // lists its own; where each selects a part, what it finds.
   const int words = a.row_bytes / (int)sizeof(V);
   const int each = min(Lay::kPer, Lay::kStageWords / (2 * words));
   const int each_shift = (each & (each - 1)) ? -1 : __ffs(each) - 1;
   auto turn_of = [&](int k) { return each_shift >= 0 ? k >> each_shift : k / each; };
-  auto mine_at_all = [&](int k) { return P == C || turn_of(k) % C == rank; };
-#pragma unroll 4
-  for (int i = r0; i < r1; ++i) {
-    const uint32_t key = key_at(i);
-    if (key > limit || (key == limit && b_at < need)) {
-      const int pos = a.sinks + (int)(b_above + min(b_at, need));
-      if (mine_at_all(pos)) kept[pos] = i;
-    }
-    b_above += key > limit;
-    b_at += key == limit;
-  }
-  if (P > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  // weights and rows of this CTA's positions, kAhead of a thread at a time;
-  // its j-th position is the list's (j / each C + rank) each + j mod each
   float *stage = a.w_stage + (size_t)item * m;
   long long *src = a.w_src + (size_t)item * m;
   int first = 0x7fffffff;
+  // entries k of the list, two at a time, are slots i (nothing below 0)
+  auto list = [&](const int (&k)[2], const int (&i)[2]) {
+    int id[2];
+    float x[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (k[j] >= 0) {
+        id[j] = table[a.page_shift >= 0 ? i[j] >> a.page_shift : i[j] / a.page];
+        x[j] = w[i[j]];
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (k[j] >= 0) {
+        const int in_page = a.page_shift >= 0 ? i[j] & (a.page - 1) : i[j] % a.page;
+        kept[k[j]] = i[j];
+        stage[k[j]] = x[j];
+        src[k[j]] = id[j] * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
+        if (i[j] != k[j]) first = min(first, k[j]);
+      }
+  };
+  // A warp gathers what stays of kGather slots in the histograms' place (their
+  // positions follow one another) and lists it with all lanes.
+  int *found = (int *)s_hist + warp * kGather;
+  for (int i0 = r0; i0 < r1; i0 += kGather) {
+    const int k0 = a.sinks + (int)(b_above + min(b_at, need));
+    // 8 neighbouring slots of a lane, by two wide loads: counted, scanned over
+    // the warp, gathered (a ballot and its population counts for every 32 slots
+    // took three times as long)
+    const uint32_t *from = s_keys + (i0 - lo);
+    if (!cached) {
+#pragma unroll
+      for (int j = 0; j < kGather; j += 32) {
+        const int i = i0 + j + lane;
+        found[j + lane] = i < r1 ? (int)order_key(w[i]) : 0;
+      }
+      __syncwarp();
+      from = (const uint32_t *)found;
+    }
+    const uint4 x0 = ((const uint4 *)from)[2 * lane], x1 = ((const uint4 *)from)[2 * lane + 1];
+    uint32_t key[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    const int i_mine = i0 + 8 * lane, behind = i0 + kGather - r1;  // slots of the next run, or none
+    if (behind > 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) key[j] = i_mine + j < r1 ? key[j] : 0;
+    }
+    uint32_t c = 0;  // above the limit, and 2^16 times those at it
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (key[j] > limit) c += 1;
+      if (key[j] == limit) c += 0x10000;
+    }
+    uint32_t incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const uint32_t total = __shfl_sync(FULL, incl, 31), at0 = min(b_at, need);
+    __syncwarp();  // the keys may lie where the slots go
+    if (total >> 16) {
+      uint32_t at = b_at + ((incl - c) >> 16);
+      int *to = found + ((incl - c) & 0xffff) + min(at, need) - at0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool level = key[j] == limit;
+        if (key[j] > limit || (level && at < need)) *to++ = i_mine + j;
+        at += level;
+      }
+    } else {
+      int *to = found + (incl - c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (key[j] > limit) *to++ = i_mine + j;
+    }
+    b_above += total & 0xffff;
+    b_at += total >> 16;
+    if (limit == 0 && behind > 0) b_at -= behind;  // they came last
+    const int n_found = (int)((total & 0xffff) + min(b_at, need) - at0);
+    __syncwarp();
+    for (int e = lane; e < n_found; e += 64) {
+      int k[2], i[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        k[j] = k0 + e + 32 * j;
+        if (e + 32 * j >= n_found || (P < C && turn_of(k[j]) % C != rank)) k[j] = -1;
+        i[j] = k[j] >= 0 ? found[e + 32 * j] : 0;
+      }
+      list(k, i);
+    }
+    __syncwarp();
+  }
+  const int ends = a.sinks + a.recent;
+  for (int e = me; e < ends; e += 2 * all) {
+    int k[2], i[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int e_j = e + j * all;
+      k[j] = e_j >= ends ? -1 : e_j < a.sinks ? e_j : m - ends + e_j;
+      i[j] = e_j < a.sinks ? k[j] : n - m + k[j];
+    }
+    list(k, i);
+  }
+  // this CTA's j-th position is the list's (j / each C + rank) each + j mod each
   auto position = [&](int j) {
     const int turn = turn_of(j);
     return j + (turn * (C - 1) + rank) * each;
   };
-  for (int j0 = threadIdx.x; position(j0) < m; j0 += T * kAhead) {
-    int i[kAhead], id[kAhead];
-    float x[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = position(j0 + j * T);
-      i[j] = k >= m ? 0 : k < a.sinks ? k : k >= m - a.recent ? n - m + k : kept[k];
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      id[j] = table[a.page_shift >= 0 ? i[j] >> a.page_shift : i[j] / a.page];
-      x[j] = w[i[j]];
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = position(j0 + j * T);
-      if (k < m) {
-        const int in_page = a.page_shift >= 0 ? i[j] & (a.page - 1) : i[j] % a.page;
-        stage[k] = x[j];
-        src[k] = id[j] * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
-        if (k < a.sinks || k >= m - a.recent) kept[k] = i[j];
-        if (i[j] != k) first = min(first, k);
-      }
-    }
-  }
   first = __reduce_min_sync(FULL, first);
   if (lane == 0) atomicMin(&s_first, first);
   // No weight is read again, and the ring takes the keys' place.
