@@ -93,7 +93,7 @@ template <typename V, int T> struct Layout {
   static constexpr int kPer = T / 4;  // rows of a stage, at most
   static constexpr int kOnePerSm = 208 * 1024;
   static int bytes(int cached) {
-    const int select = kKeysAt + (cached + kGather) * 4;  // (the last lanes read past the keys)
+    const int select = kKeysAt + (cached + kGather) * 4;  // (the last lanes go past the keys)
     return select > kRing ? select : kRing;
   }
   static_assert(T / 32 * kGather * 4 <= kKeysAt, "the histograms hold what the warps gather");
@@ -175,22 +175,32 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
       if (round == 2)  // read in round 0, which every CTA has left
         for (int i = threadIdx.x; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
-      auto count = [&](int i, uint32_t key) {
+      auto count = [&](bool in, uint32_t key) {
         // (equal digits of a warp cost no more than different ones)
-        if (i < hi && (key & mask) == limit) atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
+        if (in && (key & mask) == limit) atomicAdd(&hist[key >> shift & (bins - 1)], 1u);
       };
-      if (cached) {  // a thread's keys stay its own until the ranks
+      if (cached) {
         if (round == 0) {
           const uint32_t at = (uint32_t)__cvta_generic_to_shared(s_keys) - 4 * (uint32_t)lo;
           for (int i = lo + threadIdx.x; i < hi; i += T)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4 * (uint32_t)i), "l"(w + i) : "memory");
           asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncthreads();
         }
-#pragma unroll 4
-        for (int i = lo + threadIdx.x; i < hi; i += T) {
-          uint32_t key = s_keys[i - lo];
-          if (round == 0) s_keys[i - lo] = key = order_key(__uint_as_float(key));
-          count(i, key);
+        // four neighbouring keys of a thread, its own from here to the ranks
+        for (int i = lo + 4 * (int)threadIdx.x; i < hi; i += 4 * T) {
+          uint4 *at = (uint4 *)(s_keys + (i - lo)), x = *at;
+          if (round == 0) {
+            x.x = order_key(__uint_as_float(x.x));
+            x.y = order_key(__uint_as_float(x.y));
+            x.z = order_key(__uint_as_float(x.z));
+            x.w = order_key(__uint_as_float(x.w));
+            *at = x;
+          }
+          count(true, x.x);
+          count(i + 1 < hi, x.y);
+          count(i + 2 < hi, x.z);
+          count(i + 3 < hi, x.w);
         }
       } else {  // too many to keep: read again each round
         constexpr int kMany = 16;  // loads of a thread in flight
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
 #pragma unroll
           for (int j = 0; j < kMany; ++j) x[j] = i0 + j * T < hi ? w[i0 + j * T] : 0.0f;
 #pragma unroll
-          for (int j = 0; j < kMany; ++j) count(i0 + j * T, order_key(x[j]));
+          for (int j = 0; j < kMany; ++j) count(i0 + j * T < hi, order_key(x[j]));
         }
       }
       if (P > 1)
@@ -260,15 +270,25 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   // Slots above the limit all stay, those at it while `need` lasts.  A warp
   // takes a run of slots, 32 side by side.
   __syncthreads();
-  auto key_at = [&](int i) { return cached ? s_keys[i - lo] : order_key(w[i]); };
   const int run = ((hi - lo + W - 1) / W + 31) & ~31;
   const int r0 = min(lo + warp * run, hi), r1 = none ? r0 : min(r0 + run, hi);
   uint32_t b_above = 0, b_at = 0;  // in this warp's run, then before its next slots
+  auto tally = [&](bool in, uint32_t key) {
+    b_above += in && key > limit;
+    b_at += in && key == limit;
+  };
+  if (cached) {
+#pragma unroll 2
+    for (int i = r0 + 4 * lane; i < r1; i += 128) {
+      const uint4 x = *(const uint4 *)(s_keys + (i - lo));
+      tally(true, x.x);
+      tally(i + 1 < r1, x.y);
+      tally(i + 2 < r1, x.z);
+      tally(i + 3 < r1, x.w);
+    }
+  } else {
 #pragma unroll 4
-  for (int i = r0 + lane; i < r1; i += 32) {
-    const uint32_t key = key_at(i);
-    b_above += key > limit;
-    b_at += key == limit;
+    for (int i = r0 + lane; i < r1; i += 32) tally(true, order_key(w[i]));
   }
   b_above = __reduce_add_sync(FULL, b_above);
   b_at = __reduce_add_sync(FULL, b_at);
