@@ -15,8 +15,8 @@
 //              kLocal slots every CTA of the cluster selects by itself (an
 //              exchange costs 2.5 us a round), beyond that each a part, the
 //              counts added over the cluster's shared memory;
-//   ranks      the kept slots in their order, by a scan: their list, weights
-//              and where their rows lie;
+//   ranks      the kept slots in their order, by a scan over the warps: their
+//              list, weights and where their rows lie;
 //   moves      the rows in place, K and V together.  kept[k] >= k and strictly
 //              increasing, so in increasing k no write reaches a slot whose
 //              read is still to come: a ring of asynchronous copies runs ahead
@@ -24,9 +24,10 @@
 //              reads and its writes.
 // Bound: the rows that move, read and written once: memory.  With many CTAs
 // the selections of some run under the moves of others.  Measured (of the copy
-// rate, 6788 GB/s): 2048 items of about 2100 slots to 1024, 349 us for 2.18 GB
-// (0.92); 16 items of 131001 to 32768, 126 us for 0.56 GB (0.65: 33 us of
-// selection with idle memory, then 92); 8 items of 1101 to 1024, 15 us, of
+// rate, 6788 GB/s): 2048 items of about 2100 slots to 1024, 346 us for 2.18 GB
+// (0.93); 256 of 60000 to 16384, 847 us (0.77: keys that do not fit are read in
+// each round); 16 of 131001 to 32768, 119 us for 0.56 GB (0.69: 29 us of
+// selection and ranks with idle memory, then 86); 8 of 1101 to 1024, 14.5 us, of
 // which 3.5 select, 4 rank and list, 4 move.
 #include <math.h>
 
@@ -36,7 +37,6 @@ namespace sv {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kAhead = 4;  // loads of a thread in flight
 constexpr int kGather = 256;  // slots of a warp that are listed together, 8 of a lane
 constexpr unsigned kMaxCluster = 8;
 constexpr int kLocal = 8192;
@@ -351,8 +351,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   for (int i0 = r0; i0 < r1; i0 += kGather) {
     const int k0 = a.sinks + (int)(b_above + min(b_at, need));
     // 8 neighbouring slots of a lane, by two wide loads: counted, scanned over
-    // the warp, gathered (a ballot and its population counts for every 32 slots
-    // took three times as long)
+    // the warp, gathered (a ballot and population counts for every 32 slots took
+    // twice as long: the integer pipe bounds this)
     const uint32_t *from = s_keys + (i0 - lo);
     if (!cached) {
 #pragma unroll
@@ -427,11 +427,6 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     }
     list(k, i);
   }
-  // this CTA's j-th position is the list's (j / each C + rank) each + j mod each
-  auto position = [&](int j) {
-    const int turn = turn_of(j);
-    return j + (turn * (C - 1) + rank) * each;
-  };
   first = __reduce_min_sync(FULL, first);
   if (lane == 0) atomicMin(&s_first, first);
   // No weight is read again, and the ring takes the keys' place.
@@ -463,14 +458,21 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     off[j] = word < words ? word * (long long)sizeof(V) : (word - words) * (long long)sizeof(V) + a.kv_stride;
     if (row[j] >= each) row[j] = 0x40000000;  // no word
   }
+  // Weights: each stage's with its rows, where a few CTAs have to keep the memory
+  // busy (16 items of 131001 slots: 119 us, all before the first row moves 121);
+  // before the moves where others move meanwhile (2048 items: 344 us, with the
+  // moves 346; 256 of 20000 slots: 389 and 394).
+  constexpr bool kWithMoves = T == 512;
   V *mine = (V *)smem + threadIdx.x;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
   long long next_from = 0;
   int next_id = 0;
+  float next_w = 0.0f;
   auto fetch = [&](int s) {  // what the look-up of stage s needs from memory
     const int k = start(s) + (int)threadIdx.x;
     if ((int)threadIdx.x < each && k < m) {
       next_from = src[k];
+      if (kWithMoves) next_w = stage[k];
       next_id = table[a.page_shift >= 0 ? k >> a.page_shift : k / a.page];
     }
   };
@@ -478,6 +480,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     if ((int)threadIdx.x >= each) return;
     const int k = start(s) + (int)threadIdx.x;
     const int in_page = a.page_shift >= 0 ? k & (a.page - 1) : k % a.page;
+    if (kWithMoves && k < m) out_w[k] = next_w;
     s_from[at][threadIdx.x] = next_from;
     s_to[at][threadIdx.x] = next_id * (long long)a.page_stride + in_page * (long long)a.tok_bytes;
   };
@@ -493,38 +496,49 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
   {  // the first look-ups side by side
     long long from[kStages];
     int id[kStages];
+    float weight[kStages];
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
       fetch(s0 + s);
       from[s] = next_from;
       id[s] = next_id;
+      weight[s] = next_w;
     }
     fetch(s0 + kStages);
     const long long keep_from = next_from;
     const int keep_id = next_id;
+    const float keep_w = next_w;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
       next_from = from[s];
       next_id = id[s];
+      next_w = weight[s];
       look_up(s0 + s, s);
     }
     next_from = keep_from;
     next_id = keep_id;
+    next_w = keep_w;
   }
   __syncthreads();
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(s0 + s, s, s);
-  // the weights, while the first rows are on their way
-  for (int j0 = threadIdx.x; position(j0) < m; j0 += T * kAhead) {
-    float x[kAhead];
+  // (the first stages' weights stay where they are)
+  const int before_moves = kWithMoves ? a.out_w == a.w ? 0 : (int)min((long long)s0 * each * C, (long long)m) : m;
+  for (int k = me; k < before_moves; k += 4 * all) {
+    float x[4];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) x[j] = position(j0 + j * T) < m ? stage[position(j0 + j * T)] : 0.0f;
+    for (int j = 0; j < 4; ++j) x[j] = k + j * all < before_moves ? stage[k + j * all] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (position(j0 + j * T) < m) out_w[position(j0 + j * T)] = x[j];
+    for (int j = 0; j < 4; ++j)
+      if (k + j * all < before_moves) out_w[k + j * all] = x[j];
   }
+  int zero = m + me;  // the weights behind the list
+  auto clear = [&](int end) {
 #pragma unroll 4
-  for (int k = m + me; k < n; k += all) out_w[k] = 0.0f;
+    for (; zero < end; zero += all) out_w[zero] = 0.0f;
+  };
+  const long long zeros = (n - m) / max(stages - s0, 1) + all;  // of a stage
+  if (!kWithMoves) clear(n);
   int slot = 0, place = 0;  // of stage s: (s - s0) mod kStages, mod (kStages + 1)
   for (int s = s0; s < stages; ++s) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -546,10 +560,12 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
       if (row[j] < left) *(V *)(base + s_to[place][row[j]] + off[j]) = v[j];
     look_up(s + kStages, before);  // in the place of stage s - 1
     fetch(s + kStages + 1);
+    if (kWithMoves) clear((int)min((long long)n, m + (s - s0 + 1) * zeros));
     slot = slot + 1 == kStages ? 0 : slot + 1;
     place = place == kStages ? 0 : place + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  clear(n);
 }
 
 // How many clusters of C CTAs, one CTA to an SM, the device runs at once: GPCs
