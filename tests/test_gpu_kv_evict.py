@@ -122,6 +122,25 @@ def test_odd_weights():
     check(kv, table, lens, w, 360, 2, 20)          # NaN slots have to stay too
 
 
+@pytest.mark.parametrize("L,lens,Hkv,D,budget", [
+    (1, [1000, 77], 2, 8, 60),                           # a few CTAs choose the same
+    (1, [12345], 2, 64, 9000),                           # and each a part
+    (1, [50003] + [30] * 24, 4, 8, 30000),               # large CTAs, keys read again
+    (2, [701, 260] + [90] * 18, 4, 8, 200),              # small CTAs
+    (2, [9001, 700] + [60] * 18, 4, 8, 8500),            # keys read again
+])
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (3, 11)])
+def test_so_many_nan_that_some_stay(L, lens, Hkv, D, budget, sinks, recent):
+    """NaN ranks below every number, so the lowest limit there is counts the
+    slots of NaN, and nothing that lies behind a part's last slot."""
+    kv, table, n, w = make(L, lens, Hkv, D, 16, seed=budget)
+    g = torch.Generator().manual_seed(5)
+    for share, head in ((0.97, 0), (1.0, -1)):
+        w[:, :, head][torch.rand(w[:, :, head].shape, generator=g) < share] = float("nan")
+    check(kv, table, n, w, budget, sinks, recent)
+
+
+
 def test_bad_lengths_and_pages_move_nothing():
     kv, table, lens, w = make(1, [100] * 6, 2, 64, 16, seed=4)
     cap = table.shape[1] * 16
