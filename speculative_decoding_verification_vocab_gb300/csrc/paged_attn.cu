@@ -21,23 +21,25 @@
 // Work: a unit is a run of 64-key tiles of one (sequence, KV head, up to 16
 // query heads); KV heads of the same tiles are neighbouring CTAs, so that the
 // D-wide slices of one token's row are read at about the same time.  Units are
-// cut from the lengths on the device (a sum and a scan over the batch), so the
-// host never sees them and a captured graph follows them.  Within a unit
-// each of the 4 warps owns 16 keys of every tile: it loads them (cp.async, 16
-// bytes a lane), multiplies, and keeps its own m, l and O; nothing but the last
-// merge crosses warps, and no CTA barrier stands in the loop.
+// cut from the lengths on the device (a scan over the batch): up to a few
+// hundred sequences into as many equal shares of all tiles as are resident, a
+// CTA going from one sequence to the next.  So the host never sees them and a
+// captured graph follows them.  Within a unit each of the 4 warps owns 16 keys of
+// every tile: it loads them (cp.async, 16 bytes a lane), multiplies, and keeps its
+// own m, l and O; nothing but the last merge crosses warps, and no CTA barrier
+// stands in the loop.
 //
 // Groups of 16 keys start at multiples of 16 slots, so with pages of a multiple
 // of 16 slots one table entry serves a group; other page sizes look up every
 // row.  Rows that are not visible are zero-filled in shared memory, not read.
 //
 // Measured (of the copy rate, 6788 GB/s): 128 sequences of 3585-4096 tokens, 64
-// query heads on 8 KV heads of 128, 302 us for 2.02 GB (0.98; pages of 20 or of
+// query heads on 8 KV heads of 128, 303 us for 2.02 GB (0.98; pages of 20 or of
 // 1 slot: 330 us); one of 131001 tokens, 84 us (0.94); windows of 2048 at D =
-// 64, 64 x 16 heads, 89 us (0.89); 24 ragged sequences with weight sums, 56 us
-// (0.62: units of unequal size, the scores' way to memory and back, two
-// launches).  With queries on the long side of the products (heads padded to
-// 16 rows) the same took 342, 109, 106 and 83 us.
+// 64, 64 x 16 heads, 88 us (0.90); 24 ragged sequences with weight sums, 53 us
+// (0.65: the scores' way to memory and back, two launches).  With queries on the
+// long side of the products (heads padded to 16 rows) the same took 342, 109, 106
+// and 83 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -53,9 +55,8 @@ constexpr int kGroup = 16;                // keys of a warp in a tile
 constexpr int kTile = kWarps * kGroup;    // keys of a CTA tile
 constexpr int kRows = 16;                 // query heads of a unit, at most
 // CTAs that are resident at once on 152 SMs (2 per SM at D = 128), and the
-// fewest tiles of a unit: below that its fixed cost shows (24 ragged sequences:
-// 56 us with 8, 59 with 16; one of 200 tokens: 8.4 us of GPU time with 8, 12.4
-// with 2 and a join).
+// fewest tiles of a unit: below that its fixed cost shows (one of 200 tokens: 8.4
+// us of GPU time with 8, 12.4 with 2 and a join).
 template <int D> constexpr int kSlots = D == 64 ? 608 : D == 128 ? 304 : 152;
 constexpr int kMinTiles = 8;
 constexpr int kMaxSlots = 1 << 30;
@@ -80,7 +81,7 @@ struct PagedArgs {
   int page, page_shift, max_pages, num_pages;
   int window, sinks, cap;
   int units;   // aimed at
-  int groups;  // of units, one per KV head group, that the grid has room for
+  int groups;  // the grid's groups of CTAs, one for each head group
   int finding;  // how a CTA finds its unit: one of the below
   float scale_log2;
   int rows;  // query heads of a unit: min(G, 16)
@@ -132,21 +133,30 @@ struct Plan {
   int b, i, n;   // sequence, unit within it, units of it
   int first;     // group index of the sequence's first unit
 };
-// How a CTA finds its unit.  kWhole: no sequence has room for two.  kOne: a
-// single sequence.  kScan: by a scan of the lengths in every CTA.  kMap: from a
-// map that a launch of its own has written (128 sequences of 90-1110 tokens: 62
-// us either way; 256: 110 us with the map, 117 with the scan; 2000: 752 and
-// 1326; 16 of 2000-4000: 46 and 44).
-enum { kWhole, kOne, kScan, kMap };
-constexpr int kMapFrom = 160;
+// How a CTA finds its unit.
+//   kWhole  no sequence has room for two
+//   kOne    a single sequence
+//   kScan   a scan of the lengths in every CTA; sequences cut one by one
+//   kShare  a scan too; an equal share of the batch's tiles, wherever the
+//           sequences end
+//   kMap    a map that a launch of its own has written; one by one
+// Shares leave no CTA with less to do (sequences cut one by one in brackets): 24
+// ragged sequences 51 us (54), 128 of 500-8000 tokens 355 (379), 32 of 500-20000
+// 234 (240), 128 of 3585-4096 301 (310), windows of 2052 at D = 64 91 (95).  They
+// cost a CTA the way to a first load once more where a sequence ends, and every
+// CTA the scan: with more heads than kShareHeads to a resident CTA, or sequences
+// than kShareBatch, the map is as good (1000 of 200-2000: 105 us, shares 109; 2000
+// of 90-1110: 111 and 160), and sequences that are cut into 8 units and more each
+// have equal ones anyway (4 of 700: 19 us, shares 21).
+enum { kWhole, kOne, kScan, kShare, kMap };
+constexpr int kShareHeads = 4, kShareBatch = 512;
 
-// Units aimed at.  Where each (sequence, KV head) is cut into 8 and more, their
-// sizes are nearly equal, and one wave of as many as are resident is best (one
-// of 131001 tokens: 84 us, in two waves 93; two of 20000: 36 and 40).  Fewer
-// units each leave them unequal: twice as many, so that the early ones make
-// room (24 ragged sequences: 56 us, in one wave 61; 8 of 8000: 55 and 56).
-// Rounding up adds half a unit to each (sequence, head); a batch of more of
-// those than units is left whole.
+// Units aimed at where sequences are cut one by one.  Into 8 and more for each
+// (sequence, KV head) they are nearly equal, and one wave of as many as are
+// resident is best (one of 131001 tokens: 84 us, in two waves 93).  Fewer units
+// each leave them unequal: twice as many, so that the early ones make room.
+// Rounding up adds half a unit to each (sequence, head); a batch of more of those
+// than units is left whole.
 int slots_of(int D) { return D == 64 ? kSlots<64> : D == 128 ? kSlots<128> : kSlots<256>; }
 int units_for(int D, int B, int NH) {
   return 8LL * B * NH <= slots_of(D) ? slots_of(D) : 2 * slots_of(D);
@@ -211,18 +221,75 @@ __device__ int cut_batch(const PagedArgs &a, F out) {
   return all;
 }
 
-// The sequence and part that group g is (by_group), or the units of sequence g.
-// Every thread of the CTA calls it; b = -1 when there is no such group.
-template <int THREADS>
-__device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
+// The batch as one row of tiles, sequence after sequence (an empty one counts as
+// a tile): calls out(b, first tile, tiles, tiles in all) for every sequence, each
+// from one thread.  Every thread of the CTA calls it.
+template <int THREADS, typename F>
+__device__ void walk_batch(const PagedArgs &a, F out) {
+  constexpr int W = THREADS / 32;
+  __shared__ long long s_sum[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = (a.B + THREADS - 1) / THREADS;
+  const int b0 = min((int)threadIdx.x * k, a.B), b1 = min(b0 + k, a.B);
+  auto read = [&](int b) { return max(tiles_of(visible(a, __ldcg(a.seq_len + b))), 1); };
+  const int t0 = b0 < b1 ? read(b0) : 0;  // read once where k = 1
+  auto tiles_at = [&](int b) { return b == b0 ? t0 : read(b); };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_at(b);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  long long at = incl - mine, all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) at += s_sum[w];
+    all += s_sum[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int t = tiles_at(b);
+    out(b, at, t, all);
+    at += t;
+  }
+}
+// Group g of G takes the tiles from g all / G to (g + 1) all / G; a part of a
+// sequence in a group is unit (group + sequence): with every part one or the other
+// grows by one.
+__device__ __forceinline__ long long share_groups(const PagedArgs &a, long long all) {
+  return min((long long)a.groups, max(all / kMinTiles, 1LL));
+}
+struct Share {
+  int b;
+  long long first, at, end;  // the sequence's first tile; the group's tiles from `at` to `end`
+};
+template <int THREADS> __device__ Share find_share(const PagedArgs &a, int g) {
+  __shared__ Share s_share;
+  if (threadIdx.x == 0) s_share.b = -1;
+  __syncthreads();
+  walk_batch<THREADS>(a, [&](int b, long long first, int t, long long all) {
+    const long long G = share_groups(a, all), at = g * all / G;
+    if (g < G && first <= at && at < first + t) s_share = Share{b, first, at, (g + 1) * all / G};
+  });
+  __syncthreads();
+  return s_share;
+}
+
+// The sequence and part that group g is (BY_GROUP; not for kShare), or the units
+// of sequence g.  Every thread of the CTA calls it; b = -1: no such group.
+template <int THREADS, bool BY_GROUP>
+__device__ Plan find_plan(const PagedArgs &a, int g) {
   if (a.finding == kWhole) return Plan{g, 0, 1, g};
   if (a.finding == kOne) {
     const int t = tiles_of(visible(a, __ldcg(a.seq_len)));
     const int n = units_of(t, unit_tiles(a, t));
-    return Plan{by_group && g >= n ? -1 : 0, by_group ? g : 0, n, 0};
+    return Plan{BY_GROUP && g >= n ? -1 : 0, BY_GROUP ? g : 0, n, 0};
   }
   if (a.finding == kMap) {
-    if (by_group) {
+    if (BY_GROUP) {
       const int4 e = __ldcg(a.w_map + g);
       return Plan{e.x, e.y, e.z, g - e.y};
     }
@@ -230,10 +297,20 @@ __device__ Plan find_plan(const PagedArgs &a, int g, bool by_group) {
     return Plan{g, 0, e.y, e.x};
   }
   __shared__ Plan s_plan;
-  if (threadIdx.x == 0) s_plan.b = -1;
-  __syncthreads();
-  cut_batch<THREADS>(a, [&](int b, int first, int n) {
-    if (by_group ? g >= first && g < first + n : b == g) s_plan = Plan{b, by_group ? g - first : 0, n, first};
+  if (BY_GROUP || a.finding == kScan) {
+    if (threadIdx.x == 0) s_plan.b = -1;
+    __syncthreads();
+    cut_batch<THREADS>(a, [&](int b, int first, int n) {
+      if (BY_GROUP ? g >= first && g < first + n : b == g) s_plan = Plan{b, BY_GROUP ? g - first : 0, n, first};
+    });
+    __syncthreads();
+    return s_plan;
+  }
+  walk_batch<THREADS>(a, [&](int b, long long first, int t, long long all) {
+    if (b != g) return;
+    const long long G = share_groups(a, all);
+    const int g0 = (int)(((first + 1) * G - 1) / all), g1 = (int)(((first + t) * G - 1) / all);
+    s_plan = Plan{b, 0, g1 - g0 + 1, g0 + b};
   });
   __syncthreads();
   return s_plan;
@@ -329,8 +406,11 @@ template <int D, int NT> struct Shape {
   static_assert((size_t)kWarps * kHeads * kMergeRow * 4 <= (size_t)kWarps * kWarpBytes, "merge");
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
+// SHARING: kShare; a kernel of its own, since its loop over the parts costs the
+// other findings registers and a longer way to their first load (4 of 700: 19 us,
+// in one kernel 21).
+template <typename T, int D, int NT, bool SHARING>
+__global__ void __launch_bounds__(kThreads, SHARING && D == 64 ? 4 : 0) paged_attn_kernel(PagedArgs a) {
   grid_dep_sync();
   using Sh = Shape<D, NT>;
   // the operands' rows are addressed by exclusive or: they start at 512 bytes
@@ -342,354 +422,375 @@ __global__ void __launch_bounds__(kThreads) paged_attn_kernel(PagedArgs a) {
   const int g4 = lane >> 2, t4 = lane & 3;
   const int unit = blockIdx.x;
   const int h = unit % a.NH;
-  const Plan plan = find_plan<kThreads>(a, unit / a.NH, true);
-  if (plan.b < 0) return;
-  const int b = plan.b;
   const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
   const int rows = min(kRows, a.G - (h % a.gt) * kRows);
-  const Visible vis = visible(a, a.finding == kMap ? __ldcg(&a.w_map[unit / a.NH].w) : __ldcg(a.seq_len + b));
-  const int tiles = tiles_of(vis);
-  const int t0 = (int)((long long)tiles * plan.i / plan.n);
-  const int t1 = (int)((long long)tiles * (plan.i + 1) / plan.n);
+  Share share;
+  Plan plan;
+  if constexpr (SHARING)
+    share = find_share<kThreads>(a, unit / a.NH);
+  else
+    plan = find_plan<kThreads, true>(a, unit / a.NH);
+  if ((SHARING ? share.b : plan.b) < 0) return;
 
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ uint32_t s_bad[kWarps];
   __shared__ long long s_row[kWarps][32];  // offsets of two groups' rows (pages not of 16)
 
-  // query heads as the right-hand operand: head g4 (+ 8), dimensions 2 t4 ...
-  const T *q = (const T *)a.q + ((size_t)b * a.Hq + head0) * D;
-  uint32_t qf[Sh::kQRegs ? D / 16 : 1][NT][2];
-  const uint32_t sm_q = sm0 + kWarps * Sh::kWarpBytes;
-  if (Sh::kQRegs) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t *r = (const uint32_t *)(q + (size_t)(g4 + 8 * n) * D + 2 * t4);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][n][0] = g4 + 8 * n < rows ? r[8 * k] : 0;
-        qf[k][n][1] = g4 + 8 * n < rows ? r[8 * k + 4] : 0;
-      }
+  // one part of a sequence after the other (one only, unless CTAs share the batch)
+  for (;;) {
+    const int b = SHARING ? share.b : plan.b;
+    const Visible vis = visible(a, a.finding == kMap ? __ldcg(&a.w_map[unit / a.NH].w) : __ldcg(a.seq_len + b));
+    const int tiles = tiles_of(vis);
+    int t0, t1;
+    if constexpr (SHARING) {
+      t0 = (int)(share.at - share.first);
+      t1 = (int)min(share.end - share.first, (long long)tiles);
+    } else {
+      t0 = (int)((long long)tiles * plan.i / plan.n);
+      t1 = (int)((long long)tiles * (plan.i + 1) / plan.n);
     }
-  } else {
-    for (int i = threadIdx.x; i < Sh::kHeads * (D / 8); i += kThreads) {
-      const int r = i / (D / 8), c = i % (D / 8);
-      const uint4 v = r < rows ? *(const uint4 *)(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
-      *(uint4 *)(smem + kWarps * Sh::kWarpBytes + r * Sh::kRowBytes + ((c ^ (r & 7)) * 16)) = v;
-    }
-    __syncthreads();
-  }
+    const bool whole = SHARING ? t0 == 0 && t1 == tiles : plan.n == 1;
+    const size_t part = SHARING ? (size_t)(unit / a.NH + b) * a.NH + h : unit;
 
-  // ------------------------------------------------------------ the loads
-  // This warp's group i is the 16 positions from (t0 + i) kTile + 16 warp.
-  const int groups = t1 - t0;
-  auto pos_of = [&](int i) { return (t0 + i) * kTile + warp * kGroup; };
-  const uint32_t sm_w = sm0 + warp * Sh::kWarpBytes;
-  const int32_t *table = a.table + (size_t)b * a.max_pages;
-  const T *kv = (const T *)a.kv + (int64_t)hkv * D;
-  const int64_t row_elems = (int64_t)a.Hkv * D;
-  constexpr int CPR = D / 8;     // 16-byte pieces of a row
-  constexpr int RPI = 32 / CPR;  // rows of one round of the warp's copies
-  const int lr = lane / CPR, lc = lane % CPR;
-  const bool by_row = a.page % kGroup != 0;
-  bool bad = false;
-  // Lanes look rows up in parallel: lane l the first row of group i0 + l
-  // (`ids` of 32 groups), or by_row the row l % 16 of group i0 + l / 16 (of 2).
-  // The table entries are loaded a batch ahead; an offset is -1 where nothing
-  // is visible, and odd where not all of the group's 16 slots are.
-  const int batch = by_row ? 2 : 32;
-  int next_id = 0;
-  auto position = [&](int i0) { return by_row ? pos_of(i0 + (lane >> 4)) + (lane & 15) : pos_of(i0 + lane); };
-  auto wanted = [&](int i0) {  // whether the lane's row or group has a slot to load
-    const int i = i0 + (by_row ? lane >> 4 : lane), p = position(i0);
-    return i < groups && (by_row ? seen(vis, p) : p < vis.n);
-  };
-  auto fetch_ids = [&](int i0) {
-    if (wanted(i0)) {
-      const int slot = slot_of(vis, position(i0));
-      next_id = table[a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page];
+    // query heads as the right-hand operand: head g4 (+ 8), dimensions 2 t4 ...
+    const T *q = (const T *)a.q + ((size_t)b * a.Hq + head0) * D;
+    uint32_t qf[Sh::kQRegs ? D / 16 : 1][NT][2];
+    const uint32_t sm_q = sm0 + kWarps * Sh::kWarpBytes;
+    if (Sh::kQRegs) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t *r = (const uint32_t *)(q + (size_t)(g4 + 8 * n) * D + 2 * t4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][n][0] = g4 + 8 * n < rows ? r[8 * k] : 0;
+          qf[k][n][1] = g4 + 8 * n < rows ? r[8 * k + 4] : 0;
+        }
+      }
+    } else {
+      for (int i = threadIdx.x; i < Sh::kHeads * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        const uint4 v = r < rows ? *(const uint4 *)(q + (size_t)r * D + c * 8) : make_uint4(0, 0, 0, 0);
+        *(uint4 *)(smem + kWarps * Sh::kWarpBytes + r * Sh::kRowBytes + ((c ^ (r & 7)) * 16)) = v;
+      }
+      __syncthreads();
     }
-  };
-  auto offsets = [&](int i0) -> long long {
-    if (!wanted(i0)) return -1;
-    if ((unsigned)next_id >= (unsigned)a.num_pages) {
-      bad = true;
-      return -1;
-    }
-    const int p = position(i0), slot = slot_of(vis, p);
-    const int in_page = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
-    const long long off = next_id * (long long)a.page_stride + in_page * (long long)row_elems;
-    return by_row || (seen(vis, p) && seen(vis, p + kGroup - 1)) ? off : off | 1;
-  };
-  long long offs = -1;
-  auto load_group = [&](int i, int stage) {
-    if (i >= groups || pos_of(i) >= vis.n) return;  // nothing, and nothing after it
-    if ((i & (batch - 1)) == 0) {
-      offs = offsets(i);
-      fetch_ids(i + batch);
+
+    // ------------------------------------------------------------ the loads
+    // This warp's group i is the 16 positions from (t0 + i) kTile + 16 warp.
+    const int groups = t1 - t0;
+    auto pos_of = [&](int i) { return (t0 + i) * kTile + warp * kGroup; };
+    const uint32_t sm_w = sm0 + warp * Sh::kWarpBytes;
+    const int32_t *table = a.table + (size_t)b * a.max_pages;
+    const T *kv = (const T *)a.kv + (int64_t)hkv * D;
+    const int64_t row_elems = (int64_t)a.Hkv * D;
+    constexpr int CPR = D / 8;     // 16-byte pieces of a row
+    constexpr int RPI = 32 / CPR;  // rows of one round of the warp's copies
+    const int lr = lane / CPR, lc = lane % CPR;
+    const bool by_row = a.page % kGroup != 0;
+    bool bad = false;
+    // Lanes look rows up in parallel: lane l the first row of group i0 + l
+    // (`ids` of 32 groups), or by_row the row l % 16 of group i0 + l / 16 (of 2).
+    // The table entries are loaded a batch ahead; an offset is -1 where nothing
+    // is visible, and odd where not all of the group's 16 slots are.
+    const int batch = by_row ? 2 : 32;
+    int next_id = 0;
+    auto position = [&](int i0) { return by_row ? pos_of(i0 + (lane >> 4)) + (lane & 15) : pos_of(i0 + lane); };
+    auto wanted = [&](int i0) {  // whether the lane's row or group has a slot to load
+      const int i = i0 + (by_row ? lane >> 4 : lane), p = position(i0);
+      return i < groups && (by_row ? seen(vis, p) : p < vis.n);
+    };
+    auto fetch_ids = [&](int i0) {
+      if (wanted(i0)) {
+        const int slot = slot_of(vis, position(i0));
+        next_id = table[a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page];
+      }
+    };
+    auto offsets = [&](int i0) -> long long {
+      if (!wanted(i0)) return -1;
+      if ((unsigned)next_id >= (unsigned)a.num_pages) {
+        bad = true;
+        return -1;
+      }
+      const int p = position(i0), slot = slot_of(vis, p);
+      const int in_page = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
+      const long long off = next_id * (long long)a.page_stride + in_page * (long long)row_elems;
+      return by_row || (seen(vis, p) && seen(vis, p + kGroup - 1)) ? off : off | 1;
+    };
+    long long offs = -1;
+    auto load_group = [&](int i, int stage) {
+      if (i >= groups || pos_of(i) >= vis.n) return;  // nothing, and nothing after it
+      if ((i & (batch - 1)) == 0) {
+        offs = offsets(i);
+        fetch_ids(i + batch);
+        if (by_row) {
+          __syncwarp();
+          s_row[warp][lane] = offs;
+          __syncwarp();
+        }
+      }
+      const uint32_t dst = (sm_w + stage * 2 * Sh::kPart) + lr * Sh::kRowBytes + ((lc ^ lr) * 16);
       if (by_row) {
-        __syncwarp();
-        s_row[warp][lane] = offs;
-        __syncwarp();
-      }
-    }
-    const uint32_t dst = (sm_w + stage * 2 * Sh::kPart) + lr * Sh::kRowBytes + ((lc ^ lr) * 16);
-    if (by_row) {
 #pragma unroll
-      for (int j = 0; j < kGroup / RPI; ++j) {
-        const long long off = s_row[warp][(i & 1) * kGroup + j * RPI + lr];
-        const uint32_t n = off >= 0 ? 16u : 0u;
-        const T *src = kv + (off >= 0 ? off : 0) + lc * 8;
-        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
-        cp16(d, src, n);
-        cp16(d + Sh::kPart, src + a.kv_stride, n);
+        for (int j = 0; j < kGroup / RPI; ++j) {
+          const long long off = s_row[warp][(i & 1) * kGroup + j * RPI + lr];
+          const uint32_t n = off >= 0 ? 16u : 0u;
+          const T *src = kv + (off >= 0 ? off : 0) + lc * 8;
+          const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+          cp16(d, src, n);
+          cp16(d + Sh::kPart, src + a.kv_stride, n);
+        }
+        return;
       }
-      return;
-    }
-    const long long off = __shfl_sync(FULL, offs, i & 31);
-    if (!(off & 1)) {  // all 16 rows
-      const T *k = kv + off + lr * row_elems + lc * 8, *v = k + a.kv_stride;
+      const long long off = __shfl_sync(FULL, offs, i & 31);
+      if (!(off & 1)) {  // all 16 rows
+        const T *k = kv + off + lr * row_elems + lc * 8, *v = k + a.kv_stride;
 #pragma unroll
-      for (int j = 0; j < kGroup / RPI; ++j) {
-        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
-        cp16(d, k);
-        cp16(d + Sh::kPart, v);
-        k += RPI * row_elems;
-        v += RPI * row_elems;
-      }
-    } else {  // some, or none
-      const int p = pos_of(i);
+        for (int j = 0; j < kGroup / RPI; ++j) {
+          const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+          cp16(d, k);
+          cp16(d + Sh::kPart, v);
+          k += RPI * row_elems;
+          v += RPI * row_elems;
+        }
+      } else {  // some, or none
+        const int p = pos_of(i);
 #pragma unroll 1
-      for (int j = 0; j < kGroup / RPI; ++j) {
-        const int r = j * RPI + lr;
-        const uint32_t n = off >= 0 && seen(vis, p + r) ? 16u : 0u;
-        const T *src = kv + (n ? (off ^ 1) + r * row_elems : 0) + lc * 8;
-        const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
-        cp16(d, src, n);
-        cp16(d + Sh::kPart, src + a.kv_stride, n);
+        for (int j = 0; j < kGroup / RPI; ++j) {
+          const int r = j * RPI + lr;
+          const uint32_t n = off >= 0 && seen(vis, p + r) ? 16u : 0u;
+          const T *src = kv + (n ? (off ^ 1) + r * row_elems : 0) + lc * 8;
+          const uint32_t d = (dst ^ ((j * RPI & 7) * 16)) + j * RPI * Sh::kRowBytes;
+          cp16(d, src, n);
+          cp16(d + Sh::kPart, src + a.kv_stride, n);
+        }
       }
-    }
-  };
+    };
 
-  float o[D / 16][NT][4];
+    float o[D / 16][NT][4];
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j)
+    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
-  // per head 2 t4 + e (+ 8 n): the reference m (log2 units), l, and the z that
-  // is subtracted (m, or 0 while there is no finite score)
-  float m[NT][2], z[NT][2], l[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      m[n][e] = -INFINITY;
-      z[n][e] = l[n][e] = 0.0f;
-    }
-  const float sc = a.scale_log2;
-  float *scores = a.w_score ? a.w_score + ((size_t)b * a.Hkv + hkv) * a.vis_max * a.G + (h % a.gt) * kRows
-                            : nullptr;
-
-  fetch_ids(0);
-#pragma unroll
-  for (int i = 0; i < Sh::kStages - 1; ++i) {
-    load_group(i, i);
-    cp_commit();
-  }
-  // addresses of this lane's rows of the operands: K's row (key) and V's
-  const int ka = (((lane >> 3) & 1) << 3) + (lane & 7), kh = lane >> 4;
-  const int va = ((lane >> 4) << 3) + (lane & 7), vh = (lane >> 3) & 1;
-  const uint32_t k_lane = sm_w + ka * Sh::kRowBytes + ((kh ^ (ka & 7)) * 16);
-  const uint32_t v_lane = sm_w + Sh::kPart + va * Sh::kRowBytes + ((vh ^ (va & 7)) * 16);
-  int st_load = Sh::kStages - 1, st = 0;
-  uint32_t partial = 0;  // of the 32 groups from i & ~31: those with slots that are not visible
-  for (int i = 0; i < groups; ++i) {
-    cp_wait<Sh::kStages - 2>();
-    __syncwarp();
-    load_group(i + Sh::kStages - 1, st_load);  // into the stage read last round
-    cp_commit();
-    const uint32_t k_at = k_lane + st * 2 * Sh::kPart, v_at = v_lane + st * 2 * Sh::kPart;
-    st = st + 1 == Sh::kStages ? 0 : st + 1;
-    st_load = st_load + 1 == Sh::kStages ? 0 : st_load + 1;
-    if ((i & 31) == 0) {
-      const int p = pos_of(i + lane);
-      partial = __ballot_sync(FULL, !(seen(vis, p) && seen(vis, p + kGroup - 1)));
-    }
-    const int pos0 = pos_of(i);
-    if (pos0 >= vis.n) continue;  // the last tile's groups past the end
-
-    // S^T = K Q^T: 16 keys x 8 NT heads, even and odd steps apart
-    float s[NT][4] = {}, s2[NT][4] = {};
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      uint32_t ak[4];
-      ldsm4(ak, k_at ^ (k * 32));
-      if (Sh::kQRegs) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, qf[k][n][0], qf[k][n][1]);
-      } else {
-        uint32_t bq[4];  // heads 0-7 and 8-15, 16 dimensions
-        const int qr = (lane & 7) + ((lane >> 4) << 3), qh = (lane >> 3) & 1;
-        ldsm4(bq, sm_q + qr * Sh::kRowBytes + (((2 * k + qh) ^ (qr & 7)) * 16));
-#pragma unroll
-        for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, bq[2 * n], bq[2 * n + 1]);
-      }
-    }
+      for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+    // per head 2 t4 + e (+ 8 n): the reference m (log2 units), l, and the z that
+    // is subtracted (m, or 0 while there is no finite score)
+    float m[NT][2], z[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
-    // keys pos0 + g4 and pos0 + g4 + 8 of this lane; whole groups need no test
-    if (partial >> (i & 31) & 1) {
-      const bool in0 = seen(vis, pos0 + g4), in1 = seen(vis, pos0 + g4 + 8);
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = -INFINITY;
+        z[n][e] = l[n][e] = 0.0f;
+      }
+    const float sc = a.scale_log2;
+    float *scores = a.w_score ? a.w_score + ((size_t)b * a.Hkv + hkv) * a.vis_max * a.G + (h % a.gt) * kRows
+                              : nullptr;
+
+    fetch_ids(0);
+#pragma unroll
+    for (int i = 0; i < Sh::kStages - 1; ++i) {
+      load_group(i, i);
+      cp_commit();
+    }
+    // addresses of this lane's rows of the operands: K's row (key) and V's
+    const int ka = (((lane >> 3) & 1) << 3) + (lane & 7), kh = lane >> 4;
+    const int va = ((lane >> 4) << 3) + (lane & 7), vh = (lane >> 3) & 1;
+    const uint32_t k_lane = sm_w + ka * Sh::kRowBytes + ((kh ^ (ka & 7)) * 16);
+    const uint32_t v_lane = sm_w + Sh::kPart + va * Sh::kRowBytes + ((vh ^ (va & 7)) * 16);
+    int st_load = Sh::kStages - 1, st = 0;
+    uint32_t partial = 0;  // of the 32 groups from i & ~31: those with slots that are not visible
+    for (int i = 0; i < groups; ++i) {
+      cp_wait<Sh::kStages - 2>();
+      __syncwarp();
+      load_group(i + Sh::kStages - 1, st_load);  // into the stage read last round
+      cp_commit();
+      const uint32_t k_at = k_lane + st * 2 * Sh::kPart, v_at = v_lane + st * 2 * Sh::kPart;
+      st = st + 1 == Sh::kStages ? 0 : st + 1;
+      st_load = st_load + 1 == Sh::kStages ? 0 : st_load + 1;
+      if ((i & 31) == 0) {
+        const int p = pos_of(i + lane);
+        partial = __ballot_sync(FULL, !(seen(vis, p) && seen(vis, p + kGroup - 1)));
+      }
+      const int pos0 = pos_of(i);
+      if (pos0 >= vis.n) continue;  // the last tile's groups past the end
+
+      // S^T = K Q^T: 16 keys x 8 NT heads, even and odd steps apart
+      float s[NT][4] = {}, s2[NT][4] = {};
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t ak[4];
+        ldsm4(ak, k_at ^ (k * 32));
+        if (Sh::kQRegs) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, qf[k][n][0], qf[k][n][1]);
+        } else {
+          uint32_t bq[4];  // heads 0-7 and 8-15, 16 dimensions
+          const int qr = (lane & 7) + ((lane >> 4) << 3), qh = (lane >> 3) & 1;
+          ldsm4(bq, sm_q + qr * Sh::kRowBytes + (((2 * k + qh) ^ (qr & 7)) * 16));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) Pair<T>::mma(k & 1 ? s2[n] : s[n], ak, bq[2 * n], bq[2 * n + 1]);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[n][e] = in0 ? s[n][e] : -INFINITY;
-          s[n][2 + e] = in1 ? s[n][2 + e] : -INFINITY;
-        }
-    }
-    if (scores) {
+        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+      // keys pos0 + g4 and pos0 + g4 + 8 of this lane; whole groups need no test
+      if (partial >> (i & 31) & 1) {
+        const bool in0 = seen(vis, pos0 + g4), in1 = seen(vis, pos0 + g4 + 8);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[n][e] = in0 ? s[n][e] : -INFINITY;
+            s[n][2 + e] = in1 ? s[n][2 + e] : -INFINITY;
+          }
+      }
+      if (scores) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float *w = scores + (size_t)(pos0 + g4 + 8 * r) * a.G;
+            const int c = 2 * t4 + 8 * n;
+            if (pos0 + g4 + 8 * r < vis.n) {
+              if (c < rows) w[c] = s[n][2 * r];
+              if (c + 1 < rows) w[c + 1] = s[n][2 * r + 1];
+            }
+          }
+      }
+      // a score above the reference by more than the slack moves it
+      bool up = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][2 + e]) * sc > m[n][e] + (kBias<T> + kSlack<T>);
+      if (__any_sync(FULL, up)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[n][e], s[n][2 + e]) * sc;
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, w));
+            x = fmaxf(x - kBias<T>, m[n][e]);
+            // a head without a finite score yet has nothing to rescale
+            const float f = x == -INFINITY ? 1.0f : ex2_approx(m[n][e] - x);
+            m[n][e] = x;
+            z[n][e] = x == -INFINITY ? 0.0f : x;
+            l[n][e] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[j][n][e] *= f;
+              o[j][n][2 + e] *= f;
+            }
+          }
+      }
+      // P^T as the sum of two 16-bit parts: the weights keep twice the type's
+      // bits (one part alone would add a rounding as large as the output's own:
+      // 2.2e-3 from 64 bits where bf16 rounds by 1.7e-3; it costs 1 % of the time)
+      uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float *w = scores + (size_t)(pos0 + g4 + 8 * r) * a.G;
-          const int c = 2 * t4 + 8 * n;
-          if (pos0 + g4 + 8 * r < vis.n) {
-            if (c < rows) w[c] = s[n][2 * r];
-            if (c + 1 < rows) w[c + 1] = s[n][2 * r + 1];
-          }
+          const float x = ex2_approx(fmaf(s[n][2 * r], sc, -z[n][0]));
+          const float y = ex2_approx(fmaf(s[n][2 * r + 1], sc, -z[n][1]));
+          l[n][0] += x;
+          l[n][1] += y;
+          const uint32_t hi = Pair<T>::pack(x, y);
+          const float2 back = Pair<T>::unpack(hi);
+          ph[n][r] = transpose8(hi);
+          pl[n][r] = transpose8(Pair<T>::pack(x - back.x, y - back.y));
         }
-    }
-    // a score above the reference by more than the slack moves it
-    bool up = false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) up |= fmaxf(s[n][e], s[n][2 + e]) * sc > m[n][e] + (kBias<T> + kSlack<T>);
-    if (__any_sync(FULL, up)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(s[n][e], s[n][2 + e]) * sc;
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, w));
-          x = fmaxf(x - kBias<T>, m[n][e]);
-          // a head without a finite score yet has nothing to rescale
-          const float f = x == -INFINITY ? 1.0f : ex2_approx(m[n][e] - x);
-          m[n][e] = x;
-          z[n][e] = x == -INFINITY ? 0.0f : x;
-          l[n][e] *= f;
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[j][n][e] *= f;
-            o[j][n][2 + e] *= f;
-          }
-        }
-    }
-    // P^T as the sum of two 16-bit parts: the weights keep twice the type's
-    // bits (one part alone would add a rounding as large as the output's own:
-    // 2.2e-3 from 64 bits where bf16 rounds by 1.7e-3; it costs 1 % of the time)
-    uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float x = ex2_approx(fmaf(s[n][2 * r], sc, -z[n][0]));
-        const float y = ex2_approx(fmaf(s[n][2 * r + 1], sc, -z[n][1]));
-        l[n][0] += x;
-        l[n][1] += y;
-        const uint32_t hi = Pair<T>::pack(x, y);
-        const float2 back = Pair<T>::unpack(hi);
-        ph[n][r] = transpose8(hi);
-        pl[n][r] = transpose8(Pair<T>::pack(x - back.x, y - back.y));
-      }
-    // O^T += V^T P^T
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      uint32_t av[4];
-      ldsm4t(av, v_at ^ (j * 32));
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        Pair<T>::mma(o[j][n], av, ph[n][0], ph[n][1]);
-        Pair<T>::mma(o[j][n], av, pl[n][0], pl[n][1]);
-      }
-    }
-    __syncwarp();  // every lane is done with this stage before it is filled again
-  }
-  cp_wait<0>();
-
-  // ------------------------------------------------------------ merge the warps
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], w);
-      if (g4 == 0) {
-        s_m[warp][8 * n + 2 * t4 + e] = m[n][e];
-        s_l[warp][8 * n + 2 * t4 + e] = l[n][e];
-      }
-    }
-  bad = __any_sync(FULL, bad);
-  if (lane == 0) s_bad[warp] = bad ? 1 : 0;
-  __syncthreads();  // the ring is free too: O goes there
-  float *mo = (float *)smem + (size_t)warp * Sh::kHeads * Sh::kMergeRow;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = 8 * n + 2 * t4 + e;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][c]);
-      const float f = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - M);
+      // O^T += V^T P^T
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
-        mo[c * Sh::kMergeRow + 16 * j + g4] = o[j][n][e] * f;
-        mo[c * Sh::kMergeRow + 16 * j + 8 + g4] = o[j][n][2 + e] * f;
+        uint32_t av[4];
+        ldsm4t(av, v_at ^ (j * 32));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          Pair<T>::mma(o[j][n], av, ph[n][0], ph[n][1]);
+          Pair<T>::mma(o[j][n], av, pl[n][0], pl[n][1]);
+        }
       }
+      __syncwarp();  // every lane is done with this stage before it is filled again
     }
-  uint32_t flag = vis.bad ? SV_ROW_BAD_LEN : 0;
+    cp_wait<0>();
+
+    // ------------------------------------------------------------ merge the warps
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (s_bad[w]) flag |= SV_ROW_BAD_PAGE;
-  __syncthreads();
-  const float *mr = (const float *)smem;
-  const bool whole = plan.n == 1;
-  for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
-    const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    float x = 0.0f, y = 0.0f, sum = 0.0f, M = -INFINITY;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 p = *(const float2 *)(mr + ((size_t)w * Sh::kHeads + r) * Sh::kMergeRow + c);
-      x += p.x;
-      y += p.y;
-      M = fmaxf(M, s_m[w][r]);
-    }
-    // (a sum without a finite reference is 0, or NaN from the data: it stays)
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], w);
+        if (g4 == 0) {
+          s_m[warp][8 * n + 2 * t4 + e] = m[n][e];
+          s_l[warp][8 * n + 2 * t4 + e] = l[n][e];
+        }
+      }
+    bad = __any_sync(FULL, bad);
+    if (lane == 0) s_bad[warp] = bad ? 1 : 0;
+    __syncthreads();  // the ring is free too: O goes there
+    float *mo = (float *)smem + (size_t)warp * Sh::kHeads * Sh::kMergeRow;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = 8 * n + 2 * t4 + e;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][c]);
+        const float f = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - M);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          mo[c * Sh::kMergeRow + 16 * j + g4] = o[j][n][e] * f;
+          mo[c * Sh::kMergeRow + 16 * j + 8 + g4] = o[j][n][2 + e] * f;
+        }
+      }
+    uint32_t flag = vis.bad ? SV_ROW_BAD_LEN : 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2_approx(s_m[w][r] - M);
-    if (whole) {
-      const float nan = __int_as_float(0x7fffffff);
-      const float inv = 1.0f / sum;
-      x = flag ? nan : sum == 0.0f ? 0.0f : x * inv;
-      y = flag ? nan : sum == 0.0f ? 0.0f : y * inv;
-      *(uint32_t *)((T *)a.out + ((size_t)b * a.Hq + head0 + r) * D + c) = Pair<T>::pack(x, y);
-      if (c == 0 && a.lse)
-        a.lse[(size_t)b * a.Hq + head0 + r] =
-            flag ? nan : sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
-    } else {
-      *(float2 *)(a.w_o + ((size_t)unit * a.rows + r) * D + c) = make_float2(x, y);
+      if (s_bad[w]) flag |= SV_ROW_BAD_PAGE;
+    __syncthreads();
+    const float *mr = (const float *)smem;
+    for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
+      const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+      float x = 0.0f, y = 0.0f, sum = 0.0f, M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 p = *(const float2 *)(mr + ((size_t)w * Sh::kHeads + r) * Sh::kMergeRow + c);
+        x += p.x;
+        y += p.y;
+        M = fmaxf(M, s_m[w][r]);
+      }
+      // (a sum without a finite reference is 0, or NaN from the data: it stays)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2_approx(s_m[w][r] - M);
+      if (whole) {
+        const float nan = __int_as_float(0x7fffffff);
+        const float inv = 1.0f / sum;
+        x = flag ? nan : sum == 0.0f ? 0.0f : x * inv;
+        y = flag ? nan : sum == 0.0f ? 0.0f : y * inv;
+        *(uint32_t *)((T *)a.out + ((size_t)b * a.Hq + head0 + r) * D + c) = Pair<T>::pack(x, y);
+        if (c == 0 && a.lse)
+          a.lse[(size_t)b * a.Hq + head0 + r] =
+              flag ? nan : sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+      } else {
+        *(float2 *)(a.w_o + (part * a.rows + r) * D + c) = make_float2(x, y);
+      }
+      if (c == 0 && a.w_ml) a.w_ml[part * a.rows + r] = make_float2(M, sum);
     }
-    if (c == 0 && a.w_ml) a.w_ml[(size_t)unit * a.rows + r] = make_float2(M, sum);
-  }
-  if (threadIdx.x == 0) {
-    if (a.w_flag) a.w_flag[unit] = flag;
-    if (whole && h == 0 && a.status) a.status[b] = flag;
+    if (threadIdx.x == 0) {
+      if (a.w_flag) a.w_flag[part] = flag;
+      if (whole && h == 0 && a.status) a.status[b] = flag;
+    }
+    if constexpr (!SHARING) return;
+    share.first += max(tiles, 1);
+    share.at = share.first;
+    if (share.at >= share.end || ++share.b >= a.B) return;
+    __syncthreads();  // the merge's rows are read: the ring is free
   }
 }
 
@@ -734,7 +835,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   if ((int)blockIdx.x < joins) {
     const int at = wide ? blockIdx.x / a.rows : blockIdx.x;
     const int h = at % a.NH, b = at / a.NH;
-    const Plan plan = find_plan<kEndThreads>(a, b, false);
+    const Plan plan = find_plan<kEndThreads, false>(a, b);
     grid_dep_sync();
     if (plan.n == 1) return;  // written already
     const int hkv = h / a.gt, head0 = hkv * a.G + (h % a.gt) * kRows;
@@ -798,7 +899,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
     grid_dep_sync();
     return;
   }
-  const Plan plan = find_plan<kEndThreads>(a, b, false);
+  const Plan plan = find_plan<kEndThreads, false>(a, b);
   grid_dep_sync();
   extern __shared__ float s_lse[];  // [G]: log2 of the row's sum of exponentials
   __shared__ uint32_t s_flag;
@@ -835,7 +936,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
 // ------------------------------------------------------------------ host side
 struct Sizes {
   int G, gt, NH, rows, cap, vis_max;
-  long long groups, units;
+  long long groups, units;  // of the grid; of the workspace, for all heads
   int finding;
   size_t map, first, o, ml, flag, score, total;
 };
@@ -858,15 +959,23 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
   }
   z.vis_max = (int)most;
   const long long tiles = (z.vis_max + kTile - 1) / kTile;
+  const long long most_tiles = B * (tiles > 1 ? tiles : 1);
   const long long by_len = (long long)B * ((tiles + kMinTiles - 1) / kMinTiles);
   const long long by_units = (long long)B + units_for(D, B, z.NH) / z.NH;
   z.groups = by_len < by_units ? by_len : by_units;
   if (z.groups < B) z.groups = B;
-  z.finding = z.groups == B ? kWhole : B == 1 ? kOne : B < kMapFrom ? kScan : kMap;
+  z.finding = z.groups == B ? kWhole : B == 1 ? kOne : 8LL * B * z.NH <= slots_of(D) ? kScan : kMap;
   z.units = z.groups * z.NH;
+  if (z.finding == kMap && B <= kShareBatch && (long long)B * z.NH <= (long long)kShareHeads * slots_of(D) &&
+      z.NH <= slots_of(D)) {
+    z.finding = kShare;
+    const long long by_slots = slots_of(D) / z.NH, by_tiles = most_tiles / kMinTiles;
+    z.groups = by_tiles < 1 ? 1 : by_tiles < by_slots ? by_tiles : by_slots;
+    z.units = (z.groups + B) * z.NH;
+  }
   const long long rows = (long long)B * z.NH * kRows;  // CTAs of the join, at most
   if (z.units > 0x3fffffffLL || rows > 0x1fffffffLL || z.G > 8192) return false;
-  const bool split = z.groups > B;
+  const bool split = z.finding != kWhole;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t r = at;
@@ -883,22 +992,22 @@ bool sizes_of(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages, 
   return true;
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool SHARING>
 sv_status attend(const PagedArgs &a, const Sizes &z, cudaStream_t st) {
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
     const cudaError_t e =
-        cudaFuncSetAttribute(paged_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(paged_attn_kernel<T, D, NT, SHARING>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)Shape<D, NT>::kSmem);
     if (e != cudaSuccess) return check_launch("paged_attention", e);
     set_dev = dev;
   }
   LaunchScope ls("paged_attention", st);
   return check_launch("paged_attention",
-                      launch_pdl(paged_attn_kernel<T, D, NT>, dim3((unsigned)z.units), dim3(kThreads),
-                                 Shape<D, NT>::kSmem, st, a));
+                      launch_pdl(paged_attn_kernel<T, D, NT, SHARING>, dim3((unsigned)(z.groups * z.NH)),
+                                 dim3(kThreads), Shape<D, NT>::kSmem, st, a));
 }
 
 template <typename T, int D>
@@ -909,9 +1018,12 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
     s = check_launch("paged_map", launch_pdl(paged_map_kernel, dim3(1), dim3(kMapThreads), 0, st, a));
     if (s != SV_OK) return s;
   }
-  s = z.rows <= 8 ? attend<T, D, 1>(a, z, st) : attend<T, D, 2>(a, z, st);
+  if (a.finding == kShare)
+    s = z.rows <= 8 ? attend<T, D, 1, true>(a, z, st) : attend<T, D, 2, true>(a, z, st);
+  else
+    s = z.rows <= 8 ? attend<T, D, 1, false>(a, z, st) : attend<T, D, 2, false>(a, z, st);
   if (s != SV_OK) return s;
-  const bool split = z.groups > a.B;
+  const bool split = a.finding != kWhole;
   if (!split && !weights) return SV_OK;
   // a CTA to each row where a head has 8 units and more, spread over its warps
   // (8 sequences of 8000: 53 us, with a warp to each 55); a warp to each row
@@ -1030,7 +1142,7 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
   a.lse = out_lse;
   a.status = out_status;
   char *w = (char *)workspace;
-  const bool split = z.groups > B, wt = weight_sum != nullptr;
+  const bool split = z.finding != kWhole, wt = weight_sum != nullptr;
   a.groups = (int)z.groups;
   a.finding = z.finding;
   a.w_map = z.finding == kMap ? (int4 *)(w + z.map) : nullptr;

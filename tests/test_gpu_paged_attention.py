@@ -151,6 +151,50 @@ def test_many_sequences(B):
     check(*make(lens, 2, 1, 64, 16, seed=B), weights=B == 130)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 1, 64, 16), (20, 2, 128, 33), (6, 3, 256, 16)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+def test_shares_that_cross_sequences(Hq, Hkv, D, page, window, sinks):
+    """A batch in equal shares: sequences of many shares, shares of many
+    sequences, empty ones first, last and between."""
+    for seed, lens in enumerate(([0, 0, 3000, 1, 0, 64, 65, 5000, 0, 512, 511, 513, 7, 0, 1500, 0] + [20, 0, 300] * 12,
+                                 [1] * 39 + [9000],
+                                 [2500] + [0] * 40,
+                                 [0] * 45,
+                                 [640] * 40)):
+        check(*make(lens, Hq, Hkv, D, page, seed=seed, window=window, sinks=sinks), window=window, sinks=sinks,
+              weights=seed != 1)
+
+
+def test_faults_among_shares():
+    """A sequence with a bad length or page fails alone, wherever it lies in
+    the shares."""
+    lens = [700, 900, 30, 4000, 2000, 0, 1500, 800] * 6
+    q, kv, table, n = make(lens, 4, 2, 128, 16, seed=9)
+    want = check(q, kv, table, n)[0]
+    n2, table2 = n.clone(), table.clone()
+    n2[0], n2[17], n2[47] = -1, table.shape[1] * 16 + 1, 2 ** 31 - 1
+    table2[3, 249] = kv.shape[1]
+    table2[22, 0] = -1
+    sums = torch.zeros(len(lens), 2, table.shape[1] * 16, device=DEV)
+    out, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table2.to(DEV), n2.to(DEV), weight_sum=sums,
+                                      return_lse=True)
+    bad = {0: 256, 17: 256, 47: 256, 3: 512, 22: 512}
+    assert st.tolist() == [bad.get(b, 0) for b in range(len(lens))]
+    for b in range(len(lens)):
+        if b in bad:
+            assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all() and not sums[b].any()
+        else:  # two orders of the same sum: half a step of bf16 each, and the sums' own error
+            assert torch.allclose(out[b].float(), want[b].float(), rtol=2.0 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("B", [511, 512, 513])
+def test_batches_around_the_largest_that_is_shared(B):
+    g = torch.Generator().manual_seed(B)
+    lens = [int(x) for x in torch.randint(0, 90, (B,), generator=g)]
+    lens[B - 1], lens[3] = 1400, 900
+    check(*make(lens, 2, 1, 64, 16, seed=B, extra_pages=0), weights=True)
+
+
 def test_more_sequences_than_are_split():
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(0, 5, 2100)]
