@@ -36,8 +36,8 @@
 // Measured (of the copy rate, 6788 GB/s): 128 sequences of 3585-4096 tokens, 64
 // query heads on 8 KV heads of 128, 303 us for 2.02 GB (0.98; pages of 20 or of
 // 1 slot: 330 us); one of 131001 tokens, 84 us (0.94); windows of 2048 at D =
-// 64, 64 x 16 heads, 88 us (0.90); 24 ragged sequences with weight sums, 53 us
-// (0.65: the scores' way to memory and back, two launches).  With queries on the
+// 64, 64 x 16 heads, 88 us (0.90); 24 ragged sequences with weight sums, 52 us
+// (0.67: the scores' way to memory and back, two launches).  With queries on the
 // long side of the products (heads padded to 16 rows) the same took 342, 109, 106
 // and 83 us.
 #include <cuda_bf16.h>
@@ -798,10 +798,12 @@ __global__ void __launch_bounds__(kThreads, SHARING && D == 64 ? 4 : 0) paged_at
 // The end of a call that was split or sums weights.  CTAs below `joins`: the
 // join, one query row of a (sequence, head group) with its units spread over
 // the warps (wide), or a warp to each row (many sequences, few units each).
-// The others: weight_sum += sum over the G query heads of exp(s - lse), one
-// thread per visible slot, so no two add to one place.  Both find their units
-// from the lengths (read past L1) before they wait for the attention: it
-// started after whatever wrote those had ended.
+// The others: weight_sum += sum over the G query heads of exp(s - lse), each
+// visible slot by one thread, so no two add to one place; a thread has the scores
+// of 4 slots on their way together (24 ragged sequences: 52.4 us, one after the
+// other 53.6; 128 of 500-8000: 431 and 452).  Both find their units from the
+// lengths (read past L1), and the sums so far, before they wait for the
+// attention: it started after whatever wrote those had ended.
 constexpr int kEndThreads = 256;
 constexpr int kEndWarps = kEndThreads / 32;
 constexpr int kSumKeys = 1024;  // positions of a CTA
@@ -899,6 +901,20 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
     grid_dep_sync();
     return;
   }
+  // the sums so far, before the wait too
+  constexpr int kEach = kSumKeys / kEndThreads;  // slots of a thread
+  float *sums = a.weight_sum + ((size_t)b * a.Hkv + hkv) * a.S;
+  int to[kEach];
+  float before[kEach];
+  auto read_sums = [&]() {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int p = p0 + j * kEndThreads + (int)threadIdx.x;
+      to[j] = p < vis.n && seen(vis, p) ? slot_of(vis, p) : -1;
+      before[j] = to[j] >= 0 ? __ldcg(sums + to[j]) : 0.0f;
+    }
+  };
+  read_sums();
   const Plan plan = find_plan<kEndThreads, false>(a, b);
   grid_dep_sync();
   extern __shared__ float s_lse[];  // [G]: log2 of the row's sum of exponentials
@@ -915,22 +931,33 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   }
   __syncthreads();
   if (s_flag) return;
-  for (; p0 < vis.n; p0 += key_ctas * kSumKeys)
-    for (int p = p0 + threadIdx.x; p < min(p0 + kSumKeys, vis.n); p += kEndThreads) {
-      if (!seen(vis, p)) continue;
-      const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + p) * a.G;
-      float w = 0.0f;
-      if (a.G % 4 == 0) {
-        for (int g = 0; g < a.G; g += 4) {
-          const float4 x = *(const float4 *)(sc + g);
-          w += ex2_approx(fmaf(x.x, a.scale_log2, -s_lse[g])) + ex2_approx(fmaf(x.y, a.scale_log2, -s_lse[g + 1])) +
-               ex2_approx(fmaf(x.z, a.scale_log2, -s_lse[g + 2])) + ex2_approx(fmaf(x.w, a.scale_log2, -s_lse[g + 3]));
-        }
-      } else {
-        for (int g = 0; g < a.G; ++g) w += ex2_approx(fmaf(sc[g], a.scale_log2, -s_lse[g]));
+  for (;;) {
+    float w[kEach] = {};
+    const float *sc = a.w_score + (((size_t)b * a.Hkv + hkv) * a.vis_max + p0 + threadIdx.x) * a.G;
+    for (int g = 0; g < a.G; g += a.G % 4 == 0 ? 4 : 1) {
+      float4 x[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const float *at = sc + (size_t)j * kEndThreads * a.G + g;
+        if (to[j] >= 0) x[j] = a.G % 4 == 0 ? *(const float4 *)at : make_float4(*at, 0.0f, 0.0f, 0.0f);
       }
-      a.weight_sum[((size_t)b * a.Hkv + hkv) * a.S + slot_of(vis, p)] += w;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        if (to[j] < 0) continue;
+        w[j] += ex2_approx(fmaf(x[j].x, a.scale_log2, -s_lse[g]));
+        if (a.G % 4 == 0)
+          w[j] += ex2_approx(fmaf(x[j].y, a.scale_log2, -s_lse[g + 1])) +
+                  ex2_approx(fmaf(x[j].z, a.scale_log2, -s_lse[g + 2])) +
+                  ex2_approx(fmaf(x[j].w, a.scale_log2, -s_lse[g + 3]));
+      }
     }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (to[j] >= 0) sums[to[j]] = before[j] + w[j];
+    p0 += key_ctas * kSumKeys;
+    if (p0 >= vis.n) return;
+    read_sums();
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1025,9 +1052,9 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   if (s != SV_OK) return s;
   const bool split = a.finding != kWhole;
   if (!split && !weights) return SV_OK;
-  // a CTA to each row where a head has 8 units and more, spread over its warps
-  // (8 sequences of 8000: 53 us, with a warp to each 55); a warp to each row
-  // otherwise (24 ragged ones: 56 us, with a CTA to each 60)
+  // a CTA to each row where a head has many units, spread over its warps (8
+  // sequences of 8000: 53 us, with a warp to each 55); a warp to each row otherwise
+  // (24 ragged ones: 51 us, with a CTA to each 53; 128 of 90-1110: 31 and 38)
   const int wide = 4LL * a.B * a.NH <= slots_of(D);
   const int joins = split ? a.B * a.NH * (wide ? a.rows : 1) : 0;
   // CTAs for a head's slots: as the table has room for, but no more in all than
