@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
 
   // ------------------------------------------------------------ ranks
   // Slots above the limit all stay, those at it while `need` lasts.  A warp
-  // takes a run of slots, 32 side by side.
+  // takes a run of slots.
   __syncthreads();
   const int run = ((hi - lo + W - 1) / W + 31) & ~31;
   const int r0 = min(lo + warp * run, hi), r1 = none ? r0 : min(r0 + run, hi);
@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1) evict_kernel(EvictArgs a)
     s_scan[warp][1] = b_at;
   }
   __syncthreads();
-  const uint32_t of_warp[2] = {lane < W ? s_scan[lane < W ? lane : 0][0] : 0, lane < W ? s_scan[lane < W ? lane : 0][1] : 0};
+  const uint32_t of_warp[2] = {lane < W ? s_scan[lane < W ? lane : 0][0] : 0,
+                               lane < W ? s_scan[lane < W ? lane : 0][1] : 0};
   b_above = __reduce_add_sync(FULL, lane < warp ? of_warp[0] : 0);
   b_at = __reduce_add_sync(FULL, lane < warp ? of_warp[1] : 0);
   const uint32_t t_above = __reduce_add_sync(FULL, of_warp[0]), t_at = __reduce_add_sync(FULL, of_warp[1]);

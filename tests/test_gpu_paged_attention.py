@@ -382,6 +382,47 @@ def test_repeats_streams_and_graphs():
         assert torch.equal(out, sv.paged_attention(d[0], kv2, table2, ln)), step
 
 
+@pytest.mark.parametrize("B,Hkv", [(60, 2), (700, 1)])
+def test_streams_and_graphs_of_batches(B, Hkv):
+    """As above for a batch in shares and one found by a map, with weight sums:
+    every sequence's length changes between replays, some to 0 and back."""
+    top = 90000 // B
+    g = torch.Generator().manual_seed(B)
+    lens = [int(x) for x in torch.randint(0, top, (B,), generator=g)]
+    q, kv, table, n = [t.to(DEV) for t in make(lens, 4 * Hkv, Hkv, 64, 16, seed=B)]
+    kv = torch.nan_to_num(kv, nan=0.5)
+    table = torch.arange(B * table.shape[1], dtype=torch.int32, device=DEV).view(B, -1)
+    cap = table.shape[1] * 16
+    sums = [torch.zeros(B, Hkv, cap, device=DEV) for _ in range(4)]
+
+    def call(n, w, **kw):
+        return sv.paged_attention(q, kv, table, n, weight_sum=w, return_lse=True, **kw)
+    want = call(n, sums[0])
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = call(n, sums[1], stream=s1), call(n, sums[2], stream=s2)
+    torch.cuda.synchronize()
+    for x, y, z in zip(want, a, b):
+        assert torch.equal(x, y) and torch.equal(x, z)
+    assert torch.equal(sums[0], sums[1]) and torch.equal(sums[0], sums[2])
+    ln = n.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(ln, sums[3])
+    sums[3].zero_()
+    for seed in range(4):
+        ln.copy_(torch.randint(0, top, (B,), generator=torch.Generator().manual_seed(seed), dtype=torch.int32))
+        ln[seed::7] = 0
+        ln[3] = cap if seed % 2 else 1
+        before = sums[3].clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = call(ln, before)
+        for x, y in zip(want, out):
+            assert torch.equal(x, y), seed
+        assert torch.equal(before, sums[3]), seed
+
+
 def test_empty_batch_host_memory_and_refusals():
     q, kv, table, lens = make([150, 90], 8, 2, 64, 16, seed=12)
     d = [t.to(DEV) for t in (q, kv, table, lens)]
