@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, SHARING && D == 64 ? 4 : 0) paged_at
 // The end of a call that was split or sums weights.  CTAs below `joins`: the
 // join, one query row of a (sequence, head group) with its units spread over
 // the warps (wide), or a warp to each row (many sequences, few units each).
-// The others: weight_sum += sum over the G query heads of exp(s - lse), each
+// The others: weight_sum += sum over the G query heads of 2^(s - m) / l, each
 // visible slot by one thread, so no two add to one place; a thread has the scores
 // of 4 slots on their way together (24 ragged sequences: 52.4 us, one after the
 // other 53.6; 128 of 500-8000: 431 and 452).  Both find their units from the
@@ -917,7 +917,10 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
   read_sums();
   const Plan plan = find_plan<kEndThreads, false>(a, b);
   grid_dep_sync();
-  extern __shared__ float s_lse[];  // [G]: log2 of the row's sum of exponentials
+  // [G]: reference and 1 / sum of a row, apart: in one number, the log2 of the sum
+  // of exponentials, a weight would be off by half a step of that number (2^-12 of
+  // itself where scores lie about 4096; the output has no such error)
+  extern __shared__ float2 s_ml[];
   __shared__ uint32_t s_flag;
   if (threadIdx.x == 0) s_flag = 0;
   __syncthreads();
@@ -925,7 +928,8 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
     uint32_t flag;
     const float2 ml = join_ml(a, plan, hkv * a.gt + g / kRows, g % kRows, flag);
     if (lane == 0) {
-      s_lse[g] = ml.y == 0.0f ? INFINITY : ml.x + log2f(ml.y);  // no weight at all: exp2(-inf)
+      // without a finite score every exponential is 2^-inf: weights 0, or NaN from the data
+      s_ml[g] = make_float2(ml.x == -INFINITY ? INFINITY : ml.x, ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
       if (flag) s_flag = 1;
     }
   }
@@ -944,11 +948,10 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
         if (to[j] < 0) continue;
-        w[j] += ex2_approx(fmaf(x[j].x, a.scale_log2, -s_lse[g]));
+        auto weight = [&](float s, const float2 &ml) { return ex2_approx(fmaf(s, a.scale_log2, -ml.x)) * ml.y; };
+        w[j] += weight(x[j].x, s_ml[g]);
         if (a.G % 4 == 0)
-          w[j] += ex2_approx(fmaf(x[j].y, a.scale_log2, -s_lse[g + 1])) +
-                  ex2_approx(fmaf(x[j].z, a.scale_log2, -s_lse[g + 2])) +
-                  ex2_approx(fmaf(x[j].w, a.scale_log2, -s_lse[g + 3]));
+          w[j] += weight(x[j].y, s_ml[g + 1]) + weight(x[j].z, s_ml[g + 2]) + weight(x[j].w, s_ml[g + 3]);
       }
     }
 #pragma unroll
@@ -1064,10 +1067,16 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   const long long want = (z.vis_max + kSumKeys - 1) / kSumKeys;
   const int key_ctas = weights ? (int)(want < room ? want : room) : 0;
   const long long ctas = joins + key_ctas * heads;
+  const size_t smem = weights ? (size_t)a.G * sizeof(float2) : 0;
+  if (smem > 32 * 1024) {  // beside the join's 8 KB more than a kernel has unasked
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_finish_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return check_launch("paged_finish", e);
+  }
   LaunchScope ls("paged_finish", st);
   return check_launch("paged_finish",
                       launch_pdl(paged_finish_kernel<T, D>, dim3((unsigned)ctas), dim3(kEndThreads),
-                                 weights ? (size_t)a.G * 4 : 0, st, a, joins, wide, key_ctas ? key_ctas : 1));
+                                 smem, st, a, joins, wide, key_ctas ? key_ctas : 1));
 }
 
 bool bad_shape(int B, int Hq, int Hkv, int D, int page, int max_pages, int window, int sinks) {

@@ -506,3 +506,48 @@ def test_the_layer_of_the_dynamic_tree_workload():
         tol = 2.0 ** -8 * np.abs(ref) + (2 * d + 2.0 ** -17) * 6
         assert (np.abs(out[b:b + 1].double().cpu().numpy() - ref) <= tol).all()
         assert np.abs(lse[b:b + 1].double().cpu().numpy() - rlse).max() <= d + 60 * U
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("level,lens,Hkv,G", [
+    (64, [200, 33, 1, 130], 8, 1),       # scores about 4096, whole sequences
+    (128, [200, 64], 4, 3),              # about 16384
+    (64, [140, 7], 2, 4),                # four heads' scores in one load
+    (128, [2000, 500], 4, 4),            # split and joined
+    (128, [1500] + [90] * 59, 2, 1),     # shares
+])
+def test_weights_of_large_scores_sum_to_one(level, lens, Hkv, G, dtype):
+    """Scores c + x, c = level (level + head) thousands and x a multiple of 1/64
+    in [-2, 2], scale 1: exact in fp32 whatever the order, so a weight is
+    softmax(x) however large c is.  In units of u, relative: fp32 log2 e is off
+    by 1, for scores 4 apart 4 log2 e of it; the exponent, one rounding of at most
+    2 + 4 log2 e + 15 < 32 (the reference lies within 15 of the largest, and its
+    own rounding is common to a row): (6 + 32) ln 2 < 27 and 4 for the base-2
+    exponential, in the weight and in the sum alike; n for the sum; 6 for each
+    of at most five changes of reference; 1 / sum, the product and G additions."""
+    D, page = 64, 16
+    q, kv, table, n = make(lens, Hkv * G, Hkv, D, page, dtype, seed=level + G)
+    q.zero_()
+    q[..., 0] = (level + torch.arange(Hkv * G)).to(dtype)
+    q[..., 1] = 1
+    x = torch.randint(-128, 129, kv[0, ..., 0].shape, generator=torch.Generator().manual_seed(G)) / 64
+    kv[0, ..., 0] = level
+    kv[0, ..., 1] = x.to(dtype)
+    kv[0, ..., 2:] = 0
+    sums = torch.zeros(len(lens), Hkv, table.shape[1] * page, device=DEV)
+    _, lse, st = sv.paged_attention(q.to(DEV), kv.to(DEV), table.to(DEV), n.to(DEV), 1.0, weight_sum=sums,
+                                    return_lse=True)
+    assert not st.any() and lse.min() > level * level
+    for b, k in enumerate(lens):
+        j = torch.arange(k)
+        want = G * torch.softmax(x[table[b, j // page].long(), j % page].double(), 0).T
+        d = (2 * (27 + 4) + k + 5 * 6 + 2 + G) * U
+        got = sums[b, :, :k].double().cpu()
+        assert ((got - want).abs() <= d * want).all(), float(((got - want).abs() / want).max() / d)
+        assert not sums[b, :, k:].any()
+
+
+def test_weights_of_the_most_query_heads():
+    """8192 query heads on one KV head: every row's reference and sum wait beside
+    one another."""
+    check(*make([20, 70], 8192, 1, 64, 16, seed=5), weights=True)
