@@ -66,3 +66,19 @@ def test_verify_probs(seed):
                       rng.random() < 0.3, sigma=rng.choice([0.5, 2.0, 8.0]), noise=rng.choice([0.0, 0.1, 1.0, 4.0]))
     n = torch.tensor([rng.randint(0, N) for _ in range(B)], dtype=torch.int32) if rng.random() < 0.5 else None
     probs.check(*args, n)
+
+
+@pytest.mark.parametrize("window", [1, 5, 16, 17, 100, 1000])
+@pytest.mark.parametrize("seed", range(4))
+def test_paged_attention_windows(window, seed):
+    """Windows at the edges of a group and of a tile, against odd pages,
+    groupings and first tokens."""
+    rng = random.Random(3000 + 10 * window + seed)
+    Hkv, G = rng.choice([1, 2, 3]), rng.choice([1, 3, 7, 16, 17])
+    D, page = rng.choice([64, 128]), (1, 16, 20, 48)[seed]
+    lens = [rng.choice([0, 1, window, window + 1, window + 15, window + 16, rng.randint(1, 2500)])
+            for _ in range(rng.choice([1, 4, 40]))]
+    sinks = rng.choice([0, 1, 15, 16, 33])
+    q, kv, table, n = paged.make(lens, Hkv * G, Hkv, D, page, rng.choice([torch.bfloat16, torch.float16]),
+                                 seed, window, sinks)
+    paged.check(q, kv, table, n, window=window, sinks=sinks, weights=seed % 2 == 0)
