@@ -626,8 +626,10 @@ struct Sizes {
   size_t stage, src, total;
 };
 bool sizes_of(Sizes &z, int L, int B, int H, int budget) {
+  constexpr long long most = 1 << 24;
+  if ((long long)L * B > most) return false;  // the product of three may pass 63 bits
   z.items = (long long)L * B * H;
-  if (z.items > (1 << 24) || budget > kMaxSlots) return false;
+  if (z.items > most || budget > kMaxSlots) return false;
   z.stage = 0;
   z.src = align_up((size_t)z.items * budget * 4, 256);
   z.total = align_up(z.src + (size_t)z.items * budget * 8, 256);
@@ -666,9 +668,11 @@ extern "C" sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stri
   if (S < cap) return set_error(SV_ERR_INVALID_ARG, "weight sums have %d slots a head, the page table %lld", S, cap);
   const int row = D * elem_bytes;
   if (row % 4) return set_error(SV_ERR_UNSUPPORTED, "rows of %d bytes (a multiple of 4 is needed)", row);
-  const int64_t inner = (int64_t)page * Hkv * row, limit = INT64_MAX / 4;
-  if (page_stride > limit / elem_bytes / num_pages || page_stride * elem_bytes < inner || kv_stride < 1 ||
-      kv_stride > limit / elem_bytes || layer_stride < 0 || layer_stride > limit / elem_bytes / L)
+  const int64_t limit = INT64_MAX / 4;
+  // (slots that a page has room for: a page's own bytes may pass 63 bits)
+  if (page_stride < 1 || page_stride > limit / elem_bytes / num_pages ||
+      page_stride * elem_bytes / row / Hkv < page || kv_stride < 1 || kv_stride > limit / elem_bytes ||
+      layer_stride < 0 || layer_stride > limit / elem_bytes / L)
     return set_error(SV_ERR_INVALID_ARG, "page_stride must cover a page, kv_stride be positive, layer_stride >= 0");
   if (L > 1 && layer_stride < 1) return set_error(SV_ERR_INVALID_ARG, "layer_stride must be positive");
   if (B == 0) return SV_OK;

@@ -223,3 +223,19 @@ def test_kv_evict_binding_refusals(sv):
     call(w=w.double()), call(w=w[..., ::2], ow=w), call(ow=w[..., :40]), call(budget=9)
     call(kept=kept.long()), call(kl=kl[:1]), call(st=torch.zeros(3, dtype=torch.int32))
     call()                                                 # pageable host memory
+
+
+def test_kv_evict_sizes_whose_products_pass_63_bits(sv):
+    lib, x, most = sv.load_library(), 4096, 2 ** 31 - 1
+
+    def call(L=1, B=1, H=1, page=16, ps=16 * 2048, ls=1 << 30):
+        return lib.sv_kv_evict(None, ls, 1 << 20, ps, 2, x, x, x, x, L, B, H, 1024, page, 1, 8, 1 << 30, 32, 2, 4,
+                               x, x, None, x, 1 << 62, None)
+    for shape in ((most, most, 4), (most, 2, most), (1, most, most), (1 << 20, 1 << 20, 1 << 25)):
+        assert sv.sv_kv_evict_workspace(*shape, 9) == 0
+        assert call(*shape, ps=1 << 50, ls=4) == 2 and b"2^24" in lib.sv_last_error()
+    # a page of 2^30 slots of 2^24 heads of 2 KB: 2^65 bytes, which no stride covers
+    assert call(H=1 << 24, page=1 << 30) == 1 and b"page_stride" in lib.sv_last_error()
+    assert call(ps=-(2 ** 63)) == 1 and b"page_stride" in lib.sv_last_error()
+    assert call(ps=16 * 1024) == 1 and b"null" in lib.sv_last_error()
+    assert call(ps=16 * 1024 - 1) == 1 and b"page_stride" in lib.sv_last_error()
