@@ -321,6 +321,14 @@ def sv_tree_level(dlogits, K, level, n0, frontier, cand_parent, cand_token, cand
         _p(cand_score), _p(cand_level), _stream(stream)))
 
 
+def _int32(name, x):
+    """A number that the C side takes as an int; ctypes would drop its upper bits."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def _want(name, t, dtype, shape):
     """A packed tensor of this type and shape."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
@@ -389,8 +397,8 @@ def _pages(kv, lead):
 
 
 def sv_paged_attention_workspace(B, Hq, Hkv, D, page, max_pages, window=0, sinks=0, weights=False):
-    return int(load_library().sv_paged_attention_workspace(B, Hq, Hkv, D, page, max_pages, window,
-                                                           sinks, 1 if weights else 0))
+    sizes = [_int32("size", x) for x in (B, Hq, Hkv, D, page, max_pages, window, sinks)]
+    return int(load_library().sv_paged_attention_workspace(*sizes, 1 if weights else 0))
 
 
 def sv_paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_sum, out,
@@ -421,22 +429,23 @@ def _paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_s
     _want("q", q, q.dtype, (B, Hq, D))
     _want("block_table", block_table, torch.int32, (B, max_pages))
     _want("seq_len", seq_len, torch.int32, (B,))
-    S = 0
+    window, sinks, S = _int32("window", window), _int32("sinks", sinks), 0
     if weight_sum is not None:
-        S = weight_sum.shape[-1]
+        S = _int32("weight_sum's slots", weight_sum.shape[-1])
         _want("weight_sum", weight_sum, torch.float32, (B, Hkv, S))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: need a contiguous tensor")
     return _check(load_library().sv_paged_attention(
         _p(q), _p(kv), kv_stride, page_stride, dt, _p(block_table), _p(seq_len), B, Hq, Hkv, D,
-        page, max_pages, P, int(window), int(sinks), float(scale), _p(weight_sum), S, _p(out),
+        page, max_pages, P, window, sinks, float(scale), _p(weight_sum), S, _p(out),
         _p(out_lse), _p(out_status), _p(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _stream(stream)))
 
 
 def sv_kv_evict_workspace(L, B, Hkv, budget):
-    return int(load_library().sv_kv_evict_workspace(L, B, Hkv, budget))
+    return int(load_library().sv_kv_evict_workspace(
+        *[_int32("size", x) for x in (L, B, Hkv, budget)]))
 
 
 def sv_kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sinks, recent,
@@ -444,7 +453,8 @@ def sv_kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, si
     """kv [L][2][pages][page][Hkv][D], moved in place; weight_sum and
     out_weight_sum [L][B][Hkv][S] (may be the same tensor)."""
     B = seq_len.shape[0]
-    _want("out_kept", out_kept, torch.int32, (kv.shape[0], B, kv.shape[-2], int(budget)))
+    budget = _int32("budget", budget)
+    _want("out_kept", out_kept, torch.int32, (kv.shape[0], B, kv.shape[-2], budget))
     _want("out_kv_len", out_kv_len, torch.int32, (B,))
     if out_status is not None:
         _want("out_status", out_status, torch.int32, (B,))
@@ -457,7 +467,8 @@ def _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sink
     kv_stride, page_stride = _pages(kv, 1)
     L, _, P, page, Hkv, D = kv.shape
     B, max_pages = block_table.shape if block_table.dim() == 2 else (seq_len.shape[0], 0)
-    S = weight_sum.shape[-1]
+    S = _int32("weight_sum's slots", weight_sum.shape[-1])
+    sinks, recent = _int32("sinks", sinks), _int32("recent", recent)
     _want("block_table", block_table, torch.int32, (B, max_pages))
     _want("seq_len", seq_len, torch.int32, (B,))
     _want("weight_sum", weight_sum, torch.float32, (L, B, Hkv, S))
@@ -468,7 +479,7 @@ def _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sink
     return _check(load_library().sv_kv_evict(
         _p(kv), kv.stride(0) if L > 1 else 0, kv_stride, page_stride, kv.element_size(),
         _p(block_table), _p(seq_len), _p(weight_sum), _p(out_weight_sum), L, B, Hkv, D, page,
-        max_pages, P, S, int(budget), int(sinks), int(recent), _p(out_kept), _p(out_kv_len),
+        max_pages, P, S, budget, sinks, recent, _p(out_kept), _p(out_kv_len),
         _p(out_status), _p(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _stream(stream)))
@@ -609,7 +620,7 @@ def kv_evict(kv, block_table, seq_len, weight_sum, budget, sinks=0, recent=0, ou
     Returns the kept slots [L][B][Hkv][budget], the new lengths [B] and the
     status words [B]."""
     L, Hkv, B = kv.shape[0], kv.shape[-2], seq_len.shape[0]
-    budget = int(budget)
+    budget = _int32("budget", budget)
     dev = _out_dev(kv)
     with _allocating(stream):
         kept = torch.empty(L, B, Hkv, max(budget, 0), dtype=torch.int32, device=dev)

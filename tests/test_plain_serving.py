@@ -239,3 +239,31 @@ def test_kv_evict_sizes_whose_products_pass_63_bits(sv):
     assert call(ps=-(2 ** 63)) == 1 and b"page_stride" in lib.sv_last_error()
     assert call(ps=16 * 1024) == 1 and b"null" in lib.sv_last_error()
     assert call(ps=16 * 1024 - 1) == 1 and b"page_stride" in lib.sv_last_error()
+
+
+def test_numbers_beyond_32_bits_are_refused(sv):
+    """They would reach the library without their upper bits: another window, or
+    a far smaller budget."""
+    bf, i32 = torch.bfloat16, torch.int32
+    q, kv = torch.zeros(2, 8, 64, dtype=bf), torch.zeros(1, 2, 6, 16, 2, 64, dtype=bf)
+    t, n = torch.zeros(2, 3, dtype=i32), torch.ones(2, dtype=i32)
+    w = torch.zeros(1, 2, 2, 48)
+    for window, sinks in ((2 ** 32 + 5, 0), (2 ** 31, 0), (0, 2 ** 32 + 4), (-2 ** 32, 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sv.sv_paged_attention(q, kv[0], t, n, window, sinks, 1.0, None, torch.empty_like(q))
+        with pytest.raises(ValueError, match="32 bits"):
+            sv.sv_paged_attention_workspace(2, 8, 2, 64, 16, 3, window, sinks)
+    for sinks, recent in ((2 ** 32 + 1, 1), (1, 2 ** 40)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sv.sv_kv_evict(kv, t, n, w, w, 8, sinks, recent, torch.zeros(1, 2, 2, 8, dtype=i32), n.clone())
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.sv_kv_evict(kv, t, n, w, w, 2 ** 32 + 8, 1, 1, torch.zeros(1, 2, 2, 8, dtype=i32), n.clone())
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.sv_kv_evict_workspace(1, 2, 2, 2 ** 32 + 8)
+    assert sv.sv_kv_evict_workspace(1, 2, 2, 2 ** 31 - 1) == 0    # beyond the library's own limit
+    # more slots a head than an int holds: a view, no such memory
+    far = torch.zeros(1).expand(1, 2, 2, 2 ** 32 + 48)
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.sv_kv_evict(kv, t, n, far, far, 8, 1, 1, torch.zeros(1, 2, 2, 8, dtype=i32), n.clone())
+    with pytest.raises(ValueError, match="32 bits"):
+        sv.sv_paged_attention(q, kv[0], t, n, 0, 0, 1.0, far[0], torch.empty_like(q))
