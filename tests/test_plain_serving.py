@@ -267,3 +267,16 @@ def test_numbers_beyond_32_bits_are_refused(sv):
         sv.sv_kv_evict(kv, t, n, far, far, 8, 1, 1, torch.zeros(1, 2, 2, 8, dtype=i32), n.clone())
     with pytest.raises(ValueError, match="32 bits"):
         sv.sv_paged_attention(q, kv[0], t, n, 0, 0, 1.0, far[0], torch.empty_like(q))
+
+
+def test_paged_attention_workspace_sizes(sv):
+    """A table of 4 pages of 16 leaves no room for two units: nothing to join, and
+    with sums a score for each query head and slot, a reference and sum for each
+    head and a flag for each KV head, each from a multiple of 256 bytes.  The scores
+    are what a long table costs."""
+    ws = sv.sv_paged_attention_workspace
+    assert ws(1, 8, 2, 128, 16, 4) == 0
+    assert ws(1, 8, 2, 128, 16, 4, weights=True) == 256 + 256 + 8 * 64 * 4
+    long, sums = ws(128, 64, 8, 128, 16, 8192), ws(128, 64, 8, 128, 16, 8192, weights=True)
+    assert sums - long == 128 * 64 * 131072 * 4
+    assert ws(128, 64, 8, 128, 16, 8192, 4096, 4, True) < sums // 16
