@@ -452,10 +452,9 @@ sv_status sv_tree_attention_ex(const void *q, const void *kv, const int32_t *bas
  * out_status [B], written in full.  Only what the walk reaches is read: the
  * tested tokens' probabilities and the row (or pair of rows) sampled from.  A
  * fault there -- an entry that is NaN, negative or at least 2, weights that
- * sum to 2 or more (an fp32 sum) or to 0 (SV_ROW_NAN), a tested token outside
- * [0, V) (SV_ROW_BAD_TOKEN), a used random number outside [0, 1)
- * (SV_ROW_BAD_RAND) or n_draft outside [0, N] (SV_ROW_BAD_LEN) -- makes the
- * sequence emit nothing: accept_len 0, tokens all -1.  V <= SV_MAX_VOCAB,
+ * sum to 2 or more or to 0 (SV_ROW_NAN), a tested token outside [0, V)
+ * (SV_ROW_BAD_TOKEN), a used random number outside [0, 1) (SV_ROW_BAD_RAND) or
+ * n_draft outside [0, N] (SV_ROW_BAD_LEN) -- makes the sequence emit nothing: accept_len 0, tokens all -1.  V <= SV_MAX_VOCAB,
  * N <= SV_MAX_POSITIONS.  One launch, no workspace; capturable.  The outputs
  * overlap no input.
  * --------------------------------------------------------------------------- */

@@ -72,7 +72,7 @@ __device__ __forceinline__ unsigned long long threshold(float u, unsigned long l
 
 struct Sums {
   unsigned long long w;  // exact weights
-  float f;               // the same in fp32, to see an overflow
+  float f;               // the same in fp32, to see that 64 bits overflowed
   uint32_t top;          // largest entry_bits
 };
 
@@ -296,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, 6) verify_probs_kernel(ProbArgs a, u
 #pragma unroll
       for (int o = 16; o; o >>= 1) f += __shfl_xor_sync(FULL, f, o);
       tp = __reduce_max_sync(FULL, tp);
-      const bool bad = tp >= kTwo || !(f < 2.0f);
+      // A sum of 2 or more is 2^63 or more in integers, exactly; from 4 on those
+      // wrap around, which the fp32 sum, off by 2^-12 of itself at most (2048
+      // additions a lane), tells from less than 2.
+      const bool bad = tp >= kTwo || !(f < 3.0f) || total >> 63;
       const bool none = !bad && total == 0;
       if (lane == 0) {
         s_again = none && rejected && round == 0;

@@ -271,3 +271,34 @@ def test_large_batch_against_the_definition():
     for k, w in zip(("tokens", "accept_len", "status"), want):
         assert np.array_equal(r[k][pick].cpu().numpy(), w), k
     assert int(r["status"].abs().max()) == 0
+
+
+@pytest.mark.parametrize("V", [5, 300, 40000])
+def test_weights_that_sum_to_almost_two(V):
+    """Rows need not be normalised: below 2 they are drawn from, at 2 and above
+    they are a fault, exactly and wherever the row lies.  Most of these sums round
+    to 2 in fp32; from 4 on the integers wrap around."""
+    e = 2.0 ** -24
+    rows = [(1.0, 1 - e), (1.0, 1.0), (1.5, 0.5 - e / 2), (1 - e, 1 - e, e, e), (1 - e, 1 - e, e, e / 2),
+            (1.75, 0.25, 2.0 ** -62), (1.75, 0.25 - e / 4, e / 8), (1.9, 1.9), (1.25,) * 4, (1.0,) * 4, (1.99,) * 5]
+    B = len(rows)
+    q = torch.zeros(2, B, 2, V)
+    for b, row in enumerate(rows):
+        at = torch.linspace(0, V - 1, len(row)).long()
+        for j, x in enumerate(row):
+            q[0, b, 0, at[j]] = x                  # side by side in a warp, or CTAs apart
+            q[1, b, 0, V - 1 - j] = x
+    us = torch.tensor([0.0, 0.5, 1 - e])
+    none = torch.zeros(B, 0, dtype=torch.int32), torch.zeros(B, 0)
+    for rows_at in q:
+        for u in us:
+            for pad in (0, 1, 4):
+                wide = torch.zeros(B, 1, V + pad)
+                wide[..., :V] = rows_at[:, :1]
+                want = check(wide[..., :V], None, *none, u.repeat(B))
+                assert want[2].tolist() == [0, 1, 0, 1, 0, 1, 0, 1, 1, 1, 1]
+    # after a rejection: q apart from the token that was copied
+    d = torch.full((B, 1), 2, dtype=torch.int32)
+    one = q[1].clone()
+    one[:, 0, 2] = torch.where(one[:, 0, 2] == 0, 0.25, one[:, 0, 2])
+    check(one, None, d, torch.full((B, 1), 0.9999), us[1].repeat(B))
