@@ -483,9 +483,11 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row
  *         further (elements of dt; page id, row r, KV head h): [2][num_pages]
  *         [page][Hkv][D] and [num_pages][2][page][Hkv][D] alike, and a
  *         contiguous cache [2][B][S][Hkv][D] with page = S, block_table[b] =
- *         b.  Both strides multiples of 8, page_stride >= page Hkv D
+ *         b (the only layout that sv_tree_attention and sv_kv_compact
+ *         take).  Both strides multiples of 8, page_stride >= page Hkv D
  *   block_table int32 [B][max_pages]; seq_len int32 [B], 0..max_pages page
- *   scale > 0, finite; D 64, 128 or 256; any G
+ *   scale > 0, finite; D 64, 128 or 256; G up to 8192 (K and V are read once
+ *         for every 16 query heads of a KV head)
  *   weight_sum fp32 [B][Hkv][S] or NULL, S >= max_pages page: at every visible
  *         slot the weights of the G query heads exp(scale q.k - lse) are added
  *         (what sv_kv_evict evicts by); other slots are left as they are
@@ -504,6 +506,11 @@ sv_status sv_verify_chain_probs(const void *qprobs, int64_t q_seq, int64_t q_row
  * captured launch serves growing sequences.  The workspace (bytes from the
  * query, `weights` nonzero when weight_sum is given; 0: none needed, or bad
  * sizes) is written before it is read; calls that may overlap need one each.
+ * With weight_sum it holds a score for every query head and every slot that the
+ * table has room for, 4 B Hq max_pages page bytes (B = 128, Hq = 64, 131072
+ * slots: 4.3 GB), or about 4 B Hq (window + sinks): there max_pages is best taken
+ * from the longest sequence of the batch.  Without, it grows with the units that
+ * the device runs at once and with B, not with the table.
  * Results do not depend on scheduling.
  * --------------------------------------------------------------------------- */
 size_t sv_paged_attention_workspace(int B, int Hq, int Hkv, int D, int page, int max_pages,

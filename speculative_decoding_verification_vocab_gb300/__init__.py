@@ -593,8 +593,9 @@ def paged_attention(q, kv, block_table, seq_len, scale=None, window=0, sinks=0, 
     q [B][Hq][D], kv [2][pages][page][Hkv][D] (one layer), block_table int32
     [B][max_pages], seq_len int32 [B]; scale defaults to 1/sqrt(D); window and
     sinks narrow the visible slots; weight_sum fp32 [B][Hkv][S] gets the
-    attention weights added.  Returns out (like q), and with return_lse the
-    log-sum-exp [B][Hq] and the status words [B]."""
+    attention weights added, by way of a workspace of 4 bytes for each query
+    head and slot that the table has room for.  Returns out (like q), and with
+    return_lse the log-sum-exp [B][Hq] and the status words [B]."""
     B, Hq, D = q.shape
     dev = _out_dev(q)
     with _allocating(stream):

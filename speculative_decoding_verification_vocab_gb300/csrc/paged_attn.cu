@@ -9,8 +9,9 @@
 // slots join exactly: m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), and
 // the same for the weighted sums of the values (scores are kept in log2 units).
 //
-// Bound: every visible K and V row is read once (4 D bytes a slot and KV
-// head), 4 D G operations on it: memory, for any G a model has.  The matrix
+// Bound: every visible K and V row is read once for 16 query heads of its KV
+// head (4 D bytes a slot and KV head), 4 D G operations on it: memory up to G = 16;
+// above, each further 16 heads read the rows again, mostly from L2.  The matrix
 // products only have to keep up with HBM (45 GB/s per SM), so they run as
 // m16n8k16 tensor instructions on registers, transposed: S^T = K Q^T with 16
 // keys as rows and 8 (or 16) query heads as columns, O^T = V^T P^T with 16
@@ -36,10 +37,11 @@
 // Measured (of the copy rate, 6788 GB/s): 128 sequences of 3585-4096 tokens, 64
 // query heads on 8 KV heads of 128, 303 us for 2.02 GB (0.98; pages of 20 or of
 // 1 slot: 330 us); one of 131001 tokens, 84 us (0.94); windows of 2048 at D =
-// 64, 64 x 16 heads, 88 us (0.90); 24 ragged sequences with weight sums, 52 us
-// (0.67: the scores' way to memory and back, two launches).  With queries on the
-// long side of the products (heads padded to 16 rows) the same took 342, 109, 106
-// and 83 us.
+// 64, 64 x 16 heads, 88 us (0.90); 24 ragged sequences with weight sums, 53 us of
+// GPU time (0.66: the scores' way to memory and back, two launches), 54 to 61 in a
+// stream of calls.  256 query heads on 8 KV heads, 468 us for the same batch (0.64),
+// 512 on 8, 32 sequences, 191 us (0.40).  With queries on the long side of the
+// products (heads padded to 16 rows) the first four took 342, 109, 106 and 83 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
