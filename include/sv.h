@@ -65,7 +65,8 @@ typedef enum {
   SV_ERR_TIMEOUT = 4      /* reserved: no call of this build waits on the device */
 } sv_status;
 
-/* SV_F16 is taken by sv_paged_attention only. */
+/* SV_F16 is taken by the attention of single tokens (sv_paged_attention,
+ * sv_prefix_attention), sv_token_logprobs and sv_distill_* only. */
 typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype;
 
 /* Bits of the per-sequence out_status word. */
@@ -79,6 +80,7 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype;
 #define SV_ROW_BAD_RAND 128u /* sv_verify_chain_probs: a used random number outside [0, 1) */
 #define SV_ROW_BAD_LEN 256u  /* a length outside its range (n_draft, seq_len) */
 #define SV_ROW_BAD_PAGE 512u /* a used page table entry outside [0, num_pages) */
+#define SV_ROW_BAD_ROW 1024u /* sv_token_logprobs: a row index outside [0, T) */
 
 /* Build limits. */
 #define SV_MAX_VOCAB (1 << 22)  /* fixed-point sampling sums stay below 2^63 */
@@ -563,6 +565,90 @@ sv_status sv_kv_evict(void *kv, int64_t layer_stride, int64_t kv_stride, int64_t
                       int sinks, int recent, int32_t *out_kept, int32_t *out_kv_len,
                       uint32_t *out_status, void *workspace, size_t workspace_bytes,
                       void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_token_logprobs -- log probabilities of given tokens, entropy and the most
+ * likely alternatives: what a round answers with beside its tokens, and the
+ * teacher's side of sv_distill_loss.  Reads the logits of sv_verify_chain and
+ * sv_verify_tree where they are; the pages have no counterpart.
+ *
+ * Entry (b, i), i < P, looks at row r = rows[b][i] (rows NULL: r = i) of
+ * sequence b and, in it, at token tokens[b][i], with p = softmax(row / T):
+ *   out_logprob [B][P]        ln p(token)
+ *   out_entropy [B][P]        -sum p ln p (nats)
+ *   out_top_token, out_top_logprob [B][P][K]  the K largest logits, equal ones
+ *               in ascending token id, and their ln p; a token of -inf is no
+ *               alternative: -1 and -inf in the places left
+ *   out_status [B][P]         written in full
+ * A round's outputs fit as they come: tokens = out_tokens, and for a tree rows =
+ * out_path_nodes.  An entry whose token or row is -1 asks for nothing, and its
+ * row is not read: 0, 0, -1, -inf.
+ *
+ *   logits  row r of sequence b starts b seq_stride + r row_stride elements in
+ *           (strides >= 0; [B][T][V] of SV_F32, SV_BF16 or SV_F16)
+ *   rows    int32 [B][P] or NULL (P <= T); tokens int32 [B][P] or NULL (no
+ *           out_logprob then)
+ *   temperature > 0, finite; K 0..128, K <= V (K = 0: the outputs may be NULL)
+ * A row outside [0, T) (SV_ROW_BAD_ROW) or with a NaN or +inf, or all -inf
+ * (SV_ROW_NAN), gives NaN, tokens -1; a token outside [0, V) (SV_ROW_BAD_TOKEN)
+ * a NaN log probability.  One launch, no workspace; capturable.  The outputs
+ * overlap no input.  Results do not depend on scheduling.
+ * --------------------------------------------------------------------------- */
+sv_status sv_token_logprobs(const void *logits, int64_t seq_stride, int64_t row_stride,
+                            sv_dtype dt, const int32_t *rows, const int32_t *tokens, int B, int T,
+                            int P, int V, int K, float temperature, float *out_logprob,
+                            float *out_entropy, int32_t *out_top_token, float *out_top_logprob,
+                            uint32_t *out_status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_distill_loss, sv_distill_grad -- train a draft on its teacher's most likely
+ * tokens.  [Lesson] "O que determina a aceleração": the acceptance is the
+ * overlap of draft and verifier, so a draft is trained towards the verifier's
+ * distribution, kept as its top tokens (what sv_token_logprobs gives).
+ *
+ * Row r: s = softmax(logits[r] / T) over V, the teacher's tokens v_k with the
+ * values a_k, k < K (token -1: an unused entry).
+ *   tail = 1  a_k are log probabilities, at the same temperature: t_k =
+ *             exp(a_k), and the rest of the vocabulary is one class more, with
+ *             t_r = max(0, 1 - sum t_k) and s_r, the sum of its s_v
+ *   tail = 0  t = softmax(a) over the list, t_r = 0 (a_k: logits or log
+ *             probabilities)
+ *   out_loss[r] = sum t_k (ln t_k - ln s(v_k)) + t_r (ln t_r - ln s_r)
+ *   out_grad[r][v] = weight[r] / T (s_v - t_v) for a listed v, weight[r] / T
+ *             s_v (1 - t_r / s_r) for the others: weight[r] dloss[r] / dlogits
+ * Terms with t = 0 are 0; s = 0 under t > 0 gives a loss of +inf.  A row whose
+ * list has no entries has loss 0 and a gradient of zeros.
+ *
+ * sv_distill_loss gives the loss, with out_grad the gradient too (from one read
+ * of the logits), with out_stat what sv_distill_grad needs to give the gradient
+ * later, from the same logits, list, T and tail (weight: the gradient that
+ * arrives at each row's loss).
+ *
+ *   logits  [R][V] of dt (SV_F32, SV_BF16, SV_F16), row_stride >= 0 elements
+ *   teacher_token int32, teacher_logprob fp32 [R][K]; K 1..128, K <= V
+ *   weight  fp32 [R] or NULL: 1
+ *   out_loss fp32 [R]; out_stat fp32 [R][4] or NULL (16-byte aligned)
+ *   out_grad [R][V] of dt, grad_stride >= V elements, or NULL; may be logits
+ *           itself at the same stride; rows that lie on the 16-byte grid as the
+ *           logits' do are faster
+ *   out_status [R], written in full
+ * A row with a NaN or +inf, or all -inf, or a teacher's value that is NaN or
+ * +inf, or (tail) values that add up to more than 1 + 2^-8, or (no tail) whose
+ * values are all -inf (SV_ROW_NAN), and a teacher's token outside [0, V) or
+ * listed twice (SV_ROW_BAD_TOKEN), give a loss of NaN and a gradient of zeros.
+ * R <= 2^22.  One launch each, no workspace; capturable.  But for out_grad =
+ * logits the outputs overlap no input.  Results do not depend on scheduling.
+ * --------------------------------------------------------------------------- */
+sv_status sv_distill_loss(const void *logits, int64_t row_stride, sv_dtype dt,
+                          const int32_t *teacher_token, const float *teacher_logprob,
+                          const float *weight, int R, int V, int K, float temperature, int tail,
+                          float *out_loss, float *out_stat, void *out_grad, int64_t grad_stride,
+                          uint32_t *out_status, void *stream);
+sv_status sv_distill_grad(const void *logits, int64_t row_stride, sv_dtype dt,
+                          const int32_t *teacher_token, const float *teacher_logprob,
+                          const float *stat, const float *weight, int R, int V, int K,
+                          float temperature, int tail, void *out_grad, int64_t grad_stride,
+                          uint32_t *out_status, void *stream);
 
 /* Thread-local message for the last non-OK status returned on this thread. */
 const char *sv_last_error(void);

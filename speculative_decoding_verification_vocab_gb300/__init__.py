@@ -23,6 +23,7 @@ SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_ROW_NAN, SV_ROW_BAD_TOKEN, SV_ROW_RESID_ZERO, SV_ROW_P_ZERO, SV_ROW_BAD_TREE = 1, 2, 4, 8, 16
 SV_ROW_BAD_BASE, SV_ROW_TIMEOUT = 32, 64
 SV_ROW_BAD_RAND, SV_ROW_BAD_LEN, SV_ROW_BAD_PAGE = 128, 256, 512
+SV_ROW_BAD_ROW = 1024
 SV_MAX_VOCAB, SV_MAX_POSITIONS, SV_MAX_TREE_NODES = 1 << 22, 1024, 1024
 
 EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_verify_chain",
@@ -33,7 +34,7 @@ EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_ve
            "sv_launch_count", "sv_trace_enable", "sv_trace_collect", "sv_tree_expand",
            "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs",
            "sv_paged_attention_workspace", "sv_paged_attention", "sv_kv_evict_workspace",
-           "sv_kv_evict")
+           "sv_kv_evict", "sv_token_logprobs", "sv_distill_loss", "sv_distill_grad")
 
 
 class SvError(RuntimeError):
@@ -114,6 +115,15 @@ def load_library(path: str = LIB_PATH):
     L.sv_kv_evict.argtypes = ([vp, i64, i64, i64, i32, vp, vp, vp, vp] + [i32] * 11 +
                               [vp, vp, vp, vp, sz, vp])
     L.sv_kv_evict.restype = i32
+    L.sv_token_logprobs.argtypes = ([vp, i64, i64, i32, vp, vp] + [i32] * 5 +
+                                    [f32, vp, vp, vp, vp, vp, vp])
+    L.sv_token_logprobs.restype = i32
+    L.sv_distill_loss.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, i32, f32, i32, vp, vp, vp,
+                                  i64, vp, vp]
+    L.sv_distill_loss.restype = i32
+    L.sv_distill_grad.argtypes = [vp, i64, i32, vp, vp, vp, vp, i32, i32, i32, f32, i32, vp, i64,
+                                  vp, vp]
+    L.sv_distill_grad.restype = i32
     L.sv_last_error.argtypes = []
     L.sv_last_error.restype = C.c_char_p
     L.sv_launch_count.argtypes = []
@@ -485,6 +495,101 @@ def _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sink
         _stream(stream)))
 
 
+_ROW_DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
+
+
+def _row_dtype(t):
+    dt = _ROW_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported logit dtype {t.dtype}")
+    return dt
+
+
+def sv_token_logprobs(logits, rows, tokens, temperature, out_logprob, out_entropy, out_top_token,
+                      out_top_logprob, out_status, stream=None):
+    """logits [B][T][V]; rows and tokens int32 [B][P] or None; out_logprob,
+    out_entropy, out_status [B][P]; out_top_token, out_top_logprob [B][P][K] or
+    None."""
+    B, P = out_entropy.shape
+    K = 0 if out_top_token is None else out_top_token.shape[2]
+    _want("out_entropy", out_entropy, torch.float32, (B, P))
+    _want("out_status", out_status, torch.int32, (B, P))
+    if tokens is not None:
+        _want("out_logprob", out_logprob, torch.float32, (B, P))
+    if K:
+        _want("out_top_token", out_top_token, torch.int32, (B, P, K))
+        _want("out_top_logprob", out_top_logprob, torch.float32, (B, P, K))
+    return _token_logprobs(logits, rows, tokens, P, K, temperature, out_logprob, out_entropy,
+                           out_top_token, out_top_logprob, out_status, stream)
+
+
+def _token_logprobs(logits, rows, tokens, P, K, temperature, out_logprob, out_entropy,
+                    out_top_token, out_top_logprob, out_status, stream):
+    if logits.dim() != 3:
+        raise ValueError(f"logits: need [B, T, V], got {tuple(logits.shape)}")
+    B, T, V = logits.shape
+    dt = _row_dtype(logits)
+    seq, row = _row_strides("logits", logits, logits.dtype, (B, T, V))
+    for name, t in (("rows", rows), ("tokens", tokens)):
+        if t is not None:
+            _want(name, t, torch.int32, (B, P))
+    return _check(load_library().sv_token_logprobs(
+        _p(logits), seq, row, dt, _p(rows), _p(tokens), B, T, P, V, K, float(temperature),
+        _p(out_logprob) if tokens is not None else None, _p(out_entropy),
+        _p(out_top_token) if K else None, _p(out_top_logprob) if K else None, _p(out_status),
+        _stream(stream)))
+
+
+def _distill_args(logits, teacher_token, teacher_logprob, weight):
+    if logits.dim() != 2:
+        raise ValueError(f"logits: need [R, V], got {tuple(logits.shape)}")
+    R, V = logits.shape
+    _, row = _row_strides("logits", logits[None], logits.dtype, (1, R, V))
+    K = teacher_token.shape[-1]
+    _want("teacher_token", teacher_token, torch.int32, (R, K))
+    _want("teacher_logprob", teacher_logprob, torch.float32, (R, K))
+    if weight is not None:
+        _want("weight", weight, torch.float32, (R,))
+    return R, V, K, row
+
+
+def _grad_stride(out_grad, logits):
+    if out_grad is None:
+        return 0
+    if out_grad.dim() != 2:
+        raise ValueError(f"out_grad: need [R, V], got {tuple(out_grad.shape)}")
+    _, row = _row_strides("out_grad", out_grad[None], logits.dtype, (1, *logits.shape))
+    return row
+
+
+def sv_distill_loss(logits, teacher_token, teacher_logprob, weight, temperature, tail, out_loss,
+                    out_stat, out_grad, out_status, stream=None):
+    """logits [R][V]; teacher_token, teacher_logprob [R][K]; weight [R] or None;
+    out_loss, out_status [R]; out_stat [R][4] or None; out_grad like logits or
+    None."""
+    R, V, K, row = _distill_args(logits, teacher_token, teacher_logprob, weight)
+    _want("out_loss", out_loss, torch.float32, (R,))
+    _want("out_status", out_status, torch.int32, (R,))
+    if out_stat is not None:
+        _want("out_stat", out_stat, torch.float32, (R, 4))
+    return _check(load_library().sv_distill_loss(
+        _p(logits), row, _row_dtype(logits), _p(teacher_token), _p(teacher_logprob), _p(weight),
+        R, V, K, float(temperature), 1 if tail else 0, _p(out_loss), _p(out_stat), _p(out_grad),
+        _grad_stride(out_grad, logits), _p(out_status), _stream(stream)))
+
+
+def sv_distill_grad(logits, teacher_token, teacher_logprob, stat, weight, temperature, tail,
+                    out_grad, out_status, stream=None):
+    """As sv_distill_loss; stat [R][4] is its out_stat."""
+    R, V, K, row = _distill_args(logits, teacher_token, teacher_logprob, weight)
+    _want("stat", stat, torch.float32, (R, 4))
+    _want("out_status", out_status, torch.int32, (R,))
+    return _check(load_library().sv_distill_grad(
+        _p(logits), row, _row_dtype(logits), _p(teacher_token), _p(teacher_logprob), _p(stat),
+        _p(weight), R, V, K, float(temperature), 1 if tail else 0, _p(out_grad),
+        _grad_stride(out_grad, logits), _p(out_status), _stream(stream)))
+
+
 def sv_last_error():
     return load_library().sv_last_error().decode()
 
@@ -633,6 +738,76 @@ def kv_evict(kv, block_table, seq_len, weight_sum, budget, sinks=0, recent=0, ou
               weight_sum if out_weight_sum is None else out_weight_sum, budget, sinks, recent,
               kept, kv_len, status, workspace, stream)
     return kept, kv_len, status
+
+
+def token_logprobs(logits, tokens=None, rows=None, top_k=0, temperature=1.0, stream=None):
+    """Log probabilities of given tokens, entropy and the top_k most likely
+    alternatives (see sv_token_logprobs): logits [B][T][V] in fp32, bf16 or fp16,
+    rows padded, sliced or broadcast as they come; tokens int32 [B][P] (-1: none)
+    or None; rows int32 [B][P], the row each entry looks at (-1: none), or None:
+    row i for entry i.  After a round: tokens = its tokens, for a tree rows = its
+    path.  Returns a dict of tensors: logprob [B][P] (with tokens), entropy
+    [B][P], top_token and top_logprob [B][P][top_k] (with top_k), status [B][P]."""
+    B, T, _ = logits.shape
+    given = tokens if tokens is not None else rows
+    P = T if given is None else given.shape[-1]
+    K = _int32("top_k", top_k)
+    if K < 0:
+        raise ValueError(f"top_k: {K}")
+    dev = _out_dev(logits)
+    out = {}
+    with _allocating(stream):
+        if tokens is not None:
+            out["logprob"] = torch.empty(B, P, dtype=torch.float32, device=dev)
+        out["entropy"] = torch.empty(B, P, dtype=torch.float32, device=dev)
+        if K:
+            out["top_token"] = torch.empty(B, P, K, dtype=torch.int32, device=dev)
+            out["top_logprob"] = torch.empty(B, P, K, dtype=torch.float32, device=dev)
+        out["status"] = torch.empty(B, P, dtype=torch.int32, device=dev)
+    _token_logprobs(logits, rows, tokens, P, K, temperature, out.get("logprob"), out["entropy"],
+                    out.get("top_token"), out.get("top_logprob"), out["status"], stream)
+    return out
+
+
+def distill_loss(logits, teacher_token, teacher_logprob, weight=None, temperature=1.0, tail=True,
+                 grad=False, out_grad=None, stream=None):
+    """The loss of a draft's logits [R][V] (fp32, bf16, fp16) against a teacher's
+    most likely tokens [R][K] and their log probabilities (see sv_distill_loss;
+    token_logprobs gives both).  With ``grad`` (or out_grad, which may be logits
+    itself) its gradient times weight fp32 [R] too, for
+    ``logits.backward(r["grad"])``; without, ``stat`` is what distill_grad needs
+    for it later.  Returns a dict of tensors: loss [R], stat [R][4], grad (if
+    asked), status [R]."""
+    R = logits.shape[0]
+    dev = _out_dev(logits)
+    out = {}
+    with _allocating(stream):
+        out["loss"] = torch.empty(R, dtype=torch.float32, device=dev)
+        out["stat"] = torch.empty(R, 4, dtype=torch.float32, device=dev)
+        out["status"] = torch.empty(R, dtype=torch.int32, device=dev)
+        if grad and out_grad is None:
+            out_grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    if out_grad is not None:
+        out["grad"] = out_grad
+    sv_distill_loss(logits, teacher_token, teacher_logprob, weight, temperature, tail, out["loss"],
+                    out["stat"], out_grad, out["status"], stream)
+    return out
+
+
+def distill_grad(logits, teacher_token, teacher_logprob, stat, weight=None, temperature=1.0,
+                 tail=True, out_grad=None, stream=None):
+    """The gradient of distill_loss times weight fp32 [R], from the ``stat`` it
+    returned for the same logits and teacher (see sv_distill_grad).  Returns the
+    gradient [R][V] of logits' type (out_grad, which may be logits itself) and
+    the status words [R]."""
+    dev = _out_dev(logits)
+    with _allocating(stream):
+        if out_grad is None:
+            out_grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        status = torch.empty(logits.shape[0], dtype=torch.int32, device=dev)
+    sv_distill_grad(logits, teacher_token, teacher_logprob, stat, weight, temperature, tail,
+                    out_grad, status, stream)
+    return out_grad, status
 
 
 def tree_expand(dlogits, frontier_score, K, temperature=1.0, stream=None):
