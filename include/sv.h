@@ -526,6 +526,46 @@ sv_status sv_paged_attention(const void *q, const void *kv, int64_t kv_stride,
                              void *stream);
 
 /* ---------------------------------------------------------------------------
+ * sv_prefix_attention -- sv_paged_attention for a batch whose sequences share
+ * long prefixes: many candidates of one prompt (samples, drafts verified apart,
+ * users of one system prompt), each prefix read once for all of its sequences.
+ *
+ * B = N W: sequences n W .. n W + W - 1 share prefix n.  Sequence b attends to
+ * all slots of prefix b / W and to its own, in that order as it were one cache:
+ * slot j of prefix n is row j % page of page prefix_table[n][j / page], j <
+ * prefix_len[n]; slot j of its own is row j % page of page block_table[b][j /
+ * page], j < seq_len[b] (the new token's own row among them; 0: none yet).  So a
+ * prefix may end inside a page, and a sequence's own slots start with a page.
+ *
+ *   q, kv, kv_stride, page_stride, dt, scale, out, out_lse, out_status as for
+ *         sv_paged_attention (one pool of pages for both tables); D 64 or 128
+ *   prefix_table int32 [N][max_prefix_pages]; prefix_len int32 [N]
+ *   block_table  int32 [B][max_pages]; seq_len int32 [B]
+ * Rows without a visible slot give 0 and lse -inf.  Pages that hold no visible
+ * slot are never read, and what their table entries hold is not looked at.  A
+ * length out of range (SV_ROW_BAD_LEN) or a needed page outside [0, num_pages)
+ * (SV_ROW_BAD_PAGE) gives NaN rows: of the sequence, or of all that share the
+ * prefix.  The outputs overlap no input.  Weights of a prefix are rounded to dt
+ * where they multiply the values (2^-8 or 2^-11 of each weight); sums are held in
+ * 32 bits, unnormalised as in sv_paged_attention.
+ *
+ * Work is split by the lengths found on the device: one captured launch serves
+ * growing prefixes and sequences.  The workspace is written before it is read;
+ * calls that may overlap need one each.  Results do not depend on scheduling.
+ * Waits on the device are bounded (2 s); one that runs out, which a working
+ * device never does, sets SV_ROW_TIMEOUT.
+ * --------------------------------------------------------------------------- */
+size_t sv_prefix_attention_workspace(int B, int N, int Hq, int Hkv, int D, int page,
+                                     int max_prefix_pages, int max_pages);
+sv_status sv_prefix_attention(const void *q, const void *kv, int64_t kv_stride,
+                              int64_t page_stride, sv_dtype dt, const int32_t *prefix_table,
+                              const int32_t *prefix_len, const int32_t *block_table,
+                              const int32_t *seq_len, int B, int N, int Hq, int Hkv, int D,
+                              int page, int max_prefix_pages, int max_pages, int num_pages,
+                              float scale, void *out, float *out_lse, uint32_t *out_status,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * sv_kv_evict -- bring a paged KV cache back under a budget by the attention
  * its slots received.  [Lesson] "Reversão de KV cache" (a physical cache with a
  * logical length); the pages leave the choice of the rows open.

@@ -34,7 +34,8 @@ EXPORTS = ("sv_verify_chain_workspace", "sv_verify_chain_workspace_host", "sv_ve
            "sv_launch_count", "sv_trace_enable", "sv_trace_collect", "sv_tree_expand",
            "sv_tree_select", "sv_tree_finalize", "sv_tree_level", "sv_verify_chain_probs",
            "sv_paged_attention_workspace", "sv_paged_attention", "sv_kv_evict_workspace",
-           "sv_kv_evict", "sv_token_logprobs", "sv_distill_loss", "sv_distill_grad")
+           "sv_kv_evict", "sv_token_logprobs", "sv_distill_loss", "sv_distill_grad",
+           "sv_prefix_attention_workspace", "sv_prefix_attention")
 
 
 class SvError(RuntimeError):
@@ -110,6 +111,11 @@ def load_library(path: str = LIB_PATH):
     L.sv_paged_attention.argtypes = ([vp, vp, i64, i64, i32, vp, vp] + [i32] * 9 +
                                      [f32, vp, i32, vp, vp, vp, vp, sz, vp])
     L.sv_paged_attention.restype = i32
+    L.sv_prefix_attention_workspace.argtypes = [i32] * 8
+    L.sv_prefix_attention_workspace.restype = sz
+    L.sv_prefix_attention.argtypes = ([vp, vp, i64, i64, i32, vp, vp, vp, vp] + [i32] * 9 +
+                                      [f32, vp, vp, vp, vp, sz, vp])
+    L.sv_prefix_attention.restype = i32
     L.sv_kv_evict_workspace.argtypes = [i32] * 4
     L.sv_kv_evict_workspace.restype = sz
     L.sv_kv_evict.argtypes = ([vp, i64, i64, i64, i32, vp, vp, vp, vp] + [i32] * 11 +
@@ -453,6 +459,57 @@ def _paged_attention(q, kv, block_table, seq_len, window, sinks, scale, weight_s
         _stream(stream)))
 
 
+def sv_prefix_attention_workspace(B, N, Hq, Hkv, D, page, max_prefix_pages, max_pages):
+    return int(load_library().sv_prefix_attention_workspace(
+        *[_int32("size", x) for x in (B, N, Hq, Hkv, D, page, max_prefix_pages, max_pages)]))
+
+
+def sv_prefix_attention(q, kv, prefix_table, prefix_len, block_table, seq_len, scale, out,
+                        out_lse=None, out_status=None, workspace=None, stream=None):
+    """q [B][Hq][D]; kv [2][pages][page][Hkv][D] as for sv_paged_attention;
+    prefix_table [N][max_prefix_pages], prefix_len [N], block_table
+    [B][max_pages], seq_len [B]."""
+    B, Hq, D = q.shape
+    _want("out", out, q.dtype, (B, Hq, D))
+    if out_lse is not None:
+        _want("out_lse", out_lse, torch.float32, (B, Hq))
+    if out_status is not None:
+        _want("out_status", out_status, torch.int32, (B,))
+    return _prefix_attention(q, kv, prefix_table, prefix_len, block_table, seq_len, scale, out,
+                             out_lse, out_status, workspace, stream)
+
+
+def _prefix_attention(q, kv, prefix_table, prefix_len, block_table, seq_len, scale, out, out_lse,
+                      out_status, workspace, stream):
+    B, Hq, D = q.shape
+    kv_stride, page_stride = _pages(kv, 0)
+    P, page, Hkv, Dk = kv.shape[1:]
+    if kv.dtype != q.dtype or Dk != D:
+        raise ValueError(f"kv: {kv.dtype} rows of {Dk}, q has {q.dtype} rows of {D}")
+    dt = _CACHE_DTYPES.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported cache dtype {q.dtype}")
+    N = prefix_len.shape[0] if prefix_len.dim() == 1 else 0
+    if N < 1 or B % N:
+        raise ValueError(f"prefix_len: {B} sequences do not share {N} prefixes evenly")
+    max_prefix = prefix_table.shape[1] if prefix_table.dim() == 2 else 0
+    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    i32 = torch.int32
+    _want("q", q, q.dtype, (B, Hq, D))
+    _want("prefix_table", prefix_table, i32, (N, max_prefix))
+    _want("prefix_len", prefix_len, i32, (N,))
+    _want("block_table", block_table, i32, (B, max_pages))
+    _want("seq_len", seq_len, i32, (B,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor")
+    return _check(load_library().sv_prefix_attention(
+        _p(q), _p(kv), kv_stride, page_stride, dt, _p(prefix_table), _p(prefix_len),
+        _p(block_table), _p(seq_len), B, N, Hq, Hkv, D, page, max_prefix, max_pages, P,
+        float(scale), _p(out), _p(out_lse), _p(out_status), _p(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
 def sv_kv_evict_workspace(L, B, Hkv, budget):
     return int(load_library().sv_kv_evict_workspace(
         *[_int32("size", x) for x in (L, B, Hkv, budget)]))
@@ -714,6 +771,31 @@ def paged_attention(q, kv, block_table, seq_len, scale=None, window=0, sinks=0, 
     _paged_attention(q, kv, block_table, seq_len, window, sinks,
                      D ** -0.5 if scale is None else scale, weight_sum, out, lse, status,
                      workspace, stream)
+    return (out, lse, status) if return_lse else out
+
+
+def prefix_attention(q, kv, prefix_table, prefix_len, block_table, seq_len, scale=None,
+                     return_lse=False, workspace=None, stream=None):
+    """paged_attention for a batch whose sequences share prefixes (see
+    sv_prefix_attention): the B sequences of q [B][Hq][D] are N groups of B / N
+    neighbours; group n attends to prefix_len[n] slots by prefix_table int32
+    [N][max_prefix_pages], read once for all of it, and each sequence to its own
+    seq_len[b] slots by block_table int32 [B][max_pages]; kv
+    [2][pages][page][Hkv][D] holds both.  scale defaults to 1/sqrt(D).  Returns
+    out (like q), and with return_lse the log-sum-exp [B][Hq] and the status
+    words [B]."""
+    B, Hq, D = q.shape
+    dev = _out_dev(q)
+    with _allocating(stream):
+        out = torch.empty(B, Hq, D, dtype=q.dtype, device=dev)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
+        status = torch.empty(B, dtype=torch.int32, device=dev) if return_lse else None
+        if workspace is None and kv.dim() == 5 and prefix_table.dim() == block_table.dim() == 2:
+            workspace = _ws(sv_prefix_attention_workspace(
+                B, prefix_table.shape[0], Hq, kv.shape[3], D, kv.shape[2], prefix_table.shape[1],
+                block_table.shape[1]), dev)
+    _prefix_attention(q, kv, prefix_table, prefix_len, block_table, seq_len,
+                      D ** -0.5 if scale is None else scale, out, lse, status, workspace, stream)
     return (out, lse, status) if return_lse else out
 
 

@@ -15,7 +15,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsv.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["runtime.cu", "verify.cu", "tree_kv.cu", "tree_build.cu", "tree_attn.cu",
-           "verify_probs.cu", "paged_attn.cu", "kv_evict.cu", "token_logprobs.cu", "distill.cu"]
+           "verify_probs.cu", "paged_attn.cu", "kv_evict.cu", "token_logprobs.cu", "distill.cu",
+           "prefix_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,6 +47,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 namespace sv {
 namespace {
@@ -93,6 +94,10 @@ struct PagedArgs {
   void *out;
   float *lse;
   uint32_t *status;
+  // in place of out and lse, where another call joins the rows with its own
+  // (paged.cuh): the unnormalised sums, references and sums of exponentials
+  float *sum_o;
+  float2 *sum_ml;
   // workspace
   int4 *w_map;       // [groups]: sequence (or -1), unit within it, its units, its length
   int2 *w_first;     // [B]: index of the sequence's first group, its units
@@ -770,7 +775,10 @@ __global__ void __launch_bounds__(kThreads, SHARING && D == 64 ? 4 : 0) paged_at
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         sum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2_approx(s_m[w][r] - M);
-      if (whole) {
+      if (whole && a.sum_o) {
+        *(float2 *)(a.sum_o + ((size_t)b * a.Hq + head0 + r) * D + c) = make_float2(x, y);
+        if (c == 0) a.sum_ml[(size_t)b * a.Hq + head0 + r] = make_float2(M, sum);
+      } else if (whole) {
         const float nan = __int_as_float(0x7fffffff);
         const float inv = 1.0f / sum;
         x = flag ? nan : sum == 0.0f ? 0.0f : x * inv;
@@ -866,6 +874,10 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
       const size_t row = (size_t)b * a.Hq + head0 + r;
       const float inv = 1.0f / ml.y;
       auto put = [&](int c, float x, float y) {
+        if (a.sum_o) {
+          *(float2 *)(a.sum_o + row * D + c) = make_float2(x, y);
+          return;
+        }
         x = flag ? nan : ml.y == 0.0f ? 0.0f : x * inv;
         y = flag ? nan : ml.y == 0.0f ? 0.0f : y * inv;
         *(uint32_t *)((T *)a.out + row * D + c) = Pair<T>::pack(x, y);
@@ -889,6 +901,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
         for (int e = 0; e < E; e += 2) put(e * 32 + lane * 2, acc[e], acc[e + 1]);
       }
       if (lane == 0 && (!wide || warp == 0)) {
+        if (a.sum_o) a.sum_ml[row] = ml;
         if (a.lse) a.lse[row] = flag ? nan : ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
         if (h == 0 && r == 0 && a.status) a.status[b] = flag;
       }
@@ -1086,7 +1099,84 @@ bool bad_shape(int B, int Hq, int Hkv, int D, int page, int max_pages, int windo
          sinks < 0;
 }
 
+// Fills in the arguments, all of them checked, and launches.
+sv_status enqueue(const Sizes &z, const void *q, const void *kv, int64_t kv_stride, int64_t page_stride, sv_dtype dt,
+                  const int32_t *block_table, const int32_t *seq_len, int B, int Hq, int Hkv, int D, int page,
+                  int max_pages, int num_pages, int window, int sinks, float scale, float *weight_sum, int S, void *out,
+                  float *out_lse, uint32_t *out_status, float *sum_o, float2 *sum_ml, void *workspace,
+                  cudaStream_t st) {
+  PagedArgs a;
+  a.q = q;
+  a.kv = kv;
+  a.kv_stride = kv_stride;
+  a.page_stride = page_stride;
+  a.table = block_table;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = z.G;
+  a.gt = z.gt;
+  a.NH = z.NH;
+  a.page = page;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page == 1 << i) a.page_shift = i;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.window = window;
+  a.sinks = sinks;
+  a.cap = z.cap;
+  a.units = units_for(D, B, z.NH);
+  a.scale_log2 = scale * kLog2e;
+  a.rows = z.rows;
+  a.vis_max = z.vis_max;
+  a.weight_sum = weight_sum;
+  a.S = S;
+  a.out = out;
+  a.lse = out_lse;
+  a.status = out_status;
+  a.sum_o = sum_o;
+  a.sum_ml = sum_ml;
+  char *w = (char *)workspace;
+  const bool split = z.finding != kWhole, wt = weight_sum != nullptr;
+  a.groups = (int)z.groups;
+  a.finding = z.finding;
+  a.w_map = z.finding == kMap ? (int4 *)(w + z.map) : nullptr;
+  a.w_first = z.finding == kMap ? (int2 *)(w + z.first) : nullptr;
+  a.w_o = split ? (float *)(w + z.o) : nullptr;
+  a.w_ml = split || wt ? (float2 *)(w + z.ml) : nullptr;
+  a.w_flag = split || wt ? (uint32_t *)(w + z.flag) : nullptr;
+  a.w_score = wt ? (float *)(w + z.score) : nullptr;
+  if (dt == SV_BF16)
+    return D == 64    ? run<__nv_bfloat16, 64>(a, z, wt, st)
+           : D == 128 ? run<__nv_bfloat16, 128>(a, z, wt, st)
+                      : run<__nv_bfloat16, 256>(a, z, wt, st);
+  return D == 64    ? run<__half, 64>(a, z, wt, st)
+         : D == 128 ? run<__half, 128>(a, z, wt, st)
+                    : run<__half, 256>(a, z, wt, st);
+}
+
 }  // namespace
+
+bool paged_sums_workspace(size_t *bytes, int B, int Hq, int Hkv, int D, int page, int max_pages) {
+  Sizes z;
+  if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, 0, 0, 0)) return false;
+  *bytes = z.total;
+  return true;
+}
+
+sv_status paged_sums(const void *q, const void *kv, int64_t kv_stride, int64_t page_stride, sv_dtype dt,
+                     const int32_t *block_table, const int32_t *seq_len, int B, int Hq, int Hkv, int D, int page,
+                     int max_pages, int num_pages, float scale, float *o, float2 *ml, uint32_t *flags, void *workspace,
+                     cudaStream_t st) {
+  Sizes z;
+  if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, 0, 0, 0))
+    return set_error(SV_ERR_UNSUPPORTED, "more than 2^30 slots a sequence, or too many work units");
+  return enqueue(z, q, kv, kv_stride, page_stride, dt, block_table, seq_len, B, Hq, Hkv, D, page, max_pages, num_pages,
+                 0, 0, scale, nullptr, 0, nullptr, nullptr, flags, o, ml, workspace, st);
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -1148,53 +1238,7 @@ extern "C" sv_status sv_paged_attention(const void *q, const void *kv, int64_t k
       (s = map_arg(out_lse, "out_lse")) != SV_OK || (s = map_arg(out_status, "out_status")) != SV_OK ||
       (s = map_arg(workspace, "workspace")) != SV_OK)
     return s;
-  PagedArgs a;
-  a.q = q;
-  a.kv = kv;
-  a.kv_stride = kv_stride;
-  a.page_stride = page_stride;
-  a.table = block_table;
-  a.seq_len = seq_len;
-  a.B = B;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.G = z.G;
-  a.gt = z.gt;
-  a.NH = z.NH;
-  a.page = page;
-  a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (page == 1 << i) a.page_shift = i;
-  a.max_pages = max_pages;
-  a.num_pages = num_pages;
-  a.window = window;
-  a.sinks = sinks;
-  a.cap = z.cap;
-  a.units = units_for(D, B, z.NH);
-  a.scale_log2 = scale * kLog2e;
-  a.rows = z.rows;
-  a.vis_max = z.vis_max;
-  a.weight_sum = weight_sum;
-  a.S = S;
-  a.out = out;
-  a.lse = out_lse;
-  a.status = out_status;
-  char *w = (char *)workspace;
-  const bool split = z.finding != kWhole, wt = weight_sum != nullptr;
-  a.groups = (int)z.groups;
-  a.finding = z.finding;
-  a.w_map = z.finding == kMap ? (int4 *)(w + z.map) : nullptr;
-  a.w_first = z.finding == kMap ? (int2 *)(w + z.first) : nullptr;
-  a.w_o = split ? (float *)(w + z.o) : nullptr;
-  a.w_ml = split || wt ? (float2 *)(w + z.ml) : nullptr;
-  a.w_flag = split || wt ? (uint32_t *)(w + z.flag) : nullptr;
-  a.w_score = wt ? (float *)(w + z.score) : nullptr;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (dt == SV_BF16)
-    return D == 64    ? run<__nv_bfloat16, 64>(a, z, wt, st)
-           : D == 128 ? run<__nv_bfloat16, 128>(a, z, wt, st)
-                      : run<__nv_bfloat16, 256>(a, z, wt, st);
-  return D == 64    ? run<__half, 64>(a, z, wt, st)
-         : D == 128 ? run<__half, 128>(a, z, wt, st)
-                    : run<__half, 256>(a, z, wt, st);
+  return enqueue(z, q, kv, kv_stride, page_stride, dt, block_table, seq_len, B, Hq, Hkv, D, page, max_pages, num_pages,
+                 window, sinks, scale, weight_sum, S, out, out_lse, out_status, nullptr, nullptr, workspace,
+                 (cudaStream_t)stream);
 }

@@ -139,3 +139,78 @@ def test_binding_refusals(sv):
         sv.sv_distill_grad(stat=torch.zeros(4, 3), **ok)
     with pytest.raises(ValueError):
         sv.sv_distill_loss(out_loss=torch.zeros(5), out_stat=None, **ok)
+
+
+def test_prefix_attention_pin():
+    """Torch's dense attention over the two parts of each sequence, laid out as
+    one; with the parts of another sequence it differs."""
+    g = torch.Generator().manual_seed(3)
+    page, Hkv, G, D = 4, 2, 3, 8
+    q = torch.randn(4, Hkv * G, D, generator=g, dtype=torch.float64)
+    kv = torch.randn(2, 12, page, Hkv, D, generator=g, dtype=torch.float64)
+    pt, pl = np.array([[3, 7, 0], [5, 1, -1]]), np.array([11, 8])
+    t, n = np.array([[2], [4], [6], [8]]), np.array([1, 4, 0, 3])
+    out, lse, st = plain.prefix_attention(q.numpy(), kv.numpy(), pt, pl, t, n, 0.5)
+    assert not st.any()
+    for b in range(4):
+        rows = [(pt[b // 2][j // page], j % page) for j in range(pl[b // 2])]
+        rows += [(t[b][j // page], j % page) for j in range(n[b])]
+        i, r = torch.tensor([x for x, _ in rows]), torch.tensor([x for _, x in rows])
+        k, v = kv[0, i, r].transpose(0, 1), kv[1, i, r].transpose(0, 1)
+        want = torch.nn.functional.scaled_dot_product_attention(
+            q[b].view(Hkv, G, D), k, v, scale=0.5).reshape(Hkv * G, D)
+        assert np.abs(out[b] - want.numpy()).max() < 1e-12
+        x = torch.einsum("hgd,hjd->hgj", q[b].view(Hkv, G, D), k) * 0.5
+        assert np.abs(lse[b] - torch.logsumexp(x, -1).reshape(-1).numpy()).max() < 1e-12
+    assert np.abs(out - plain.prefix_attention(q.numpy(), kv.numpy(), pt[::-1], pl[::-1], t, n, 0.5)[0]).max() > 0.01
+    st = plain.prefix_attention(q.numpy(), kv.numpy(), pt, np.array([13, 9]), t, n, 0.5)[2]
+    assert st.tolist() == [plain.BAD_LEN] * 2 + [plain.BAD_PAGE] * 2
+
+
+def test_prefix_attention_refusals(sv):
+    lib, x = sv.load_library(), 4096
+    need = sv.sv_prefix_attention_workspace(6, 2, 8, 2, 128, 16, 4, 3)
+    assert need > 0
+
+    def call(q=x, kv=x, ks=1 << 20, ps=16 * 2 * 128, dt=1, pt=x, pl=x, t=x, n=x, B=6, N=2, Hq=8, Hkv=2, D=128, page=16,
+             mp=4, m=3, P=40, scale=0.1, out=x, lse=x, st=x, ws=x, wb=need):
+        return lib.sv_prefix_attention(q, kv, ks, ps, dt, pt, pl, t, n, B, N, Hq, Hkv, D, page, mp, m, P, scale, out,
+                                       lse, st, ws, wb, None)
+    for bad in (dict(B=-2), dict(N=0), dict(N=4), dict(Hq=7), dict(Hkv=0), dict(D=0), dict(page=0), dict(mp=0),
+                dict(m=0), dict(P=0), dict(dt=0), dict(scale=0.0), dict(scale=math.inf), dict(scale=math.nan),
+                dict(ps=16 * 2 * 128 - 8), dict(ps=16 * 2 * 128 + 1), dict(ks=0), dict(ks=12), dict(ks=2 ** 62),
+                dict(ps=2 ** 62), dict(q=None), dict(kv=None), dict(pt=None), dict(pl=None), dict(t=None),
+                dict(n=None), dict(out=None), dict(ws=None), dict(q=x + 8), dict(kv=x + 8), dict(out=x + 8),
+                dict(pt=x + 2), dict(pl=x + 2), dict(t=x + 1), dict(n=x + 2), dict(lse=x + 2), dict(st=x + 2),
+                dict(ws=x + 64), dict(wb=need - 1)):
+        assert call(**bad) == 1, bad
+    for far in (dict(D=256, ps=16 * 2 * 256), dict(mp=1 << 27), dict(m=1 << 27), dict(B=1 << 26, N=1 << 26)):
+        assert call(**far) == 2, far
+    assert call(B=0, q=None) == 0
+    assert call() == 1 and b"q" in lib.sv_last_error()
+    size = sv.sv_prefix_attention_workspace
+    for bad in ((6, 4, 8, 2, 128, 16, 4, 3), (0, 2, 8, 2, 128, 16, 4, 3), (6, 0, 8, 2, 128, 16, 4, 3),
+                (6, 2, 7, 2, 128, 16, 4, 3)):
+        assert size(*bad) == 0
+    with pytest.raises(ValueError, match="32 bits"):
+        size(6, 2, 8, 2, 128, 16, 2 ** 32 + 4, 3)
+    # rows that are not there are not stored: 4 rows to a part, not 128
+    assert size(1, 1, 4, 1, 128, 16, 4, 3) * 16 < size(32, 1, 4, 1, 128, 16, 4, 3)
+
+
+def test_prefix_attention_binding_refusals(sv):
+    bf, i32 = torch.bfloat16, torch.int32
+    q, kv = torch.zeros(6, 8, 64, dtype=bf), torch.zeros(2, 9, 16, 2, 64, dtype=bf)
+    ok = dict(q=q, kv=kv, prefix_table=torch.zeros(2, 3, dtype=i32), prefix_len=torch.zeros(2, dtype=i32),
+              block_table=torch.zeros(6, 2, dtype=i32), seq_len=torch.zeros(6, dtype=i32), scale=1.0,
+              out=torch.zeros_like(q))
+    for bad in (dict(q=q.float()), dict(kv=kv.half()), dict(kv=kv[..., :32]), dict(kv=kv[0]),
+                dict(kv=kv.transpose(2, 3)), dict(prefix_len=torch.zeros(4, dtype=i32)),
+                dict(prefix_len=torch.zeros(0, dtype=i32)), dict(prefix_len=torch.zeros(2)),
+                dict(prefix_table=torch.zeros(3, 3, dtype=i32)), dict(prefix_table=torch.zeros(6, dtype=i32)),
+                dict(block_table=torch.zeros(5, 2, dtype=i32)), dict(block_table=torch.zeros(6, 2)),
+                dict(seq_len=torch.zeros(6, 1, dtype=i32)), dict(out=q.float()), dict(out=q[:5]),
+                dict(out_lse=torch.zeros(6, 7)), dict(out_status=torch.zeros(6)),
+                dict(workspace=torch.zeros(8, 8)[:, ::2]), dict()):   # the last: pageable host memory
+        with pytest.raises(ValueError):
+            sv.sv_prefix_attention(**{**ok, **bad})
