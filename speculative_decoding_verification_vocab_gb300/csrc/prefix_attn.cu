@@ -14,21 +14,23 @@
 // Bound: a slot of a prefix is 4 D bytes a KV head and 4 D W G operations: memory
 // up to some 280 rows, above the tensor cores and the softmax's exponentials.
 //
-// Work: segments, one for each prefix, KV head and tile of 128 query rows (row r =
-// sequence r / G, head r % G), lie one after the other as a row of 128-key tiles,
-// and each CTA, one to an SM, takes an equal share of it, from one segment to the
-// next: parts of a segment, whose sums go to the workspace.  Shares are cut from
-// the lengths on the device, so a captured launch follows growing prefixes.
+// Work: segments, one for each prefix, KV head and pair of 128-row query tiles (row
+// r = sequence r / G, head r % G), lie one after the other as a row of 128-key
+// tiles, and each CTA, one to an SM, takes an equal share of it, from one segment
+// to the next: parts of a segment, whose sums go to the workspace.  Shares are cut
+// from the lengths on the device, so a captured launch follows growing prefixes.
+// A CTA works on two S buffers in turn, so that the tensor cores have one while
+// the softmax is at the other: those of the pair's two query tiles with the same
+// keys or, where a segment has one query tile only, those of even and odd key
+// tiles, which the join puts together like any two parts.
 //   warps 0-1   producer: page table entries a tile ahead, K and V rows by
 //               asynchronous copies of 16 bytes into a ring (rows of 128-byte
 //               swizzled boxes of 64 columns; pages may end anywhere in a tile);
 //               rows past the end are zeros;
-//   warp 2      MMA issuer: S_j = Q K_j^T once S_{j-1} has been read out of tensor
-//               memory, O += P_j V_j once P_j is there; A operands (Q, P) in
-//               tensor memory;
-//   warps 3-10  softmax: query rows to tensor memory, S_j to registers (a row over
-//               a quad of threads), the running maximum with a lazy rescale of O,
-//               P_j as 16-bit values to one of two buffers; at a segment's end O,
+//   warp 2      MMA issuer: S = Q K^T from shared memory, O += P V with P in tensor
+//               memory, in the place of the S it comes from;
+//   warps 3-10  softmax, four to a buffer, a row to a thread: the running maximum
+//               with a lazy rescale of O, P as 16-bit values; at a segment's end O,
 //               m and l to the workspace.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
 // with SV_ROW_TIMEOUT.
@@ -42,16 +44,17 @@
 namespace sv {
 namespace {
 
-constexpr int kRows = 128;   // query rows of a segment = tensor-memory lanes
+constexpr int kRows = 128;   // query rows of a tile = tensor-memory lanes
 constexpr int kKeys = 128;   // keys of a tile
 constexpr int kProducers = 64;
-constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = kProducers / 32, kFirstSoftmax = kMmaWarp + 1;
-constexpr int kThreads = kProducers + 32 + 32 * kSoftmaxWarps;
+// 11 warps: registers are given out to four warps at a time, and the softmax needs
+// more than the 128 that 13 to 16 leave a thread
+constexpr int kThreads = kProducers + 32 + 256;
 constexpr uint32_t kBox = kKeys * 128;  // bytes of a box of 64 columns
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.4426950408889634f;
-// tensor-memory columns: S, O, Q and two buffers of P (16-bit pairs)
-constexpr uint32_t kColS = 0, kColO = 128, kColQ = 256, kColP = 320, kTmemCols = 512;
+// tensor-memory columns: two S (P, 16-bit pairs, in their first halves), two O
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
 // A score moves the reference only when it is more than kSlack above it (log2
 // units).  Weights go into the product as 16-bit numbers: in fp16 the reference
@@ -74,16 +77,15 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 }
 
 template <int D> struct Ring {
-  static constexpr uint32_t kTileBytes = kKeys * D * 2;  // K or V rows of a tile
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr uint32_t kOffBar = kStages * 2 * kTileBytes;
-  static constexpr uint32_t kOffRows = kOffBar + 32 * 8;         // two tiles' row offsets
-  static constexpr uint32_t kOffMisc = kOffRows + 2 * kKeys * 8;
+  static constexpr uint32_t kTileBytes = kKeys * D * 2;  // K or V rows of a key tile, or a query tile
+  static constexpr int kPlaces = D == 128 ? 5 : 11;      // K, V, K, V, ...
+  static constexpr uint32_t kOffQ = kPlaces * kTileBytes;
+  static constexpr uint32_t kOffBar = kOffQ + 2 * kTileBytes;
+  static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
   static constexpr size_t kSmem = kOffMisc + 128 + 1024;  // + alignment
-  // barriers: stage filled and free; Q there; S there and read out; P there and
-  // its product done, by parity
-  static constexpr int kFull = 0, kFree = kStages, kQ = 2 * kStages, kS = kQ + 1, kSF = kS + 1, kP = kSF + 1,
-                       kPV = kP + 2, kCount = kPV + 2;
+  // barriers: a place filled and free; by buffer: Q there, S there, P there, PV done
+  static constexpr int kFull = 0, kFree = kPlaces, kQ = 2 * kPlaces, kS = kQ + 2, kP = kS + 2, kPV = kP + 2,
+                       kCount = kPV + 2;
   static_assert(kCount <= 32, "barriers");
 };
 
@@ -91,12 +93,12 @@ struct PrefixArgs {
   const void *q, *kv;
   int64_t kv_stride, page_stride;
   const int32_t *table, *len;  // [N][max_pages], [N]
-  int B, N, W, Hq, Hkv, G, mtiles, HM;  // HM = Hkv mtiles segments to a prefix
+  int B, N, W, Hq, Hkv, G, mtiles, pairs;  // query tiles of a KV head, and pairs of them
   int page, page_shift, max_pages, num_pages, cap;
-  int ctas, rows;  // rows of a part: min(128, W G)
+  int ctas, rows;  // rows of a part's buffer: min(128, W G)
   float scale_log2;
-  // workspace: sums [parts][rows][D], references and sums of exponentials
-  // [parts][rows], status bits [parts]
+  // workspace: sums [parts][2][rows][D], references and sums of exponentials
+  // [parts][2][rows], status bits [parts]
   float *w_o;
   float2 *w_ml;
   uint32_t *w_flag;
@@ -121,63 +123,117 @@ __device__ __forceinline__ longlong2 count_tiles(const PrefixArgs &a, int p) {
   return n;
 }
 
-// CTAs that share so many tiles: none without one
-__device__ __forceinline__ long long sharing(const PrefixArgs &a, long long all) {
-  return min((long long)a.ctas, max(all, 1LL));
+// The work of the batch in units, one for each key tile and query tile: a tile of
+// a pair counts 2.  CTAs that share so many units: two and more to each, so that
+// every share has the beginning of a tile of each segment that it runs through.
+__device__ __forceinline__ long long sharing(const PrefixArgs &a, long long units) {
+  return min((long long)a.ctas, max(units / 2, 1LL));
 }
 
-// A CTA's way through its share: the part of a segment it is at.  Part index:
-// CTA + segment, of which from part to part one or the other grows.
+// A CTA's way through its share: the part of a segment it is at, tiles [t0, t1),
+// those that begin in the share.  Part index: CTA + segment, of which from part to
+// part one or the other grows.
 struct Walk {
-  long long at, end, first;  // tiles in the row of all; the first of prefix p's segments
-  int p, hm, t0, t1, len;
+  long long at, end, first;  // units; the first of prefix p's segments
+  int p, head, pr, pair, t0, t1, len;  // pair: two query tiles, 2 pr and 2 pr + 1
   __device__ __forceinline__ bool next(const PrefixArgs &a) {
-    for (;;) {
-      if (at >= end || p >= a.N) return false;
+    while (at < end && p < a.N) {
       len = __ldcg(a.len + p);
       const int tiles = tiles_of(a, len);
-      const long long block = (long long)a.HM * tiles;
-      if (at < first + block) {
-        hm = (int)((at - first) / tiles);
-        t0 = (int)((at - first) % tiles);
-        t1 = (int)min((long long)tiles, t0 + (end - at));
-        at += t1 - t0;
-        return true;
+      const long long of_head = (long long)tiles * a.mtiles, block = of_head * a.Hkv;
+      if (at >= first + block) {
+        first += block;
+        ++p;
+        continue;
       }
-      first += block;
-      ++p;
+      head = (int)((at - first) / of_head);
+      const long long head0 = first + head * of_head, v = at - head0;
+      pr = (int)(v / (2 * tiles));
+      pair = 2 * pr + 1 < a.mtiles;
+      const long long seg0 = head0 + (long long)pr * 2 * tiles, to = min(end, seg0 + (tiles << pair));
+      t0 = (int)(at - seg0 + pair) >> pair;
+      t1 = (int)(to - seg0 + pair) >> pair;
+      at = to;
+      if (t1 > t0) return true;
     }
+    return false;
   }
+  __device__ __forceinline__ size_t part(const PrefixArgs &a) const {
+    return (size_t)blockIdx.x + ((size_t)p * a.Hkv + head) * a.pairs + pr;
+  }
+  // tiles of buffer s, and the i-th of them
+  __device__ __forceinline__ int tiles_for(int s) const { return pair ? t1 - t0 : (t1 - t0 + 1 - s) >> 1; }
+  __device__ __forceinline__ int tile(int s, int i) const { return pair ? t0 + i : t0 + 2 * i + s; }
 };
+
+// D = A B with both operands in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 consecutive columns of this thread's tensor-memory lane; the values are there
+// after tm_wait_ld
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// (the registers pass through, so that nothing reads them before the wait)
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) {
   using R = Ring<D>;
-  constexpr int kStages = R::kStages;
+  constexpr int kPlaces = R::kPlaces;
   constexpr uint32_t kTileBytes = R::kTileBytes;
+  const unsigned FULL = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t *bars = (uint64_t *)(sm + R::kOffBar);
-  long long *s_row = (long long *)(sm + R::kOffRows);  // [2][kKeys]
   uint32_t *tmem_slot = (uint32_t *)(sm + R::kOffMisc);
   volatile int *abort = (volatile int *)(sm + R::kOffMisc + 4);
   Walk *s_walk = (Walk *)(sm + R::kOffMisc + 8);
-  volatile uint8_t *s_bad = sm + R::kOffMisc + 8 + sizeof(Walk);  // [kStages][2], by producer warp
-  static_assert(8 + sizeof(Walk) + kStages * 2 <= 128, "misc");
+  static_assert(8 + sizeof(Walk) <= 128, "misc");
   const uint32_t bar0 = smem_addr(bars), sm0 = smem_addr(sm);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(R::kFull + s), kProducers / 32);
-      mbar_init(bar(R::kFree + s), 1);
+    for (int i = 0; i < kPlaces; ++i) {
+      mbar_init(bar(R::kFull + i), kProducers);
+      mbar_init(bar(R::kFree + i), 1);
     }
-    mbar_init(bar(R::kQ), kSoftmaxWarps);
-    mbar_init(bar(R::kS), 1);
-    mbar_init(bar(R::kSF), kSoftmaxWarps);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(R::kP + s), kSoftmaxWarps);
+      mbar_init(bar(R::kQ + s), 4);
+      mbar_init(bar(R::kS + s), 1);
+      mbar_init(bar(R::kP + s), 4);
       mbar_init(bar(R::kPV + s), 1);
     }
     *abort = 0;
@@ -191,31 +247,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
   }
   grid_dep_sync();
   if (warp == 0) {
-    // this CTA's share of all tiles, and the prefix it starts in
-    const long long all = (long long)a.HM * count_tiles(a, 0).x;
+    // this CTA's share of all units, and the prefix it starts in
+    const long long per = (long long)a.Hkv * a.mtiles, all = per * count_tiles(a, 0).x, ctas = sharing(a, all);
     Walk w;
-    const long long ctas = sharing(a, all);
     w.at = min((long long)blockIdx.x, ctas) * all / ctas;
     w.end = min((long long)blockIdx.x + 1, ctas) * all / ctas;
     w.first = 0;
     w.p = 0;
     for (int p0 = 0; p0 < a.N && w.at < w.end; p0 += 32) {
       const int p = p0 + lane;
-      const long long n = p < a.N ? (long long)a.HM * tiles_of(a, __ldcg(a.len + p)) : 0;
+      const long long n = p < a.N ? per * tiles_of(a, __ldcg(a.len + p)) : 0;
       long long incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        const long long x = __shfl_up_sync(FULL, incl, o);
         if (lane >= o) incl += x;
       }
-      const unsigned past = __ballot_sync(0xffffffffu, w.first + incl > w.at);
+      const unsigned past = __ballot_sync(FULL, w.first + incl > w.at);
       if (past) {
         const int l = __ffs(past) - 1;
         w.p = p0 + l;
-        w.first += __shfl_sync(0xffffffffu, incl - n, l);
+        w.first += __shfl_sync(FULL, incl - n, l);
         break;
       }
-      w.first += __shfl_sync(0xffffffffu, incl, 31);
+      w.first += __shfl_sync(FULL, incl, 31);
     }
     if (lane == 0) *s_walk = w;
   }
@@ -224,325 +279,297 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk w = *s_walk;
+  auto all = [&](bool x) { return __all_sync(FULL, x) != 0; };
 
   if (warp < kMmaWarp) {
     // ------------------------------------------------------------ producer
-    // Thread t finds rows t and t + 64 of a tile, one tile ahead; 16 bytes of a
-    // row to a lane, CPR lanes to a row.
-    constexpr int CPR = D / 8, RPI = kProducers / CPR;  // rows of one round of copies
-    const int lr = threadIdx.x / CPR, lc = threadIdx.x % CPR;
+    // Warp w fills rows 64 w to 64 w + 63 of every tile: lane l looks rows l and l +
+    // 32 of them up, one tile ahead; CPR lanes copy a row, 16 bytes each.  A place is
+    // full when the copies of all producers into it have arrived.
+    constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows of one round of copies
+    const int lr = lane / CPR, lc = lane % CPR;
     const int64_t row_elems = (int64_t)a.Hkv * D;
-    int g = 0;  // tiles so far
+    int g = 0;  // places filled so far
     bool ok = true;
-    // a barrier of the producer warps, with their votes: they go on or end together
-    auto producers_all = [](bool x) {
-      uint32_t r;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-          : "=r"(r)
-          : "r"((uint32_t)x), "n"(kProducers)
-          : "memory");
-      return r != 0;
-    };
-    auto finish = [&](int t) {  // tile t is in shared memory: this warp's share of it
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(R::kFull + t % kStages));
-    };
-    while (ok && w.next(a)) {
-      const T *kv = (const T *)a.kv + (int64_t)(w.hm / a.mtiles) * D + lc * 8;
+    while (w.next(a)) {
+      bool bad = false;
+      const T *kv = (const T *)a.kv + (int64_t)w.head * D + lc * 8;
       const int32_t *table = a.table + (size_t)w.p * a.max_pages;
+      auto slot_of = [&](int t, int e) { return t * kKeys + warp * 64 + e * 32 + lane; };
       int id[2];
       auto fetch = [&](int t) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int slot = t * kKeys + (int)threadIdx.x + e * kProducers;
+          const int slot = slot_of(t, e);
           id[e] = t < w.t1 && slot < w.len ? __ldg(table + (a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page)) : -1;
         }
       };
       fetch(w.t0);
-      for (int t = w.t0; t < w.t1; ++t, ++g) {
-        const int st = g % kStages;
-        long long *rows = s_row + (g & 1) * kKeys;
-        bool bad = false;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        long long off[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = (int)threadIdx.x + e * kProducers, slot = t * kKeys + r;
-          long long off = -1;
+          const int slot = slot_of(t, e);
+          off[e] = -1;
           if (slot < w.len) {
             if ((unsigned)id[e] < (unsigned)a.num_pages) {
               const int in_page = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
-              off = id[e] * (long long)a.page_stride + in_page * (long long)row_elems;
+              off[e] = id[e] * (long long)a.page_stride + in_page * (long long)row_elems;
             } else {
               bad = true;
             }
           }
-          rows[r] = off;
         }
-        bad = __any_sync(0xffffffffu, bad);
         fetch(t + 1);
-        // the stage's last tile has been multiplied; both warps' rows are there
-        ok = g < kStages || mbar_wait(bar(R::kFree + st), (g / kStages - 1) & 1, abort);
-        ok = producers_all(ok);
-        if (!ok) break;
-        if (lane == 0) s_bad[st * 2 + warp] = bad;
-        const uint32_t dst = sm0 + st * 2 * kTileBytes + (lc >> 3) * kBox + lr * 128;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {  // K, V
-#pragma unroll 4
-          for (int r = 0; r < kKeys; r += RPI) {
-            const long long off = rows[r + lr];
-            const uint32_t n = off >= 0 ? 16u : 0u;
-            const T *src = kv + (off >= 0 ? off : 0) + part * a.kv_stride;
-            const uint32_t d = dst + part * kTileBytes + r * 128 + (((lc & 7) ^ ((r + lr) & 7)) << 4);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+        for (int part = 0; part < 2; ++part, ++g) {  // K, V
+          const int at = g % kPlaces;
+          ok = all(g < kPlaces || mbar_wait(bar(R::kFree + at), (g / kPlaces - 1) & 1, abort));
+          if (!ok) break;
+          const T *from = kv + part * a.kv_stride;
+          const uint32_t dst = sm0 + at * kTileBytes + (lc >> 3) * kBox + (warp * 64 + lr) * 128;
+#pragma unroll 8
+          for (int i = 0; i < 64 / RPI; ++i) {
+            const long long o = __shfl_sync(FULL, i < 32 / RPI ? off[0] : off[1], (i * RPI + lr) & 31);
+            const uint32_t d = dst + i * RPI * 128 + (((lc & 7) ^ ((i * RPI + lr) & 7)) << 4);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from + (o >= 0 ? o : 0)),
+                         "r"(o >= 0 ? 16u : 0u)
+                         : "memory");
           }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (g > 0) {  // the tile before has arrived
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          finish(g - 1);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(R::kFull + at)) : "memory");
         }
       }
+      // the part's status: a barrier of the producers with their votes, which they
+      // all come to, whatever became of their waits
+      uint32_t some;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+          : "=r"(some)
+          : "r"((uint32_t)bad), "n"(kProducers)
+          : "memory");
+      if (threadIdx.x == 0) a.w_flag[w.part(a)] = some ? SV_ROW_BAD_PAGE : 0u;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok && g > 0) finish(g - 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA
-    // The warp runs converged and elect.sync picks the issuing lane.  gS and gP
-    // count the S and PV tiles of the CTA.
+    // A segment's products as a row of items, buffers in turn: S of the first two,
+    // then, item by item, O += P V and the S two items on, into the place of P.  The
+    // warp runs converged and elect.sync picks the issuing lane.
     constexpr uint32_t kIdesc = (1u << 4) | (kAbType<T> << 7) | (kAbType<T> << 10) | ((uint32_t)(kRows >> 4) << 24);
     constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kKeys >> 3) << 17);
     constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: head dim contiguous
-    int gS = 0, gP = 0, nq = 0;
+    constexpr uint64_t kStep = kTileBytes >> 4;
+    const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0, kBox, 1024), dQ0 = sdesc(sm0 + R::kOffQ, 16, 1024);
+    int base = 0;                // tiles of the parts before
+    int nq[2] = {0, 0}, done[2] = {0, 0};  // query tiles and PV products of each buffer
+    int ns[2] = {0, 0};            // S products
     bool ok = true;
-    const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0 + kTileBytes, kBox, 1024);
-    constexpr uint64_t kStageStep = 2 * kTileBytes >> 4;
-    auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-    auto issue_s = [&]() {  // S_gS: its K has landed, S_{gS - 1} is read out
-      ok = all((gS < 1 || mbar_wait(bar(R::kSF), (gS - 1) & 1, abort)) &&
-               mbar_wait(bar(R::kFull + gS % kStages), (gS / kStages) & 1, abort));
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t dk = dK0 + (gS % kStages) * kStageStep;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ts(tmem + kColS, tmem + kColQ + ks * 8, dk + (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4), kIdescS,
-                 ks > 0);
-        mma_commit(bar(R::kS));
-      }
-      __syncwarp();
-      ++gS;
+    auto landed = [&](int g) {  // the copies were made by the generic proxy
+      const bool r = all(mbar_wait(bar(R::kFull + g % kPlaces), (g / kPlaces) & 1, abort));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      return r;
     };
     while (ok && w.next(a)) {
-      ok = all(mbar_wait(bar(R::kQ), nq & 1, abort));
-      ++nq;
+      const int n = w.t1 - w.t0, items = n << w.pair;
+      for (int s = 0; ok && s < 2 && s < items; ++s) ok = all(mbar_wait(bar(R::kQ + s), nq[s]++ & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      issue_s();
-      const int n = w.t1 - w.t0;
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) issue_s();
-        if (!ok) break;
-        ok = all(mbar_wait(bar(R::kP + (gP & 1)), (gP >> 1) & 1, abort));
-        if (!ok) break;
+      auto issue_s = [&](int k) {
+        const int s = k & 1, tile = base + (w.pair ? k >> 1 : k), g = 2 * tile;
+        // its K has landed; the product that read P there is done
+        ok = landed(g) && all(done[s] == 0 || mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, abort));
+        if (!ok) return;
         tc_fence_after();
-        const int st = gP % kStages;
         if (elect_one()) {
-          const uint64_t dv = dV0 + st * kStageStep;
-          const uint32_t pa = tmem + kColP + (gP & 1) * 64;
+          const uint64_t dk = dK0 + (g % kPlaces) * kStep, dq = dQ0 + s * kStep;
 #pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            mma_ts(tmem + kColO, pa + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
-          mma_commit(bar(R::kPV + (gP & 1)));
-          mma_commit(bar(R::kFree + st));
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t at = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
+            mma_ss(tmem + kColS + s * 128, dq + at, dk + at, kIdescS, ks > 0);
+          }
+          mma_commit(bar(R::kS + s));
+          if (!w.pair || s == 1) mma_commit(bar(R::kFree + g % kPlaces));
         }
         __syncwarp();
-        ++gP;
+        ++ns[s];
+      };
+      for (int k = 0; ok && k < 2 && k < items; ++k) issue_s(k);
+      for (int k = 0; ok && k < items; ++k) {
+        const int s = k & 1, tile = base + (w.pair ? k >> 1 : k), g = 2 * tile + 1;
+        ok = landed(g) && all(mbar_wait(bar(R::kP + s), done[s] & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dv = dV0 + (g % kPlaces) * kStep;
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            mma_ts(tmem + kColO + s * D, tmem + kColS + s * 128 + ks * 8, dv + (uint64_t)(ks * 128), kIdescO,
+                   (k > 1 || ks > 0) ? 1u : 0u);
+          mma_commit(bar(R::kPV + s));
+          if (!w.pair || s == 1) mma_commit(bar(R::kFree + g % kPlaces));
+        }
+        __syncwarp();
+        ++done[s];
+        if (k + 2 < items) issue_s(k + 2);
       }
+      base += n;
     }
     if (!ok) {
-      // products in flight end before tensor memory is released: the last S and
-      // the last PV are the newest phases of their barriers
+      // products in flight end before tensor memory is released: the newest phases
+      // of the barriers that the last ones commit to
       volatile int no_abort = 0;
-      if (gS > 0) mbar_wait(bar(R::kS), (gS - 1) & 1, &no_abort);
-      if (gP > 0) mbar_wait(bar(R::kPV + ((gP - 1) & 1)), ((gP - 1) >> 1) & 1, &no_abort);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (ns[s]) mbar_wait(bar(R::kS + s), (ns[s] - 1) & 1, &no_abort);
+        if (done[s]) mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, &no_abort);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
-    // A warp reads the tensor-memory lanes of quarter warp % 4; the two warps of a
-    // quarter take 16 lanes each.  Thread t holds rows t / 4 and t / 4 + 8 of them
-    // and in every 8 columns the pair 2 (t % 4): row maxima and sums are two
-    // shuffles, and P's pair column 4 c + t % 4 is the thread's own.
-    const int quarter = warp & 3, half = (warp - kFirstSoftmax) >> 2, q4 = lane & 3;
-    const uint32_t lane16 = (uint32_t)(quarter * 32 + half * 16) << 16;
-    const int rowA = quarter * 32 + half * 16 + (lane >> 2);  // and rowA + 8
-    int gT = 0;
+    // Four warps to a buffer; a thread has the query row of its tensor-memory lane.
+    const int s = (warp - kFirstSoftmax) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + lanes + kColS + s * 128, tO = tmem + lanes + kColO + s * D;
+    int g = 0;  // tiles of this buffer so far
     bool ok = true;
-    auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-    auto wait_pv = [&](int i) { return all(mbar_wait(bar(R::kPV + (i & 1)), (i >> 1) & 1, abort)); };
     while (ok && w.next(a)) {
-      const int mt = w.hm % a.mtiles, hkv = w.hm / a.mtiles, n = w.t1 - w.t0;
+      const int mt = w.pair ? 2 * w.pr + s : 2 * w.pr, n = w.tiles_for(s);
       const int rows = min(kRows, a.W * a.G - mt * kRows);
-      {
-        // this warp's columns (a half of the head for D = 128) of the quarter's 32
-        // rows to tensor memory, a lane a row; rows behind the last are zeros
-        const int r = quarter * 32 + lane;
-        if (D == 128 || half == 0) {
-          uint32_t qv[32];
-          const int at = mt * kRows + r;
-          const uint4 *src = (const uint4 *)((const T *)a.q + ((size_t)((size_t)w.p * a.W + at / a.G) * a.Hq +
-                                                               (size_t)hkv * a.G + at % a.G) * D + half * 64);
+      if (n > 0) {
+        // This row of the query tile; rows behind the last are zeros.  (A buffer
+        // without a tile takes no query: nothing would hold its warps back until
+        // the last one had been seen.)
+        const int at = mt * kRows + row;
+        const uint4 *src = (const uint4 *)((const T *)a.q +
+                                           (((size_t)w.p * a.W + at / a.G) * a.Hq + (size_t)w.head * a.G + at % a.G) * D);
+        uint8_t *dst = sm + R::kOffQ + s * kTileBytes + row * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = r < rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            qv[4 * c] = x.x;
-            qv[4 * c + 1] = x.y;
-            qv[4 * c + 2] = x.z;
-            qv[4 * c + 3] = x.w;
-          }
-          tm_st32u(tmem + ((uint32_t)(quarter * 32) << 16) + kColQ + 32 * half, qv);
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        }
+        for (int c = 0; c < D / 8; ++c)
+          *(uint4 *)(dst + (c >> 3) * kBox + (((c & 7) ^ (row & 7)) << 4)) =
+              row < rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(R::kQ));
+        if (lane == 0) mbar_arrive(bar(R::kQ + s));
       }
-      float m_ref[2] = {-INFINITY, -INFINITY};  // log2 units
-      float l[2] = {0.0f, 0.0f};                // of this thread's columns
-      uint32_t bad = 0;
-      for (int j = 0; j < n; ++j) {
-        const int g = gT + j, pb = g & 1;
-        ok = all(mbar_wait(bar(R::kS), g & 1, abort));
+      float m_ref = -INFINITY;  // log2 units
+      unsigned long long l2[2] = {0ull, 0ull};
+      for (int i = 0; i < n; ++i, ++g) {
+        ok = all(mbar_wait(bar(R::kS + s), g & 1, abort));
         if (!ok) break;
         tc_fence_after();
-        // s[4 c + 0, 1]: row A, keys 8 c + 2 q4 + {0, 1}; s[4 c + 2, 3]: row B
-        float s[64];
-        tm_ld16x256_x8(tmem + lane16 + kColS, s);
-        tm_ld16x256_x8(tmem + lane16 + kColS + 64, s + 32);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(R::kSF));
-        bad |= s_bad[g % kStages * 2] | s_bad[g % kStages * 2 + 1];
-        const int left = w.len - (w.t0 + j) * kKeys;  // keys of this tile
-        if (left < kKeys) {
+        const int left = w.len - w.tile(s, i) * kKeys;  // keys of this tile
+        uint32_t x[4][32];
+        auto mask = [&](int c) {
+          if (left < kKeys) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (8 * c + 2 * q4 + e >= left) s[4 * c + e] = s[4 * c + 2 + e] = -INFINITY;
-        }
-        float factor[2], mneg[2];
-        bool any_grow = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float pm[4] = {s[2 * e], s[2 * e + 1], s[4 + 2 * e], s[4 + 2 * e + 1]};
-#pragma unroll
-          for (int c = 2; c < 16; c += 2) {
-            pm[0] = fmaxf(pm[0], s[4 * c + 2 * e]);
-            pm[1] = fmaxf(pm[1], s[4 * c + 2 * e + 1]);
-            pm[2] = fmaxf(pm[2], s[4 * c + 4 + 2 * e]);
-            pm[3] = fmaxf(pm[3], s[4 * c + 4 + 2 * e + 1]);
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= left) x[c][e] = 0xff800000u;
           }
-          float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx *= a.scale_log2;  // > 0: the maximum commutes with it
-          const bool grow = mx > m_ref[e] + (kSlack<T> + kBias<T>);
-          const float m_new = grow ? mx - kBias<T> : m_ref[e];
-          factor[e] = grow && m_ref[e] != -INFINITY ? ex2(m_ref[e] - m_new) : 1.0f;
-          any_grow |= factor[e] != 1.0f;
-          l[e] *= factor[e];
-          m_ref[e] = m_new;
-          mneg[e] = m_new == -INFINITY ? 0.0f : -m_new;
-        }
-        uint32_t pk[32];
-        unsigned long long la2 = 0ull, lb2 = 0ull;
-        const unsigned long long sc2 = f2_splat(a.scale_log2);
-        const unsigned long long ma2 = f2_splat(mneg[0]), mb2 = f2_splat(mneg[1]);
+        };
+        auto most = [&](int c) {
+          float v[4];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const unsigned long long pa = ex2_2(f2_fma(f2_pack(s[4 * c], s[4 * c + 1]), sc2, ma2));
-          const unsigned long long pb2 = ex2_2(f2_fma(f2_pack(s[4 * c + 2], s[4 * c + 3]), sc2, mb2));
-          la2 = f2_add(la2, pa);
-          lb2 = f2_add(lb2, pb2);
-          float p0, p1, p2, p3;
-          f2_unpack(pa, p0, p1);
-          f2_unpack(pb2, p2, p3);
-          pk[2 * c] = pack2<T>(p0, p1);      // row A, pair column 4 c + q4
-          pk[2 * c + 1] = pack2<T>(p2, p3);  // row B
-        }
-        {
-          float u0, u1, v0, v1;
-          f2_unpack(la2, u0, u1);
-          f2_unpack(lb2, v0, v1);
-          l[0] += u0 + u1;
-          l[1] += v0 + v1;
-        }
-        if (g >= 2) {  // P buffer pb is free
-          ok = wait_pv(g - 2);
-          if (!ok) break;
-        }
-        if (__any_sync(0xffffffffu, any_grow)) {
-          // bring these rows of O, once it covers the tiles before, to the new
-          // reference (at j = 0 there is none: no factor differs from 1)
-          ok = wait_pv(g - 1);
-          if (!ok) break;
-          tc_fence_after();
+          for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[c][e]);
 #pragma unroll
-          for (int c = 0; c < D; c += 64) {
-            float o[32];
-            tm_ld16x256_x8(tmem + lane16 + kColO + c, o);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          for (int e = 4; e < 32; ++e) v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[c][e]));
+          return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        };
+        // the second half for its maximum, then the first, which stays: P's columns
+        // take the place of S's in that order
+        tm_ld32(tS + 64, x[2]);
+        tm_ld32(tS + 96, x[3]);
+        tm_wait_ld(x[2]);
+        tm_wait_ld(x[3]);
+        tm_ld32(tS, x[0]);
+        tm_ld32(tS + 32, x[1]);
+        mask(2);
+        mask(3);
+        float mx = fmaxf(most(2), most(3));
+        tm_wait_ld(x[0]);
+        tm_wait_ld(x[1]);
+        mask(0);
+        mask(1);
+        mx = fmaxf(mx, fmaxf(most(0), most(1))) * a.scale_log2;  // > 0: the maximum commutes with it
+        const bool grow = mx > m_ref + (kSlack<T> + kBias<T>);
+        const float m_new = grow ? mx - kBias<T> : m_ref;
+        const float factor = grow && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.0f;
+        m_ref = m_new;
+        if (__any_sync(FULL, factor != 1.0f)) {
+          // O covers the tiles before: S was issued after their products
+          l2[0] = f2_mul(l2[0], f2_splat(factor));
+          l2[1] = f2_mul(l2[1], f2_splat(factor));
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tm_ld32(tO + c, o);
+            tm_wait_ld(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= factor[(k >> 1) & 1];
-            tm_st16x256_x8(tmem + lane16 + kColO + c, o);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+            tm_st32u(tO + c, o);
           }
         }
-        tm_st16x128_x16(tmem + lane16 + kColP + pb * 64, pk);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        const unsigned long long sc2 = f2_splat(a.scale_log2), mn2 = f2_splat(m_ref == -INFINITY ? 0.0f : -m_ref);
+        auto weights = [&](int c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const unsigned long long y =
+                ex2_2(f2_fma(f2_pack(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, mn2));
+            l2[e & 1] = f2_add(l2[e & 1], y);
+            float y0, y1;
+            f2_unpack(y, y0, y1);
+            p[e] = pack2<T>(y0, y1);
+          }
+          tm_st16(tS + 16 * c, p);
+        };
+        weights(0);
+        tm_ld32(tS + 64, x[2]);
+        weights(1);
+        tm_wait_ld(x[2]);
+        tm_ld32(tS + 96, x[3]);
+        mask(2);
+        weights(2);
+        tm_wait_ld(x[3]);
+        mask(3);
+        weights(3);
+        tm_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(R::kP + pb));
+        if (lane == 0) mbar_arrive(bar(R::kP + s));
       }
       if (!ok) break;
-      ok = wait_pv(gT + n - 1);
-      if (!ok) break;
-      tc_fence_after();
-      const size_t part = (size_t)blockIdx.x + (size_t)w.p * a.HM + w.hm;
+      const size_t at = (w.part(a) * 2 + s) * a.rows + row;
+      if (n > 0) {
+        ok = all(mbar_wait(bar(R::kPV + s), (g - 1) & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tm_ld32(tO + c, o);
+          tm_wait_ld(o);
+          if (row < rows) {
+            uint4 *dst = (uint4 *)(a.w_o + at * D + c);
 #pragma unroll
-      for (int c = 0; c < D; c += 64) {
-        float o[32];
-        tm_ld16x256_x8(tmem + lane16 + kColO + c, o);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        // o[4 k + 0, 1]: row A, columns c + 8 k + 2 q4 + {0, 1}; o[4 k + 2, 3]: row B
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (rowA + 8 * e >= rows) continue;
-          float *dst = a.w_o + (part * a.rows + rowA + 8 * e) * D + c + 2 * q4;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) *(float2 *)(dst + 8 * k) = make_float2(o[4 * k + 2 * e], o[4 * k + 2 * e + 1]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
         }
+        tc_fence_before();
       }
-      tc_fence_before();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l[e];
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        if (q4 == 0 && rowA + 8 * e < rows) a.w_ml[part * a.rows + rowA + 8 * e] = make_float2(m_ref[e], v);
+      if (row < rows) {
+        float l0, l1, l3, l4;
+        f2_unpack(l2[0], l0, l1);
+        f2_unpack(l2[1], l3, l4);
+        a.w_ml[at] = make_float2(m_ref, (l0 + l1) + (l3 + l4));
       }
-      if (warp == kFirstSoftmax && lane == 0) a.w_flag[part] = bad ? SV_ROW_BAD_PAGE : 0u;
-      gT += n;
     }
   }
   tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 0) {
     Walk again = *s_walk;
-    while (again.next(a)) a.w_flag[(size_t)blockIdx.x + (size_t)again.p * a.HM + again.hm] = SV_ROW_TIMEOUT;
+    while (again.next(a)) a.w_flag[again.part(a)] = SV_ROW_TIMEOUT;
   }
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -568,7 +595,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   const bool live = row < (long long)a.B * a.Hq;
   const int b = live ? (int)(row / a.Hq) : 0, h = live ? (int)(row % a.Hq) : 0;
   const int p = b / a.W, at = b % a.W * a.G + h % a.G;
-  const int hm = h / a.G * a.mtiles + at / kRows, r = at % kRows;
+  const int mt = at / kRows, r = at % kRows, pr = mt / 2, pair = 2 * pr + 1 < a.mtiles;
   // lengths were there before the launches that this one waits for
   const longlong2 n = count_tiles(a, p);
   const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
@@ -578,15 +605,20 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   const float2 own = j.own_ml[row];
   long long c0 = 0, c1 = -1;  // CTAs with a part
   if (tiles > 0) {
-    const long long all = n.x * a.HM, first = n.y * a.HM + (long long)hm * tiles, ctas = sharing(a, all);
+    const long long per = (long long)a.Hkv * a.mtiles, all = n.x * per, ctas = sharing(a, all);
+    const long long first = n.y * per + (long long)tiles * ((long long)(h / a.G) * a.mtiles + 2 * pr);
     c0 = ((first + 1) * ctas - 1) / all;
-    c1 = ((first + tiles) * ctas - 1) / all;
+    c1 = ((first + ((long long)(tiles - 1) << pair) + 1) * ctas - 1) / all;
   }
-  const size_t part0 = (size_t)p * a.HM + hm;
+  const size_t part0 = ((size_t)p * a.Hkv + h / a.G) * a.pairs + pr;
+  // places in the parts: that of the row's query tile in a pair, both otherwise
+  const int s0 = pair ? mt & 1 : 0, ns = pair ? 1 : 2;
+  const long long places = (c1 - c0 + 1) * ns;
+  auto place = [&](long long i) { return ((part0 + c0 + i / ns) * 2 + s0 + i % ns) * a.rows + r; };
   float M = own.x;
-  for (long long c = c0 + lane; c <= c1; c += 32) {
-    M = fmaxf(M, a.w_ml[(part0 + c) * a.rows + r].x);
-    flag |= a.w_flag[part0 + c];
+  for (long long i = lane; i < places; i += 32) {
+    M = fmaxf(M, a.w_ml[place(i)].x);
+    flag |= a.w_flag[part0 + c0 + i / ns];
   }
   M = warp_max(M);
   flag = __reduce_or_sync(0xffffffffu, flag);
@@ -607,9 +639,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   };
   take(j.own_o + row * D, own, false);
 #pragma unroll 4
-  for (long long c = c0; c <= c1; ++c) {
-    const size_t u = (part0 + c) * a.rows + r;
-    take(a.w_o + u * D, a.w_ml[u], true);
+  for (long long i = 0; i < places; ++i) {
+    const size_t u = place(i);
+    const float2 ml = a.w_ml[u];
+    // a buffer without a tile has no sums
+    if (ml.x != -INFINITY || ml.y != 0.0f) take(a.w_o + u * D, ml, true);
   }
   const float nan = __int_as_float(0x7fffffff), inv = 1.0f / sum;
   uint32_t *out = (uint32_t *)((T *)j.out + row * D);
@@ -626,27 +660,29 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
 
 // ------------------------------------------------------------------ host side
 struct Sizes {
-  int W, G, mtiles, HM, rows, ctas;
+  int W, G, mtiles, pairs, rows, ctas;
   size_t o, ml, flag, own_o, own_ml, own_flag, own, own_bytes, total;
 };
 bool sizes_of(Sizes &z, int B, int N, int Hq, int Hkv, int D, int page, int max_pages) {
   z.W = B / N;
   z.G = Hq / Hkv;
-  const long long wg = (long long)z.W * z.G, mtiles = (wg + kRows - 1) / kRows, HM = mtiles * Hkv;
-  if (wg > (1 << 24) || HM > (1 << 24) || HM * N > (1 << 24) || (long long)B * Hq > (1 << 26)) return false;
+  const long long wg = (long long)z.W * z.G, mtiles = (wg + kRows - 1) / kRows, segments = (mtiles + 1) / 2 * Hkv * N;
+  if (wg > (1 << 24) || Hkv > (1 << 24) || N > (1 << 24) || mtiles * Hkv > (1 << 24) || segments > (1 << 24) ||
+      (long long)B * Hq > (1 << 26))
+    return false;
   z.mtiles = (int)mtiles;
-  z.HM = (int)HM;
+  z.pairs = (int)(mtiles + 1) / 2;
   z.rows = wg < kRows ? (int)wg : kRows;
   z.ctas = 152;  // one to an SM of this part; the parts' places follow it
-  const size_t parts = (size_t)z.ctas + (size_t)N * z.HM;
+  const size_t parts = (size_t)z.ctas + (size_t)segments;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t r = at;
     at = align_up(at + n, 256);
     return r;
   };
-  z.o = take(parts * z.rows * D * 4);
-  z.ml = take(parts * z.rows * 8);
+  z.o = take(parts * 2 * z.rows * D * 4);
+  z.ml = take(parts * 2 * z.rows * 8);
   z.flag = take(parts * 4);
   z.own_o = take((size_t)B * Hq * D * 4);
   z.own_ml = take((size_t)B * Hq * 8);
@@ -769,7 +805,7 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   a.Hkv = Hkv;
   a.G = z.G;
   a.mtiles = z.mtiles;
-  a.HM = z.HM;
+  a.pairs = z.pairs;
   a.page = page;
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
