@@ -23,10 +23,13 @@
 // the softmax is at the other: those of the pair's two query tiles with the same
 // keys or, where a segment has one query tile only, those of even and odd key
 // tiles, which the join puts together like any two parts.
-//   warps 0-1   producer: page table entries a tile ahead, K and V rows by
-//               asynchronous copies of 16 bytes into a ring (rows of 128-byte
-//               swizzled boxes of 64 columns; pages may end anywhere in a tile);
-//               rows past the end are zeros;
+//   warps 0-1   producers, of K and of V: page table entries a tile ahead, TMA
+//               boxes of 64 columns of as many rows as divide the page (128-byte
+//               swizzled) into a ring; pages behind the last are out of the map's
+//               bounds and arrive as zeros.  Pages that four rows do not divide,
+//               and caches in host memory, go by asynchronous copies of 16 bytes
+//               (twice the time: a box is one instruction, and 32 copies are one
+//               for 512 bytes);
 //   warp 2      MMA issuer: S = Q K^T from shared memory, O += P V with P in tensor
 //               memory, in the place of the S it comes from;
 //   warps 3-10  softmax, four to a buffer, a row to a thread: the running maximum
@@ -95,6 +98,7 @@ struct PrefixArgs {
   const int32_t *table, *len;  // [N][max_pages], [N]
   int B, N, W, Hq, Hkv, G, mtiles, pairs;  // query tiles of a KV head, and pairs of them
   int page, page_shift, max_pages, num_pages, cap;
+  int box;  // rows of a TMA box
   int ctas, rows;  // rows of a part's buffer: min(128, W G)
   float scale_log2;
   // workspace: sums [parts][2][rows][D], references and sums of exponentials
@@ -166,6 +170,15 @@ struct Walk {
   __device__ __forceinline__ int tile(int s, int i) const { return pair ? t0 + i : t0 + 2 * i + s; }
 };
 
+// 5-D tiled TMA load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap *map, int x, int h, int r, int page, int kv,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(h), "r"(r), "r"(page), "r"(kv), "r"(bar)
+      : "memory");
+}
 // D = A B with both operands in shared memory
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -208,8 +221,9 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16])
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) {
+template <typename T, int D, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
   using R = Ring<D>;
   constexpr int kPlaces = R::kPlaces;
   constexpr uint32_t kTileBytes = R::kTileBytes;
@@ -221,13 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
   uint32_t *tmem_slot = (uint32_t *)(sm + R::kOffMisc);
   volatile int *abort = (volatile int *)(sm + R::kOffMisc + 4);
   Walk *s_walk = (Walk *)(sm + R::kOffMisc + 8);
-  static_assert(8 + sizeof(Walk) <= 128, "misc");
+  volatile int *s_filled = (volatile int *)(sm + R::kOffMisc + 8 + sizeof(Walk));  // tiles, by producer warp
+  static_assert(8 + sizeof(Walk) + 8 <= 128, "misc");
   const uint32_t bar0 = smem_addr(bars), sm0 = smem_addr(sm);
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPlaces; ++i) {
-      mbar_init(bar(R::kFull + i), kProducers);
+      mbar_init(bar(R::kFull + i), TMA ? 1 : kProducers);
       mbar_init(bar(R::kFree + i), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -281,7 +296,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
   Walk w = *s_walk;
   auto all = [&](bool x) { return __all_sync(FULL, x) != 0; };
 
-  if (warp < kMmaWarp) {
+  if (TMA && warp < kMmaWarp) {
+    // ------------------------------------------------------------ producers
+    // Warp 0 loads K, warp 1 V; a lane to each box of a tile.
+    const int boxes = kKeys / a.box;
+    int t_all = 0;  // tiles so far
+    bool ok = true;
+    while (w.next(a)) {
+      bool bad = false;
+      const int32_t *table = a.table + (size_t)w.p * a.max_pages;
+      auto fetch = [&](int t) {
+        const int slot = t * kKeys + lane * a.box;
+        return lane < boxes && t < w.t1 && slot < w.len
+                   ? __ldg(table + (a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page))
+                   : -1;
+      };
+      int id = fetch(w.t0);
+      for (int t = w.t0; ok && t < w.t1; ++t, ++t_all) {
+        const int slot = t * kKeys + lane * a.box, r = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
+        const bool there = (unsigned)id < (unsigned)a.num_pages;
+        bad |= lane < boxes && slot < w.len && !there;
+        const int page = there ? id : a.num_pages;  // out of bounds: zeros
+        id = fetch(t + 1);
+        const int g = 2 * t_all + warp, at = g % kPlaces;
+        ok = all(g < kPlaces || mbar_wait(bar(R::kFree + at), (g / kPlaces - 1) & 1, abort));
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(bar(R::kFull + at), kTileBytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t dst = sm0 + at * kTileBytes + lane * a.box * 128;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load5(dst + c * kBox, &map, c * 64, w.head, r, page, warp, bar(R::kFull + at));
+        }
+      }
+      if (warp == 0) {
+        bad = __any_sync(FULL, bad);
+        if (lane == 0) a.w_flag[w.part(a)] = bad ? SV_ROW_BAD_PAGE : 0u;
+      }
+    }
+    if (lane == 0) s_filled[warp] = t_all;
+  } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ producer
     // Warp w fills rows 64 w to 64 w + 63 of every tile: lane l looks rows l and l +
     // 32 of them up, one tile ahead; CPR lanes copy a row, 16 bytes each.  A place is
@@ -364,9 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
     int nq[2] = {0, 0}, done[2] = {0, 0};  // query tiles and PV products of each buffer
     int ns[2] = {0, 0};            // S products
     bool ok = true;
-    auto landed = [&](int g) {  // the copies were made by the generic proxy
+    auto landed = [&](int g) {
       const bool r = all(mbar_wait(bar(R::kFull + g % kPlaces), (g / kPlaces) & 1, abort));
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (!TMA) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the generic proxy's copies
       return r;
     };
     while (ok && w.next(a)) {
@@ -395,14 +450,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
       };
       for (int k = 0; ok && k < 2 && k < items; ++k) issue_s(k);
       for (int k = 0; ok && k < items; ++k) {
-        const int s = k & 1, tile = base + (w.pair ? k >> 1 : k), g = 2 * tile + 1;
+        const int s = k & 1, j = w.pair ? k >> 1 : k, g = 2 * (base + j) + 1;
         ok = landed(g) && all(mbar_wait(bar(R::kP + s), done[s] & 1, abort));
         if (!ok) break;
+        // The last tile's product takes the steps of 16 keys that hold one; a box
+        // may bring rows behind the last key, which may hold anything: zeros there,
+        // so that weights of 0 add 0.
+        const int left = w.len - (w.t0 + j) * kKeys, steps = left < kKeys ? (left + 15) >> 4 : kKeys / 16;
+        if (TMA && left < kKeys && (left & 15)) {
+          const int at = left + (lane >> 1);
+          if (at < 16 * steps) {
+            uint8_t *v = sm + (g % kPlaces) * kTileBytes + at * 128 + (lane & 1) * 64;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) *(uint4 *)(v + c * kBox + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
         tc_fence_after();
         if (elect_one()) {
           const uint64_t dv = dV0 + (g % kPlaces) * kStep;
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
+          for (int ks = 0; ks < steps; ++ks)
             mma_ts(tmem + kColO + s * D, tmem + kColS + s * 128 + ks * 8, dv + (uint64_t)(ks * 128), kIdescO,
                    (k > 1 || ks > 0) ? 1u : 0u);
           mma_commit(bar(R::kPV + s));
@@ -568,6 +638,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_attn_kernel(PrefixArgs a) 
   tc_fence_before();
   __syncthreads();
   if (*abort && threadIdx.x == 0) {
+    // every copy has landed before the CTA exits: the newest into each place (all
+    // have been waited for where no wait ran out)
+    if (TMA) {
+      volatile int no_abort = 0;
+      const int nk = s_filled[0], nv = s_filled[1], from = max(0, 2 * max(nk, nv) - 2 * kPlaces);
+      for (int i = 0; i < kPlaces; ++i) {
+        int newest = -1;
+        for (int g = from; g < 2 * max(nk, nv); ++g)
+          if (g % kPlaces == i && g / 2 < (g & 1 ? nv : nk)) newest = g;
+        if (newest >= 0) mbar_wait(bar(R::kFull + i), (newest / kPlaces) & 1, &no_abort);
+      }
+    }
     Walk again = *s_walk;
     while (again.next(a)) a.w_flag[again.part(a)] = SV_ROW_TIMEOUT;
   }
@@ -697,15 +779,15 @@ bool bad_shape(int B, int N, int Hq, int Hkv, int D, int page, int max_prefix_pa
          max_pages < 1;
 }
 
-template <typename T, int D>
-sv_status launch(const PrefixArgs &a, const JoinArgs &j, const Sizes &z, const int32_t *block_table,
+template <typename T, int D, bool TMA>
+sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j, const Sizes &z, const int32_t *block_table,
                  const int32_t *seq_len, int max_pages, float scale, sv_dtype dt, float *own_o, float2 *own_ml,
                  uint32_t *own_flag, void *own_ws, cudaStream_t st) {
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
-    const cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<T, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)Ring<D>::kSmem);
     if (e != cudaSuccess) return check_launch("prefix_attention", e);
     set_dev = dev;
@@ -714,7 +796,7 @@ sv_status launch(const PrefixArgs &a, const JoinArgs &j, const Sizes &z, const i
   {
     LaunchScope ls("prefix_attention", st);
     s = check_launch("prefix_attention",
-                     launch_pdl(prefix_attn_kernel<T, D>, dim3((unsigned)z.ctas), dim3(kThreads), Ring<D>::kSmem, st, a));
+                     launch_pdl(prefix_attn_kernel<T, D, TMA>, dim3((unsigned)z.ctas), dim3(kThreads), Ring<D>::kSmem, st, map, a));
     if (s != SV_OK) return s;
   }
   s = paged_sums(a.q, a.kv, a.kv_stride, a.page_stride, dt, block_table, seq_len, a.B, a.Hq, a.Hkv, D, a.page, max_pages,
@@ -825,9 +907,31 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   const JoinArgs j{own_o, own_ml, own_flag, out, out_lse, out_status};
   void *own_ws = z.own_bytes ? w + z.own : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
-  if (dt == SV_BF16)
-    return D == 64 ? launch<__nv_bfloat16, 64>(a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st)
-                   : launch<__nv_bfloat16, 128>(a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st);
-  return D == 64 ? launch<__half, 64>(a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st)
-                 : launch<__half, 128>(a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st);
+  // Boxes of as many rows as divide the page, four at least: smaller ones are
+  // more instructions than the copies they replace.
+  a.box = kKeys;
+  while (page % a.box) a.box /= 2;
+  CUtensorMap map = {};
+  bool tma = a.box >= 4 && is_device_memory(kv);
+  if (tma) {
+    EncodeTiledFn fn = encode_fn();
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page, (cuuint64_t)num_pages, 2};
+    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2, (cuuint64_t)page_stride * 2,
+                                   (cuuint64_t)kv_stride * 2};
+    const cuuint32_t box[5] = {64, 1, (cuuint32_t)a.box, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+    tma = fn && page_stride < (1LL << 39) && kv_stride < (1LL << 39) &&
+          fn(&map, dt == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+             const_cast<void *>(kv), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  auto go = [&](auto kernel) {
+    return kernel(map, a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st);
+  };
+  if (dt == SV_BF16) {
+    if (D == 64) return tma ? go(launch<__nv_bfloat16, 64, true>) : go(launch<__nv_bfloat16, 64, false>);
+    return tma ? go(launch<__nv_bfloat16, 128, true>) : go(launch<__nv_bfloat16, 128, false>);
+  }
+  if (D == 64) return tma ? go(launch<__half, 64, true>) : go(launch<__half, 64, false>);
+  return tma ? go(launch<__half, 128, true>) : go(launch<__half, 128, false>);
 }

@@ -29,7 +29,6 @@
 //               at the end of the item O / l to global memory.
 // Every wait on an mbarrier is bounded by a wall-clock limit; a wait that runs
 // out sets SV_ROW_TIMEOUT for the sequences left and the CTA drains and exits.
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -632,28 +631,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                  "r"(kTmemCols)
                  : "memory");
   }
-}
-
-// cuTensorMapEncodeTiled, fetched from the driver at run time (the library
-// does not link libcuda).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)p;
-  }
-  return fn;
 }
 
 // 4-D bf16 map with 128-byte swizzle; dims innermost first, strides in bytes
