@@ -86,8 +86,9 @@ template <int D> struct Ring {
   static constexpr uint32_t kOffBar = kOffQ + 2 * kTileBytes;
   static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
   static constexpr size_t kSmem = kOffMisc + 128 + 1024;  // + alignment
-  // barriers: a place filled and free; by buffer: Q there, S there, P there, PV done
-  static constexpr int kFull = 0, kFree = kPlaces, kQ = 2 * kPlaces, kS = kQ + 2, kP = kS + 2, kPV = kP + 2,
+  // barriers: a place filled and free; by buffer: Q there, S there, P's halves there,
+  // PV done
+  static constexpr int kFull = 0, kFree = kPlaces, kQ = 2 * kPlaces, kS = kQ + 2, kP = kS + 2, kPV = kP + 4,
                        kCount = kPV + 2;
   static_assert(kCount <= 32, "barriers");
 };
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(R::kQ + s), 4);
       mbar_init(bar(R::kS + s), 1);
-      mbar_init(bar(R::kP + s), 4);
+      mbar_init(bar(R::kP + 2 * s), 4);
+      mbar_init(bar(R::kP + 2 * s + 1), 4);
       mbar_init(bar(R::kPV + s), 1);
     }
     *abort = 0;
@@ -415,12 +417,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: head dim contiguous
     constexpr uint64_t kStep = kTileBytes >> 4;
     const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0, kBox, 1024), dQ0 = sdesc(sm0 + R::kOffQ, 16, 1024);
-    int base = 0;                // tiles of the parts before
-    int nq[2] = {0, 0}, done[2] = {0, 0};  // query tiles and PV products of each buffer
-    int ns[2] = {0, 0};            // S products
+    // The ring's place of the next K tile and of the next V tile, and the phase that
+    // fills it: two places on from tile to tile.  (Kept, not divided out: this warp's
+    // own instructions stand between the products.)
+    struct Place {
+      int at;
+      uint32_t phase;
+      __device__ __forceinline__ void next() {
+        at += 2;
+        if (at >= kPlaces) {
+          at -= kPlaces;
+          phase ^= 1;
+        }
+      }
+    } kp{0, 0}, vp{1, 0};
+    // by buffer: query tiles, S and PV products so far
+    uint32_t nq[2] = {0, 0}, ns[2] = {0, 0}, done[2] = {0, 0};
     bool ok = true;
-    auto landed = [&](int g) {
-      const bool r = all(mbar_wait(bar(R::kFull + g % kPlaces), (g / kPlaces) & 1, abort));
+    auto landed = [&](const Place &p) {
+      const bool r = all(mbar_wait(bar(R::kFull + p.at), p.phase, abort));
       if (!TMA) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the generic proxy's copies
       return r;
     };
@@ -429,38 +444,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; ok && s < 2 && s < items; ++s) ok = all(mbar_wait(bar(R::kQ + s), nq[s]++ & 1, abort));
       if (!ok) break;
       tc_fence_after();
-      auto issue_s = [&](int k) {
-        const int s = k & 1, tile = base + (w.pair ? k >> 1 : k), g = 2 * tile;
+      const bool pair = w.pair;
+      auto issue_s = [&](int s) {
         // its K has landed; the product that read P there is done
-        ok = landed(g) && all(done[s] == 0 || mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, abort));
+        ok = (pair && s == 1) || landed(kp);
+        ok = ok && all(done[s] == 0 || mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, abort));
         if (!ok) return;
         tc_fence_after();
+        const bool last = !pair || s == 1;  // of this K
         if (elect_one()) {
-          const uint64_t dk = dK0 + (g % kPlaces) * kStep, dq = dQ0 + s * kStep;
+          const uint64_t dk = dK0 + kp.at * kStep, dq = dQ0 + s * kStep;
+          const uint32_t d = tmem + kColS + s * 128;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t at = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-            mma_ss(tmem + kColS + s * 128, dq + at, dk + at, kIdescS, ks > 0);
+            mma_ss(d, dq + at, dk + at, kIdescS, ks > 0);
           }
           mma_commit(bar(R::kS + s));
-          if (!w.pair || s == 1) mma_commit(bar(R::kFree + g % kPlaces));
+          if (last) mma_commit(bar(R::kFree + kp.at));
         }
         __syncwarp();
+        if (last) kp.next();
         ++ns[s];
       };
-      for (int k = 0; ok && k < 2 && k < items; ++k) issue_s(k);
+      issue_s(0);
+      if (ok && items > 1) issue_s(1);
       for (int k = 0; ok && k < items; ++k) {
-        const int s = k & 1, j = w.pair ? k >> 1 : k, g = 2 * (base + j) + 1;
-        ok = landed(g) && all(mbar_wait(bar(R::kP + s), done[s] & 1, abort));
+        const int s = k & 1, j = pair ? k >> 1 : k;
+        const bool last = !pair || s == 1;  // of this V
+        ok = (pair && s == 1) || landed(vp);
         if (!ok) break;
         // The last tile's product takes the steps of 16 keys that hold one; a box
         // may bring rows behind the last key, which may hold anything: zeros there,
         // so that weights of 0 add 0.
         const int left = w.len - (w.t0 + j) * kKeys, steps = left < kKeys ? (left + 15) >> 4 : kKeys / 16;
-        if (TMA && left < kKeys && (left & 15)) {
+        if (TMA && left < kKeys && (left & 15) && !(pair && s == 1)) {
           const int at = left + (lane >> 1);
           if (at < 16 * steps) {
-            uint8_t *v = sm + (g % kPlaces) * kTileBytes + at * 128 + (lane & 1) * 64;
+            uint8_t *v = sm + vp.at * kTileBytes + at * 128 + (lane & 1) * 64;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -469,20 +490,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dv = dV0 + (g % kPlaces) * kStep;
-          for (int ks = 0; ks < steps; ++ks)
-            mma_ts(tmem + kColO + s * D, tmem + kColS + s * 128 + ks * 8, dv + (uint64_t)(ks * 128), kIdescO,
-                   (k > 1 || ks > 0) ? 1u : 0u);
-          mma_commit(bar(R::kPV + s));
-          if (!w.pair || s == 1) mma_commit(bar(R::kFree + g % kPlaces));
+        const uint64_t dv = dV0 + vp.at * kStep;
+        const uint32_t o = tmem + kColO + s * D, p = tmem + kColS + s * 128;
+        // P comes in two halves of 64 keys
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = all(mbar_wait(bar(R::kP + 2 * s + half), done[s] & 1, abort));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+              if (ks < steps) mma_ts(o, p + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (k > 1 || ks > 0) ? 1u : 0u);
+            if (half) {
+              mma_commit(bar(R::kPV + s));
+              if (last) mma_commit(bar(R::kFree + vp.at));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
+        if (last) vp.next();
         ++done[s];
-        if (k + 2 < items) issue_s(k + 2);
+        if (k + 2 < items) issue_s(s);
       }
-      base += n;
     }
     if (!ok) {
       // products in flight end before tensor memory is released: the newest phases
@@ -593,20 +624,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tm_st16(tS + 16 * c, p);
         };
+        auto there = [&](int half) {
+          tm_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(R::kP + 2 * s + half));
+        };
         weights(0);
-        tm_ld32(tS + 64, x[2]);
         weights(1);
-        tm_wait_ld(x[2]);
+        there(0);
+        tm_ld32(tS + 64, x[2]);
         tm_ld32(tS + 96, x[3]);
+        tm_wait_ld(x[2]);
+        tm_wait_ld(x[3]);
         mask(2);
         weights(2);
-        tm_wait_ld(x[3]);
         mask(3);
         weights(3);
-        tm_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(R::kP + s));
+        there(1);
       }
       if (!ok) break;
       const size_t at = (w.part(a) * 2 + s) * a.rows + row;
