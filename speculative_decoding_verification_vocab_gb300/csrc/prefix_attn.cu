@@ -14,14 +14,17 @@
 // Bound: a slot of a prefix is 4 D bytes a KV head and 4 D W G operations: memory
 // up to some 280 rows, above the tensor cores and the softmax's exponentials.
 //
-// Work: segments, one for each prefix, KV head and pair of 128-row query tiles (row
-// r = sequence r / G, head r % G), lie one after the other as a row of 128-key
-// tiles, and each CTA, one to an SM, takes an equal share of it, from one segment
-// to the next: parts of a segment, whose sums go to the workspace.  Shares are cut
-// from the lengths on the device, so a captured launch follows growing prefixes.
+// Work: the query rows of a KV head (row r = sequence r / G, head r % G) are cut
+// into columns of 256 (two tiles of 128), and a column's keys, of all prefixes and
+// KV heads one after the other as a row of 128-key tiles, into equal shares, one for
+// each of its CTAs: parts of a segment (prefix, KV head), whose sums go to the
+// workspace.  The CTAs of the columns that have the same share are neighbours and
+// read the same keys at the same time, once from memory (with a column's share
+// beside the next column's instead, 7 times).  Shares are cut from the lengths on
+// the device, so a captured launch follows growing prefixes.
 // A CTA works on two S buffers in turn, so that the tensor cores have one while
-// the softmax is at the other: those of the pair's two query tiles with the same
-// keys or, where a segment has one query tile only, those of even and odd key
+// the softmax is at the other: those of the column's two query tiles with the
+// same keys or, where the last column has one tile only, those of even and odd key
 // tiles, which the join puts together like any two parts.
 //   warps 0-1   producers, of K and of V: page table entries a tile ahead, TMA
 //               boxes of 64 columns of as many rows as divide the page (128-byte
@@ -97,10 +100,10 @@ struct PrefixArgs {
   const void *q, *kv;
   int64_t kv_stride, page_stride;
   const int32_t *table, *len;  // [N][max_pages], [N]
-  int B, N, W, Hq, Hkv, G, mtiles, pairs;  // query tiles of a KV head, and pairs of them
+  int B, N, W, Hq, Hkv, G, mtiles;  // query tiles of a KV head
   int page, page_shift, max_pages, num_pages, cap;
   int box;  // rows of a TMA box
-  int ctas, rows;  // rows of a part's buffer: min(128, W G)
+  int shares2, shares1, rows;  // CTAs of a column of two tiles, and of one; rows of a part's buffer: min(128, W G)
   float scale_log2;
   // workspace: sums [parts][2][rows][D], references and sums of exponentials
   // [parts][2][rows], status bits [parts]
@@ -128,43 +131,40 @@ __device__ __forceinline__ longlong2 count_tiles(const PrefixArgs &a, int p) {
   return n;
 }
 
-// The work of the batch in units, one for each key tile and query tile: a tile of
-// a pair counts 2.  CTAs that share so many units: two and more to each, so that
-// every share has the beginning of a tile of each segment that it runs through.
-__device__ __forceinline__ long long sharing(const PrefixArgs &a, long long units) {
-  return min((long long)a.ctas, max(units / 2, 1LL));
+// Shares of a column that so many tiles are cut into: none without one.
+__device__ __forceinline__ long long cut_into(long long shares, long long tiles) {
+  return min(shares, max(tiles, 1LL));
+}
+// Part of a column's share r in segment sg: from part to part of a column one or
+// the other grows.
+__device__ __forceinline__ size_t part_at(const PrefixArgs &a, int column, long long r_sg) {
+  return (size_t)column * (max(a.shares2, a.shares1) + (size_t)a.N * a.Hkv) + r_sg;
 }
 
-// A CTA's way through its share: the part of a segment it is at, tiles [t0, t1),
-// those that begin in the share.  Part index: CTA + segment, of which from part to
-// part one or the other grows.
+// A CTA's way through its share: the part of a segment it is at, tiles [t0, t1).
 struct Walk {
-  long long at, end, first;  // units; the first of prefix p's segments
-  int p, head, pr, pair, t0, t1, len;  // pair: two query tiles, 2 pr and 2 pr + 1
+  long long at, end, first;  // tiles of the column; the first of prefix p's segments
+  int column, share, pair;   // pair: two query tiles, 2 column and 2 column + 1
+  int p, head, t0, t1, len;
   __device__ __forceinline__ bool next(const PrefixArgs &a) {
     while (at < end && p < a.N) {
       len = __ldcg(a.len + p);
       const int tiles = tiles_of(a, len);
-      const long long of_head = (long long)tiles * a.mtiles, block = of_head * a.Hkv;
-      if (at >= first + block) {
-        first += block;
-        ++p;
-        continue;
+      const long long block = (long long)tiles * a.Hkv;
+      if (at < first + block) {
+        head = (int)((at - first) / tiles);
+        t0 = (int)((at - first) % tiles);
+        t1 = (int)min((long long)tiles, t0 + (end - at));
+        at += t1 - t0;
+        return true;
       }
-      head = (int)((at - first) / of_head);
-      const long long head0 = first + head * of_head, v = at - head0;
-      pr = (int)(v / (2 * tiles));
-      pair = 2 * pr + 1 < a.mtiles;
-      const long long seg0 = head0 + (long long)pr * 2 * tiles, to = min(end, seg0 + (tiles << pair));
-      t0 = (int)(at - seg0 + pair) >> pair;
-      t1 = (int)(to - seg0 + pair) >> pair;
-      at = to;
-      if (t1 > t0) return true;
+      first += block;
+      ++p;
     }
     return false;
   }
   __device__ __forceinline__ size_t part(const PrefixArgs &a) const {
-    return (size_t)blockIdx.x + ((size_t)p * a.Hkv + head) * a.pairs + pr;
+    return part_at(a, column, (long long)share + (long long)p * a.Hkv + head);
   }
   // tiles of buffer s, and the i-th of them
   __device__ __forceinline__ int tiles_for(int s) const { return pair ? t1 - t0 : (t1 - t0 + 1 - s) >> 1; }
@@ -264,11 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_sync();
   if (warp == 0) {
-    // this CTA's share of all units, and the prefix it starts in
-    const long long per = (long long)a.Hkv * a.mtiles, all = per * count_tiles(a, 0).x, ctas = sharing(a, all);
+    // this CTA's column and share, and the prefix it starts in
     Walk w;
-    w.at = min((long long)blockIdx.x, ctas) * all / ctas;
-    w.end = min((long long)blockIdx.x + 1, ctas) * all / ctas;
+    const int columns2 = a.mtiles / 2, cta = blockIdx.x;
+    w.pair = cta < columns2 * a.shares2;
+    w.column = w.pair ? cta % columns2 : columns2;
+    w.share = w.pair ? cta / columns2 : cta - columns2 * a.shares2;
+    const long long per = a.Hkv, all = per * count_tiles(a, 0).x, shares = cut_into(w.pair ? a.shares2 : a.shares1, all);
+    w.at = min((long long)w.share, shares) * all / shares;
+    w.end = min((long long)w.share + 1, shares) * all / shares;
     w.first = 0;
     w.p = 0;
     for (int p0 = 0; p0 < a.N && w.at < w.end; p0 += 32) {
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;  // tiles of this buffer so far
     bool ok = true;
     while (ok && w.next(a)) {
-      const int mt = w.pair ? 2 * w.pr + s : 2 * w.pr, n = w.tiles_for(s);
+      const int mt = 2 * w.column + (w.pair ? s : 0), n = w.tiles_for(s);
       const int rows = min(kRows, a.W * a.G - mt * kRows);
       if (n > 0) {
         // This row of the query tile; rows behind the last are zeros.  (A buffer
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   const bool live = row < (long long)a.B * a.Hq;
   const int b = live ? (int)(row / a.Hq) : 0, h = live ? (int)(row % a.Hq) : 0;
   const int p = b / a.W, at = b % a.W * a.G + h % a.G;
-  const int mt = at / kRows, r = at % kRows, pr = mt / 2, pair = 2 * pr + 1 < a.mtiles;
+  const int mt = at / kRows, r = at % kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
   // lengths were there before the launches that this one waits for
   const longlong2 n = count_tiles(a, p);
   const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
@@ -720,22 +724,22 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   if (!live) return;
   uint32_t flag = (len < 0 || len > a.cap ? SV_ROW_BAD_LEN : 0u) | j.own_flag[b];
   const float2 own = j.own_ml[row];
-  long long c0 = 0, c1 = -1;  // CTAs with a part
+  long long c0 = 0, c1 = -1;  // shares with a part
   if (tiles > 0) {
-    const long long per = (long long)a.Hkv * a.mtiles, all = n.x * per, ctas = sharing(a, all);
-    const long long first = n.y * per + (long long)tiles * ((long long)(h / a.G) * a.mtiles + 2 * pr);
-    c0 = ((first + 1) * ctas - 1) / all;
-    c1 = ((first + ((long long)(tiles - 1) << pair) + 1) * ctas - 1) / all;
+    const long long all = n.x * a.Hkv, first = n.y * a.Hkv + (long long)tiles * (h / a.G);
+    const long long shares = cut_into(pair ? a.shares2 : a.shares1, all);
+    c0 = ((first + 1) * shares - 1) / all;
+    c1 = ((first + tiles) * shares - 1) / all;
   }
-  const size_t part0 = ((size_t)p * a.Hkv + h / a.G) * a.pairs + pr;
+  const size_t part0 = part_at(a, column, (long long)p * a.Hkv + h / a.G + c0);
   // places in the parts: that of the row's query tile in a pair, both otherwise
   const int s0 = pair ? mt & 1 : 0, ns = pair ? 1 : 2;
   const long long places = (c1 - c0 + 1) * ns;
-  auto place = [&](long long i) { return ((part0 + c0 + i / ns) * 2 + s0 + i % ns) * a.rows + r; };
+  auto place = [&](long long i) { return ((part0 + i / ns) * 2 + s0 + i % ns) * a.rows + r; };
   float M = own.x;
   for (long long i = lane; i < places; i += 32) {
     M = fmaxf(M, a.w_ml[place(i)].x);
-    flag |= a.w_flag[part0 + c0 + i / ns];
+    flag |= a.w_flag[part0 + i / ns];
   }
   M = warp_max(M);
   flag = __reduce_or_sync(0xffffffffu, flag);
@@ -776,22 +780,25 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
 }
 
 // ------------------------------------------------------------------ host side
+constexpr int kSms = 152;
 struct Sizes {
-  int W, G, mtiles, pairs, rows, ctas;
+  int W, G, mtiles, rows, shares2, shares1, ctas;
   size_t o, ml, flag, own_o, own_ml, own_flag, own, own_bytes, total;
 };
 bool sizes_of(Sizes &z, int B, int N, int Hq, int Hkv, int D, int page, int max_pages) {
   z.W = B / N;
   z.G = Hq / Hkv;
-  const long long wg = (long long)z.W * z.G, mtiles = (wg + kRows - 1) / kRows, segments = (mtiles + 1) / 2 * Hkv * N;
-  if (wg > (1 << 24) || Hkv > (1 << 24) || N > (1 << 24) || mtiles * Hkv > (1 << 24) || segments > (1 << 24) ||
-      (long long)B * Hq > (1 << 26))
+  const long long wg = (long long)z.W * z.G, mtiles = (wg + kRows - 1) / kRows, columns = (mtiles + 1) / 2;
+  const long long segments = (long long)Hkv * N;
+  if (wg > (1 << 24) || segments > (1 << 24) || columns * segments > (1 << 24) || (long long)B * Hq > (1 << 26))
     return false;
   z.mtiles = (int)mtiles;
-  z.pairs = (int)(mtiles + 1) / 2;
   z.rows = wg < kRows ? (int)wg : kRows;
-  z.ctas = 152;  // one to an SM of this part; the parts' places follow it
-  const size_t parts = (size_t)z.ctas + (size_t)segments;
+  // the SMs of this part over the columns, by their tiles, and what they come to
+  z.shares2 = mtiles >= 2 ? (int)(2 * kSms / mtiles > 1 ? 2 * kSms / mtiles : 1) : 0;
+  z.shares1 = mtiles % 2 ? (int)(kSms / mtiles > 1 ? kSms / mtiles : 1) : 0;
+  z.ctas = (int)(mtiles / 2 * z.shares2 + z.shares1);
+  const size_t parts = (size_t)columns * ((size_t)(z.shares2 > z.shares1 ? z.shares2 : z.shares1) + (size_t)segments);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t r = at;
@@ -922,7 +929,6 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   a.Hkv = Hkv;
   a.G = z.G;
   a.mtiles = z.mtiles;
-  a.pairs = z.pairs;
   a.page = page;
   a.page_shift = -1;
   for (int i = 0; i < 31; ++i)
@@ -930,7 +936,8 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   a.max_pages = max_prefix_pages;
   a.num_pages = num_pages;
   a.cap = page * max_prefix_pages;
-  a.ctas = z.ctas;
+  a.shares2 = z.shares2;
+  a.shares1 = z.shares1;
   a.rows = z.rows;
   a.scale_log2 = scale * kLog2e;
   a.w_o = (float *)(w + z.o);
