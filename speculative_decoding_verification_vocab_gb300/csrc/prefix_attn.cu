@@ -33,9 +33,10 @@
 //               and caches in host memory, go by asynchronous copies of 16 bytes
 //               (twice the time: a box is one instruction, and 32 copies are one
 //               for 512 bytes);
-//   warp 2      MMA issuer: S = Q K^T from shared memory, O += P V with P in tensor
-//               memory, in the place of the S it comes from;
-//   warps 3-10  softmax, four to a buffer, a row to a thread: the running maximum
+//   warps 2-3   MMA issuers, one to a buffer, so that one's waits lie behind the
+//               other's products: S = Q K^T from shared memory, O += P V with P in
+//               tensor memory, in the place of the S it comes from;
+//   warps 4-11  softmax, four to a buffer, a row to a thread: the running maximum
 //               with a lazy rescale of O, P as 16-bit values; at a segment's end O,
 //               m and l to the workspace.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
@@ -53,10 +54,10 @@ namespace {
 constexpr int kRows = 128;   // query rows of a tile = tensor-memory lanes
 constexpr int kKeys = 128;   // keys of a tile
 constexpr int kProducers = 64;
-constexpr int kMmaWarp = kProducers / 32, kFirstSoftmax = kMmaWarp + 1;
-// 11 warps: registers are given out to four warps at a time, and the softmax needs
+constexpr int kMmaWarp = kProducers / 32, kFirstSoftmax = kMmaWarp + 2;
+// 12 warps: registers are given out to four warps at a time, and the softmax needs
 // more than the 128 that 13 to 16 leave a thread
-constexpr int kThreads = kProducers + 32 + 256;
+constexpr int kThreads = kProducers + 64 + 256;
 constexpr uint32_t kBox = kKeys * 128;  // bytes of a box of 64 columns
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.4426950408889634f;
 // tensor-memory columns: two S (P, 16-bit pairs, in their first halves), two O
@@ -82,17 +83,26 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
   return *(const uint32_t *)&v;
 }
 
+// A barrier tells one phase from the next by its parity alone, so whoever waits for a
+// phase has to know that the one before is over.  K and V have places of their own,
+// each filled by one producer, which has waited for every phase in turn; and the
+// places are even in number, so that where the buffers take even and odd tiles a
+// place is one buffer's, whose issuer has seen all of its phases.  (With K and V in
+// one ring an issuer a tile and a half ahead of the other let K be loaded into a
+// place that was still to be read: the launch failed.)
 template <int D> struct Ring {
   static constexpr uint32_t kTileBytes = kKeys * D * 2;  // K or V rows of a key tile, or a query tile
-  static constexpr int kPlaces = D == 128 ? 5 : 11;      // K, V, K, V, ...
-  static constexpr uint32_t kOffQ = kPlaces * kTileBytes;
+  static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 2 : 6;  // places
+  static_assert(kK % 2 == 0 && kV % 2 == 0, "places of even and odd tiles");
+  static constexpr uint32_t kOffV = kK * kTileBytes;
+  static constexpr uint32_t kOffQ = kOffV + kV * kTileBytes;
   static constexpr uint32_t kOffBar = kOffQ + 2 * kTileBytes;
   static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
   static constexpr size_t kSmem = kOffMisc + 128 + 1024;  // + alignment
-  // barriers: a place filled and free; by buffer: Q there, S there, P's halves there,
-  // PV done
-  static constexpr int kFull = 0, kFree = kPlaces, kQ = 2 * kPlaces, kS = kQ + 2, kP = kS + 2, kPV = kP + 4,
-                       kCount = kPV + 2;
+  // barriers: a place of K or V filled and free; by buffer: Q there, S there, P's
+  // halves there, PV done
+  static constexpr int kFullK = 0, kFreeK = kK, kFullV = 2 * kK, kFreeV = kFullV + kV, kQ = kFreeV + kV, kS = kQ + 2,
+                       kP = kS + 2, kPV = kP + 4, kCount = kPV + 2;
   static_assert(kCount <= 32, "barriers");
 };
 
@@ -145,8 +155,9 @@ __device__ __forceinline__ size_t part_at(const PrefixArgs &a, int column, long 
 struct Walk {
   long long at, end, first;  // tiles of the column; the first of prefix p's segments
   int column, share, pair;   // pair: two query tiles, 2 column and 2 column + 1
-  int p, head, t0, t1, len;
+  int p, head, t0, t1, len, base;
   __device__ __forceinline__ bool next(const PrefixArgs &a) {
+    base += t1 - t0;
     while (at < end && p < a.N) {
       len = __ldcg(a.len + p);
       const int tiles = tiles_of(a, len);
@@ -161,14 +172,18 @@ struct Walk {
       first += block;
       ++p;
     }
+    t0 = t1;
     return false;
   }
   __device__ __forceinline__ size_t part(const PrefixArgs &a) const {
     return part_at(a, column, (long long)share + (long long)p * a.Hkv + head);
   }
-  // tiles of buffer s, and the i-th of them
-  __device__ __forceinline__ int tiles_for(int s) const { return pair ? t1 - t0 : (t1 - t0 + 1 - s) >> 1; }
-  __device__ __forceinline__ int tile(int s, int i) const { return pair ? t0 + i : t0 + 2 * i + s; }
+  // Tiles of buffer s: all of a pair's, or every other one, by the CTA's count of
+  // tiles (`base` before this part); the first of them, and how many.
+  __device__ __forceinline__ int first_for(int s) const { return pair ? t0 : t0 + ((s ^ base) & 1); }
+  __device__ __forceinline__ int tiles_for(int s) const {
+    return pair ? t1 - t0 : (t1 - first_for(s) + 1) >> 1;
+  }
 };
 
 // 5-D tiled TMA load of one box into shared memory, completing on `bar`.
@@ -226,7 +241,7 @@ template <typename T, int D, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
   using R = Ring<D>;
-  constexpr int kPlaces = R::kPlaces;
+  constexpr int kK = R::kK, kV = R::kV;
   constexpr uint32_t kTileBytes = R::kTileBytes;
   const unsigned FULL = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
@@ -242,9 +257,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPlaces; ++i) {
-      mbar_init(bar(R::kFull + i), TMA ? 1 : kProducers);
-      mbar_init(bar(R::kFree + i), 1);
+    // a place is free when both buffers' products are done with it, or that of the
+    // one it is for
+    const int users = blockIdx.x < a.mtiles / 2 * a.shares2 ? 2 : 1;
+    for (int i = 0; i < kK; ++i) {
+      mbar_init(bar(R::kFullK + i), TMA ? 1 : kProducers);
+      mbar_init(bar(R::kFreeK + i), users);
+    }
+    for (int i = 0; i < kV; ++i) {
+      mbar_init(bar(R::kFullV + i), TMA ? 1 : kProducers);
+      mbar_init(bar(R::kFreeV + i), users);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(R::kQ + s), 4);
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.at = min((long long)w.share, shares) * all / shares;
     w.end = min((long long)w.share + 1, shares) * all / shares;
     w.first = 0;
-    w.p = 0;
+    w.p = w.base = w.t0 = w.t1 = 0;
     for (int p0 = 0; p0 < a.N && w.at < w.end; p0 += 32) {
       const int p = p0 + lane;
       const long long n = p < a.N ? per * tiles_of(a, __ldcg(a.len + p)) : 0;
@@ -306,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producers
     // Warp 0 loads K, warp 1 V; a lane to each box of a tile.
     const int boxes = kKeys / a.box;
-    int t_all = 0;  // tiles so far
+    const int places = warp ? kV : kK, full = warp ? R::kFullV : R::kFullK, free = warp ? R::kFreeV : R::kFreeK;
+    int t_all = 0, at = 0;  // tiles so far, and the next one's place
+    uint32_t seen = 1;      // parity of the phase that frees it
     bool ok = true;
     while (w.next(a)) {
       bool bad = false;
@@ -324,16 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad |= lane < boxes && slot < w.len && !there;
         const int page = there ? id : a.num_pages;  // out of bounds: zeros
         id = fetch(t + 1);
-        const int g = 2 * t_all + warp, at = g % kPlaces;
-        ok = all(g < kPlaces || mbar_wait(bar(R::kFree + at), (g / kPlaces - 1) & 1, abort));
+        ok = all(t_all < places || mbar_wait(bar(free + at), seen, abort));
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(bar(R::kFull + at), kTileBytes);
+        if (lane == 0) mbar_expect_tx(bar(full + at), kTileBytes);
         __syncwarp();
         if (lane < boxes) {
-          const uint32_t dst = sm0 + at * kTileBytes + lane * a.box * 128;
+          const uint32_t dst = sm0 + (warp ? R::kOffV : 0) + at * kTileBytes + lane * a.box * 128;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load5(dst + c * kBox, &map, c * 64, w.head, r, page, warp, bar(R::kFull + at));
+            tma_load5(dst + c * kBox, &map, c * 64, w.head, r, page, warp, bar(full + at));
+        }
+        if (++at == places) {
+          at = 0;
+          seen ^= 1;
         }
       }
       if (warp == 0) {
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CPR = D / 8, RPI = 32 / CPR;  // rows of one round of copies
     const int lr = lane / CPR, lc = lane % CPR;
     const int64_t row_elems = (int64_t)a.Hkv * D;
-    int g = 0;  // places filled so far
+    int t_all = 0;  // tiles so far
     bool ok = true;
     while (w.next(a)) {
       bool bad = false;
@@ -366,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       fetch(w.t0);
-      for (int t = w.t0; ok && t < w.t1; ++t) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++t_all) {
         long long off[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -383,12 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fetch(t + 1);
 #pragma unroll
-        for (int part = 0; part < 2; ++part, ++g) {  // K, V
-          const int at = g % kPlaces;
-          ok = all(g < kPlaces || mbar_wait(bar(R::kFree + at), (g / kPlaces - 1) & 1, abort));
+        for (int part = 0; part < 2; ++part) {  // K, V
+          const int places = part ? kV : kK, at = t_all % places;
+          ok = all(t_all < places ||
+                   mbar_wait(bar((part ? R::kFreeV : R::kFreeK) + at), (t_all / places - 1) & 1, abort));
           if (!ok) break;
           const T *from = kv + part * a.kv_stride;
-          const uint32_t dst = sm0 + at * kTileBytes + (lc >> 3) * kBox + (warp * 64 + lr) * 128;
+          const uint32_t dst = sm0 + (part ? R::kOffV : 0) + at * kTileBytes + (lc >> 3) * kBox + (warp * 64 + lr) * 128;
 #pragma unroll 8
           for (int i = 0; i < 64 / RPI; ++i) {
             const long long o = __shfl_sync(FULL, i < 32 / RPI ? off[0] : off[1], (i * RPI + lr) & 31);
@@ -397,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                          "r"(o >= 0 ? 16u : 0u)
                          : "memory");
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(R::kFull + at)) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar((part ? R::kFullV : R::kFullK) + at))
+                       : "memory");
         }
       }
       // the part's status: a barrier of the producers with their votes, which they
@@ -411,81 +440,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 0) a.w_flag[w.part(a)] = some ? SV_ROW_BAD_PAGE : 0u;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kFirstSoftmax) {
     // ------------------------------------------------------------ MMA
-    // A segment's products as a row of items, buffers in turn: S of the first two,
-    // then, item by item, O += P V and the S two items on, into the place of P.  The
-    // warp runs converged and elect.sync picks the issuing lane.
+    // A buffer's tiles in turn: S of the first, then, tile by tile, O += P V and the
+    // next S, into the place of P.  The warp runs converged and elect.sync picks the
+    // issuing lane.
+    const int s = warp - kMmaWarp;
     constexpr uint32_t kIdesc = (1u << 4) | (kAbType<T> << 7) | (kAbType<T> << 10) | ((uint32_t)(kRows >> 4) << 24);
     constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kKeys >> 3) << 17);
     constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: head dim contiguous
     constexpr uint64_t kStep = kTileBytes >> 4;
-    const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0, kBox, 1024), dQ0 = sdesc(sm0 + R::kOffQ, 16, 1024);
-    // The ring's place of the next K tile and of the next V tile, and the phase that
-    // fills it: two places on from tile to tile.  (Kept, not divided out: this warp's
-    // own instructions stand between the products.)
-    struct Place {
-      int at;
-      uint32_t phase;
-      __device__ __forceinline__ void next() {
-        at += 2;
-        if (at >= kPlaces) {
-          at -= kPlaces;
-          phase ^= 1;
-        }
-      }
-    } kp{0, 0}, vp{1, 0};
-    // by buffer: query tiles, S and PV products so far
-    uint32_t nq[2] = {0, 0}, ns[2] = {0, 0}, done[2] = {0, 0};
+    const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0 + R::kOffV, kBox, 1024);
+    const uint64_t dq = sdesc(sm0 + R::kOffQ + s * kTileBytes, 16, 1024);
+    const uint32_t tS = tmem + kColS + s * 128, tO = tmem + kColO + s * D;
+    // The places of the next tile's K and V, and the phases that fill them.  (Kept,
+    // not divided out: this warp's own instructions stand between the products.)
+    const int step = w.pair ? 1 : 2, first = w.pair ? 0 : s;
+    int k_at = first, v_at = first;
+    uint32_t k_phase = 0, v_phase = 0;
+    uint32_t nq = 0, ns = 0, done = 0;  // query tiles, S and PV products so far
     bool ok = true;
-    auto landed = [&](const Place &p) {
-      const bool r = all(mbar_wait(bar(R::kFull + p.at), p.phase, abort));
+    auto landed = [&](int full, uint32_t phase) {
+      const bool r = all(mbar_wait(bar(full), phase, abort));
       if (!TMA) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the generic proxy's copies
       return r;
     };
     while (ok && w.next(a)) {
-      const int n = w.t1 - w.t0, items = n << w.pair;
-      for (int s = 0; ok && s < 2 && s < items; ++s) ok = all(mbar_wait(bar(R::kQ + s), nq[s]++ & 1, abort));
-      if (!ok) break;
-      tc_fence_after();
-      const bool pair = w.pair;
-      auto issue_s = [&](int s) {
-        // its K has landed; the product that read P there is done
-        ok = (pair && s == 1) || landed(kp);
-        ok = ok && all(done[s] == 0 || mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, abort));
+      const int n = w.tiles_for(s);
+      auto issue_s = [&]() {  // its K has landed; the product that read P there is done
+        ok = landed(R::kFullK + k_at, k_phase) && all(done == 0 || mbar_wait(bar(R::kPV + s), (done - 1) & 1, abort));
         if (!ok) return;
         tc_fence_after();
-        const bool last = !pair || s == 1;  // of this K
         if (elect_one()) {
-          const uint64_t dk = dK0 + kp.at * kStep, dq = dQ0 + s * kStep;
-          const uint32_t d = tmem + kColS + s * 128;
+          const uint64_t dk = dK0 + k_at * kStep;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t at = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-            mma_ss(d, dq + at, dk + at, kIdescS, ks > 0);
+            mma_ss(tS, dq + at, dk + at, kIdescS, ks > 0);
           }
           mma_commit(bar(R::kS + s));
-          if (last) mma_commit(bar(R::kFree + kp.at));
+          mma_commit(bar(R::kFreeK + k_at));
         }
         __syncwarp();
-        if (last) kp.next();
-        ++ns[s];
+        if ((k_at += step) >= kK) {
+          k_at -= kK;
+          k_phase ^= 1;
+        }
+        ++ns;
       };
-      issue_s(0);
-      if (ok && items > 1) issue_s(1);
-      for (int k = 0; ok && k < items; ++k) {
-        const int s = k & 1, j = pair ? k >> 1 : k;
-        const bool last = !pair || s == 1;  // of this V
-        ok = (pair && s == 1) || landed(vp);
+      if (n > 0) {
+        ok = all(mbar_wait(bar(R::kQ + s), nq++ & 1, abort));
+        if (!ok) break;
+        tc_fence_after();
+        issue_s();
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        ok = landed(R::kFullV + v_at, v_phase);
         if (!ok) break;
         // The last tile's product takes the steps of 16 keys that hold one; a box
-        // may bring rows behind the last key, which may hold anything: zeros there,
-        // so that weights of 0 add 0.
-        const int left = w.len - (w.t0 + j) * kKeys, steps = left < kKeys ? (left + 15) >> 4 : kKeys / 16;
-        if (TMA && left < kKeys && (left & 15) && !(pair && s == 1)) {
+        // may bring rows behind the last key, which may hold anything: zeros there
+        // (from both issuers), so that weights of 0 add 0.
+        const int left = w.len - (w.first_for(s) + i * step) * kKeys, steps = left < kKeys ? (left + 15) >> 4 : kKeys / 16;
+        if (TMA && left < kKeys && (left & 15)) {
           const int at = left + (lane >> 1);
           if (at < 16 * steps) {
-            uint8_t *v = sm + vp.at * kTileBytes + at * 128 + (lane & 1) * 64;
+            uint8_t *v = sm + R::kOffV + v_at * kTileBytes + at * 128 + (lane & 1) * 64;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -494,40 +513,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        const uint64_t dv = dV0 + vp.at * kStep;
-        const uint32_t o = tmem + kColO + s * D, p = tmem + kColS + s * 128;
+        const uint64_t dv = dV0 + v_at * kStep;
         // P comes in two halves of 64 keys
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          ok = all(mbar_wait(bar(R::kP + 2 * s + half), done[s] & 1, abort));
+          ok = all(mbar_wait(bar(R::kP + 2 * s + half), done & 1, abort));
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-              if (ks < steps) mma_ts(o, p + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (k > 1 || ks > 0) ? 1u : 0u);
+              if (ks < steps) mma_ts(tO, tS + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
             if (half) {
               mma_commit(bar(R::kPV + s));
-              if (last) mma_commit(bar(R::kFree + vp.at));
+              mma_commit(bar(R::kFreeV + v_at));
             }
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (last) vp.next();
-        ++done[s];
-        if (k + 2 < items) issue_s(s);
+        ++done;
+        if ((v_at += step) >= kV) {
+          v_at -= kV;
+          v_phase ^= 1;
+        }
+        if (i + 1 < n) issue_s();
       }
     }
     if (!ok) {
       // products in flight end before tensor memory is released: the newest phases
       // of the barriers that the last ones commit to
       volatile int no_abort = 0;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (ns[s]) mbar_wait(bar(R::kS + s), (ns[s] - 1) & 1, &no_abort);
-        if (done[s]) mbar_wait(bar(R::kPV + s), (done[s] - 1) & 1, &no_abort);
-      }
+      if (ns) mbar_wait(bar(R::kS + s), (ns - 1) & 1, &no_abort);
+      if (done) mbar_wait(bar(R::kPV + s), (done - 1) & 1, &no_abort);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -563,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = all(mbar_wait(bar(R::kS + s), g & 1, abort));
         if (!ok) break;
         tc_fence_after();
-        const int left = w.len - w.tile(s, i) * kKeys;  // keys of this tile
+        const int left = w.len - (w.first_for(s) + (w.pair ? i : 2 * i)) * kKeys;  // keys of this tile
         uint32_t x[4][32];
         auto mask = [&](int c) {
           if (left < kKeys) {
@@ -681,12 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // have been waited for where no wait ran out)
     if (TMA) {
       volatile int no_abort = 0;
-      const int nk = s_filled[0], nv = s_filled[1], from = max(0, 2 * max(nk, nv) - 2 * kPlaces);
-      for (int i = 0; i < kPlaces; ++i) {
-        int newest = -1;
-        for (int g = from; g < 2 * max(nk, nv); ++g)
-          if (g % kPlaces == i && g / 2 < (g & 1 ? nv : nk)) newest = g;
-        if (newest >= 0) mbar_wait(bar(R::kFull + i), (newest / kPlaces) & 1, &no_abort);
+      for (int i = 0; i < kK + kV; ++i) {
+        const bool k = i < kK;
+        const int places = k ? kK : kV, at = k ? i : i - kK, filled = (s_filled[k ? 0 : 1] - 1 - at + places) / places;
+        if (filled > 0) mbar_wait(bar((k ? R::kFullK : R::kFullV) + at), (filled - 1) & 1, &no_abort);
       }
     }
     Walk again = *s_walk;
