@@ -36,9 +36,10 @@
 //   warps 2-3   MMA issuers, one to a buffer, so that one's waits lie behind the
 //               other's products: S = Q K^T from shared memory, O += P V with P in
 //               tensor memory, in the place of the S it comes from;
-//   warps 4-11  softmax, four to a buffer, a row to a thread: the running maximum
-//               with a lazy rescale of O, P as 16-bit values; at a segment's end O,
-//               m and l to the workspace.
+//   warps 4-11  softmax, four to a buffer, a row to a thread, 64 keys at a time: the
+//               running maximum with a lazy rescale of O, P as 16-bit values (its
+//               first half is multiplied while the second is made); at a segment's
+//               end O, m and l to the workspace.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
 // with SV_ROW_TIMEOUT.
 #include <cuda_bf16.h>
@@ -100,10 +101,14 @@ template <int D> struct Ring {
   static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
   static constexpr size_t kSmem = kOffMisc + 128 + 1024;  // + alignment
   // barriers: a place of K or V filled and free; by buffer: Q there, S there, P's
-  // halves there, PV done
+  // halves there, PV done, its first half done
   static constexpr int kFullK = 0, kFreeK = kK, kFullV = 2 * kK, kFreeV = kFullV + kV, kQ = kFreeV + kV, kS = kQ + 2,
-                       kP = kS + 2, kPV = kP + 4, kCount = kPV + 2;
+                       kP = kS + 2, kPV = kP + 4, kPV0 = kPV + 2, kCount = kPV0 + 2;
   static_assert(kCount <= 32, "barriers");
+};
+
+template <int V> struct Int {
+  static constexpr int value = V;
 };
 
 struct PrefixArgs {
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(R::kP + 2 * s), 4);
       mbar_init(bar(R::kP + 2 * s + 1), 4);
       mbar_init(bar(R::kPV + s), 1);
+      mbar_init(bar(R::kPV0 + s), 1);
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -524,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
               if (ks < steps) mma_ts(tO, tS + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
-            if (half) {
+            if (!half) {
+              mma_commit(bar(R::kPV0 + s));
+            } else {
               mma_commit(bar(R::kPV + s));
               mma_commit(bar(R::kFreeV + v_at));
             }
@@ -583,87 +591,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int left = w.len - (w.first_for(s) + (w.pair ? i : 2 * i)) * kKeys;  // keys of this tile
         uint32_t x[4][32];
-        auto mask = [&](int c) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tm_ld32(tS + 32 * c, x[c]);
+        auto do_half = [&](auto which) -> bool {
+          constexpr int half = decltype(which)::value;
+#pragma unroll
+          for (int c = 2 * half; c < 2 * half + 2; ++c) tm_wait_ld(x[c]);
           if (left < kKeys) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= left) x[c][e] = 0xff800000u;
+            for (int c = 2 * half; c < 2 * half + 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= left) x[c][e] = 0xff800000u;
           }
-        };
-        auto most = [&](int c) {
-          float v[4];
+          float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[c][e]);
+          for (int c = 2 * half; c < 2 * half + 2; ++c)
 #pragma unroll
-          for (int e = 4; e < 32; ++e) v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[c][e]));
-          return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        };
-        // the second half for its maximum, then the first, which stays: P's columns
-        // take the place of S's in that order
-        tm_ld32(tS + 64, x[2]);
-        tm_ld32(tS + 96, x[3]);
-        tm_wait_ld(x[2]);
-        tm_wait_ld(x[3]);
-        tm_ld32(tS, x[0]);
-        tm_ld32(tS + 32, x[1]);
-        mask(2);
-        mask(3);
-        float mx = fmaxf(most(2), most(3));
-        tm_wait_ld(x[0]);
-        tm_wait_ld(x[1]);
-        mask(0);
-        mask(1);
-        mx = fmaxf(mx, fmaxf(most(0), most(1))) * a.scale_log2;  // > 0: the maximum commutes with it
-        const bool grow = mx > m_ref + (kSlack<T> + kBias<T>);
-        const float m_new = grow ? mx - kBias<T> : m_ref;
-        const float factor = grow && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.0f;
-        m_ref = m_new;
-        if (__any_sync(FULL, factor != 1.0f)) {
-          // O covers the tiles before: S was issued after their products
-          l2[0] = f2_mul(l2[0], f2_splat(factor));
-          l2[1] = f2_mul(l2[1], f2_splat(factor));
+            for (int e = 0; e < 32; ++e) v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[c][e]));
+          // scale > 0: the maximum commutes with it
+          const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
+          const bool grow = mx > m_ref + (kSlack<T> + kBias<T>);
+          const float m_new = grow ? mx - kBias<T> : m_ref;
+          const float factor = grow && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.0f;
+          m_ref = m_new;
+          if (__any_sync(FULL, factor != 1.0f)) {
+            // O covers the keys before: S was issued after the product of the tile
+            // before, and that of this tile's first half is waited for
+            if (half) {
+              if (!all(mbar_wait(bar(R::kPV0 + s), g & 1, abort))) return false;
+              tc_fence_after();
+            }
+            l2[0] = f2_mul(l2[0], f2_splat(factor));
+            l2[1] = f2_mul(l2[1], f2_splat(factor));
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tm_ld32(tO + c, o);
-            tm_wait_ld(o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tm_ld32(tO + c, o);
+              tm_wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-            tm_st32u(tO + c, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tm_st32u(tO + c, o);
+            }
           }
-        }
-        const unsigned long long sc2 = f2_splat(a.scale_log2), mn2 = f2_splat(m_ref == -INFINITY ? 0.0f : -m_ref);
-        auto weights = [&](int c) {
-          uint32_t p[16];
+          if (half == 0)  // the second half comes while the first is worked on
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const unsigned long long y =
-                ex2_2(f2_fma(f2_pack(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, mn2));
-            l2[e & 1] = f2_add(l2[e & 1], y);
-            float y0, y1;
-            f2_unpack(y, y0, y1);
-            p[e] = pack2<T>(y0, y1);
+            for (int c = 2; c < 4; ++c) tm_ld32(tS + 32 * c, x[c]);
+          const unsigned long long sc2 = f2_splat(a.scale_log2), mn2 = f2_splat(m_ref == -INFINITY ? 0.0f : -m_ref);
+#pragma unroll
+          for (int c = 2 * half; c < 2 * half + 2; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const unsigned long long y =
+                  ex2_2(f2_fma(f2_pack(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, mn2));
+              l2[e & 1] = f2_add(l2[e & 1], y);
+              float y0, y1;
+              f2_unpack(y, y0, y1);
+              p[e] = pack2<T>(y0, y1);
+            }
+            tm_st16(tS + 16 * c, p);  // in the place of keys that have been read
           }
-          tm_st16(tS + 16 * c, p);
-        };
-        auto there = [&](int half) {
           tm_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(R::kP + 2 * s + half));
+          return true;
         };
-        weights(0);
-        weights(1);
-        there(0);
-        tm_ld32(tS + 64, x[2]);
-        tm_ld32(tS + 96, x[3]);
-        tm_wait_ld(x[2]);
-        tm_wait_ld(x[3]);
-        mask(2);
-        weights(2);
-        mask(3);
-        weights(3);
-        there(1);
+        ok = do_half(Int<0>()) && do_half(Int<1>());
+        if (!ok) break;
       }
       if (!ok) break;
       const size_t at = (w.part(a) * 2 + s) * a.rows + row;
