@@ -208,6 +208,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // 32 consecutive columns of this thread's tensor-memory lane; the values are there
 // after tm_wait_ld
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -608,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 2 * half; c < 2 * half + 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[c][e]));
+            for (int e = 0; e < 32; e += 2)
+              v[e / 2 & 3] = max3(v[e / 2 & 3], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
           // scale > 0: the maximum commutes with it
           const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
           const bool grow = mx > m_ref + (kSlack<T> + kBias<T>);
