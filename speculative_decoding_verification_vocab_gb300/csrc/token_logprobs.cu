@@ -12,13 +12,15 @@
 // its K best, stores them to the first CTA, which joins them.  One launch, no
 // workspace.
 //
-// The K best of a slice: a list in shared memory takes every element that is at
-// least tau, a value that K elements are known to reach.  The first 4096 to 8192
-// elements give a first tau without a sort (below), and whenever the list has
-// grown to twice K it is cut back to the K best, whose last is the next tau.
-// Elements in random order pass it K times a group at first and ever more seldom
-// (K ln(n) in all); elements in ascending order overflow the list, and their
-// group is gone through again 256 elements at a time.
+// The K best of a slice cost the pass a maximum: a thread keeps, in shared memory,
+// the largest of each run of its elements (32 and more; 8 runs), rounded up to 16
+// bits.  In the end the threads' maxima give a value tau that K elements are known
+// to reach (below), the runs that reach it (K and a few) are read again, from L2,
+// and their elements of at least tau, K and some, are sorted.  A row of which too
+// many elements reach tau (constant ones, say) goes through a list that is cut
+// back to the K best whenever it is full.  (With that list filled in the pass, 16 KB
+// by 16 KB between barriers, 4096 rows of V = 128256 bf16 took 378 us at K = 20 and
+// 676 at K = 128.)
 #include <math.h>
 
 #include "vocab_rows.cuh"
@@ -29,7 +31,10 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kMaxTop = 128;
 constexpr int kRing = 3;       // groups: one in work, two on their way
-constexpr int kList = 512;     // keys, a power of two of at least kMaxTop + kRowThreads
+constexpr int kRuns = 8;       // of a thread's elements
+constexpr int kList = 2048;    // keys, in the ring's place; a power of two
+constexpr int kSlowList = 512; // of them, where the list is cut back: at least kMaxTop + kRowThreads
+static_assert(kList * 8 <= kRing * kGroupBytes && kSlowList >= kMaxTop + kRowThreads, "lists");
 
 struct LogArgs {
   const void *logits;
@@ -108,6 +113,100 @@ __device__ __forceinline__ float warp_jth(float x, int j) {
   return __shfl_sync(0xffffffffu, x, j - 1);
 }
 
+// x rounded up to the upper 16 bits of a float
+__device__ __forceinline__ uint16_t up16(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return (uint16_t)((b >> 31 ? b : b + 0xffffu) >> 16);
+}
+// the slice's piece v
+template <typename T> __device__ __forceinline__ uint4 piece_at(const T *row, const RowSlice &s, int v) {
+  return __ldg((const uint4 *)(row + s.head) + v);
+}
+
+// The K best of a slice by a list that is cut back as it fills, a group of pieces
+// after the other.  Every thread of the CTA calls it and finds the list's first
+// min(K, elements) in order; returns their number.  s_n: a counter.
+template <typename T>
+__device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32_t rank, u64 *list, int K, int *s_n) {
+  constexpr int VEC = RowElem<T>::VEC;
+  float tau = -INFINITY;  // what an element has to reach, and its key to exceed
+  u64 tau_key = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) *s_n = 0;
+  __syncthreads();
+  auto offer = [&](float x, int index) {
+    if (x >= tau && x > -INFINITY) {
+      const u64 key = key_of(x, index);
+      if (key > tau_key) {
+        const int at = atomicAdd(s_n, 1);
+        if (at < kSlowList) list[at] = key;
+      }
+    }
+  };
+  // after a barrier behind the last offer
+  auto cut = [&](int n) {
+    keep_best(list, n, K);
+    if (n >= K) {
+      tau_key = list[K - 1];
+      tau = value_of(tau_key);
+    }
+    if (threadIdx.x == 0) *s_n = min(n, K);
+    __syncthreads();
+  };
+  if (rank == 0 && (int)threadIdx.x < s.singles) {
+    const int i = single_at<T>(s, threadIdx.x);
+    offer(RowElem<T>::load(row + i), i);
+  }
+  __syncthreads();
+  const int groups = row_groups(s);
+  for (int g = 0; g < groups; ++g) {
+    auto piece = [&](int j) { return s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x; };
+    const int before = *s_n;  // settled by the barriers that ended the last group
+    float most[kPieces], top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      most[j] = piece(j) < s.v1 ? RowElem<T>::most(piece_at(row, s, piece(j))) : -INFINITY;
+      top = fmaxf(top, most[j]);
+    }
+    const bool some = top >= tau && top > -INFINITY;
+    // (the votes' barrier stands behind every thread's look at the counter)
+    if (!__syncthreads_or(some)) continue;
+    if (some) {
+      for (int j = 0; j < kPieces; ++j) {
+        if (most[j] < tau || most[j] == -INFINITY) continue;
+        float x[VEC];
+        RowElem<T>::unpack(piece_at(row, s, piece(j)), x);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) offer(x[i], s.head + piece(j) * VEC + i);
+      }
+    }
+    __syncthreads();
+    int n = *s_n;
+    __syncthreads();
+    if (n > kSlowList) {  // again, an element of each thread at a time
+      if (threadIdx.x == 0) *s_n = before;
+      __syncthreads();
+      n = before;
+      for (int j = 0; j < kPieces; ++j) {
+        for (int i = 0; i < VEC; ++i) {
+          if (n > kSlowList - kRowThreads) cut(n);
+          if (piece(j) < s.v1) {
+            const int at = s.head + piece(j) * VEC + i;
+            offer(RowElem<T>::load(row + at), at);
+          }
+          __syncthreads();
+          n = *s_n;
+          __syncthreads();
+        }
+      }
+    }
+    if (n >= 2 * K + 32) cut(n);
+  }
+  const int n = *s_n;
+  keep_best(list, n, K);
+  return min(n, K);
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs a, unsigned C) {
   grid_dep_sync();
@@ -116,8 +215,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const size_t item = blockIdx.x / C;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
-  u64 *list = (u64 *)(smem + kRing * kGroupBytes);  // [kList]
-  u64 *all = list + kList;                          // [C][K], the first CTA's
+  u64 *list = (u64 *)smem;                                         // [kList], when the ring is free
+  uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes);       // [kRuns][kRowThreads]
+  u64 *all = (u64 *)(smem + kRing * kGroupBytes + (TOP ? kRuns * kRowThreads * 2 : 0));  // [C][K], the first CTA's
   __shared__ RowPart s_part[kRowWarps];
   __shared__ RowPart s_all[kMaxRowCluster];
   __shared__ int s_n;
@@ -154,115 +254,40 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   }
   const bool known = token >= 0 && token < a.V;
   const float given = rank == 0 && a.tokens && known ? RowElem<T>::load(row + token) : 0.0f;
-  float tau = -INFINITY;  // what an element has to reach, and its key to exceed
-  u64 tau_key = 0;
   const float k = a.k;
   RowSums sums = row_sums();
-  if (TOP) {
-    if (threadIdx.x == 0) s_n = 0;
-    __syncthreads();
-  }
-  auto offer = [&](float x, int index) {
-    if (x >= tau && x > -INFINITY) {
-      const u64 key = key_of(x, index);
-      if (key > tau_key) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kList) list[at] = key;
-      }
-    }
-  };
-  // every thread, after a barrier behind the last offer: the list's K best
-  auto cut = [&](int n) {
-    keep_best(list, n, a.K);
-    if (n >= a.K) {
-      tau_key = list[a.K - 1];
-      tau = value_of(tau_key);
-    }
-    if (threadIdx.x == 0) s_n = min(n, a.K);
-    __syncthreads();
-  };
-  if (rank == 0 && (int)threadIdx.x < s.singles) {
-    const int i = single_at<T>(s, threadIdx.x);
-    const float x = RowElem<T>::load(row + i);
-    add_single<true>(sums, x, k);
-    if (TOP) offer(x, i);
-  }
+  const bool has_single = rank == 0 && (int)threadIdx.x < s.singles;
+  const int single = has_single ? single_at<T>(s, threadIdx.x) : 0;
+  const float single_x = has_single ? RowElem<T>::load(row + single) : -INFINITY;
+  if (has_single) add_single<true>(sums, single_x, k);
+  if (TOP && threadIdx.x == 0) s_n = 0;
 
+  // run i of a thread: its groups [i per, (i + 1) per)
+  const int per = (groups + kRuns - 1) / kRuns;
+  float run_top = -INFINITY, thread_top = single_x;
+  int run = 0, left = per;
   int slot = 0, slot_load = kRing - 1;
   for (int g = 0; g < groups; ++g) {
     if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
     group_commit();
     group_wait<kRing - 1>();
     uint4 w[kPieces];
-    float most[kPieces];
+    float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, slot, j);
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) most[j] = RowElem<T>::most(w[j]);
-    const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    for (int j = 0; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
     if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k);
     if (TOP) {
-      // first element of this thread's piece j in the row
-      auto first = [&](int j) { return s.head + (s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x) * VEC; };
-      int before = 0;
-      if (g == 0) {
-        // In each of the W warps that have pieces, ceil(K / W) threads have an
-        // element of at least the warp's ceil(K / W)-th largest maximum (-inf
-        // where fewer threads have one): K elements reach the least of the
-        // warps' numbers.
-        const int W = min((s.v1 - s.v0 + 31) / 32, kRowWarps);
-        const float mine = warp_jth(top, min((a.K + W - 1) / W, 32));
-        if (lane == 0) s_warp[warp] = mine;
-        __syncthreads();
-        before = s_n;
-        tau = s_warp[0];
-        for (int i = 1; i < W; ++i) tau = fminf(tau, s_warp[i]);
-        if (32 * W < a.K) tau = -INFINITY;
-        __syncthreads();  // s_n is read by all before it grows
-      } else {
-        before = s_n;  // settled by the barriers that ended the last group
-      }
-      const bool some = top >= tau && top > -INFINITY;
-      // a barrier with the votes: s_n is read above by all before it grows
-      if (__syncthreads_or(some)) {
-        if (some) {
-#pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            if (most[j] < tau) continue;
-            float x[VEC];
-            RowElem<T>::unpack(w[j], x);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) offer(x[i], first(j) + i);
-          }
-        }
-        __syncthreads();
-        int n = s_n;
-        __syncthreads();
-        if (n > kList) {  // again, an element of each thread at a time
-          if (threadIdx.x == 0) s_n = before;
-          __syncthreads();
-          n = before;
-          for (int j = 0; j < kPieces; ++j) {
-            const uint4 again = ring_piece(smem, slot, j);
-            float x[VEC];
-            RowElem<T>::unpack(again, x);
-            for (int i = 0; i < VEC; ++i) {
-              if (n > kList - kRowThreads) {
-                cut(n);
-              }
-              float xi = x[0];
-#pragma unroll
-              for (int e = 1; e < VEC; ++e) xi = e == i ? x[e] : xi;
-              offer(xi, first(j) + i);
-              __syncthreads();
-              n = s_n;
-              __syncthreads();
-            }
-          }
-        }
-        if (n >= 2 * a.K + 32) cut(n);
+      run_top = fmaxf(run_top, top);
+      thread_top = fmaxf(thread_top, top);
+      if (--left == 0 || g == groups - 1) {
+        runs[run * kRowThreads + threadIdx.x] = up16(run_top);
+        run_top = -INFINITY;
+        left = per;
+        ++run;
       }
     }
     slot = slot + 1 == kRing ? 0 : slot + 1;
@@ -275,9 +300,54 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   __syncthreads();
   int n = 0;
   if (TOP) {
+    // In each of the W warps that have pieces, ceil(K / W) threads have an element
+    // of at least the warp's ceil(K / W)-th largest maximum (-inf where fewer threads
+    // have one): K elements reach the least of the warps' numbers.
+    const int W = max(1, min((s.v1 - s.v0 + 31) / 32, kRowWarps));
+    const float jth = warp_jth(thread_top, min((a.K + W - 1) / W, 32));
+    if (lane == 0) s_warp[warp] = jth;
+    __syncthreads();  // the ring is free, too
+    float tau = s_warp[0];
+    for (int i = 1; i < W; ++i) tau = fminf(tau, s_warp[i]);
+    if (32 * W < a.K) tau = -INFINITY;
+    auto offer = [&](float x, int index) {
+      if (x >= tau && x > -INFINITY) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kList) list[at] = key_of(x, index);
+      }
+    };
+    if (has_single) offer(single_x, single);
+    for (int i = 0; i < run; ++i) {
+      const float top = __uint_as_float((uint32_t)runs[i * kRowThreads + threadIdx.x] << 16);
+      if (!(top >= tau) || top == -INFINITY) continue;
+      for (int g = i * per; g < min((i + 1) * per, groups); ++g) {
+        uint4 w[kPieces];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const int v = s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x;
+          w[j] = v < s.v1 ? piece_at(row, s, v)
+                          : make_uint4(RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf);
+        }
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const float m = RowElem<T>::most(w[j]);
+          if (!(m >= tau) || m == -INFINITY) continue;
+          float x[VEC];
+          RowElem<T>::unpack(w[j], x);
+          const int first = s.head + (s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x) * VEC;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) offer(x[e], first + e);
+        }
+      }
+    }
+    __syncthreads();
     n = s_n;
-    keep_best(list, n, a.K);
-    n = min(n, a.K);
+    if (n > kList) {
+      n = best_by_list(row, s, rank, list, a.K, &s_n);
+    } else {
+      keep_best(list, n, a.K);
+      n = min(n, a.K);
+    }
   }
   auto join = [&](const RowPart *parts, int count) {
     return warp_join(lane < count ? parts[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
@@ -332,19 +402,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
 template <typename T, bool TOP>
 cudaError_t launch(const LogArgs &a, unsigned items, unsigned C, cudaStream_t st) {
   // dynamic memory beyond 48 KB has to be asked for, once for each device
-  size_t keys = TOP ? (size_t)kList : 0;
+  size_t keys = 0;
   if (TOP && C > 1) {
-    size_t room = 2 * kRowThreads;  // keep_best sorts powers of two
-    while (room < (size_t)C * a.K) room *= 2;
-    keys += room;
+    keys = 2 * kRowThreads;  // keep_best sorts powers of two
+    while (keys < (size_t)C * a.K) keys *= 2;
   }
-  const size_t smem = (size_t)kRing * kGroupBytes + keys * 8;
+  const size_t smem = (size_t)kRing * kGroupBytes + (TOP ? kRuns * kRowThreads * 2 : 0) + keys * 8;
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
     const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kRing * kGroupBytes + (kList + (int)kMaxRowCluster * kMaxTop) * 8);
+                                               kRing * kGroupBytes + kRuns * kRowThreads * 2 + (int)kMaxRowCluster * kMaxTop * 8);
     if (e != cudaSuccess) return e;
     set_dev = dev;
   }
