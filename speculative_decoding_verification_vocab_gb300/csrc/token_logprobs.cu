@@ -34,7 +34,7 @@ constexpr int kRing = 3;       // groups: one in work, two on their way
 constexpr int kRuns = 8;       // of a thread's elements
 constexpr int kList = 2048;    // keys, in the ring's place; a power of two
 constexpr int kSlowList = 512; // of them, where the list is cut back: at least kMaxTop + kRowThreads
-static_assert(kList * 8 <= kRing * kGroupBytes && kSlowList >= kMaxTop + kRowThreads, "lists");
+static_assert(kList * 8 + kRuns * kRowThreads * 2 <= kRing * kGroupBytes && kSlowList >= kMaxTop + kRowThreads, "lists");
 
 struct LogArgs {
   const void *logits;
@@ -216,11 +216,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
   u64 *list = (u64 *)smem;                                         // [kList], when the ring is free
+  uint16_t *hits = (uint16_t *)(list + kList);                     // [kRuns kRowThreads], as the list
   uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes);       // [kRuns][kRowThreads]
   u64 *all = (u64 *)(smem + kRing * kGroupBytes + (TOP ? kRuns * kRowThreads * 2 : 0));  // [C][K], the first CTA's
   __shared__ RowPart s_part[kRowWarps];
   __shared__ RowPart s_all[kMaxRowCluster];
-  __shared__ int s_n;
+  __shared__ int s_n, s_hits;
   __shared__ float s_warp[kRowWarps];
 
   const int b = (int)(item / a.P);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const int single = has_single ? single_at<T>(s, threadIdx.x) : 0;
   const float single_x = has_single ? RowElem<T>::load(row + single) : -INFINITY;
   if (has_single) add_single<true>(sums, single_x, k);
-  if (TOP && threadIdx.x == 0) s_n = 0;
+  if (TOP && threadIdx.x == 0) s_n = s_hits = 0;
 
   // run i of a thread: its groups [i per, (i + 1) per)
   const int per = (groups + kRuns - 1) / kRuns;
@@ -317,28 +318,25 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
       }
     };
     if (has_single) offer(single_x, single);
+    // the runs that reach it, then their pieces over all threads: one way to L2
     for (int i = 0; i < run; ++i) {
       const float top = __uint_as_float((uint32_t)runs[i * kRowThreads + threadIdx.x] << 16);
-      if (!(top >= tau) || top == -INFINITY) continue;
-      for (int g = i * per; g < min((i + 1) * per, groups); ++g) {
-        uint4 w[kPieces];
+      if (top >= tau && top > -INFINITY) hits[atomicAdd(&s_hits, 1)] = (uint16_t)(i * kRowThreads + threadIdx.x);
+    }
+    __syncthreads();
+    const int of_run = per * kPieces, pieces = s_hits * of_run;
+    for (int i = threadIdx.x; i < pieces; i += kRowThreads) {
+      const int hit = hits[i / of_run], q = i % of_run;
+      const int g = hit / kRowThreads * per + q / kPieces;
+      const int v = s.v0 + g * kGroupVecs + q % kPieces * kRowThreads + hit % kRowThreads;
+      if (g >= groups || v >= s.v1) continue;
+      const uint4 w = piece_at(row, s, v);
+      const float m = RowElem<T>::most(w);
+      if (!(m >= tau) || m == -INFINITY) continue;
+      float x[VEC];
+      RowElem<T>::unpack(w, x);
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-          const int v = s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x;
-          w[j] = v < s.v1 ? piece_at(row, s, v)
-                          : make_uint4(RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf);
-        }
-#pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-          const float m = RowElem<T>::most(w[j]);
-          if (!(m >= tau) || m == -INFINITY) continue;
-          float x[VEC];
-          RowElem<T>::unpack(w[j], x);
-          const int first = s.head + (s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x) * VEC;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) offer(x[e], first + e);
-        }
-      }
+      for (int e = 0; e < VEC; ++e) offer(x[e], s.head + v * VEC + e);
     }
     __syncthreads();
     n = s_n;
