@@ -141,7 +141,7 @@ __device__ __forceinline__ uint4 grad_piece(const uint4 &w, float m, float coef,
   RowElem<T>::unpack(w, x);
 #pragma unroll
   for (int i = 0; i < VEC; i += 2) {
-    const unsigned long long y = f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), f2_splat(m)), f2_splat(k));
+    const unsigned long long y = f2_mul(f2_add(f2_pack(x[i], x[i + 1]), f2_splat(-m)), f2_splat(k));
     float y0, y1;
     f2_unpack(y, y0, y1);
     f2_unpack(f2_mul(f2_pack(ex2_approx(y0), ex2_approx(y1)), f2_splat(coef)), x[i], x[i + 1]);
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
   read_list(li, a, r, row);
   const bool skip = li.used == 0 && li.flags == 0;  // the same in every CTA
   const float k = a.k;
+  const unsigned long long k2 = f2_splat(k);
   RowSums sums = row_sums();
   uint32_t flags = li.flags;
   if (!skip && !flags) {
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
       for (int j = 1; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
       if (top > sums.lim) raise<false>(sums, top, k);
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k);
+      for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k2);
       slot = slot + 1 == kRing ? 0 : slot + 1;
       slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
     }

@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const bool known = token >= 0 && token < a.V;
   const float given = rank == 0 && a.tokens && known ? RowElem<T>::load(row + token) : 0.0f;
   const float k = a.k;
+  const unsigned long long k2 = f2_splat(k);
   RowSums sums = row_sums();
   const bool has_single = rank == 0 && (int)threadIdx.x < s.singles;
   const int single = has_single ? single_at<T>(s, threadIdx.x) : 0;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     for (int j = 0; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
     if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k);
+    for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k2);
     if (TOP) {
       run_top = fmaxf(run_top, top);
       thread_top = fmaxf(thread_top, top);

@@ -129,17 +129,25 @@ __device__ __forceinline__ int row_groups(const RowSlice &s) { return (s.v1 - s.
 // reads there it has copied itself, so no barrier stands between.
 template <typename T>
 __device__ __forceinline__ void load_group(const T *row, const RowSlice &s, int g, int slot, unsigned char *ring) {
-  const uint4 *src = (const uint4 *)(row + s.head);
+  const int v = s.v0 + g * kGroupVecs + (int)threadIdx.x;
+  const uint4 *src = (const uint4 *)(row + s.head) + v;
   unsigned char *at = ring + (size_t)slot * kGroupBytes + threadIdx.x * 16;
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
+  if (s.v0 + (g + 1) * kGroupVecs <= s.v1) {  // all of them
 #pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRowThreads * 16), "l"(src + j * kRowThreads)
+                   : "memory");
+    return;
+  }
+#pragma unroll 1
   for (int j = 0; j < kPieces; ++j) {
-    const int v = s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x;
-    unsigned char *dst = at + j * kRowThreads * 16;
-    if (v < s.v1)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src + v)
+    if (v + j * kRowThreads < s.v1)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRowThreads * 16), "l"(src + j * kRowThreads)
                    : "memory");
     else
-      *(uint4 *)dst = make_uint4(RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf);
+      *(uint4 *)(at + j * kRowThreads * 16) =
+          make_uint4(RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf);
   }
 }
 __device__ __forceinline__ void group_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -157,39 +165,42 @@ __device__ __forceinline__ uint4 ring_piece(const unsigned char *ring, int slot,
 // of -inf adds 0 to s too (y is held above -150, where 2^y is 0); a NaN or +inf
 // makes l NaN.
 struct RowSums {
-  float top;     // the reference, or -inf while nothing is above -inf
-  float ref;     // the same, 0 in place of -inf
-  float lim;     // raise the reference above this
+  float top;                  // the reference, or -inf while nothing is above -inf
+  float lim;                  // raise the reference above this
+  unsigned long long nref;    // minus the reference (0 in place of -inf), twice
   unsigned long long l2, s2;  // packed pairs of partial sums
 };
-__device__ __forceinline__ RowSums row_sums() { return RowSums{-INFINITY, 0.0f, -INFINITY, 0ull, 0ull}; }
+__device__ __forceinline__ RowSums row_sums() { return RowSums{-INFINITY, -INFINITY, 0ull, 0ull, 0ull}; }
 
 template <bool ENT> __device__ __forceinline__ void raise(RowSums &r, float to, float k) {
   // y grows by d: 2^y y becomes 2^d (2^y y + d 2^y)
-  const float d = r.top == -INFINITY ? 0.0f : (r.ref - to) * k;
+  const float d = r.top == -INFINITY ? 0.0f : (r.top - to) * k;
   const unsigned long long f = f2_splat(r.top == -INFINITY ? 0.0f : ex2_approx(d));
   if (ENT) r.s2 = f2_mul(f2_fma(f2_splat(fmaxf(d, -150.0f)), r.l2, r.s2), f);
   r.l2 = f2_mul(r.l2, f);
-  r.top = r.ref = to;
+  r.top = to;
+  r.nref = f2_splat(-to);
   r.lim = to + kRefSlack / k;
 }
-template <bool ENT> __device__ __forceinline__ void add_pair(RowSums &r, float a, float b, float k) {
-  const unsigned long long y = f2_mul(f2_sub(f2_pack(a, b), f2_splat(r.ref)), f2_splat(k));
+// k2: k, twice
+template <bool ENT> __device__ __forceinline__ void add_pair(RowSums &r, float a, float b, unsigned long long k2) {
+  const unsigned long long y = f2_mul(f2_add(f2_pack(a, b), r.nref), k2);
   float y0, y1;
   f2_unpack(y, y0, y1);
   const unsigned long long e = f2_pack(ex2_approx(y0), ex2_approx(y1));
   r.l2 = f2_add(r.l2, e);
   if (ENT) r.s2 = f2_fma(e, f2_pack(fmaxf(y0, -150.0f), fmaxf(y1, -150.0f)), r.s2);
 }
-template <typename T, bool ENT> __device__ __forceinline__ void add_piece(RowSums &r, const uint4 &w, float k) {
+template <typename T, bool ENT>
+__device__ __forceinline__ void add_piece(RowSums &r, const uint4 &w, unsigned long long k2) {
   float x[RowElem<T>::VEC];
   RowElem<T>::unpack(w, x);
 #pragma unroll
-  for (int i = 0; i < RowElem<T>::VEC; i += 2) add_pair<ENT>(r, x[i], x[i + 1], k);
+  for (int i = 0; i < RowElem<T>::VEC; i += 2) add_pair<ENT>(r, x[i], x[i + 1], k2);
 }
 template <bool ENT> __device__ __forceinline__ void add_single(RowSums &r, float x, float k) {
   if (x > r.lim) raise<ENT>(r, x, k);
-  add_pair<ENT>(r, x, -INFINITY, k);
+  add_pair<ENT>(r, x, -INFINITY, f2_splat(k));
 }
 
 // The sums as three numbers that join: reference (-inf: none), l, s.
