@@ -273,34 +273,31 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
 
   // run i of a thread: its groups [i per, (i + 1) per)
   const int per = (groups + kRuns - 1) / kRuns;
-  float run_top = -INFINITY, thread_top = single_x;
-  int run = 0, left = per;
-  int slot = 0, slot_load = kRing - 1;
-  for (int g = 0; g < groups; ++g) {
-    if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
-    group_commit();
-    group_wait<kRing - 1>();
-    uint4 w[kPieces];
-    float top = -INFINITY;
+  float thread_top = single_x;
+  int run = 0, slot = 0, slot_load = kRing - 1;
+  for (int g = 0; g < groups; ++run) {
+    float run_top = -INFINITY;
+    for (const int end = min(g + per, groups); g < end; ++g) {
+      if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
+      group_commit();
+      group_wait<kRing - 1>();
+      uint4 w[kPieces];
+      float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, slot, j);
+      for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, slot, j);
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
-    if (top > sums.lim) raise<true>(sums, top, k);
+      for (int j = 0; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
+      if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k2);
-    if (TOP) {
-      run_top = fmaxf(run_top, top);
-      thread_top = fmaxf(thread_top, top);
-      if (--left == 0 || g == groups - 1) {
-        runs[run * kRowThreads + threadIdx.x] = up16(run_top);
-        run_top = -INFINITY;
-        left = per;
-        ++run;
-      }
+      for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k2);
+      if (TOP) run_top = fmaxf(run_top, top);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
     }
-    slot = slot + 1 == kRing ? 0 : slot + 1;
-    slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
+    if (TOP) {
+      runs[run * kRowThreads + threadIdx.x] = up16(run_top);
+      thread_top = fmaxf(thread_top, run_top);
+    }
   }
   group_wait<0>();
 
