@@ -45,92 +45,113 @@ struct DistillArgs {
   int resident;  // groups' places in shared memory
 };
 
-// The teacher's list, by the CTA's first warps (thread i: entry i): weights t_k
-// and their logarithms; what they add up to and what they leave.  Faults:
-// entries outside [0, V) but -1 (an unused one), log probabilities that are NaN
-// or +inf, and a list that adds up to more than 1 by more than rounding (tail).
-struct List {
-  int token[kMaxList];
-  float t[kMaxList], log_t[kMaxList], x[kMaxList];
-  float rest;       // t_r
-  int used;         // entries
-  uint32_t flags;
+// The teacher's list, an entry to each of the CTA's first threads: its token (-1:
+// unused), value a_k and the draft's logit there.  Asked for before the row is gone
+// through, so that the two ways to memory lie behind the row's.
+struct Entry {
+  int token;
+  float value, x;
+  uint32_t flags;  // of the entry: a token outside [0, V), a value that is NaN or +inf
 };
-// Every thread of the CTA calls it; ends with a barrier.  x: the draft's logits
-// of the listed tokens (0 for the unused).
-template <typename T> __device__ void read_list(List &li, const DistillArgs &a, size_t r, const T *row) {
-  const unsigned FULL = 0xffffffffu;
-  constexpr int E = kMaxList / 32;
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    float v[E], most = -INFINITY;
-    int tok[E];
-    uint32_t flags = 0;
-    int used = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = lane + 32 * e;
-      tok[e] = i < a.K ? a.token[r * a.K + i] : -1;
-      v[e] = tok[e] != -1 ? a.logprob[r * a.K + i] : -INFINITY;
-      if (tok[e] < -1 || tok[e] >= a.V) {
-        flags |= SV_ROW_BAD_TOKEN;
-        tok[e] = -1;
+constexpr int kListWarps = kMaxList / 32;
+static_assert(kMaxList <= kRowThreads, "an entry to a thread");
+template <typename T> __device__ __forceinline__ Entry read_entry(const DistillArgs &a, size_t r, const T *row) {
+  Entry e{-1, -INFINITY, 0.0f, 0u};
+  if ((int)threadIdx.x < a.K) {
+    const size_t i = r * a.K + threadIdx.x;
+    e.token = a.token[i];
+    if (e.token != -1) {
+      e.value = a.logprob[i];
+      if (e.token < 0 || e.token >= a.V) {
+        e.flags |= SV_ROW_BAD_TOKEN;
+        e.token = -1;
+      } else {
+        e.x = RowElem<T>::load(row + e.token);
       }
-      if (!(v[e] < INFINITY)) flags |= SV_ROW_NAN;
-      most = fmaxf(most, v[e]);
-      used += tok[e] != -1;
-    }
-    float x[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = tok[e] >= 0 ? RowElem<T>::load(row + tok[e]) : 0.0f;
-    most = warp_max(most);
-    // against 1 (the values are log probabilities) or against the list's sum
-    const float ref = a.tail || most == -INFINITY ? 0.0f : most;
-    // What the list leaves: 1 - exp of its largest value as one number, so that
-    // a teacher who is almost sure keeps the digits of its doubt.
-    int first = kMaxList;
-#pragma unroll
-    for (int e = E - 1; e >= 0; --e)
-      if (v[e] == most) first = lane + 32 * e;
-    first = __reduce_min_sync(FULL, first);
-    float sum = 0.0f, left = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float t = expf(v[e] - ref);
-      sum += t;
-      left -= lane + 32 * e == first ? expm1f(v[e]) : t;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sum += __shfl_xor_sync(FULL, sum, o);
-      left += __shfl_xor_sync(FULL, left, o);
-    }
-    const float shift = a.tail ? 0.0f : ref + (sum > 0.0f ? logf(sum) : 0.0f);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = lane + 32 * e;
-      li.token[i] = tok[e];
-      li.log_t[i] = v[e] - shift;
-      li.t[i] = a.tail ? expf(v[e]) : sum > 0.0f ? expf(v[e] - ref) / sum : 0.0f;
-      li.x[i] = x[e];
-    }
-    used = __reduce_add_sync(FULL, used);
-    flags = __reduce_or_sync(FULL, flags);
-    // a teacher's log probabilities are rounded numbers: their sum may pass 1
-    if (a.tail && !(sum < 1.0f + 0x1p-8f)) flags |= SV_ROW_NAN;
-    if (!a.tail && used && !(sum > 0.0f)) flags |= SV_ROW_NAN;  // nothing to normalise
-    if (lane == 0) {
-      li.rest = a.tail ? (used ? fmaxf(left, 0.0f) : 1.0f) : 0.0f;
-      li.used = used;
-      li.flags = flags;
+      if (!(e.value < INFINITY)) e.flags |= SV_ROW_NAN;
     }
   }
-  __syncthreads();
+  return e;
 }
-
-__device__ __forceinline__ float listed_grad(const List &li, int i, const float4 &st, float k, float w) {
-  const float share = ex2_approx((li.x[i] - st.z) * k) * st.w;
-  return (share - li.t[i]) * w;
+// What the list comes to, from a part of it for each of its warps: the largest value
+// and its exponential's companions.  (1 - exp of the largest value is taken as one
+// number, so that a teacher who is almost sure keeps the digits of its doubt.)
+struct ListPart {
+  float most, others;  // the largest value; sum of exp(value - ref) of all but it
+  float top, sum;      // the draft's largest listed logit; sum of 2^((x - top) k)
+  int used;
+  uint32_t flags;
+};
+struct List {
+  float shift, inv;  // t_k = exp(a_k - ref) inv, ln t_k = a_k - shift
+  float ref;
+  float rest;        // t_r
+  float top, sum;    // as ListPart
+  int used;
+  uint32_t flags;
+};
+// One warp's part; ref 0 with tail, the warp's own largest value without.
+__device__ __forceinline__ ListPart list_part(const Entry &e, int tail, float k) {
+  const unsigned FULL = 0xffffffffu;
+  ListPart p;
+  p.most = warp_max(e.value);
+  const unsigned who = __ballot_sync(FULL, e.value == p.most);
+  const float ref = tail || p.most == -INFINITY ? 0.0f : p.most;
+  p.others = who && (int)(threadIdx.x & 31) == __ffs(who) - 1 ? 0.0f : expf(e.value - ref);
+  const bool there = e.token >= 0;
+  p.top = warp_max(there ? e.x : -INFINITY);
+  p.sum = there ? ex2_approx((e.x - (p.top == -INFINITY ? 0.0f : p.top)) * k) : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    p.others += __shfl_xor_sync(FULL, p.others, o);
+    p.sum += __shfl_xor_sync(FULL, p.sum, o);
+  }
+  p.used = __reduce_add_sync(FULL, there ? 1 : 0);
+  p.flags = __reduce_or_sync(FULL, e.flags);
+  return p;
+}
+__device__ __forceinline__ List list_of(const ListPart *parts, int tail, float k) {
+  List li;
+  float most = -INFINITY;
+  li.top = -INFINITY;
+  li.used = 0;
+  li.flags = 0;
+  int first = 0;
+#pragma unroll
+  for (int w = 0; w < kListWarps; ++w) {
+    if (parts[w].most > most) {
+      most = parts[w].most;
+      first = w;
+    }
+    li.top = fmaxf(li.top, parts[w].top);
+    li.used += parts[w].used;
+    li.flags |= parts[w].flags;
+  }
+  li.ref = tail || most == -INFINITY ? 0.0f : most;
+  const float top = li.top == -INFINITY ? 0.0f : li.top;
+  float others = 0.0f;  // all but the largest
+  li.sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kListWarps; ++w) {
+    const ListPart &p = parts[w];
+    // with tail the parts' sums are taken against 0, as the list's is
+    const float o = p.others + (w == first || p.most == -INFINITY ? 0.0f : expf(tail ? p.most : 0.0f));
+    others += tail || p.most == -INFINITY ? o : o * expf(p.most - li.ref);
+    li.sum += p.top == -INFINITY ? p.sum : p.sum * ex2_approx((p.top - top) * k);
+  }
+  const float sum = others + expf(most - li.ref);
+  li.inv = tail ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+  li.shift = tail ? 0.0f : li.ref + (sum > 0.0f ? logf(sum) : 0.0f);
+  li.rest = tail ? (li.used ? fmaxf(-expm1f(most) - others, 0.0f) : 1.0f) : 0.0f;
+  // a teacher's log probabilities are rounded numbers: their sum may pass 1
+  if (tail && !(sum < 1.0f + 0x1p-8f)) li.flags |= SV_ROW_NAN;
+  if (!tail && li.used && !(sum > 0.0f)) li.flags |= SV_ROW_NAN;  // nothing to normalise
+  return li;
+}
+// an entry's gradient; st: the row's statistics
+__device__ __forceinline__ float listed_grad(const Entry &e, const List &li, const float4 &st, float k, float w) {
+  const float share = ex2_approx((e.x - st.z) * k) * st.w;
+  return (share - expf(e.value - li.ref) * li.inv) * w;
 }
 
 // Gradient of the unlisted elements of piece w.
@@ -218,110 +239,107 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
   const size_t r = blockIdx.x / C;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ List li;
+  __shared__ ListPart s_list[kListWarps];
   __shared__ RowPart s_part[kRowWarps];
   __shared__ unsigned long long s_all[kMaxRowCluster];  // reference and sum of each CTA
   __shared__ uint32_t s_flags[kMaxRowCluster];
   __shared__ uint32_t s_twice, s_singles;
-  __shared__ float4 s_stat;
+  __shared__ float s_loss[kListWarps];
   if (C > 1) cluster_arrive_relaxed();
   const T *row = (const T *)a.logits + (int64_t)r * a.row_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
   const int groups = row_groups(s);
   const bool resident = GRAD && groups <= a.resident;
   const int ahead = resident ? groups : kRing - 1;
-  // a byte for each piece of the slice, its bits the elements
+  // a bit for each element of the slice: a byte for a piece, the four of a thread in
+  // a group a word
   uint32_t *bits = (uint32_t *)(smem + (size_t)a.resident * kGroupBytes);
-  const unsigned char *piece_bits = (const unsigned char *)bits;
 
   for (int g = 0; g < ahead; ++g) {
     if (g < groups) load_group(row, s, g, g, smem);
     group_commit();
   }
-  for (int i = threadIdx.x; i < (s.v1 - s.v0 + 3) / 4; i += kRowThreads) bits[i] = 0;
+  const Entry e = read_entry(a, r, row);
+  const float single_x =
+      rank == 0 && (int)threadIdx.x < s.singles ? RowElem<T>::load(row + single_at<T>(s, threadIdx.x)) : -INFINITY;
+  for (int g = 0; g < groups; ++g) bits[g * kRowThreads + threadIdx.x] = 0;
   if (threadIdx.x == 0) s_twice = s_singles = 0;
-  read_list(li, a, r, row);
-  const bool skip = li.used == 0 && li.flags == 0;  // the same in every CTA
+  __syncthreads();
+  if (e.token >= 0 && in_slice<T>(s, rank, e.token)) {
+    const int i = e.token - s.head;
+    uint32_t was, bit;
+    if (i < 0 || i >= s.vecs * VEC) {
+      bit = 1u << (i < 0 ? e.token : e.token - s.vecs * VEC);
+      was = atomicOr(&s_singles, bit);
+    } else {
+      const int v = i / VEC - s.v0;
+      bit = 1u << (v % kGroupVecs / kRowThreads * 8 + i % VEC);
+      was = atomicOr(&bits[v / kGroupVecs * kRowThreads + v % kRowThreads], bit);
+    }
+    if (was & bit) s_twice = 1;
+  }
+  __syncthreads();
   const float k = a.k;
   const unsigned long long k2 = f2_splat(k);
   RowSums sums = row_sums();
-  uint32_t flags = li.flags;
-  if (!skip && !flags) {
-    if ((int)threadIdx.x < a.K) {
-      const int t = li.token[threadIdx.x];
-      if (t >= 0 && in_slice<T>(s, rank, t)) {
-        const int e = t - s.head;
-        uint32_t was, bit;
-        if (e < 0 || e >= s.vecs * VEC) {
-          bit = 1u << (e < 0 ? t : t - s.vecs * VEC);
-          was = atomicOr(&s_singles, bit);
-        } else {
-          const int v = e / VEC - s.v0;
-          bit = 1u << (8 * (v & 3) + e % VEC);
-          was = atomicOr(&bits[v >> 2], bit);
-        }
-        if (was & bit) s_twice = 1;
-      }
+  if ((int)threadIdx.x < s.singles && !(s_singles >> threadIdx.x & 1)) add_single<false>(sums, single_x, k);
+  int slot = 0, slot_load = kRing - 1;
+  for (int g = 0; g < groups; ++g) {
+    if (resident) {
+      wait_all_but(groups - 1 - g);
+    } else {
+      if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
+      group_commit();
+      group_wait<kRing - 1>();
     }
-    __syncthreads();
-    if (s_twice) flags |= SV_ROW_BAD_TOKEN;
-    if (rank == 0 && (int)threadIdx.x < s.singles && !(s_singles >> threadIdx.x & 1))
-      add_single<false>(sums, RowElem<T>::load(row + single_at<T>(s, threadIdx.x)), k);
-    int slot = 0, slot_load = kRing - 1;
-    for (int g = 0; g < groups; ++g) {
-      if (resident) {
-        wait_all_but(groups - 1 - g);
-      } else {
-        if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
-        group_commit();
-        group_wait<kRing - 1>();
-      }
-      const int at = resident ? g : slot;
-      uint4 w[kPieces];
-      uint32_t listed[kPieces], any = 0;
+    const int at = resident ? g : slot;
+    uint4 w[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, at, j);
+    const uint32_t listed = bits[g * kRowThreads + threadIdx.x];
+    if (listed) {  // -inf in their places
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        w[j] = ring_piece(smem, at, j);
-        const int v = g * kGroupVecs + j * kRowThreads + (int)threadIdx.x;
-        listed[j] = v < s.v1 - s.v0 ? piece_bits[v] : 0;
-        any |= listed[j];
+        if (!(listed >> (8 * j) & 0xffu)) continue;
+        float x[VEC];
+        RowElem<T>::unpack(w[j], x);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (listed >> (8 * j + i) & 1) x[i] = -INFINITY;
+        w[j] = RowElem<T>::pack(x);
       }
-      if (any) {  // -inf in their places
-#pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-          if (!listed[j]) continue;
-          float x[VEC];
-          RowElem<T>::unpack(w[j], x);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i)
-            if (listed[j] >> i & 1) x[i] = -INFINITY;
-          w[j] = RowElem<T>::pack(x);
-        }
-      }
-      float top = RowElem<T>::most(w[0]);
-#pragma unroll
-      for (int j = 1; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
-      if (top > sums.lim) raise<false>(sums, top, k);
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k2);
-      slot = slot + 1 == kRing ? 0 : slot + 1;
-      slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
     }
+    const float top = RowElem<T>::most4(w);
+    if (top > sums.lim) raise<false>(sums, top, k);
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k2);
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
   }
   group_wait<0>();
 
-  // the CTA's sums, then the cluster's, to every CTA
+  // the CTA's sums, then the cluster's, to every CTA; the list's in each
   const RowPart mine = warp_join(part_of(sums), k);
   if (lane == 0) s_part[warp] = mine;
+  if (warp < kListWarps) {
+    const ListPart p = list_part(e, a.tail, k);
+    if (lane == 0) s_list[warp] = p;
+  }
   __syncthreads();
   RowPart rest = warp_join(lane < kRowWarps ? s_part[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
+  const uint32_t twice = s_twice ? SV_ROW_BAD_TOKEN : 0u;
+  uint32_t flags = twice;
   if (C > 1) {
     cluster_wait();
     if (warp == 0 && lane < (int)C) {
       cluster_st_u64(&s_all[rank], lane, (unsigned long long)__float_as_uint(rest.l) << 32 | __float_as_uint(rest.top));
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&s_flags[rank], lane)), "r"(flags) : "memory");
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&s_flags[rank], lane)), "r"(twice) : "memory");
     }
-    cluster_sync();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  }
+  const List li = list_of(s_list, a.tail, k);
+  if (C > 1) {
+    cluster_wait();
     RowPart p{-INFINITY, 0.0f, 0.0f};
     if (lane < (int)C) {
       p.top = __uint_as_float((uint32_t)s_all[lane]);
@@ -330,69 +348,52 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
     rest = warp_join(p, k);
     flags = __reduce_or_sync(0xffffffffu, lane < (int)C ? s_flags[lane] : 0u);
   }
-  if (warp == 0) {
-    constexpr int E = kMaxList / 32;
-    float top = rest.top;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (li.token[lane + 32 * e] >= 0) top = fmaxf(top, li.x[lane + 32 * e]);
-    top = warp_max(top);
-    float sum = 0.0f;  // of the listed
-    const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (li.token[lane + 32 * e] >= 0) sum += ex2_approx((li.x[lane + 32 * e] - ref) * k);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const RowPart r_all = moved(rest, ref, k);
-    const float l = sum + r_all.l;
-    if (!(l > 0.0f)) flags |= SV_ROW_NAN;
-    if (skip) flags = 0;
-    const bool none = skip || flags;
+  // every warp: the row's sum, and what the unlisted elements' gradient takes
+  const bool skip = li.used == 0 && li.flags == 0;
+  const bool has_rest = rest.top != -INFINITY;
+  const float top = fmaxf(rest.top, li.top), ref = top == -INFINITY ? 0.0f : top;
+  const RowPart all = moved(rest, ref, k);
+  const float l = all.l + (li.top == -INFINITY ? 0.0f : li.sum * ex2_approx((li.top - ref) * k));
+  flags |= li.flags;
+  if (!(l > 0.0f)) flags |= SV_ROW_NAN;
+  if (skip) flags = 0;
+  // a list of the whole vocabulary leaves nothing, but for its rounding
+  const float t_rest = li.used == a.V ? 0.0f : li.rest;
+  const float coef = has_rest ? (all.l / l - t_rest) / rest.l : 0.0f;
+  const float4 st = skip || flags ? make_float4(__uint_as_float(flags), 0.0f, 0.0f, 0.0f)
+                                  : make_float4(has_rest ? rest.top : 0.0f, coef, ref, 1.0f / l);
+  if (rank == 0 && warp < kListWarps) {
     // ln s_v = (x_v - ref) / T - ln l, of the rest (rest.top - ref) / T + ln(rest.l / l)
-    const float log_l = logf(l);
-    float loss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = lane + 32 * e;
-      if (li.token[i] >= 0 && li.t[i] > 0.0f)
-        loss += li.t[i] * (li.log_t[i] - ((li.x[i] - ref) / a.temperature - log_l));
-    }
+    const float log_l = logf(l), t = expf(e.value - li.ref) * li.inv;
+    float loss = e.token >= 0 && t > 0.0f ? t * (e.value - li.shift - ((e.x - ref) / a.temperature - log_l)) : 0.0f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    const bool has_rest = rest.top != -INFINITY;
-    // a list of the whole vocabulary leaves nothing, but for its rounding
-    const float t_rest = li.used == a.V ? 0.0f : li.rest;
-    if (t_rest > 0.0f)
+    if (warp == 0 && t_rest > 0.0f)
       loss += t_rest * (logf(t_rest) - (has_rest ? (rest.top - ref) / a.temperature + logf(rest.l) - log_l : -INFINITY));
-    if (lane == 0) {
-      const float coef = has_rest ? (r_all.l / l - t_rest) / rest.l : 0.0f;
-      s_stat = none ? make_float4(__uint_as_float(flags), 0.0f, 0.0f, 0.0f)
-                    : make_float4(has_rest ? rest.top : 0.0f, coef, ref, 1.0f / l);
-      if (rank == 0) {
-        if (a.stat) a.stat[r] = s_stat;
-        a.loss[r] = skip ? 0.0f : flags ? __int_as_float(0x7fffffff) : loss;
-        a.status[r] = flags;
-      }
-    }
+    if (lane == 0) s_loss[warp] = loss;
   }
   if constexpr (GRAD) {
-    __syncthreads();
-    const float4 st = s_stat;
     const float w = (a.weight ? a.weight[r] : 1.0f) / a.temperature;
     T *grad = (T *)a.grad + (int64_t)r * a.grad_stride;
     // a row without a gradient has 0 for 1 / l
-    const float coef = st.w == 0.0f ? 0.0f : st.y * w;
+    const float c = st.w == 0.0f ? 0.0f : st.y * w;
     if (resident)
-      write_grad<T>(row, grad, s, rank, st.x, coef, k, [&](int g, int j, int) { return ring_piece(smem, g, j); });
+      write_grad<T>(row, grad, s, rank, st.x, c, k, [&](int g, int j, int) { return ring_piece(smem, g, j); });
     else
-      write_grad<T>(row, grad, s, rank, st.x, coef, k, [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
-    if (st.w == 0.0f) return;
+      write_grad<T>(row, grad, s, rank, st.x, c, k, [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
     __syncthreads();
-    if ((int)threadIdx.x < a.K) {
-      const int t = li.token[threadIdx.x];
-      if (t >= 0 && in_slice<T>(s, rank, t)) grad[t] = RowElem<T>::store(listed_grad(li, threadIdx.x, st, k, w));
-    }
+    if (st.w != 0.0f && e.token >= 0 && in_slice<T>(s, rank, e.token))
+      grad[e.token] = RowElem<T>::store(listed_grad(e, li, st, k, w));
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    float loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kListWarps; ++i) loss += s_loss[i];
+    if (a.stat) a.stat[r] = st;
+    a.loss[r] = skip ? 0.0f : flags ? __int_as_float(0x7fffffff) : loss;
+    a.status[r] = flags;
   }
 }
 
@@ -402,22 +403,26 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(DistillArg
   grid_dep_sync();
   const size_t r = blockIdx.x / C;
   const uint32_t rank = blockIdx.x % C;
-  __shared__ List li;
+  __shared__ ListPart s_list[kListWarps];
   const T *row = (const T *)a.logits + (int64_t)r * a.row_stride;
   T *grad = (T *)a.grad + (int64_t)r * a.grad_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
-  float4 st = a.stat[r];
+  const Entry e = read_entry(a, r, row);
+  const float4 st = a.stat[r];
   const float w = (a.weight ? a.weight[r] : 1.0f) / a.temperature;
-  read_list(li, a, r, row);
-  uint32_t flags = li.used == 0 ? li.flags : st.w == 0.0f ? __float_as_uint(st.x) | li.flags : li.flags;
+  if ((threadIdx.x >> 5) < kListWarps) {
+    const ListPart p = list_part(e, a.tail, a.k);
+    if ((threadIdx.x & 31) == 0) s_list[threadIdx.x >> 5] = p;
+  }
+  __syncthreads();
+  const List li = list_of(s_list, a.tail, a.k);
+  const uint32_t flags = li.flags | (li.used && st.w == 0.0f ? __float_as_uint(st.x) : 0u);
   const bool none = st.w == 0.0f || flags || li.used == 0;
   write_grad<T>(row, grad, s, rank, st.x, none ? 0.0f : st.y * w, a.k,
                 [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
   __syncthreads();
-  if (!none && (int)threadIdx.x < a.K) {
-    const int t = li.token[threadIdx.x];
-    if (t >= 0 && in_slice<T>(s, rank, t)) grad[t] = RowElem<T>::store(listed_grad(li, threadIdx.x, st, a.k, w));
-  }
+  if (!none && e.token >= 0 && in_slice<T>(s, rank, e.token))
+    grad[e.token] = RowElem<T>::store(listed_grad(e, li, st, a.k, w));
   if (rank == 0 && threadIdx.x == 0) a.status[r] = flags;
 }
 
@@ -440,7 +445,7 @@ Shape shape_of(int V, size_t es, long long R, bool grad) {
   const long long vecs = (long long)(row / 16), per = (vecs + z.C - 1) / z.C;
   const long long groups = (per + kGroupVecs - 1) / kGroupVecs;
   z.resident = grad && groups > kRing && groups <= kResident ? (int)groups : kRing;
-  z.smem = (size_t)z.resident * kGroupBytes + align_up((size_t)per, 4);
+  z.smem = (size_t)z.resident * kGroupBytes + (size_t)groups * kGroupVecs;
   return z;
 }
 
@@ -451,7 +456,7 @@ template <typename T, bool GRAD> cudaError_t launch_loss(DistillArgs a, cudaStre
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {  // as much as the longest rows take: a ring and a bit for each element
-    const size_t bits = (size_t)SV_MAX_VOCAB * sizeof(T) / 16 / kMaxRowCluster;
+    const size_t bits = (size_t)SV_MAX_VOCAB * sizeof(T) / 16 / kMaxRowCluster + kGroupVecs;
     const size_t a0 = kRing * (size_t)kGroupBytes + bits, b0 = kResident * (size_t)(kGroupBytes + kGroupVecs);
     const cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)((GRAD && b0 > a0 ? b0 : a0) + 16));

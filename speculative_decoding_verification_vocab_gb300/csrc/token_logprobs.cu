@@ -282,11 +282,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
       group_commit();
       group_wait<kRing - 1>();
       uint4 w[kPieces];
-      float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, slot, j);
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) top = fmaxf(top, RowElem<T>::most(w[j]));
+      const float top = RowElem<T>::most4(w);
       if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) add_piece<T, true>(sums, w[j], k2);

@@ -23,7 +23,15 @@ constexpr float kLog2eF = 1.4426950408889634f;
 // any does, and sums of 2^22 terms of 2^8 are far from the end of 32 bits.
 constexpr float kRefSlack = 8.0f;
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // ------------------------------------------------------------ element types
+// most, most4: the largest element of a piece, of a group's pieces (NaN ones passed
+// over)
 template <typename T> struct RowElem;
 template <> struct RowElem<float> {
   static constexpr int VEC = 4;
@@ -35,10 +43,18 @@ template <> struct RowElem<float> {
     x[2] = __uint_as_float(w.z);
     x[3] = __uint_as_float(w.w);
   }
-  // the largest element (NaN ones passed over)
   static __device__ __forceinline__ float most(const uint4 &w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
                  fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  static __device__ __forceinline__ float most4(const uint4 (&w)[kPieces]) {
+    float m = most(w[0]);
+#pragma unroll
+    for (int j = 1; j < kPieces; ++j) {
+      m = max3(m, __uint_as_float(w[j].x), __uint_as_float(w[j].y));
+      m = max3(m, __uint_as_float(w[j].z), __uint_as_float(w[j].w));
+    }
+    return m;
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -60,6 +76,13 @@ template <> struct RowElem<__nv_bfloat16> {
   static __device__ __forceinline__ float most(const uint4 &w) {
     const uint32_t m = bf2_max(bf2_max(w.x, w.y), bf2_max(w.z, w.w));
     return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  static __device__ __forceinline__ float most4(const uint4 (&w)[kPieces]) {
+    uint32_t m[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) m[j] = bf2_max(bf2_max(w[j].x, w[j].y), bf2_max(w[j].z, w[j].w));
+    const uint32_t a = bf2_max(bf2_max(m[0], m[1]), bf2_max(m[2], m[3]));
+    return fmaxf(bf16_lo(a), bf16_hi(a));
   }
   static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -87,6 +110,15 @@ template <> struct RowElem<__half> {
     const __half2 m = __hmax2(__hmax2(*(const __half2 *)&w.x, *(const __half2 *)&w.y),
                               __hmax2(*(const __half2 *)&w.z, *(const __half2 *)&w.w));
     const float2 f = __half22float2(m);
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ float most4(const uint4 (&w)[kPieces]) {
+    __half2 m[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      m[j] = __hmax2(__hmax2(*(const __half2 *)&w[j].x, *(const __half2 *)&w[j].y),
+                     __hmax2(*(const __half2 *)&w[j].z, *(const __half2 *)&w[j].w));
+    const float2 f = __half22float2(__hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3])));
     return fmaxf(f.x, f.y);
   }
   static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
