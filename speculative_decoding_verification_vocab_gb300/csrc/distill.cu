@@ -12,13 +12,19 @@
 // of its list, and with them their gradient is 2^((x - m) k) (s_r - t_r) / l.
 //
 // Bound: a row is read once and its gradient written once, 4 to 8 operations on
-// an element: memory.  A cluster of C CTAs takes a row.  With the gradient asked
-// for, a CTA keeps its slice (64 KB at V = 128256) in shared memory: it is summed
-// as it arrives, the cluster's sums are exchanged by one barrier, and the
-// gradient is taken from the copy.  Slices beyond shared memory are read twice,
-// and the loss alone streams through a ring.  Listed elements are found by a bit
-// for each element, set before the first piece is summed; they are few, so their
-// gradients are written one by one over the others', after a barrier.
+// an element: memory.  A cluster of C CTAs takes a row, each a slice that streams
+// through a ring of shared memory; the cluster's sums are exchanged by one barrier.
+// With the gradient asked for, a CTA then goes back through its slice: the last
+// three groups are still in the ring, the others come from L2 (so that few rows are
+// under way at once, 128 KB of a row to a CTA), and the gradient is stored past the
+// lines that are still to be read.  Listed elements are found by a bit for each
+// element, set before the first piece is summed; they are few, so their gradients
+// are written one by one over the others', after a barrier.
+//
+// 2048 rows of V = 128256 bf16, K = 64, loss and gradient: 202 us (5.2 TB/s, 0.77; 30
+// % of the elements come from memory again).  Slices kept in shared memory, 64 KB to a
+// CTA: 236 us (a third of the CTAs' time stands at barriers); clusters that go from
+// row to row with the next row's slice on its way: 301.
 #include <math.h>
 
 #include "vocab_rows.cuh"
@@ -28,7 +34,6 @@ namespace {
 
 constexpr int kMaxList = 128;
 constexpr int kRing = 3;          // groups of the ring that a slice streams through
-constexpr int kResident = 10;     // groups of a slice that stays in shared memory, at most
 
 struct DistillArgs {
   const void *logits;
@@ -42,7 +47,6 @@ struct DistillArgs {
   void *grad;
   int64_t grad_stride;
   uint32_t *status;
-  int resident;  // groups' places in shared memory
 };
 
 // The teacher's list, an entry to each of the CTA's first threads: its token (-1:
@@ -110,35 +114,34 @@ __device__ __forceinline__ ListPart list_part(const Entry &e, int tail, float k)
   p.flags = __reduce_or_sync(FULL, e.flags);
   return p;
 }
+// The list's, by every warp: a lane to each part.
 __device__ __forceinline__ List list_of(const ListPart *parts, int tail, float k) {
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  ListPart p{-INFINITY, 0.0f, -INFINITY, 0.0f, 0, 0u};
+  if (lane < kListWarps) p = parts[lane];
   List li;
-  float most = -INFINITY;
-  li.top = -INFINITY;
-  li.used = 0;
-  li.flags = 0;
-  int first = 0;
-#pragma unroll
-  for (int w = 0; w < kListWarps; ++w) {
-    if (parts[w].most > most) {
-      most = parts[w].most;
-      first = w;
-    }
-    li.top = fmaxf(li.top, parts[w].top);
-    li.used += parts[w].used;
-    li.flags |= parts[w].flags;
-  }
+  const float most = warp_max(p.most);
+  li.top = warp_max(p.top);
+  li.used = __reduce_add_sync(FULL, p.used);
+  li.flags = __reduce_or_sync(FULL, p.flags);
+  const int first = __ffs(__ballot_sync(FULL, p.most == most)) - 1;
   li.ref = tail || most == -INFINITY ? 0.0f : most;
-  const float top = li.top == -INFINITY ? 0.0f : li.top;
-  float others = 0.0f;  // all but the largest
-  li.sum = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kListWarps; ++w) {
-    const ListPart &p = parts[w];
-    // with tail the parts' sums are taken against 0, as the list's is
-    const float o = p.others + (w == first || p.most == -INFINITY ? 0.0f : expf(tail ? p.most : 0.0f));
-    others += tail || p.most == -INFINITY ? o : o * expf(p.most - li.ref);
-    li.sum += p.top == -INFINITY ? p.sum : p.sum * ex2_approx((p.top - top) * k);
+  // all but the largest; with tail the parts' sums are taken against 0, as the list's
+  // is, without against their own largest
+  float others = 0.0f;
+  if (p.most != -INFINITY) {
+    others = p.others + (lane == first ? 0.0f : expf(tail ? p.most : 0.0f));
+    if (!tail) others *= expf(p.most - li.ref);
   }
+  li.sum = p.top == -INFINITY ? p.sum : p.sum * ex2_approx((p.top - li.top) * k);
+#pragma unroll
+  for (int o = kListWarps / 2; o; o >>= 1) {
+    others += __shfl_xor_sync(FULL, others, o);
+    li.sum += __shfl_xor_sync(FULL, li.sum, o);
+  }
+  others = __shfl_sync(FULL, others, 0);
+  li.sum = __shfl_sync(FULL, li.sum, 0);
   const float sum = others + expf(most - li.ref);
   li.inv = tail ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
   li.shift = tail ? 0.0f : li.ref + (sum > 0.0f ? logf(sum) : 0.0f);
@@ -175,11 +178,13 @@ __device__ __forceinline__ float grad_of(float x, float m, float coef, float k) 
 }
 
 // The slice's gradient in full but for the listed elements: pieces from
-// `piece(g, j)` where the gradient's row lies on the 16-byte grid as the logits'
-// does, single elements otherwise (those of the logits come from memory again:
-// the two rows are different ones then).  coef 0: zeros, whatever the row holds.
+// `piece(g, j, v)` where the gradient's row lies on the 16-byte grid as the logits'
+// does, the last groups first; single elements otherwise (those of the logits come
+// from memory again: the two rows are different ones then).  coef 0: zeros, whatever
+// the row holds.
 template <typename T, typename F>
-__device__ void write_grad(const T *row, T *grad, const RowSlice &s, uint32_t rank, float m, float coef, float k, F piece) {
+__device__ __forceinline__ void write_grad(const T *row, T *grad, const RowSlice &s, uint32_t rank, float m, float coef, float k,
+                                           F piece) {
   constexpr int VEC = RowElem<T>::VEC;
   const bool zero = coef == 0.0f;
   if (rank == 0 && (int)threadIdx.x < s.singles) {
@@ -188,8 +193,7 @@ __device__ void write_grad(const T *row, T *grad, const RowSlice &s, uint32_t ra
   }
   if ((uintptr_t)row % 16 == (uintptr_t)grad % 16) {
     uint4 *out = (uint4 *)(grad + s.head);
-    const int groups = row_groups(s);
-    for (int g = 0; g < groups; ++g) {
+    for (int g = row_groups(s) - 1; g >= 0; --g) {
       const int v0 = s.v0 + g * kGroupVecs + (int)threadIdx.x;
       uint4 w[kPieces];  // all on their way before the first is stored
 #pragma unroll
@@ -198,7 +202,7 @@ __device__ void write_grad(const T *row, T *grad, const RowSlice &s, uint32_t ra
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
         if (v0 + j * kRowThreads < s.v1)
-          out[v0 + j * kRowThreads] = zero ? make_uint4(0, 0, 0, 0) : grad_piece<T>(w[j], m, coef, k);
+          __stcs(out + v0 + j * kRowThreads, zero ? make_uint4(0, 0, 0, 0) : grad_piece<T>(w[j], m, coef, k));
     }
   } else {
     const int lo = s.head + s.v0 * VEC, hi = s.head + s.v1 * VEC;
@@ -214,105 +218,166 @@ template <typename T> __device__ __forceinline__ bool in_slice(const RowSlice &s
   return v / RowElem<T>::VEC >= s.v0 && v / RowElem<T>::VEC < s.v1;
 }
 
-// waits until at most n of the groups asked for are on their way
-__device__ __forceinline__ void wait_all_but(int n) {
-  switch (n) {
-    case 0: return group_wait<0>();
-    case 1: return group_wait<1>();
-    case 2: return group_wait<2>();
-    case 3: return group_wait<3>();
-    case 4: return group_wait<4>();
-    case 5: return group_wait<5>();
-    case 6: return group_wait<6>();
-    case 7: return group_wait<7>();
-    case 8: return group_wait<8>();
-    default: return group_wait<9>();
+// A byte for each piece of a slice, its bits the elements; the four of a thread in a
+// group are a word.  Sets those of an entry's token; `twice` where it was set before.
+struct ListedBits {
+  uint32_t singles, twice;
+};
+template <typename T>
+__device__ __forceinline__ void set_bit(uint32_t *bits, ListedBits &l, const RowSlice &s, uint32_t rank, int token) {
+  constexpr int VEC = RowElem<T>::VEC;
+  if (token < 0 || !in_slice<T>(s, rank, token)) return;
+  const int i = token - s.head;
+  uint32_t was, bit;
+  if (i < 0 || i >= s.vecs * VEC) {
+    bit = 1u << (i < 0 ? token : token - s.vecs * VEC);
+    was = atomicOr(&l.singles, bit);
+  } else {
+    const int v = i / VEC - s.v0;
+    bit = 1u << (v % kGroupVecs / kRowThreads * 8 + i % VEC);
+    was = atomicOr(&bits[v / kGroupVecs * kRowThreads + v % kRowThreads], bit);
   }
+  if (was & bit) l.twice = 1;
 }
-static_assert(kResident <= 10, "wait_all_but");
+// The unlisted elements of a group's pieces into the sums.
+template <typename T>
+__device__ __forceinline__ void add_group(RowSums &sums, const unsigned char *ring, int at, uint32_t listed, float k,
+                                          unsigned long long k2) {
+  constexpr int VEC = RowElem<T>::VEC;
+  uint4 w[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(ring, at, j);
+  if (listed) {  // -inf in their places
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      if (!(listed >> (8 * j) & 0xffu)) continue;
+      float x[VEC];
+      RowElem<T>::unpack(w[j], x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (listed >> (8 * j + i) & 1) x[i] = -INFINITY;
+      w[j] = RowElem<T>::pack(x);
+    }
+  }
+  const float top = RowElem<T>::most4(w);
+  if (top > sums.lim) raise<false>(sums, top, k);
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k2);
+}
+// A CTA's sums and faults to every CTA of the cluster: the beginning, which arrives
+// at the cluster's barrier, and the end, which waits for it.
+struct Exchange {
+  unsigned long long part[kMaxRowCluster];  // reference and sum of each CTA
+  uint32_t flags[kMaxRowCluster];
+};
+__device__ __forceinline__ void push(Exchange &x, const RowPart &p, uint32_t flags, uint32_t rank, unsigned C) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < C) {
+    cluster_st_u64(&x.part[rank], lane, (unsigned long long)__float_as_uint(p.l) << 32 | __float_as_uint(p.top));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&x.flags[rank], lane)), "r"(flags) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ RowPart pull(const Exchange &x, uint32_t &flags, unsigned C, float k) {
+  const int lane = threadIdx.x & 31;
+  cluster_wait();
+  RowPart p{-INFINITY, 0.0f, 0.0f};
+  if (lane < (int)C) {
+    p.top = __uint_as_float((uint32_t)x.part[lane]);
+    p.l = __uint_as_float((uint32_t)(x.part[lane] >> 32));
+  }
+  flags = __reduce_or_sync(0xffffffffu, lane < (int)C ? x.flags[lane] : 0u);
+  return warp_join(p, k);
+}
+// What a row comes to, from the unlisted elements' sums and the list.
+struct Row {
+  float4 st;  // out_stat
+  float ref, l, t_rest;
+  uint32_t flags;
+  bool skip, has_rest;
+};
+__device__ __forceinline__ Row row_of(const DistillArgs &a, const RowPart &rest, const List &li, uint32_t flags) {
+  const float k = a.k;
+  Row r;
+  r.skip = li.used == 0 && li.flags == 0;
+  r.has_rest = rest.top != -INFINITY;
+  const float top = fmaxf(rest.top, li.top);
+  r.ref = top == -INFINITY ? 0.0f : top;
+  const RowPart all = moved(rest, r.ref, k);
+  r.l = all.l + (li.top == -INFINITY ? 0.0f : li.sum * ex2_approx((li.top - r.ref) * k));
+  r.flags = flags | li.flags;
+  if (!(r.l > 0.0f)) r.flags |= SV_ROW_NAN;
+  if (r.skip) r.flags = 0;
+  // a list of the whole vocabulary leaves nothing, but for its rounding
+  r.t_rest = li.used == a.V ? 0.0f : li.rest;
+  const float coef = r.has_rest ? (all.l / r.l - r.t_rest) / rest.l : 0.0f;
+  r.st = r.skip || r.flags ? make_float4(__uint_as_float(r.flags), 0.0f, 0.0f, 0.0f)
+                           : make_float4(r.has_rest ? rest.top : 0.0f, coef, r.ref, 1.0f / r.l);
+  return r;
+}
+// A list warp's part of the loss; the first warp's has the rest's term.
+__device__ __forceinline__ float loss_part(const DistillArgs &a, const Row &r, const RowPart &rest, const List &li,
+                                           const Entry &e) {
+  // ln s_v = (x_v - ref) / T - ln l, of the rest (rest.top - ref) / T + ln(rest.l / l)
+  const float log_l = logf(r.l), t = expf(e.value - li.ref) * li.inv;
+  float loss = e.token >= 0 && t > 0.0f ? t * (e.value - li.shift - ((e.x - r.ref) / a.temperature - log_l)) : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+  if (threadIdx.x < 32 && r.t_rest > 0.0f)
+    loss += r.t_rest *
+            (logf(r.t_rest) - (r.has_rest ? (rest.top - r.ref) / a.temperature + logf(rest.l) - log_l : -INFINITY));
+  return loss;
+}
+__device__ __forceinline__ void put_row(const DistillArgs &a, size_t r, const Row &row, const float *losses) {
+  float loss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kListWarps; ++i) loss += losses[i];
+  if (a.stat) a.stat[r] = row.st;
+  a.loss[r] = row.skip ? 0.0f : row.flags ? __int_as_float(0x7fffffff) : loss;
+  a.status[r] = row.flags;
+}
 
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, unsigned C) {
   grid_dep_sync();
-  constexpr int VEC = RowElem<T>::VEC;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t r = blockIdx.x / C;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ ListPart s_list[kListWarps];
   __shared__ RowPart s_part[kRowWarps];
-  __shared__ unsigned long long s_all[kMaxRowCluster];  // reference and sum of each CTA
-  __shared__ uint32_t s_flags[kMaxRowCluster];
-  __shared__ uint32_t s_twice, s_singles;
+  __shared__ Exchange s_all;
+  __shared__ ListedBits s_bits;
   __shared__ float s_loss[kListWarps];
   if (C > 1) cluster_arrive_relaxed();
   const T *row = (const T *)a.logits + (int64_t)r * a.row_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
   const int groups = row_groups(s);
-  const bool resident = GRAD && groups <= a.resident;
-  const int ahead = resident ? groups : kRing - 1;
-  // a bit for each element of the slice: a byte for a piece, the four of a thread in
-  // a group a word
-  uint32_t *bits = (uint32_t *)(smem + (size_t)a.resident * kGroupBytes);
+  uint32_t *bits = (uint32_t *)(smem + kRing * kGroupBytes);
 
-  for (int g = 0; g < ahead; ++g) {
+#pragma unroll
+  for (int g = 0; g < kRing - 1; ++g) {
     if (g < groups) load_group(row, s, g, g, smem);
     group_commit();
   }
   const Entry e = read_entry(a, r, row);
-  const float single_x =
-      rank == 0 && (int)threadIdx.x < s.singles ? RowElem<T>::load(row + single_at<T>(s, threadIdx.x)) : -INFINITY;
+  const bool has_single = rank == 0 && (int)threadIdx.x < s.singles;
+  const float single_x = has_single ? RowElem<T>::load(row + single_at<T>(s, threadIdx.x)) : -INFINITY;
   for (int g = 0; g < groups; ++g) bits[g * kRowThreads + threadIdx.x] = 0;
-  if (threadIdx.x == 0) s_twice = s_singles = 0;
+  if (threadIdx.x == 0) s_bits = ListedBits{0, 0};
   __syncthreads();
-  if (e.token >= 0 && in_slice<T>(s, rank, e.token)) {
-    const int i = e.token - s.head;
-    uint32_t was, bit;
-    if (i < 0 || i >= s.vecs * VEC) {
-      bit = 1u << (i < 0 ? e.token : e.token - s.vecs * VEC);
-      was = atomicOr(&s_singles, bit);
-    } else {
-      const int v = i / VEC - s.v0;
-      bit = 1u << (v % kGroupVecs / kRowThreads * 8 + i % VEC);
-      was = atomicOr(&bits[v / kGroupVecs * kRowThreads + v % kRowThreads], bit);
-    }
-    if (was & bit) s_twice = 1;
-  }
+  set_bit<T>(bits, s_bits, s, rank, e.token);
   __syncthreads();
   const float k = a.k;
   const unsigned long long k2 = f2_splat(k);
   RowSums sums = row_sums();
-  if ((int)threadIdx.x < s.singles && !(s_singles >> threadIdx.x & 1)) add_single<false>(sums, single_x, k);
+  if (has_single && !(s_bits.singles >> threadIdx.x & 1)) add_single<false>(sums, single_x, k);
   int slot = 0, slot_load = kRing - 1;
   for (int g = 0; g < groups; ++g) {
-    if (resident) {
-      wait_all_but(groups - 1 - g);
-    } else {
-      if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
-      group_commit();
-      group_wait<kRing - 1>();
-    }
-    const int at = resident ? g : slot;
-    uint4 w[kPieces];
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, at, j);
-    const uint32_t listed = bits[g * kRowThreads + threadIdx.x];
-    if (listed) {  // -inf in their places
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        if (!(listed >> (8 * j) & 0xffu)) continue;
-        float x[VEC];
-        RowElem<T>::unpack(w[j], x);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (listed >> (8 * j + i) & 1) x[i] = -INFINITY;
-        w[j] = RowElem<T>::pack(x);
-      }
-    }
-    const float top = RowElem<T>::most4(w);
-    if (top > sums.lim) raise<false>(sums, top, k);
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) add_piece<T, false>(sums, w[j], k2);
+    if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
+    group_commit();
+    group_wait<kRing - 1>();
+    add_group<T>(sums, smem, slot, bits[g * kRowThreads + threadIdx.x], k, k2);
     slot = slot + 1 == kRing ? 0 : slot + 1;
     slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
   }
@@ -327,74 +392,35 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
   }
   __syncthreads();
   RowPart rest = warp_join(lane < kRowWarps ? s_part[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
-  const uint32_t twice = s_twice ? SV_ROW_BAD_TOKEN : 0u;
-  uint32_t flags = twice;
+  uint32_t flags = s_bits.twice ? SV_ROW_BAD_TOKEN : 0u;
   if (C > 1) {
     cluster_wait();
-    if (warp == 0 && lane < (int)C) {
-      cluster_st_u64(&s_all[rank], lane, (unsigned long long)__float_as_uint(rest.l) << 32 | __float_as_uint(rest.top));
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&s_flags[rank], lane)), "r"(twice) : "memory");
-    }
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    push(s_all, rest, flags, rank, C);
   }
   const List li = list_of(s_list, a.tail, k);
-  if (C > 1) {
-    cluster_wait();
-    RowPart p{-INFINITY, 0.0f, 0.0f};
-    if (lane < (int)C) {
-      p.top = __uint_as_float((uint32_t)s_all[lane]);
-      p.l = __uint_as_float((uint32_t)(s_all[lane] >> 32));
-    }
-    rest = warp_join(p, k);
-    flags = __reduce_or_sync(0xffffffffu, lane < (int)C ? s_flags[lane] : 0u);
-  }
-  // every warp: the row's sum, and what the unlisted elements' gradient takes
-  const bool skip = li.used == 0 && li.flags == 0;
-  const bool has_rest = rest.top != -INFINITY;
-  const float top = fmaxf(rest.top, li.top), ref = top == -INFINITY ? 0.0f : top;
-  const RowPart all = moved(rest, ref, k);
-  const float l = all.l + (li.top == -INFINITY ? 0.0f : li.sum * ex2_approx((li.top - ref) * k));
-  flags |= li.flags;
-  if (!(l > 0.0f)) flags |= SV_ROW_NAN;
-  if (skip) flags = 0;
-  // a list of the whole vocabulary leaves nothing, but for its rounding
-  const float t_rest = li.used == a.V ? 0.0f : li.rest;
-  const float coef = has_rest ? (all.l / l - t_rest) / rest.l : 0.0f;
-  const float4 st = skip || flags ? make_float4(__uint_as_float(flags), 0.0f, 0.0f, 0.0f)
-                                  : make_float4(has_rest ? rest.top : 0.0f, coef, ref, 1.0f / l);
+  if (C > 1) rest = pull(s_all, flags, C, k);
+  const Row out = row_of(a, rest, li, flags);
   if (rank == 0 && warp < kListWarps) {
-    // ln s_v = (x_v - ref) / T - ln l, of the rest (rest.top - ref) / T + ln(rest.l / l)
-    const float log_l = logf(l), t = expf(e.value - li.ref) * li.inv;
-    float loss = e.token >= 0 && t > 0.0f ? t * (e.value - li.shift - ((e.x - ref) / a.temperature - log_l)) : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    if (warp == 0 && t_rest > 0.0f)
-      loss += t_rest * (logf(t_rest) - (has_rest ? (rest.top - ref) / a.temperature + logf(rest.l) - log_l : -INFINITY));
+    const float loss = loss_part(a, out, rest, li, e);
     if (lane == 0) s_loss[warp] = loss;
   }
   if constexpr (GRAD) {
     const float w = (a.weight ? a.weight[r] : 1.0f) / a.temperature;
     T *grad = (T *)a.grad + (int64_t)r * a.grad_stride;
     // a row without a gradient has 0 for 1 / l
-    const float c = st.w == 0.0f ? 0.0f : st.y * w;
-    if (resident)
-      write_grad<T>(row, grad, s, rank, st.x, c, k, [&](int g, int j, int) { return ring_piece(smem, g, j); });
-    else
-      write_grad<T>(row, grad, s, rank, st.x, c, k, [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
+    const float c = out.st.w == 0.0f ? 0.0f : out.st.y * w;
+    // (the logits may be the gradient's own place: a piece is read, by whoever writes
+    // there, before it is written)
+    write_grad<T>(row, grad, s, rank, out.st.x, c, k, [&](int g, int j, int v) {
+      return g >= groups - kRing ? ring_piece(smem, g % kRing, j) : ((const uint4 *)(row + s.head))[v];
+    });
     __syncthreads();
-    if (st.w != 0.0f && e.token >= 0 && in_slice<T>(s, rank, e.token))
-      grad[e.token] = RowElem<T>::store(listed_grad(e, li, st, k, w));
+    if (out.st.w != 0.0f && e.token >= 0 && in_slice<T>(s, rank, e.token))
+      grad[e.token] = RowElem<T>::store(listed_grad(e, li, out.st, k, w));
   } else {
     __syncthreads();
   }
-  if (rank == 0 && threadIdx.x == 0) {
-    float loss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kListWarps; ++i) loss += s_loss[i];
-    if (a.stat) a.stat[r] = st;
-    a.loss[r] = skip ? 0.0f : flags ? __int_as_float(0x7fffffff) : loss;
-    a.status[r] = flags;
-  }
+  if (rank == 0 && threadIdx.x == 0) put_row(a, r, out, s_loss);
 }
 
 // The gradient from a forward pass's statistics: CTA `rank` of C of a row.
@@ -426,44 +452,30 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(DistillArg
   if (rank == 0 && threadIdx.x == 0) a.status[r] = flags;
 }
 
-// CTAs to a row and groups' places of each: with a gradient slices of 64 KB, so
-// that three CTAs fit an SM and one's sums hide behind the others' rows; smaller
-// ones where a batch of few rows would leave SMs idle.
-struct Shape {
-  unsigned C;
-  int resident;
-  size_t smem;
-};
-Shape shape_of(int V, size_t es, long long R, bool grad) {
-  const size_t row = (size_t)V * es;
-  Shape z;
-  z.C = 1;
-  if (grad)
-    while (z.C < kMaxRowCluster && (row > z.C * (size_t)65536 || (row > z.C * (size_t)16384 && R * z.C < 456))) z.C *= 2;
+template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, cudaStream_t st) {
+  // CTAs to a row: with a gradient 128 KB of it to each (256 or 64 KB, C = 1 or 4 at V =
+  // 128256 bf16: 229 and 206 us where these take 202), less where a batch of few rows
+  // would leave SMs idle
+  const size_t row = (size_t)a.V * sizeof(T);
+  unsigned C = 1;
+  if (GRAD)
+    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C < 456))) C *= 2;
   else
-    z.C = row_ctas(row, R, 16384, 1216);
-  const long long vecs = (long long)(row / 16), per = (vecs + z.C - 1) / z.C;
-  const long long groups = (per + kGroupVecs - 1) / kGroupVecs;
-  z.resident = grad && groups > kRing && groups <= kResident ? (int)groups : kRing;
-  z.smem = (size_t)z.resident * kGroupBytes + (size_t)groups * kGroupVecs;
-  return z;
-}
-
-template <typename T, bool GRAD> cudaError_t launch_loss(DistillArgs a, cudaStream_t st) {
-  const Shape z = shape_of(a.V, sizeof(T), a.R, GRAD);
-  a.resident = z.resident;
+    C = row_ctas(row, a.R, 16384, 1216);
+  auto smem_of = [](size_t bytes, unsigned c) {  // the ring, and a bit for each element in whole groups
+    const size_t per = (bytes / 16 + c - 1) / c, groups = (per + kGroupVecs - 1) / kGroupVecs;
+    return kRing * (size_t)kGroupBytes + groups * kGroupVecs;
+  };
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev != set_dev) {  // as much as the longest rows take: a ring and a bit for each element
-    const size_t bits = (size_t)SV_MAX_VOCAB * sizeof(T) / 16 / kMaxRowCluster + kGroupVecs;
-    const size_t a0 = kRing * (size_t)kGroupBytes + bits, b0 = kResident * (size_t)(kGroupBytes + kGroupVecs);
+  if (dev != set_dev) {  // as much as the longest rows take
     const cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)((GRAD && b0 > a0 ? b0 : a0) + 16));
+                                               (int)smem_of((size_t)SV_MAX_VOCAB * sizeof(T), kMaxRowCluster));
     if (e != cudaSuccess) return e;
     set_dev = dev;
   }
-  return launch_pdl_cluster(distill_kernel<T, GRAD>, dim3((unsigned)a.R * z.C), dim3(kRowThreads), z.C, z.smem, st, a, z.C);
+  return launch_pdl_cluster(distill_kernel<T, GRAD>, dim3((unsigned)a.R * C), dim3(kRowThreads), C, smem_of(row, C), st, a, C);
 }
 template <typename T> cudaError_t launch_grad(const DistillArgs &a, cudaStream_t st) {
   // 64 KB of a row to a CTA
@@ -520,7 +532,6 @@ sv_status check_args(DistillArgs &a, const void *logits, int64_t row_stride, sv_
   a.grad = grad;
   a.grad_stride = grad_stride;
   a.status = status;
-  a.resident = 0;
   return SV_OK;
 }
 

@@ -169,6 +169,40 @@ def test_many_rows(R):
         assert float(((got.double() - grad).abs() - 2.0 ** -8 * grad.abs()).max()) <= 1e-4
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [130, 5003, 20011, 70001])
+def test_many_rows_with_faults_and_short_lists(V, dtype):
+    """More rows than clusters run at once, each CTA going from row to row: rows
+    without a list, faulty ones and ordinary ones after each other."""
+    R, K = 1000 if V < 6000 else 950, 128 if V < 6000 else 33
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = (torch.randn(R, V, generator=g, device=DEV) * 3).to(dtype)
+    top = torch.log_softmax(x.double() + torch.randn(R, V, generator=g, device=DEV), -1).topk(K, -1)
+    token, value = top.indices.to(torch.int32), top.values.float()
+    r = torch.arange(R, device=DEV)
+    token[r % 7 == 1, 5:] = -1
+    token[r % 11 == 2] = -1
+    token[r % 13 == 3, 1] = token[r % 13 == 3, 4]
+    token[r % 17 == 4, 2] = V
+    x[r % 19 == 5, V // 2] = math.nan
+    value[r % 23 == 6, 3] = math.inf
+    x[r % 29 == 7, V // 3:] = -math.inf
+    weight = torch.rand(R, generator=g, device=DEV) + 0.5
+    for tail in (True, False):
+        both = sv.distill_loss(x, token, value, weight=weight, tail=tail, grad=True)
+        at = x.clone()
+        again = sv.distill_loss(at, token, value, weight=weight, tail=tail, out_grad=at)
+        assert torch.equal(at, both["grad"]) and torch.equal(again["status"], both["status"])
+        some = torch.cat([torch.arange(0, 60), torch.arange(R - 60, R)])
+        f = lambda t: t[some.to(DEV)].float().cpu().numpy()  # noqa: E731
+        compare(x.cpu()[some], token.cpu()[some], value.cpu()[some], weight.cpu()[some], 1.0, tail, f(both["loss"]),
+                f(both["grad"]), both["status"].cpu().numpy()[some])
+        few = sv.distill_loss(x[:100].contiguous(), token[:100], value[:100], weight=weight[:100], tail=tail, grad=True)
+        assert torch.equal(few["status"], both["status"][:100])
+        ok = few["loss"].isfinite()
+        assert float((few["loss"] - both["loss"][:100])[ok].abs().max()) <= 1e-4
+
+
 def test_slices_beyond_shared_memory():
     """Rows so long that the gradient reads them a second time."""
     for V, dtype in ((1 << 21, torch.float32), (sv.SV_MAX_VOCAB, torch.bfloat16), (900001, torch.float32)):
