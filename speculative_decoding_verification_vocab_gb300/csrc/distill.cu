@@ -461,7 +461,7 @@ template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, c
   if (GRAD)
     while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C < 456))) C *= 2;
   else
-    C = row_ctas(row, a.R, 16384, 1216);
+    C = row_ctas(row, a.R, 16384, 608);
   auto smem_of = [](size_t bytes, unsigned c) {  // the ring, and a bit for each element in whole groups
     const size_t per = (bytes / 16 + c - 1) / c, groups = (per + kGroupVecs - 1) / kGroupVecs;
     return kRing * (size_t)kGroupBytes + groups * kGroupVecs;

@@ -102,23 +102,30 @@ __device__ void keep_best(u64 *keys, int n, int K) {
 }
 
 // The largest 16-bit number that K of the CTA's 256 keys reach (0: fewer have more),
-// bit by bit; for one warp.
+// two bits at a time; for one warp.  The counts of the three numbers that the next
+// two bits make stand in one word.
 __device__ __forceinline__ uint32_t reached_by(const uint16_t *keys, int K) {
-  constexpr int E = kRowThreads / 32;
+  static_assert(kRowThreads == 256, "a vector of 8 keys to a lane, counts of 10 bits");
   const uint4 q = ((const uint4 *)keys)[threadIdx.x & 31];
-  static_assert(E == 8, "a vector of 8 keys to a lane");
   const uint32_t pairs[4] = {q.x, q.y, q.z, q.w};
   uint32_t t = 0;
-#pragma unroll 4
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t at = t | 1u << bit;
-    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += ((pairs[i] & 0xffffu) >= at) + (pairs[i] >> 16 >= at);
-    if (__reduce_add_sync(0xffffffffu, n) >= K) t = at;
+  for (int bit = 14; bit >= 0; bit -= 2) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+      const uint32_t at = t | (uint32_t)d << bit;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        n += ((pairs[i] & 0xffffu) >= at ? 1u << 10 * (d - 1) : 0u) + (pairs[i] >> 16 >= at ? 1u << 10 * (d - 1) : 0u);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    const uint32_t k = (uint32_t)K;
+    t |= (n >> 20 >= k ? 3u : (n >> 10 & 1023u) >= k ? 2u : (n & 1023u) >= k ? 1u : 0u) << bit;
   }
   return t;
 }
+
 // x rounded up to the upper 16 bits of a float
 __device__ __forceinline__ uint16_t up16(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -323,9 +330,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     };
     if (has_single) offer(single_x, single);
     // the runs that reach it, then their pieces over all threads: one way to L2
-    for (int i = 0; i < run; ++i) {
-      const float top = __uint_as_float((uint32_t)runs[i * kRowThreads + threadIdx.x] << 16);
-      if (top >= tau && top > -INFINITY) hits[atomicAdd(&s_hits, 1)] = (uint16_t)(i * kRowThreads + threadIdx.x);
+    if (thread_top >= tau && thread_top > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < kRuns; ++i) {
+        const float top = __uint_as_float((uint32_t)runs[i * kRowThreads + threadIdx.x] << 16);
+        if (i < run && top >= tau) hits[atomicAdd(&s_hits, 1)] = (uint16_t)(i * kRowThreads + threadIdx.x);
+      }
     }
     __syncthreads();
     const int of_run = per * kPieces, pieces = s_hits * of_run;
@@ -492,7 +502,7 @@ extern "C" sv_status sv_token_logprobs(const void *logits, int64_t seq_stride, i
   a.top_token = out_top_token;
   a.top_logprob = out_top_logprob;
   a.status = out_status;
-  const unsigned C = row_ctas((size_t)V * es, (long long)B * P, 16384, 1216);
+  const unsigned C = row_ctas((size_t)V * es, (long long)B * P, 16384, 608);
   cudaStream_t st = (cudaStream_t)stream;
   LaunchScope ls("token_logprobs", st);
   const unsigned items = (unsigned)(B * P);

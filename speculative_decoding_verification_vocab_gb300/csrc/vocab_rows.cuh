@@ -265,8 +265,10 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// CTAs to a row: one for each `bytes` of it while the grid has room for more
-// CTAs than run at once
+// CTAs to a row: one for each `bytes` of it while the grid has room for `want`, as
+// many as run at once (more of them: each has its way to the first piece and its
+// joins; 1000 rows of 201 KB with 64 alternatives take 51 us by one CTA each, 67 by
+// two, 105 by four)
 inline unsigned row_ctas(size_t row_bytes, long long rows, size_t bytes, long long want) {
   unsigned c = 1;
   while (c < kMaxRowCluster && row_bytes > c * bytes && rows * c < want) c *= 2;
