@@ -1159,9 +1159,22 @@ sv_status enqueue(const Sizes &z, const void *q, const void *kv, int64_t kv_stri
 
 }  // namespace
 
+// A batch of so many heads is left whole, a unit to each (sequence, head): what
+// follows a shared prefix is short (128 sequences of 1 to 600 slots, 8 KV heads: MEASURED).
+static bool sums_sizes(Sizes &z, int B, int Hq, int Hkv, int D, int page, int max_pages) {
+  if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, 0, 0, 0)) return false;
+  if ((long long)B * z.NH >= 2LL * slots_of(D)) {
+    z.finding = kWhole;
+    z.groups = B;
+    z.units = (long long)B * z.NH;
+    z.total = 0;
+  }
+  return true;
+}
+
 bool paged_sums_workspace(size_t *bytes, int B, int Hq, int Hkv, int D, int page, int max_pages) {
   Sizes z;
-  if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, 0, 0, 0)) return false;
+  if (!sums_sizes(z, B, Hq, Hkv, D, page, max_pages)) return false;
   *bytes = z.total;
   return true;
 }
@@ -1171,7 +1184,7 @@ sv_status paged_sums(const void *q, const void *kv, int64_t kv_stride, int64_t p
                      int max_pages, int num_pages, float scale, float *o, float2 *ml, uint32_t *flags, void *workspace,
                      cudaStream_t st) {
   Sizes z;
-  if (!sizes_of(z, B, Hq, Hkv, D, page, max_pages, 0, 0, 0))
+  if (!sums_sizes(z, B, Hq, Hkv, D, page, max_pages))
     return set_error(SV_ERR_UNSUPPORTED, "more than 2^30 slots a sequence, or too many work units");
   return enqueue(z, q, kv, kv_stride, page_stride, dt, block_table, seq_len, B, Hq, Hkv, D, page, max_pages, num_pages,
                  0, 0, scale, nullptr, 0, nullptr, nullptr, flags, o, ml, workspace, st);

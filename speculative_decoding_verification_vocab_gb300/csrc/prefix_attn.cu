@@ -27,12 +27,10 @@
 // same keys or, where the last column has one tile only, those of even and odd key
 // tiles, which the join puts together like any two parts.
 //   warps 0-1   producers, of K and of V: page table entries a tile ahead, TMA
-//               boxes of 64 columns of as many rows as divide the page (128-byte
-//               swizzled) into a ring; pages behind the last are out of the map's
-//               bounds and arrive as zeros.  Pages that four rows do not divide,
-//               and caches in host memory, go by asynchronous copies of 16 bytes
-//               (twice the time: a box is one instruction, and 32 copies are one
-//               for 512 bytes);
+//               boxes of 64 columns (128-byte swizzled) of as many rows as lie in a
+//               page, a lane to each; pages behind the last are out of the map's
+//               bounds and arrive as zeros.  Small pages and caches in host memory go
+//               by asynchronous copies of 16 bytes (both warps both);
 //   warps 2-3   MMA issuers, one to a buffer, so that one's waits lie behind the
 //               other's products: S = Q K^T from shared memory, O += P V with P in
 //               tensor memory, in the place of the S it comes from;
@@ -53,7 +51,7 @@ namespace sv {
 namespace {
 
 constexpr int kRows = 128;   // query rows of a tile = tensor-memory lanes
-constexpr int kKeys = 128;   // keys of a tile
+constexpr int kKeys = 128;   // rows of a tile of keys, of which a call uses a.keys
 constexpr int kProducers = 64;
 constexpr int kMmaWarp = kProducers / 32, kFirstSoftmax = kMmaWarp + 2;
 // 12 warps: registers are given out to four warps at a time, and the softmax needs
@@ -117,7 +115,7 @@ struct PrefixArgs {
   const int32_t *table, *len;  // [N][max_pages], [N]
   int B, N, W, Hq, Hkv, G, mtiles;  // query tiles of a KV head
   int page, page_shift, max_pages, num_pages, cap;
-  int box;  // rows of a TMA box
+  int keys, box;  // keys of a tile; rows of a TMA box
   int shares2, shares1, rows;  // CTAs of a column of two tiles, and of one; rows of a part's buffer: min(128, W G)
   float scale_log2;
   // workspace: sums [parts][2][rows][D], references and sums of exponentials
@@ -128,11 +126,15 @@ struct PrefixArgs {
 };
 
 __device__ __forceinline__ int tiles_of(const PrefixArgs &a, int len) {
-  return len < 0 || len > a.cap ? 0 : (len + kKeys - 1) / kKeys;
+  return len < 0 || len > a.cap ? 0 : (int)(((unsigned)len + (unsigned)a.keys - 1) / (unsigned)a.keys);
 }
 // tiles of all prefixes and of those before p, over the lanes of a warp
 __device__ __forceinline__ longlong2 count_tiles(const PrefixArgs &a, int p) {
   longlong2 n = make_longlong2(0, 0);
+  if (a.N == 1) {
+    n.x = tiles_of(a, __ldcg(a.len));
+    return n;
+  }
   for (int i = threadIdx.x & 31; i < a.N; i += 32) {
     const int t = tiles_of(a, __ldcg(a.len + i));
     n.x += t;
@@ -149,6 +151,11 @@ __device__ __forceinline__ longlong2 count_tiles(const PrefixArgs &a, int p) {
 // Shares of a column that so many tiles are cut into: none without one.
 __device__ __forceinline__ long long cut_into(long long shares, long long tiles) {
   return min(shares, max(tiles, 1LL));
+}
+// The share that tile t is in.
+__device__ __forceinline__ int share_of(long long t, long long shares, long long tiles) {
+  const unsigned long long x = (unsigned long long)(t + 1) * shares - 1;
+  return x >> 32 || tiles >> 32 ? (int)(x / (unsigned long long)tiles) : (int)((uint32_t)x / (uint32_t)tiles);
 }
 // Part of a column's share r in segment sg: from part to part of a column one or
 // the other grows.
@@ -295,6 +302,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (TMA && a.keys < kKeys) {
+    // rows of V that no box reaches: zeros, for weights of 0 to multiply
+    const int rows = kKeys - a.keys, per = rows * 8;  // 16-byte pieces of a box
+    for (int i = threadIdx.x; i < kV * (D / 64) * per; i += kThreads) {
+      const int b = i / per, e = i % per;
+      *(uint4 *)(sm + R::kOffV + b * kBox + a.keys * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   grid_dep_sync();
   if (warp == 0) {
     // this CTA's column and share, and the prefix it starts in
@@ -338,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (TMA && warp < kMmaWarp) {
     // ------------------------------------------------------------ producers
     // Warp 0 loads K, warp 1 V; a lane to each box of a tile.
-    const int boxes = kKeys / a.box;
+    const int boxes = a.keys / a.box;
+    const uint32_t bytes = (uint32_t)a.keys * D * 2;
     const int places = warp ? kV : kK, full = warp ? R::kFullV : R::kFullK, free = warp ? R::kFreeV : R::kFreeK;
     int t_all = 0, at = 0;  // tiles so far, and the next one's place
     uint32_t seen = 1;      // parity of the phase that frees it
@@ -347,21 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false;
       const int32_t *table = a.table + (size_t)w.p * a.max_pages;
       auto fetch = [&](int t) {
-        const int slot = t * kKeys + lane * a.box;
+        const int slot = t * a.keys + lane * a.box;
         return lane < boxes && t < w.t1 && slot < w.len
                    ? __ldg(table + (a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page))
                    : -1;
       };
       int id = fetch(w.t0);
       for (int t = w.t0; ok && t < w.t1; ++t, ++t_all) {
-        const int slot = t * kKeys + lane * a.box, r = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
+        const int slot = t * a.keys + lane * a.box, r = a.page_shift >= 0 ? slot & (a.page - 1) : slot % a.page;
         const bool there = (unsigned)id < (unsigned)a.num_pages;
         bad |= lane < boxes && slot < w.len && !there;
         const int page = there ? id : a.num_pages;  // out of bounds: zeros
         id = fetch(t + 1);
         ok = all(t_all < places || mbar_wait(bar(free + at), seen, abort));
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(bar(full + at), kTileBytes);
+        if (lane == 0) mbar_expect_tx(bar(full + at), bytes);
         __syncwarp();
         if (lane < boxes) {
           const uint32_t dst = sm0 + (warp ? R::kOffV : 0) + at * kTileBytes + lane * a.box * 128;
@@ -511,8 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The last tile's product takes the steps of 16 keys that hold one; a box
         // may bring rows behind the last key, which may hold anything: zeros there
         // (from both issuers), so that weights of 0 add 0.
-        const int left = w.len - (w.first_for(s) + i * step) * kKeys, steps = left < kKeys ? (left + 15) >> 4 : kKeys / 16;
-        if (TMA && left < kKeys && (left & 15)) {
+        const int left = w.len - (w.first_for(s) + i * step) * a.keys;
+        const int steps = (min(left, a.keys) + 15) >> 4;
+        if (TMA && left < a.keys && (left & 15)) {
           const int at = left + (lane >> 1);
           if (at < 16 * steps) {
             uint8_t *v = sm + R::kOffV + v_at * kTileBytes + at * 128 + (lane & 1) * 64;
@@ -590,11 +608,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_ref = -INFINITY;  // log2 units
       unsigned long long l2[2] = {0ull, 0ull};
-      for (int i = 0; i < n; ++i, ++g) {
+      int behind = w.len - w.first_for(s) * a.keys;  // keys from this tile's first to the last
+      const int stride = w.pair ? a.keys : 2 * a.keys;
+      for (int i = 0; i < n; ++i, ++g, behind -= stride) {
         ok = all(mbar_wait(bar(R::kS + s), g & 1, abort));
         if (!ok) break;
         tc_fence_after();
-        const int left = w.len - (w.first_for(s) + (w.pair ? i : 2 * i)) * kKeys;  // keys of this tile
+        const int left = min(behind, a.keys);  // keys of this tile
         uint32_t x[4][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) tm_ld32(tS + 32 * c, x[c]);
@@ -602,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int half = decltype(which)::value;
 #pragma unroll
           for (int c = 2 * half; c < 2 * half + 2; ++c) tm_wait_ld(x[c]);
-          if (left < kKeys) {
+          if (left < 64 * half + 64) {
 #pragma unroll
             for (int c = 2 * half; c < 2 * half + 2; ++c)
 #pragma unroll
@@ -729,63 +749,86 @@ struct JoinArgs {
 };
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, JoinArgs j) {
+  const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const bool live = row < (long long)a.B * a.Hq;
-  const int b = live ? (int)(row / a.Hq) : 0, h = live ? (int)(row % a.Hq) : 0;
-  const int p = b / a.W, at = b % a.W * a.G + h % a.G;
+  const int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // below 2^26
+  const bool live = row < a.B * a.Hq;
+  const int b = live ? row / a.Hq : 0, h = live ? row - b * a.Hq : 0;
+  const int p = b / a.W, head = h / a.G, at = (b - p * a.W) * a.G + h - head * a.G;
   const int mt = at / kRows, r = at % kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
   // lengths were there before the launches that this one waits for
   const longlong2 n = count_tiles(a, p);
   const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
+  int c0 = 0, parts = 0;  // shares with a part
+  if (tiles > 0) {
+    const long long all = n.x * a.Hkv, first = n.y * a.Hkv + (long long)tiles * head;
+    const long long shares = cut_into(pair ? a.shares2 : a.shares1, all);
+    c0 = share_of(first, shares, all);
+    parts = share_of(first + tiles - 1, shares, all) - c0 + 1;
+  }
+  // places in the parts: that of the row's query tile in a pair, both otherwise
+  const int two = pair ? 0 : 1, places = parts << two;
+  const size_t part0 = part_at(a, column, (long long)p * a.Hkv + head + c0);
+  const size_t place0 = (part0 * 2 + (pair ? mt & 1 : 0)) * a.rows + r, step = (size_t)a.rows << (1 - two);
   grid_dep_sync();
   if (!live) return;
   uint32_t flag = (len < 0 || len > a.cap ? SV_ROW_BAD_LEN : 0u) | j.own_flag[b];
   const float2 own = j.own_ml[row];
-  long long c0 = 0, c1 = -1;  // shares with a part
-  if (tiles > 0) {
-    const long long all = n.x * a.Hkv, first = n.y * a.Hkv + (long long)tiles * (h / a.G);
-    const long long shares = cut_into(pair ? a.shares2 : a.shares1, all);
-    c0 = ((first + 1) * shares - 1) / all;
-    c1 = ((first + tiles) * shares - 1) / all;
-  }
-  const size_t part0 = part_at(a, column, (long long)p * a.Hkv + h / a.G + c0);
-  // places in the parts: that of the row's query tile in a pair, both otherwise
-  const int s0 = pair ? mt & 1 : 0, ns = pair ? 1 : 2;
-  const long long places = (c1 - c0 + 1) * ns;
-  auto place = [&](long long i) { return ((part0 + i / ns) * 2 + s0 + i % ns) * a.rows + r; };
+  // the lane's place of the first 32
+  float2 ml = make_float2(-INFINITY, 0.0f);
   float M = own.x;
-  for (long long i = lane; i < places; i += 32) {
-    M = fmaxf(M, a.w_ml[place(i)].x);
-    flag |= a.w_flag[part0 + i / ns];
+  for (int i = lane; i < places; i += 32) {
+    const float2 x = a.w_ml[place0 + i * step];
+    if (i < 32) ml = x;
+    M = fmaxf(M, x.x);
+    flag |= a.w_flag[part0 + (i >> two)];
   }
   M = warp_max(M);
-  flag = __reduce_or_sync(0xffffffffu, flag);
-  // (a sum without a finite reference is 0, or NaN from the data: it stays)
-  auto weight = [&](float m) { return m == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2(m - M); };
+  flag = __reduce_or_sync(FULL, flag);
+  // A sum without a finite reference is 0, or NaN from the data: it stays, and so do
+  // its values.  A buffer without a tile has no sums: it is passed over.
+  auto factor = [&](float m) { return m == -INFINITY ? 1.0f : ex2(m - M); };
   constexpr int E = D / 32;
-  float acc[E], sum;
-  auto take = [&](const float *o, float2 ml, bool add) {
-    const float f = weight(ml.x);
-    const float y = ml.x == -INFINITY ? ml.y : ml.y * f;
-    sum = add ? sum + y : y;
+  const float f0 = factor(own.x);
+  float acc[E], sum = own.y * f0;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = *(const float2 *)(o + e * 32 + lane * 2);
-      acc[e] = add ? fmaf(x.x, f, acc[e]) : x.x * f;
-      acc[e + 1] = add ? fmaf(x.y, f, acc[e + 1]) : x.y * f;
+  for (int e = 0; e < E; e += 2) {
+    const float2 x = *(const float2 *)(j.own_o + (size_t)row * D + e * 32 + lane * 2);
+    acc[e] = x.x * f0;
+    acc[e + 1] = x.y * f0;
+  }
+  for (int i0 = 0; i0 < places; i0 += 32) {
+    if (i0) ml = i0 + lane < places ? a.w_ml[place0 + (i0 + lane) * step] : make_float2(-INFINITY, 0.0f);
+    const bool some = i0 + lane < places && (ml.x != -INFINITY || ml.y != 0.0f);
+    const float f = some ? factor(ml.x) : 0.0f;
+    float part = some ? ml.y * f : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(FULL, part, o);
+    sum += part;
+    const unsigned there = __ballot_sync(FULL, some);
+    const float *src = a.w_o + (place0 + i0 * step) * D + lane * 2;
+    constexpr int U = 4;  // rows on their way together
+    for (int i = 0; i < min(32, places - i0); i += U) {
+      float2 x[U][E / 2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          x[u][e] = i + u < 32 && there >> (i + u) & 1 ? *(const float2 *)(src + (i + u) * step * D + e * 64)
+                                                      : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float g = __shfl_sync(FULL, f, (i + u) & 31);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          acc[2 * e] = fmaf(x[u][e].x, g, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(x[u][e].y, g, acc[2 * e + 1]);
+        }
+      }
     }
-  };
-  take(j.own_o + row * D, own, false);
-#pragma unroll 4
-  for (long long i = 0; i < places; ++i) {
-    const size_t u = place(i);
-    const float2 ml = a.w_ml[u];
-    // a buffer without a tile has no sums
-    if (ml.x != -INFINITY || ml.y != 0.0f) take(a.w_o + u * D, ml, true);
   }
   const float nan = __int_as_float(0x7fffffff), inv = 1.0f / sum;
-  uint32_t *out = (uint32_t *)((T *)j.out + row * D);
+  uint32_t *out = (uint32_t *)((T *)j.out + (size_t)row * D);
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
     const float x = flag ? nan : sum == 0.0f ? 0.0f : acc[e] * inv, y = flag ? nan : sum == 0.0f ? 0.0f : acc[e + 1] * inv;
@@ -967,12 +1010,20 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   const JoinArgs j{own_o, own_ml, own_flag, out, out_lse, out_status};
   void *own_ws = z.own_bytes ? w + z.own : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
-  // Boxes of as many rows as divide the page, four at least: smaller ones are
-  // more instructions than the copies they replace.
+  // Boxes of as many rows as a power of two divides the page by, where that is 16 and
+  // more; of whole pages, with tiles of as many as 128 rows hold, for others of 8 to
+  // 128 rows (pages of 20: tiles of 120 keys by 6 boxes take 40 us where 32 boxes of 4
+  // rows take 66); of 8 rows.  What is left goes by copies.
   a.box = kKeys;
   while (page % a.box) a.box /= 2;
+  a.keys = kKeys;
+  const int whole = page <= kKeys ? kKeys / page * page : 0;
+  if (a.box < 16 && page >= 8 && whole >= 96) {
+    a.box = page;
+    a.keys = whole;
+  }
   CUtensorMap map = {};
-  bool tma = a.box >= 4 && is_device_memory(kv);
+  bool tma = a.box >= 8 && is_device_memory(kv);
   if (tma) {
     EncodeTiledFn fn = encode_fn();
     const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)page, (cuuint64_t)num_pages, 2};
@@ -985,6 +1036,7 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
+  if (!tma) a.keys = kKeys;
   auto go = [&](auto kernel) {
     return kernel(map, a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st);
   };
