@@ -177,12 +177,12 @@ __device__ __forceinline__ float grad_of(float x, float m, float coef, float k) 
   return ex2_approx((x - m) * k) * coef;
 }
 
-// The slice's gradient in full but for the listed elements: pieces from
-// `piece(g, j, v)` where the gradient's row lies on the 16-byte grid as the logits'
+// The slice's gradient in full but for the listed elements, by a CTA of THREADS:
+// pieces from `piece(g, j, v)` where the gradient's row lies on the 16-byte grid as the logits'
 // does, the last groups first; single elements otherwise (those of the logits come
 // from memory again: the two rows are different ones then).  coef 0: zeros, whatever
 // the row holds.
-template <typename T, typename F>
+template <typename T, int THREADS, typename F>
 __device__ __forceinline__ void write_grad(const T *row, T *grad, const RowSlice &s, uint32_t rank, float m, float coef, float k,
                                            F piece) {
   constexpr int VEC = RowElem<T>::VEC;
@@ -192,21 +192,22 @@ __device__ __forceinline__ void write_grad(const T *row, T *grad, const RowSlice
     grad[i] = RowElem<T>::store(zero ? 0.0f : grad_of<T>(RowElem<T>::load(row + i), m, coef, k));
   }
   if ((uintptr_t)row % 16 == (uintptr_t)grad % 16) {
+    constexpr int kVecs = kPieces * THREADS;
     uint4 *out = (uint4 *)(grad + s.head);
-    for (int g = row_groups(s) - 1; g >= 0; --g) {
-      const int v0 = s.v0 + g * kGroupVecs + (int)threadIdx.x;
+    for (int g = (s.v1 - s.v0 + kVecs - 1) / kVecs - 1; g >= 0; --g) {
+      const int v0 = s.v0 + g * kVecs + (int)threadIdx.x;
       uint4 w[kPieces];  // all on their way before the first is stored
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
-        if (v0 + j * kRowThreads < s.v1) w[j] = piece(g, j, v0 + j * kRowThreads);
+        if (v0 + j * THREADS < s.v1) w[j] = piece(g, j, v0 + j * THREADS);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j)
-        if (v0 + j * kRowThreads < s.v1)
-          __stcs(out + v0 + j * kRowThreads, zero ? make_uint4(0, 0, 0, 0) : grad_piece<T>(w[j], m, coef, k));
+        if (v0 + j * THREADS < s.v1)
+          __stcs(out + v0 + j * THREADS, zero ? make_uint4(0, 0, 0, 0) : grad_piece<T>(w[j], m, coef, k));
     }
   } else {
     const int lo = s.head + s.v0 * VEC, hi = s.head + s.v1 * VEC;
-    for (int i = lo + threadIdx.x; i < hi; i += kRowThreads)
+    for (int i = lo + threadIdx.x; i < hi; i += THREADS)
       grad[i] = RowElem<T>::store(zero ? 0.0f : grad_of<T>(RowElem<T>::load(row + i), m, coef, k));
   }
 }
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
     const float c = out.st.w == 0.0f ? 0.0f : out.st.y * w;
     // (the logits may be the gradient's own place: a piece is read, by whoever writes
     // there, before it is written)
-    write_grad<T>(row, grad, s, rank, out.st.x, c, k, [&](int g, int j, int v) {
+    write_grad<T, kRowThreads>(row, grad, s, rank, out.st.x, c, k, [&](int g, int j, int v) {
       return g >= groups - kRing ? ring_piece(smem, g % kRing, j) : ((const uint4 *)(row + s.head))[v];
     });
     __syncthreads();
@@ -423,9 +424,14 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
   if (rank == 0 && threadIdx.x == 0) put_row(a, r, out, s_loss);
 }
 
-// The gradient from a forward pass's statistics: CTA `rank` of C of a row.
+// The gradient from a forward pass's statistics: CTA `rank` of C of a row.  It streams
+// and no more, so that smaller CTAs, whose beginnings and ends lie apart, do best (2048
+// rows of V = 128256 bf16: 163 us, 6.46 TB/s, by 128 threads, 171 by 256; 777 of 40001
+// fp32: 44 and 47).
+constexpr int kGradThreads = 128;
+static_assert(kMaxList <= kGradThreads, "an entry to a thread");
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(DistillArgs a, unsigned C) {
+__global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillArgs a, unsigned C) {
   grid_dep_sync();
   const size_t r = blockIdx.x / C;
   const uint32_t rank = blockIdx.x % C;
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_grad_kernel(DistillArg
   const List li = list_of(s_list, a.tail, a.k);
   const uint32_t flags = li.flags | (li.used && st.w == 0.0f ? __float_as_uint(st.x) : 0u);
   const bool none = st.w == 0.0f || flags || li.used == 0;
-  write_grad<T>(row, grad, s, rank, st.x, none ? 0.0f : st.y * w, a.k,
+  write_grad<T, kGradThreads>(row, grad, s, rank, st.x, none ? 0.0f : st.y * w, a.k,
                 [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
   __syncthreads();
   if (!none && e.token >= 0 && in_slice<T>(s, rank, e.token))
@@ -480,7 +486,7 @@ template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, c
 template <typename T> cudaError_t launch_grad(const DistillArgs &a, cudaStream_t st) {
   // 64 KB of a row to a CTA
   const unsigned C = (unsigned)(((size_t)a.V * sizeof(T) + 65535) / 65536);
-  return launch_pdl(distill_grad_kernel<T>, dim3((unsigned)a.R * C), dim3(kRowThreads), 0, st, a, C);
+  return launch_pdl(distill_grad_kernel<T>, dim3((unsigned)a.R * C), dim3(kGradThreads), 0, st, a, C);
 }
 
 // What both calls check; fills `a` but for the outputs of one of them.
