@@ -552,6 +552,17 @@ def _kv_evict(kv, block_table, seq_len, weight_sum, out_weight_sum, budget, sink
         _stream(stream)))
 
 
+def _row_stride(name, t, dtype, shape):
+    """Elements between the rows of t [R][V]."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: need a {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: rows need unit stride, got strides {t.stride()}")
+    return row
+
+
 _ROW_DTYPES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 
 
@@ -601,7 +612,7 @@ def _distill_args(logits, teacher_token, teacher_logprob, weight):
     if logits.dim() != 2:
         raise ValueError(f"logits: need [R, V], got {tuple(logits.shape)}")
     R, V = logits.shape
-    _, row = _row_strides("logits", logits[None], logits.dtype, (1, R, V))
+    row = _row_stride("logits", logits, logits.dtype, (R, V))
     K = teacher_token.shape[-1]
     _want("teacher_token", teacher_token, torch.int32, (R, K))
     _want("teacher_logprob", teacher_logprob, torch.float32, (R, K))
@@ -611,12 +622,7 @@ def _distill_args(logits, teacher_token, teacher_logprob, weight):
 
 
 def _grad_stride(out_grad, logits):
-    if out_grad is None:
-        return 0
-    if out_grad.dim() != 2:
-        raise ValueError(f"out_grad: need [R, V], got {tuple(out_grad.shape)}")
-    _, row = _row_strides("out_grad", out_grad[None], logits.dtype, (1, *logits.shape))
-    return row
+    return 0 if out_grad is None else _row_stride("out_grad", out_grad, logits.dtype, logits.shape)
 
 
 def sv_distill_loss(logits, teacher_token, teacher_logprob, weight, temperature, tail, out_loss,
