@@ -736,8 +736,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The join: a warp to each (sequence, query head), with the parts of its segment
-// and the sums of the sequence's own slots.
+// The join: a warp to ROWS query rows of a segment, with their parts and the sums of
+// the sequences' own slots.  Rows of one segment have the same parts, so that where the
+// rows are many what it takes to find them is done once for four, and four rows' values
+// are on their way together; where they are few, a warp has one, with more of its parts
+// on their way (with 8 KV heads of 128 behind 20000 slots, 8192 rows take 127 us in all
+// by fours and 130 one by one, 32768 rows 394 and 410, 2048 rows 51 and 48, 256 rows 35
+// and 29).  32 / ROWS lanes to a row where references and sums are looked at, all of
+// them for its values.
+constexpr int kJoinRows = 4;
+constexpr long long kFewRows = 2048;
 constexpr int kJoinThreads = 256;
 struct JoinArgs {
   const float *own_o;
@@ -747,15 +755,21 @@ struct JoinArgs {
   float *lse;
   uint32_t *status;
 };
-template <typename T, int D>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, JoinArgs j) {
   const unsigned FULL = 0xffffffffu;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // below 2^26
-  const bool live = row < a.B * a.Hq;
-  const int b = live ? row / a.Hq : 0, h = live ? row - b * a.Hq : 0;
-  const int p = b / a.W, head = h / a.G, at = (b - p * a.W) * a.G + h - head * a.G;
-  const int mt = at / kRows, r = at % kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
+  static_assert(kRows % ROWS == 0, "rows of one query tile");
+  constexpr int kLanes = 32 / ROWS, E = D / 32, U = ROWS > 1 ? 4 : 8;  // U: places on their way together
+  const int lane = threadIdx.x & 31, mine = lane / kLanes, sub = lane % kLanes;
+  const int wg = a.W * a.G, fours = (wg + ROWS - 1) / ROWS;
+  const int unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // below 2^27
+  const bool live = unit < a.N * a.Hkv * fours;
+  const int seg = live ? unit / fours : 0, at0 = live ? (unit - seg * fours) * ROWS : 0;
+  const int p = seg / a.Hkv, head = seg - p * a.Hkv, count = min(ROWS, wg - at0);
+  const int mt = at0 / kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
+  // the row of the lane's eight; the last one's again behind it
+  const int r = min(mine, count - 1), b = p * a.W + (at0 + r) / a.G, h = head * a.G + (at0 + r) % a.G;
+  const int row = b * a.Hq + h;
   // lengths were there before the launches that this one waits for
   const longlong2 n = count_tiles(a, p);
   const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
@@ -766,75 +780,100 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
     c0 = share_of(first, shares, all);
     parts = share_of(first + tiles - 1, shares, all) - c0 + 1;
   }
-  // places in the parts: that of the row's query tile in a pair, both otherwise
+  // places in the parts: that of the rows' query tile in a pair, both otherwise
   const int two = pair ? 0 : 1, places = parts << two;
   const size_t part0 = part_at(a, column, (long long)p * a.Hkv + head + c0);
-  const size_t place0 = (part0 * 2 + (pair ? mt & 1 : 0)) * a.rows + r, step = (size_t)a.rows << (1 - two);
+  const size_t place0 = (part0 * 2 + (pair ? mt & 1 : 0)) * a.rows + at0 % kRows, step = (size_t)a.rows << (1 - two);
   grid_dep_sync();
   if (!live) return;
+  auto load = [&](const float *src, float *x) {
+    if constexpr (E == 4) {
+      const float4 v = *(const float4 *)(src + lane * 4);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = *(const float2 *)(src + lane * 2);
+      x[0] = v.x, x[1] = v.y;
+    }
+  };
+  // values first, whatever their references say: all loads are on their way at once
+  float acc[ROWS][E], x[U][ROWS][E];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) load(j.own_o + (size_t)__shfl_sync(FULL, row, i * kLanes) * D, acc[i]);
+  auto fetch = [&](int at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u < places) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+          load(a.w_o + (place0 + (at + u) * step + min(i, count - 1)) * D, x[u][i]);
+      }
+  };
+  fetch(0);
   uint32_t flag = (len < 0 || len > a.cap ? SV_ROW_BAD_LEN : 0u) | j.own_flag[b];
   const float2 own = j.own_ml[row];
-  // the lane's place of the first 32
-  float2 ml = make_float2(-INFINITY, 0.0f);
+  float2 ml = make_float2(-INFINITY, 0.0f);  // of the lane's place of the eight in work
   float M = own.x;
-  for (int i = lane; i < places; i += 32) {
-    const float2 x = a.w_ml[place0 + i * step];
-    if (i < 32) ml = x;
-    M = fmaxf(M, x.x);
+  for (int i = sub; i < places; i += kLanes) {
+    const float2 v = a.w_ml[place0 + i * step + r];
+    if (i < kLanes) ml = v;
+    M = fmaxf(M, v.x);
     flag |= a.w_flag[part0 + (i >> two)];
   }
-  M = warp_max(M);
-  flag = __reduce_or_sync(FULL, flag);
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    flag |= __shfl_xor_sync(FULL, flag, o);
+  }
   // A sum without a finite reference is 0, or NaN from the data: it stays, and so do
   // its values.  A buffer without a tile has no sums: it is passed over.
   auto factor = [&](float m) { return m == -INFINITY ? 1.0f : ex2(m - M); };
-  constexpr int E = D / 32;
   const float f0 = factor(own.x);
-  float acc[E], sum = own.y * f0;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float2 x = *(const float2 *)(j.own_o + (size_t)row * D + e * 32 + lane * 2);
-    acc[e] = x.x * f0;
-    acc[e + 1] = x.y * f0;
+  for (int i = 0; i < ROWS; ++i) {
+    const float g = __shfl_sync(FULL, f0, i * kLanes);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[i][e] *= g;
   }
-  for (int i0 = 0; i0 < places; i0 += 32) {
-    if (i0) ml = i0 + lane < places ? a.w_ml[place0 + (i0 + lane) * step] : make_float2(-INFINITY, 0.0f);
-    const bool some = i0 + lane < places && (ml.x != -INFINITY || ml.y != 0.0f);
-    const float f = some ? factor(ml.x) : 0.0f;
-    float part = some ? ml.y * f : 0.0f;
+  float sum = sub == 0 ? own.y * f0 : 0.0f, f = 0.0f;
+  unsigned there = 0;
+  for (int at = 0; at < places; at += U) {
+    if (at % kLanes == 0) {
+      const bool in = at + sub < places;
+      if (at && in) ml = a.w_ml[place0 + (at + sub) * step + r];
+      const bool some = in && (ml.x != -INFINITY || ml.y != 0.0f);
+      f = some ? factor(ml.x) : 0.0f;
+      if (some) sum += ml.y * f;
+      there = __ballot_sync(FULL, some);
+    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(FULL, part, o);
-    sum += part;
-    const unsigned there = __ballot_sync(FULL, some);
-    const float *src = a.w_o + (place0 + i0 * step) * D + lane * 2;
-    constexpr int U = 4;  // rows on their way together
-    for (int i = 0; i < min(32, places - i0); i += U) {
-      float2 x[U][E / 2];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int i = 0; i < ROWS; ++i) {
+        const int from = i * kLanes + (at + u) % kLanes;
+        const float g = __shfl_sync(FULL, f, from);
+        if (there >> from & 1) {
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e)
-          x[u][e] = i + u < 32 && there >> (i + u) & 1 ? *(const float2 *)(src + (i + u) * step * D + e * 64)
-                                                      : make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float g = __shfl_sync(FULL, f, (i + u) & 31);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          acc[2 * e] = fmaf(x[u][e].x, g, acc[2 * e]);
-          acc[2 * e + 1] = fmaf(x[u][e].y, g, acc[2 * e + 1]);
+          for (int e = 0; e < E; ++e) acc[i][e] = fmaf(x[u][i][e], g, acc[i][e]);
         }
       }
-    }
+    fetch(at + U);
   }
-  const float nan = __int_as_float(0x7fffffff), inv = 1.0f / sum;
-  uint32_t *out = (uint32_t *)((T *)j.out + (size_t)row * D);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float x = flag ? nan : sum == 0.0f ? 0.0f : acc[e] * inv, y = flag ? nan : sum == 0.0f ? 0.0f : acc[e + 1] * inv;
-    out[e * 16 + lane] = pack2<T>(x, y);
+  for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  const float nan = __int_as_float(0x7fffffff), inv = flag ? nan : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const float g = __shfl_sync(FULL, inv, i * kLanes);
+    const int to = __shfl_sync(FULL, row, i * kLanes);
+    if (i >= count) break;
+    uint32_t *out = (uint32_t *)((T *)j.out + (size_t)to * D) + lane * (E / 2);
+    // (a row of nothing is zeros, whatever its values were)
+    if constexpr (E == 4)
+      *(uint2 *)out = g == 0.0f ? make_uint2(0u, 0u) : make_uint2(pack2<T>(acc[i][0] * g, acc[i][1] * g), pack2<T>(acc[i][2] * g, acc[i][3] * g));
+    else
+      *out = g == 0.0f ? 0u : pack2<T>(acc[i][0] * g, acc[i][1] * g);
   }
-  if (lane == 0) {
+  if (sub == 0 && mine < count) {
     if (j.lse) j.lse[row] = flag ? nan : sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
     if (h == 0 && j.status) j.status[b] = flag;
   }
@@ -905,11 +944,12 @@ sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j,
   s = paged_sums(a.q, a.kv, a.kv_stride, a.page_stride, dt, block_table, seq_len, a.B, a.Hq, a.Hkv, D, a.page, max_pages,
                  a.num_pages, scale, own_o, own_ml, own_flag, own_ws, st);
   if (s != SV_OK) return s;
-  const long long rows = (long long)a.B * a.Hq;
+  const bool few = (long long)a.B * a.Hq <= kFewRows;
+  const long long at_once = few ? 1 : kJoinRows, units = (long long)a.N * a.Hkv * (((long long)a.W * a.G + at_once - 1) / at_once);
+  constexpr int kUnits = kJoinThreads / 32;
   LaunchScope ls("prefix_join", st);
-  return check_launch("prefix_join",
-                      launch_pdl(prefix_join_kernel<T, D>, dim3((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32))),
-                                 dim3(kJoinThreads), 0, st, a, j));
+  return check_launch("prefix_join", launch_pdl(few ? prefix_join_kernel<T, D, 1> : prefix_join_kernel<T, D, kJoinRows>,
+                                                dim3((unsigned)((units + kUnits - 1) / kUnits)), dim3(kJoinThreads), 0, st, a, j));
 }
 
 }  // namespace
