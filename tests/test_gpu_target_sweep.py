@@ -97,6 +97,20 @@ def test_prefix_workspaces(plens, lens, Hq, Hkv, page, D, fill):
         guard.check_edges()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,W,Hkv,G", [
+    (70, 3, 8, 3),        # nine rows to a segment: four, four and one
+    (9, 43, 2, 3),        # 129: the second tile has one row
+    (1, 259, 1, 9),       # 2331: ten columns, the last of one ragged tile
+    (300, 1, 8, 1),       # one row to a segment
+])
+def test_prefix_many_rows(N, W, Hkv, G, D):
+    rng = random.Random(N)
+    plens = [rng.choice([0, 1, 40, 129, 300]) for _ in range(N - 1)] + [260]
+    lens = [rng.choice([0, 1, 9, 30]) for _ in range(N * W)]
+    prefix.check(*prefix.make(plens, lens, Hkv * G, Hkv, D, 16, torch.bfloat16, seed=N))
+
+
 @pytest.mark.parametrize("page", [1, 4, 12, 16, 33, 50, 100, 128, 136])
 @pytest.mark.parametrize("D", [64, 128])
 def test_prefix_cache_in_host_memory(page, D):
