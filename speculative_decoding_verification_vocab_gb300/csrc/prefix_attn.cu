@@ -35,9 +35,10 @@
 //               other's products: S = Q K^T from shared memory, O += P V with P in
 //               tensor memory, in the place of the S it comes from;
 //   warps 4-11  softmax, four to a buffer, a row to a thread, 64 keys at a time: the
-//               running maximum with a lazy rescale of O, P as 16-bit values (its
-//               first half is multiplied while the second is made); at a segment's
-//               end O, m and l to the workspace.
+//               running maximum with a lazy rescale of O, P as 16-bit values; at a
+//               segment's end O, m and l to the workspace.  The halves of a buffer
+//               take turns too: one is multiplied and filled with the next tile's
+//               scores while the other is worked on.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
 // with SV_ROW_TIMEOUT.
 #include <cuda_bf16.h>
@@ -96,13 +97,13 @@ template <int D> struct Ring {
   static constexpr uint32_t kOffV = kK * kTileBytes;
   static constexpr uint32_t kOffQ = kOffV + kV * kTileBytes;
   static constexpr uint32_t kOffBar = kOffQ + 2 * kTileBytes;
-  static constexpr uint32_t kOffMisc = kOffBar + 32 * 8;
+  static constexpr uint32_t kOffMisc = kOffBar + 40 * 8;
   static constexpr size_t kSmem = kOffMisc + 128 + 1024;  // + alignment
-  // barriers: a place of K or V filled and free; by buffer: Q there, S there, P's
-  // halves there, PV done, its first half done
+  // barriers: a place of K or V filled and free; by buffer: Q there; by half of a
+  // buffer (2 s + half): S there, P there, its PV done
   static constexpr int kFullK = 0, kFreeK = kK, kFullV = 2 * kK, kFreeV = kFullV + kV, kQ = kFreeV + kV, kS = kQ + 2,
-                       kP = kS + 2, kPV = kP + 4, kPV0 = kPV + 2, kCount = kPV0 + 2;
-  static_assert(kCount <= 32, "barriers");
+                       kP = kS + 4, kPV = kP + 4, kCount = kPV + 4;
+  static_assert(kCount <= 40, "barriers");
 };
 
 template <int V> struct Int {
@@ -287,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(R::kQ + s), 4);
-      mbar_init(bar(R::kS + s), 1);
-      mbar_init(bar(R::kP + 2 * s), 4);
-      mbar_init(bar(R::kP + 2 * s + 1), 4);
-      mbar_init(bar(R::kPV + s), 1);
-      mbar_init(bar(R::kPV0 + s), 1);
+      for (int half = 0; half < 2; ++half) {
+        mbar_init(bar(R::kS + 2 * s + half), 1);
+        mbar_init(bar(R::kP + 2 * s + half), 4);
+        mbar_init(bar(R::kPV + 2 * s + half), 1);
+      }
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -470,12 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kFirstSoftmax) {
     // ------------------------------------------------------------ MMA
-    // A buffer's tiles in turn: S of the first, then, tile by tile, O += P V and the
-    // next S, into the place of P.  The warp runs converged and elect.sync picks the
+    // A buffer's tiles in turn, 64 keys at a time: S of both halves of the first, then,
+    // half by half, O += P V and the next tile's S into the place of P, while the
+    // softmax is at the other half.  The warp runs converged and elect.sync picks the
     // issuing lane.
     const int s = warp - kMmaWarp;
     constexpr uint32_t kIdesc = (1u << 4) | (kAbType<T> << 7) | (kAbType<T> << 10) | ((uint32_t)(kRows >> 4) << 24);
-    constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kKeys >> 3) << 17);
+    constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kKeys / 2 >> 3) << 17);
     constexpr uint32_t kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // V: head dim contiguous
     constexpr uint64_t kStep = kTileBytes >> 4;
     const uint64_t dK0 = sdesc(sm0, 16, 1024), dV0 = sdesc(sm0 + R::kOffV, kBox, 1024);
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int step = w.pair ? 1 : 2, first = w.pair ? 0 : s;
     int k_at = first, v_at = first;
     uint32_t k_phase = 0, v_phase = 0;
-    uint32_t nq = 0, ns = 0, done = 0;  // query tiles, S and PV products so far
+    uint32_t nq = 0, ns[2] = {0, 0}, done[2] = {0, 0};  // query tiles; S and PV products so far, by half
     bool ok = true;
     auto landed = [&](int full, uint32_t phase) {
       const bool r = all(mbar_wait(bar(full), phase, abort));
@@ -495,32 +497,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (ok && w.next(a)) {
       const int n = w.tiles_for(s);
-      auto issue_s = [&]() {  // its K has landed; the product that read P there is done
-        ok = landed(R::kFullK + k_at, k_phase) && all(done == 0 || mbar_wait(bar(R::kPV + s), (done - 1) & 1, abort));
+      auto issue_s = [&](auto which) {  // once its K has landed and the product that read P there is done
+        constexpr int half = decltype(which)::value;
+        ok = (half || landed(R::kFullK + k_at, k_phase)) &&
+             all(done[half] == 0 || mbar_wait(bar(R::kPV + 2 * s + half), (done[half] - 1) & 1, abort));
         if (!ok) return;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t dk = dK0 + k_at * kStep;
+          const uint64_t dk = dK0 + k_at * kStep + (half ? 64 * 128 >> 4 : 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t at = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-            mma_ss(tS, dq + at, dk + at, kIdescS, ks > 0);
+            mma_ss(tS + 64 * half, dq + at, dk + at, kIdescS, ks > 0);
           }
-          mma_commit(bar(R::kS + s));
-          mma_commit(bar(R::kFreeK + k_at));
+          mma_commit(bar(R::kS + 2 * s + half));
+          if (half) mma_commit(bar(R::kFreeK + k_at));
         }
         __syncwarp();
-        if ((k_at += step) >= kK) {
+        if (half && (k_at += step) >= kK) {
           k_at -= kK;
           k_phase ^= 1;
         }
-        ++ns;
+        ++ns[half];
       };
       if (n > 0) {
         ok = all(mbar_wait(bar(R::kQ + s), nq++ & 1, abort));
         if (!ok) break;
         tc_fence_after();
-        issue_s();
+        issue_s(Int<0>());
+        if (ok) issue_s(Int<1>());
       }
       for (int i = 0; ok && i < n; ++i) {
         ok = landed(R::kFullV + v_at, v_phase);
@@ -543,40 +548,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         const uint64_t dv = dV0 + v_at * kStep;
-        // P comes in two halves of 64 keys
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = all(mbar_wait(bar(R::kP + 2 * s + half), done & 1, abort));
-          if (!ok) break;
+        auto multiply = [&](auto which) {
+          constexpr int half = decltype(which)::value;
+          ok = all(mbar_wait(bar(R::kP + 2 * s + half), done[half] & 1, abort));
+          if (!ok) return;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-              if (ks < steps) mma_ts(tO, tS + ks * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
-            if (!half) {
-              mma_commit(bar(R::kPV0 + s));
-            } else {
-              mma_commit(bar(R::kPV + s));
-              mma_commit(bar(R::kFreeV + v_at));
-            }
+              if (ks < steps)
+                mma_ts(tO, tS + 64 * half + (ks - 4 * half) * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
+            mma_commit(bar(R::kPV + 2 * s + half));
+            if (half) mma_commit(bar(R::kFreeV + v_at));
           }
           __syncwarp();
-        }
+          ++done[half];
+          if (i + 1 < n) issue_s(which);
+        };
+        multiply(Int<0>());
+        if (ok) multiply(Int<1>());
         if (!ok) break;
-        ++done;
         if ((v_at += step) >= kV) {
           v_at -= kV;
           v_phase ^= 1;
         }
-        if (i + 1 < n) issue_s();
       }
     }
     if (!ok) {
       // products in flight end before tensor memory is released: the newest phases
       // of the barriers that the last ones commit to
       volatile int no_abort = 0;
-      if (ns) mbar_wait(bar(R::kS + s), (ns - 1) & 1, &no_abort);
-      if (done) mbar_wait(bar(R::kPV + s), (done - 1) & 1, &no_abort);
+      for (int half = 0; half < 2; ++half) {
+        if (ns[half]) mbar_wait(bar(R::kS + 2 * s + half), (ns[half] - 1) & 1, &no_abort);
+        if (done[half]) mbar_wait(bar(R::kPV + 2 * s + half), (done[half] - 1) & 1, &no_abort);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -610,18 +615,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned long long l2[2] = {0ull, 0ull};
       int behind = w.len - w.first_for(s) * a.keys;  // keys from this tile's first to the last
       const int stride = w.pair ? a.keys : 2 * a.keys;
-      for (int i = 0; i < n; ++i, ++g, behind -= stride) {
-        ok = all(mbar_wait(bar(R::kS + s), g & 1, abort));
-        if (!ok) break;
+      uint32_t x[4][32];
+      auto ask = [&](auto which) {  // a half's scores
+        constexpr int c = 2 * decltype(which)::value;
         tc_fence_after();
+        tm_ld32(tS + 32 * c, x[c]);
+        tm_ld32(tS + 32 * c + 32, x[c + 1]);
+      };
+      auto get = [&](auto which) {
+        constexpr int c = 2 * decltype(which)::value;
+        tm_wait_ld(x[c]);
+        tm_wait_ld(x[c + 1]);
+      };
+      if (n > 0) {
+        ok = all(mbar_wait(bar(R::kS + 2 * s), g & 1, abort));
+        if (!ok) break;
+        ask(Int<0>());
+        get(Int<0>());
+      }
+      for (int i = 0; i < n; ++i, ++g, behind -= stride) {
         const int left = min(behind, a.keys);  // keys of this tile
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tm_ld32(tS + 32 * c, x[c]);
         auto do_half = [&](auto which) -> bool {
           constexpr int half = decltype(which)::value;
-#pragma unroll
-          for (int c = 2 * half; c < 2 * half + 2; ++c) tm_wait_ld(x[c]);
           if (left < 64 * half + 64) {
 #pragma unroll
             for (int c = 2 * half; c < 2 * half + 2; ++c)
@@ -642,12 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float factor = grow && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.0f;
           m_ref = m_new;
           if (__any_sync(FULL, factor != 1.0f)) {
-            // O covers the keys before: S was issued after the product of the tile
-            // before, and that of this tile's first half is waited for
-            if (half) {
-              if (!all(mbar_wait(bar(R::kPV0 + s), g & 1, abort))) return false;
-              tc_fence_after();
-            }
+            // O covers the keys before: the product of the half before is waited for (a
+            // segment's first half finds no reference to move)
+            if (!all(mbar_wait(bar(R::kPV + 2 * s + 1 - half), (half ? g : g - 1) & 1, abort))) return false;
+            tc_fence_after();
             l2[0] = f2_mul(l2[0], f2_splat(factor));
             l2[1] = f2_mul(l2[1], f2_splat(factor));
 #pragma unroll 1
@@ -660,9 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tm_st32u(tO + c, o);
             }
           }
-          if (half == 0)  // the second half comes while the first is worked on
-#pragma unroll
-            for (int c = 2; c < 4; ++c) tm_ld32(tS + 32 * c, x[c]);
           const unsigned long long sc2 = f2_splat(a.scale_log2), mn2 = f2_splat(m_ref == -INFINITY ? 0.0f : -m_ref);
 #pragma unroll
           for (int c = 2 * half; c < 2 * half + 2; ++c) {
@@ -676,12 +686,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               f2_unpack(y, y0, y1);
               p[e] = pack2<T>(y0, y1);
             }
-            tm_st16(tS + 16 * c, p);  // in the place of keys that have been read
+            tm_st16(tS + 64 * half + 16 * (c - 2 * half), p);  // in the place of keys that have been read
           }
-          tm_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(R::kP + 2 * s + half));
+          auto done = [&]() {
+            tm_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(R::kP + 2 * s + half));
+          };
+          // The next half's scores are on their way meanwhile, where they are there.
+          // (Nothing but the wait stands between a load and its registers' use, a copy
+          // of them at a join of two ways included.)
+          const Int<1 - half> next;
+          const uint32_t s_bar = bar(R::kS + 2 * s + 1 - half);
+          const uint32_t s_phase = (half ? g + 1 : g) & 1;
+          if (half && i + 1 == n) {
+            done();
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e >> 5][e & 31] = 0;  // (the old ones are not kept)
+          } else if (all(mbar_test(s_bar, s_phase))) {
+            ask(next);
+            done();
+            get(next);
+          } else {
+            done();
+            if (!all(mbar_wait(s_bar, s_phase, abort))) return false;
+            ask(next);
+            get(next);
+          }
           return true;
         };
         ok = do_half(Int<0>()) && do_half(Int<1>());
@@ -690,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const size_t at = (w.part(a) * 2 + s) * a.rows + row;
       if (n > 0) {
-        ok = all(mbar_wait(bar(R::kPV + s), (g - 1) & 1, abort));
+        ok = all(mbar_wait(bar(R::kPV + 2 * s + 1), (g - 1) & 1, abort));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
