@@ -4,7 +4,9 @@
  * the best-scored path of an EAGLE-style draft tree, residual / bonus
  * sampling, the tree's ancestor attention mask, and KV-cache rollback /
  * compaction; beside them verification from given probabilities and random
- * numbers, decode attention over a paged KV cache, and eviction from it.
+ * numbers, decode attention over a paged KV cache, behind prefixes that
+ * sequences share too, eviction from it, log probabilities of given tokens with
+ * alternatives, and the distillation loss that trains a draft on them.
  *
  * Sources (web pages; cited by title and section):
  *   [Lesson] "Decodificação Especulativa e EAGLE-3" (ai-engineering.academy,

@@ -21,6 +21,12 @@
 // back to the K best whenever it is full.  (With that list filled in the pass, 16 KB
 // by 16 KB between barriers, 4096 rows of V = 128256 bf16 took 378 us at K = 20 and
 // 676 at K = 128.)
+//
+// 4096 rows of V = 128256 bf16: 155 us without alternatives (6.78 TB/s, all that memory
+// gives), 192 at K = 20 (0.81), 286 at K = 128: behind its row a CTA has another 18000
+// clocks of barriers and ways to L2, a third of its time, in which three others of the
+// SM stream.  1000 rows of 50257 fp32, K = 64: 51 us, two waves of CTAs.  Five CTAs to
+// an SM with two groups in the ring take 198 and 54, CTAs of 128 threads 191 and 62.
 #include <math.h>
 
 #include "vocab_rows.cuh"
