@@ -23,7 +23,7 @@
 // 676 at K = 128.)
 //
 // 4096 rows of V = 128256 bf16: 155 us without alternatives (6.78 TB/s, all that memory
-// gives), 192 at K = 20 (0.81), 286 at K = 128: behind its row a CTA has another 18000
+// gives), 191 at K = 20 (0.81), 266 at K = 128: behind its row a CTA has another 16000
 // clocks of barriers and ways to L2, a third of its time, in which three others of the
 // SM stream.  1000 rows of 50257 fp32, K = 64: 51 us, two waves of CTAs.  Five CTAs to
 // an SM with two groups in the ring take 198 and 54, CTAs of 128 threads 191 and 62.
@@ -107,29 +107,34 @@ __device__ void keep_best(u64 *keys, int n, int K) {
   __syncthreads();
 }
 
-// The largest 16-bit number that K of the CTA's 256 keys reach (0: fewer have more),
-// two bits at a time; for one warp.  The counts of the three numbers that the next
-// two bits make stand in one word.
-__device__ __forceinline__ uint32_t reached_by(const uint16_t *keys, int K) {
-  static_assert(kRowThreads == 256, "a vector of 8 keys to a lane, counts of 10 bits");
-  const uint4 q = ((const uint4 *)keys)[threadIdx.x & 31];
-  const uint32_t pairs[4] = {q.x, q.y, q.z, q.w};
-  uint32_t t = 0;
+// The digit of the K-th largest of the numbers counted in bins[256], and how many of K
+// are left for it (-1: fewer than K are counted); for every warp at once.
+__device__ __forceinline__ int digit_of(const uint32_t *bins, int &K) {
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const uint4 lo = ((const uint4 *)bins)[2 * lane], hi = ((const uint4 *)bins)[2 * lane + 1];
+  const int n[8] = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  int own = 0;
 #pragma unroll
-  for (int bit = 14; bit >= 0; bit -= 2) {
-    uint32_t n = 0;
+  for (int i = 0; i < 8; ++i) own += n[i];
+  int from = own;  // of this lane's bins and those above
 #pragma unroll
-    for (int d = 1; d < 4; ++d) {
-      const uint32_t at = t | (uint32_t)d << bit;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        n += ((pairs[i] & 0xffffu) >= at ? 1u << 10 * (d - 1) : 0u) + (pairs[i] >> 16 >= at ? 1u << 10 * (d - 1) : 0u);
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    const uint32_t k = (uint32_t)K;
-    t |= (n >> 20 >= k ? 3u : (n >> 10 & 1023u) >= k ? 2u : (n & 1023u) >= k ? 1u : 0u) << bit;
+  for (int o = 1; o < 32; o *= 2) {
+    const int x = __shfl_down_sync(FULL, from, o);
+    if (lane + o < 32) from += x;
   }
-  return t;
+  const unsigned reach = __ballot_sync(FULL, from >= K);
+  if (!reach) return -1;
+  const int at = 31 - __clz(reach);
+  int left = K - (from - own), digit = 8 * lane + 7;
+#pragma unroll
+  for (int i = 7; i > 0; --i)
+    if (digit == 8 * lane + i && left > n[i]) {
+      left -= n[i];
+      --digit;
+    }
+  K = __shfl_sync(FULL, left, at);
+  return __shfl_sync(FULL, digit, at);
 }
 
 // x rounded up to the upper 16 bits of a float
@@ -241,8 +246,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   __shared__ RowPart s_part[kRowWarps];
   __shared__ RowPart s_all[kMaxRowCluster];
   __shared__ int s_n, s_hits;
-  __shared__ float s_tau;
-  __shared__ __align__(16) uint16_t s_top[kRowThreads];
+  __shared__ __align__(16) uint32_t s_bins[2][256];
 
   const int b = (int)(item / a.P);
   const int token = a.tokens ? a.tokens[item] : 0;
@@ -282,7 +286,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const int single = has_single ? single_at<T>(s, threadIdx.x) : 0;
   const float single_x = has_single ? RowElem<T>::load(row + single) : -INFINITY;
   if (has_single) add_single<true>(sums, single_x, k);
-  if (TOP && threadIdx.x == 0) s_n = s_hits = 0;
+  if (TOP) {
+    if (threadIdx.x == 0) s_n = s_hits = 0;
+    for (int i = threadIdx.x; i < 512; i += kRowThreads) s_bins[0][i] = 0;
+    __syncthreads();
+  }
 
   // run i of a thread: its groups [i per, (i + 1) per)
   const int per = (groups + kRuns - 1) / kRuns;
@@ -312,22 +320,22 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   }
   group_wait<0>();
 
+  // the upper 16 bits of the thread's maximum, as an ordered number (0: none above -inf)
+  const uint32_t top_key = TOP && thread_top > -INFINITY ? order_of(thread_top) >> 16 : 0u;
+  if (top_key) atomicAdd(&s_bins[0][top_key >> 8], 1u);
   const RowPart mine = warp_join(part_of(sums), k);
   if (lane == 0) s_part[warp] = mine;
-  __syncthreads();
+  __syncthreads();  // the ring is free, too
   int n = 0;
   if (TOP) {
-    // tau: a value that K of the threads' maxima reach, to 16 bits (none: all above
-    // -inf).  That is a little more than K elements: in any order 1.04 K of 128256 at
-    // K = 20, 1.4 K at 128.
-    s_top[threadIdx.x] = thread_top > -INFINITY ? (uint16_t)(order_of(thread_top) >> 16) : 0;
-    __syncthreads();  // the ring is free, too
-    if (warp == 0) {
-      const uint32_t t = reached_by(s_top, a.K);
-      if (lane == 0) s_tau = t ? value_of(t << 16) : -INFINITY;
-    }
+    // tau: the K-th largest of the threads' maxima, to 16 bits (none: all above -inf), a
+    // byte of it at a time.  K elements reach it, and a few more: in any order 1.04 K of
+    // 128256 at K = 20, 1.4 K at 128.
+    int left = a.K;
+    const int high = digit_of(s_bins[0], left);
+    if (high >= 0 && (int)(top_key >> 8) == high) atomicAdd(&s_bins[1][top_key & 255], 1u);
     __syncthreads();
-    const float tau = s_tau;
+    const float tau = high < 0 ? -INFINITY : value_of((uint32_t)(high << 8 | digit_of(s_bins[1], left)) << 16);
     auto offer = [&](float x, int index) {
       if (x >= tau && x > -INFINITY) {
         const int at = atomicAdd(&s_n, 1);
