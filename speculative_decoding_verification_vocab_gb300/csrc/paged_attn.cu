@@ -840,7 +840,9 @@ __device__ __forceinline__ float2 join_ml(const PagedArgs &a, const Plan &p, int
   return make_float2(top, sum);
 }
 
-template <typename T, int D>
+// SUMS: the rows' sums are wanted as they are (a kernel of its own: with both ways in one
+// its registers grew from 62 to 78).
+template <typename T, int D, bool SUMS>
 __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, int joins, int wide, int key_ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float nan = __int_as_float(0x7fffffff);
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
       const size_t row = (size_t)b * a.Hq + head0 + r;
       const float inv = 1.0f / ml.y;
       auto put = [&](int c, float x, float y) {
-        if (a.sum_o) {
+        if constexpr (SUMS) {
           *(float2 *)(a.sum_o + row * D + c) = make_float2(x, y);
           return;
         }
@@ -901,7 +903,7 @@ __global__ void __launch_bounds__(kEndThreads) paged_finish_kernel(PagedArgs a, 
         for (int e = 0; e < E; e += 2) put(e * 32 + lane * 2, acc[e], acc[e + 1]);
       }
       if (lane == 0 && (!wide || warp == 0)) {
-        if (a.sum_o) a.sum_ml[row] = ml;
+        if (SUMS) a.sum_ml[row] = ml;
         if (a.lse) a.lse[row] = flag ? nan : ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
         if (h == 0 && r == 0 && a.status) a.status[b] = flag;
       }
@@ -1085,13 +1087,15 @@ sv_status run(const PagedArgs &a, const Sizes &z, bool weights, cudaStream_t st)
   const size_t smem = weights ? (size_t)a.G * sizeof(float2) : 0;
   if (smem > 32 * 1024) {  // beside the join's 8 KB more than a kernel has unasked
     const cudaError_t e =
-        cudaFuncSetAttribute(paged_finish_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(paged_finish_kernel<T, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return check_launch("paged_finish", e);
   }
   LaunchScope ls("paged_finish", st);
-  return check_launch("paged_finish",
-                      launch_pdl(paged_finish_kernel<T, D>, dim3((unsigned)ctas), dim3(kEndThreads),
-                                 smem, st, a, joins, wide, key_ctas ? key_ctas : 1));
+  auto kernel = paged_finish_kernel<T, D, false>;
+  if constexpr (D < 256)  // (the only ones whose sums another call takes)
+    if (a.sum_o) kernel = paged_finish_kernel<T, D, true>;
+  return check_launch("paged_finish", launch_pdl(kernel, dim3((unsigned)ctas), dim3(kEndThreads), smem, st, a, joins, wide,
+                                                 key_ctas ? key_ctas : 1));
 }
 
 bool bad_shape(int B, int Hq, int Hkv, int D, int page, int max_pages, int window, int sinks) {

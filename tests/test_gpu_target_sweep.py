@@ -147,3 +147,37 @@ def test_distill_in_place_at_the_largest_sizes():
         off = (g.view(n, 3, V).double() - want["grad"].double()).abs().amax(0).cpu()
         assert bool((off <= tol).all())
     assert float((r["loss"].view(n, 3) - want["loss"]).abs().max()) <= 4 * rel * 30
+
+
+def test_nothing_to_do():
+    """No sequences, entries or rows: nothing is launched, empty tensors come back."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    before = sv.sv_launch_count()
+    kv = torch.zeros(2, 3, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
+    out, lse, st = sv.prefix_attention(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV), kv, torch.zeros(1, 1, **i32),
+                                       torch.zeros(1, **i32), torch.zeros(0, 1, **i32), torch.zeros(0, **i32), return_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and st.shape == (0,)
+    x = torch.zeros(2, 3, 40, device=DEV)
+    assert sv.token_logprobs(x[:0], top_k=4)["top_token"].shape == (0, 3, 4)
+    assert sv.token_logprobs(x, torch.zeros(2, 0, **i32))["logprob"].shape == (2, 0)
+    r = sv.distill_loss(x[0, :0], torch.zeros(0, 2, **i32), torch.zeros(0, 2, device=DEV), grad=True)
+    assert r["loss"].shape == (0,) and r["grad"].shape == (0, 40)
+    g, st = sv.distill_grad(x[0, :0], torch.zeros(0, 2, **i32), torch.zeros(0, 2, device=DEV), r["stat"])
+    assert g.shape == (0, 40) and st.shape == (0,)
+    torch.cuda.synchronize()
+    assert sv.sv_launch_count() == before
+
+
+def test_one_of_everything():
+    """One sequence without a slot of its own or of a prefix, a vocabulary of one."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    kv = torch.full((2, 1, 1, 1, 128), float("nan"), dtype=torch.float16, device=DEV)
+    out, lse, st = sv.prefix_attention(torch.ones(1, 1, 128, dtype=torch.float16, device=DEV), kv, torch.full((1, 1), 9, **i32),
+                                       torch.zeros(1, **i32), torch.full((1, 1), -3, **i32), torch.zeros(1, **i32), return_lse=True)
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all()) and st.tolist() == [0]
+    r = sv.token_logprobs(torch.full((1, 1, 1), 3e38, device=DEV), torch.zeros(1, 1, **i32), top_k=1)
+    assert r["logprob"].tolist() == [[0.0]] and r["entropy"].tolist() == [[0.0]] and r["top_token"].tolist() == [[[0]]]
+    for tail in (True, False):
+        r = sv.distill_loss(torch.full((1, 1), -3e38, device=DEV), torch.zeros(1, 1, **i32), torch.zeros(1, 1, device=DEV),
+                            tail=tail, grad=True)
+        assert r["loss"].tolist() == [0.0] and r["grad"].tolist() == [[0.0]] and r["status"].tolist() == [0]
