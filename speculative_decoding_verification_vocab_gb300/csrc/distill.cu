@@ -47,6 +47,7 @@ struct DistillArgs {
   void *grad;
   int64_t grad_stride;
   uint32_t *status;
+  int ring;  // bytes of shared memory that the groups stream through
 };
 
 // The teacher's list, an entry to each of the CTA's first threads: its token (-1:
@@ -58,7 +59,6 @@ struct Entry {
   uint32_t flags;  // of the entry: a token outside [0, V), a value that is NaN or +inf
 };
 constexpr int kListWarps = kMaxList / 32;
-static_assert(kMaxList <= kRowThreads, "an entry to a thread");
 template <typename T> __device__ __forceinline__ Entry read_entry(const DistillArgs &a, size_t r, const T *row) {
   Entry e{-1, -INFINITY, 0.0f, 0u};
   if ((int)threadIdx.x < a.K) {
@@ -192,9 +192,9 @@ __device__ __forceinline__ void write_grad(const T *row, T *grad, const RowSlice
     grad[i] = RowElem<T>::store(zero ? 0.0f : grad_of<T>(RowElem<T>::load(row + i), m, coef, k));
   }
   if ((uintptr_t)row % 16 == (uintptr_t)grad % 16) {
-    constexpr int kVecs = kPieces * THREADS;
+    constexpr int kVecs = kGroupVecs<THREADS>;
     uint4 *out = (uint4 *)(grad + s.head);
-    for (int g = (s.v1 - s.v0 + kVecs - 1) / kVecs - 1; g >= 0; --g) {
+    for (int g = row_groups<THREADS>(s) - 1; g >= 0; --g) {
       const int v0 = s.v0 + g * kVecs + (int)threadIdx.x;
       uint4 w[kPieces];  // all on their way before the first is stored
 #pragma unroll
@@ -224,7 +224,7 @@ template <typename T> __device__ __forceinline__ bool in_slice(const RowSlice &s
 struct ListedBits {
   uint32_t singles, twice;
 };
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void set_bit(uint32_t *bits, ListedBits &l, const RowSlice &s, uint32_t rank, int token) {
   constexpr int VEC = RowElem<T>::VEC;
   if (token < 0 || !in_slice<T>(s, rank, token)) return;
@@ -235,19 +235,19 @@ __device__ __forceinline__ void set_bit(uint32_t *bits, ListedBits &l, const Row
     was = atomicOr(&l.singles, bit);
   } else {
     const int v = i / VEC - s.v0;
-    bit = 1u << (v % kGroupVecs / kRowThreads * 8 + i % VEC);
-    was = atomicOr(&bits[v / kGroupVecs * kRowThreads + v % kRowThreads], bit);
+    bit = 1u << (v % kGroupVecs<THREADS> / THREADS * 8 + i % VEC);
+    was = atomicOr(&bits[v / kGroupVecs<THREADS> * THREADS + v % THREADS], bit);
   }
   if (was & bit) l.twice = 1;
 }
 // The unlisted elements of a group's pieces into the sums.
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void add_group(RowSums &sums, const unsigned char *ring, int at, uint32_t listed, float k,
                                           unsigned long long k2) {
   constexpr int VEC = RowElem<T>::VEC;
   uint4 w[kPieces];
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(ring, at, j);
+  for (int j = 0; j < kPieces; ++j) w[j] = ring_piece<THREADS>(ring, at, j);
   if (listed) {  // -inf in their places
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
@@ -338,36 +338,39 @@ __device__ __forceinline__ void put_row(const DistillArgs &a, size_t r, const Ro
   a.status[r] = row.flags;
 }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, unsigned C) {
+// THREADS: the CTA's, of which as many stay on an SM as registers allow.
+template <typename T, bool GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) distill_kernel(DistillArgs a, unsigned C) {
   grid_dep_sync();
+  static_assert(kMaxList <= THREADS, "an entry to a thread");
+  constexpr int kWarps = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t r = blockIdx.x / C;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ ListPart s_list[kListWarps];
-  __shared__ RowPart s_part[kRowWarps];
+  __shared__ RowPart s_part[kWarps];
   __shared__ Exchange s_all;
   __shared__ ListedBits s_bits;
   __shared__ float s_loss[kListWarps];
   if (C > 1) cluster_arrive_relaxed();
   const T *row = (const T *)a.logits + (int64_t)r * a.row_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
-  const int groups = row_groups(s);
-  uint32_t *bits = (uint32_t *)(smem + kRing * kGroupBytes);
+  const int groups = row_groups<THREADS>(s);
+  uint32_t *bits = (uint32_t *)(smem + a.ring);
 
 #pragma unroll
   for (int g = 0; g < kRing - 1; ++g) {
-    if (g < groups) load_group(row, s, g, g, smem);
+    if (g < groups) load_group<THREADS>(row, s, g, g, smem);
     group_commit();
   }
   const Entry e = read_entry(a, r, row);
   const bool has_single = rank == 0 && (int)threadIdx.x < s.singles;
   const float single_x = has_single ? RowElem<T>::load(row + single_at<T>(s, threadIdx.x)) : -INFINITY;
-  for (int g = 0; g < groups; ++g) bits[g * kRowThreads + threadIdx.x] = 0;
+  for (int g = 0; g < groups; ++g) bits[g * THREADS + threadIdx.x] = 0;
   if (threadIdx.x == 0) s_bits = ListedBits{0, 0};
   __syncthreads();
-  set_bit<T>(bits, s_bits, s, rank, e.token);
+  set_bit<T, THREADS>(bits, s_bits, s, rank, e.token);
   __syncthreads();
   const float k = a.k;
   const unsigned long long k2 = f2_splat(k);
@@ -375,10 +378,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
   if (has_single && !(s_bits.singles >> threadIdx.x & 1)) add_single<false>(sums, single_x, k);
   int slot = 0, slot_load = kRing - 1;
   for (int g = 0; g < groups; ++g) {
-    if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
+    if (g + kRing - 1 < groups) load_group<THREADS>(row, s, g + kRing - 1, slot_load, smem);
     group_commit();
     group_wait<kRing - 1>();
-    add_group<T>(sums, smem, slot, bits[g * kRowThreads + threadIdx.x], k, k2);
+    add_group<T, THREADS>(sums, smem, slot, bits[g * THREADS + threadIdx.x], k, k2);
     slot = slot + 1 == kRing ? 0 : slot + 1;
     slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
   }
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
     if (lane == 0) s_list[warp] = p;
   }
   __syncthreads();
-  RowPart rest = warp_join(lane < kRowWarps ? s_part[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
+  RowPart rest = warp_join(lane < kWarps ? s_part[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
   uint32_t flags = s_bits.twice ? SV_ROW_BAD_TOKEN : 0u;
   if (C > 1) {
     cluster_wait();
@@ -412,8 +415,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillArgs a, 
     const float c = out.st.w == 0.0f ? 0.0f : out.st.y * w;
     // (the logits may be the gradient's own place: a piece is read, by whoever writes
     // there, before it is written)
-    write_grad<T, kRowThreads>(row, grad, s, rank, out.st.x, c, k, [&](int g, int j, int v) {
-      return g >= groups - kRing ? ring_piece(smem, g % kRing, j) : ((const uint4 *)(row + s.head))[v];
+    write_grad<T, THREADS>(row, grad, s, rank, out.st.x, c, k, [&](int g, int j, int v) {
+      return g >= groups - kRing ? ring_piece<THREADS>(smem, g % kRing, j) : ((const uint4 *)(row + s.head))[v];
     });
     __syncthreads();
     if (out.st.w != 0.0f && e.token >= 0 && in_slice<T>(s, rank, e.token))
@@ -458,30 +461,43 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillAr
   if (rank == 0 && threadIdx.x == 0) a.status[r] = flags;
 }
 
-template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, cudaStream_t st) {
-  // CTAs to a row: with a gradient 128 KB of it to each (256 or 64 KB, C = 1 or 4 at V =
-  // 128256 bf16: 229 and 206 us where these take 200), less where a batch of few rows
-  // would leave SMs idle
+template <typename T, bool GRAD, int THREADS> cudaError_t launch_loss(DistillArgs a, unsigned C, cudaStream_t st) {
+  // of a slice: its groups, as many of them as the ring has at once, and a bit for each
+  // element in whole groups
   const size_t row = (size_t)a.V * sizeof(T);
-  unsigned C = 1;
-  if (GRAD)
-    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C < 456))) C *= 2;
-  else
-    C = row_ctas(row, a.R, 16384, 608);
-  auto smem_of = [](size_t bytes, unsigned c) {  // the ring, and a bit for each element in whole groups
-    const size_t per = (bytes / 16 + c - 1) / c, groups = (per + kGroupVecs - 1) / kGroupVecs;
-    return kRing * (size_t)kGroupBytes + groups * kGroupVecs;
+  auto groups_of = [](size_t bytes, unsigned c) {
+    return ((bytes / 16 + c - 1) / c + kGroupVecs<THREADS> - 1) / kGroupVecs<THREADS>;
   };
+  const size_t groups = groups_of(row, C);
+  a.ring = kGroupBytes<THREADS> * (int)(groups < (size_t)kRing ? groups : (size_t)kRing);
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {  // as much as the longest rows take
-    const cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem_of((size_t)SV_MAX_VOCAB * sizeof(T), kMaxRowCluster));
+    const size_t most = groups_of((size_t)SV_MAX_VOCAB * sizeof(T), kMaxRowCluster) * kGroupVecs<THREADS>;
+    const cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, GRAD, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRing * kGroupBytes<THREADS> + (int)most);
     if (e != cudaSuccess) return e;
     set_dev = dev;
   }
-  return launch_pdl_cluster(distill_kernel<T, GRAD>, dim3((unsigned)a.R * C), dim3(kRowThreads), C, smem_of(row, C), st, a, C);
+  return launch_pdl_cluster(distill_kernel<T, GRAD, THREADS>, dim3((unsigned)a.R * C), dim3(THREADS), C,
+                            a.ring + groups * kGroupVecs<THREADS>, st, a, C);
+}
+template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, cudaStream_t st) {
+  // CTAs to a row: with a gradient 128 KB of it to each (256 or 64 KB, C = 1 or 4 at V =
+  // 128256 bf16: 229 and 206 us where these take 200), less where a batch of few rows
+  // would leave SMs idle.  CTAs of 128 threads for short rows, whose time is the way
+  // there and back, of which more are under way (4000 rows of 1000 fp32, loss: 18.5 us,
+  // by 256 threads 31.9; with the gradient 21 and 36; of 32000 bf16 48 and 59, with the
+  // gradient 98 and 96; of 50256 fp32 128 and 121, with the gradient 339 and 278)
+  const size_t row = (size_t)a.V * sizeof(T);
+  const bool small = row <= (GRAD ? 32768 : 131072);
+  unsigned C = 1;
+  if (GRAD)
+    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C < 456))) C *= 2;
+  else
+    C = row_ctas(row, a.R, 16384, small ? 1216 : 608);
+  return small ? launch_loss<T, GRAD, 128>(a, C, st) : launch_loss<T, GRAD, 256>(a, C, st);
 }
 template <typename T> cudaError_t launch_grad(const DistillArgs &a, cudaStream_t st) {
   // 64 KB of a row to a CTA

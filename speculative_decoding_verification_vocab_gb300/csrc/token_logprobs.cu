@@ -36,11 +36,12 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kMaxTop = 128;
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kRing = 3;       // groups: one in work, two on their way
 constexpr int kRuns = 8;       // of a thread's elements
 constexpr int kList = 2048;    // keys, in the ring's place; a power of two
 constexpr int kSlowList = 512; // of them, where the list is cut back: at least kMaxTop + kRowThreads
-static_assert(kList * 8 + kRuns * kRowThreads * 2 <= kRing * kGroupBytes && kSlowList >= kMaxTop + kRowThreads, "lists");
+static_assert(kList * 8 + kRuns * kRowThreads * 2 <= kRing * kGroupBytes<kRowThreads> && kSlowList >= kMaxTop + kRowThreads, "lists");
 
 struct LogArgs {
   const void *logits;
@@ -182,9 +183,9 @@ __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32
     offer(RowElem<T>::load(row + i), i);
   }
   __syncthreads();
-  const int groups = row_groups(s);
+  const int groups = row_groups<kRowThreads>(s);
   for (int g = 0; g < groups; ++g) {
-    auto piece = [&](int j) { return s.v0 + g * kGroupVecs + j * kRowThreads + (int)threadIdx.x; };
+    auto piece = [&](int j) { return s.v0 + g * kGroupVecs<kRowThreads> + j * kRowThreads + (int)threadIdx.x; };
     const int before = *s_n;  // settled by the barriers that ended the last group
     float most[kPieces], top = -INFINITY;
 #pragma unroll
@@ -241,8 +242,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   extern __shared__ __align__(16) unsigned char smem[];
   u64 *list = (u64 *)smem;                                         // [kList], when the ring is free
   uint16_t *hits = (uint16_t *)(list + kList);                     // [kRuns kRowThreads], as the list
-  uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes);       // [kRuns][kRowThreads]
-  u64 *all = (u64 *)(smem + kRing * kGroupBytes + (TOP ? kRuns * kRowThreads * 2 : 0));  // [C][K], the first CTA's
+  uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes<kRowThreads>);       // [kRuns][kRowThreads]
+  u64 *all = (u64 *)(smem + kRing * kGroupBytes<kRowThreads> + (TOP ? kRuns * kRowThreads * 2 : 0));  // [C][K], the first CTA's
   __shared__ RowPart s_part[kRowWarps];
   __shared__ RowPart s_all[kMaxRowCluster];
   __shared__ int s_n, s_hits;
@@ -271,10 +272,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   if (C > 1) cluster_arrive_relaxed();
   const T *row = (const T *)a.logits + b * a.seq_stride + r * a.row_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
-  const int groups = row_groups(s);
+  const int groups = row_groups<kRowThreads>(s);
 #pragma unroll
   for (int g = 0; g < kRing - 1; ++g) {
-    if (g < groups) load_group(row, s, g, g, smem);
+    if (g < groups) load_group<kRowThreads>(row, s, g, g, smem);
     group_commit();
   }
   const bool known = token >= 0 && token < a.V;
@@ -299,12 +300,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   for (int g = 0; g < groups; ++run) {
     float run_top = -INFINITY;
     for (const int end = min(g + per, groups); g < end; ++g) {
-      if (g + kRing - 1 < groups) load_group(row, s, g + kRing - 1, slot_load, smem);
+      if (g + kRing - 1 < groups) load_group<kRowThreads>(row, s, g + kRing - 1, slot_load, smem);
       group_commit();
       group_wait<kRing - 1>();
       uint4 w[kPieces];
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) w[j] = ring_piece(smem, slot, j);
+      for (int j = 0; j < kPieces; ++j) w[j] = ring_piece<kRowThreads>(smem, slot, j);
       const float top = RowElem<T>::most4(w);
       if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     for (int i = threadIdx.x; i < pieces; i += kRowThreads) {
       const int hit = hits[i / of_run], q = i % of_run;
       const int g = hit / kRowThreads * per + q / kPieces;
-      const int v = s.v0 + g * kGroupVecs + q % kPieces * kRowThreads + hit % kRowThreads;
+      const int v = s.v0 + g * kGroupVecs<kRowThreads> + q % kPieces * kRowThreads + hit % kRowThreads;
       if (g >= groups || v >= s.v1) continue;
       const uint4 w = piece_at(row, s, v);
       const float m = RowElem<T>::most(w);
@@ -436,13 +437,13 @@ cudaError_t launch(const LogArgs &a, unsigned items, unsigned C, cudaStream_t st
       while (keys < (size_t)C * a.K) keys *= 2;
     }
   }
-  const size_t smem = (size_t)kRing * kGroupBytes + (TOP ? kRuns * kRowThreads * 2 : 0) + keys * 8;
+  const size_t smem = (size_t)kRing * kGroupBytes<kRowThreads> + (TOP ? kRuns * kRowThreads * 2 : 0) + keys * 8;
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
     const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kRing * kGroupBytes + kRuns * kRowThreads * 2 + (int)kMaxRowCluster * kMaxTop * 8);
+                                               kRing * kGroupBytes<kRowThreads> + kRuns * kRowThreads * 2 + (int)kMaxRowCluster * kMaxTop * 8);
     if (e != cudaSuccess) return e;
     set_dev = dev;
   }

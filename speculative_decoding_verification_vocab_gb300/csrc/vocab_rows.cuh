@@ -11,11 +11,10 @@
 
 namespace sv {
 
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kPieces = 4;                              // of a thread in a group
-constexpr int kGroupVecs = kPieces * kRowThreads;       // 16-byte pieces of a group
-constexpr int kGroupBytes = kGroupVecs * 16;
+constexpr int kPieces = 4;  // of a thread in a group
+// a group of a CTA: 16-byte pieces, and their bytes
+template <int THREADS> constexpr int kGroupVecs = kPieces * THREADS;
+template <int THREADS> constexpr int kGroupBytes = kGroupVecs<THREADS> * 16;
 constexpr unsigned kMaxRowCluster = 8;
 constexpr float kLog2eF = 1.4426950408889634f;
 // The reference of the exponentials follows the maximum only when an element
@@ -154,31 +153,33 @@ template <typename T> __device__ __forceinline__ RowSlice row_slice(const T *row
 template <typename T> __device__ __forceinline__ int single_at(const RowSlice &s, int i) {
   return i < s.head ? i : i + s.vecs * RowElem<T>::VEC;
 }
-__device__ __forceinline__ int row_groups(const RowSlice &s) { return (s.v1 - s.v0 + kGroupVecs - 1) / kGroupVecs; }
+template <int THREADS> __device__ __forceinline__ int row_groups(const RowSlice &s) {
+  return (s.v1 - s.v0 + kGroupVecs<THREADS> - 1) / kGroupVecs<THREADS>;
+}
 
 // Group g's pieces of this thread into its own places of slot `slot`; places
 // without a piece hold -inf, which no sum and no list takes up.  What a thread
 // reads there it has copied itself, so no barrier stands between.
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ void load_group(const T *row, const RowSlice &s, int g, int slot, unsigned char *ring) {
-  const int v = s.v0 + g * kGroupVecs + (int)threadIdx.x;
+  const int v = s.v0 + g * kGroupVecs<THREADS> + (int)threadIdx.x;
   const uint4 *src = (const uint4 *)(row + s.head) + v;
-  unsigned char *at = ring + (size_t)slot * kGroupBytes + threadIdx.x * 16;
+  unsigned char *at = ring + (size_t)slot * kGroupBytes<THREADS> + threadIdx.x * 16;
   const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
-  if (s.v0 + (g + 1) * kGroupVecs <= s.v1) {  // all of them
+  if (s.v0 + (g + 1) * kGroupVecs<THREADS> <= s.v1) {  // all of them
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRowThreads * 16), "l"(src + j * kRowThreads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * THREADS * 16), "l"(src + j * THREADS)
                    : "memory");
     return;
   }
 #pragma unroll 1
   for (int j = 0; j < kPieces; ++j) {
-    if (v + j * kRowThreads < s.v1)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * kRowThreads * 16), "l"(src + j * kRowThreads)
+    if (v + j * THREADS < s.v1)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + j * THREADS * 16), "l"(src + j * THREADS)
                    : "memory");
     else
-      *(uint4 *)(at + j * kRowThreads * 16) =
+      *(uint4 *)(at + j * THREADS * 16) =
           make_uint4(RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf, RowElem<T>::kNegInf);
   }
 }
@@ -186,8 +187,8 @@ __device__ __forceinline__ void group_commit() { asm volatile("cp.async.commit_g
 template <int N> __device__ __forceinline__ void group_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 ring_piece(const unsigned char *ring, int slot, int j) {
-  return *(const uint4 *)(ring + (size_t)slot * kGroupBytes + (j * kRowThreads + threadIdx.x) * 16);
+template <int THREADS> __device__ __forceinline__ uint4 ring_piece(const unsigned char *ring, int slot, int j) {
+  return *(const uint4 *)(ring + (size_t)slot * kGroupBytes<THREADS> + (j * THREADS + threadIdx.x) * 16);
 }
 
 // ------------------------------------------------------------ online sums
