@@ -371,3 +371,19 @@ def test_streams_capture_and_two_calls_at_once():
     host = sv.distill_loss(static.cpu().pin_memory(), tok, val, grad=True)
     torch.cuda.synchronize()
     assert all(torch.equal(host[k].to(DEV), want[k]) for k in want)
+
+
+@pytest.mark.parametrize("V,dtype", [(1 << 20, torch.float32), (1 << 22, torch.float32), (1 << 21, torch.bfloat16)])
+def test_many_rows_of_large_vocabularies(V, dtype):
+    """More rows than the card has CTAs, all of them one row of memory: the same loss
+    as alone, but for the order of its sums (`rel` of compare, for each of them)."""
+    logits, token, value = make(1, V, 100, dtype, 4)
+    x, tok, val = put(logits), put(token), put(value)
+    alone = sv.distill_loss(x, tok, val)
+    R = 1300
+    many = sv.distill_loss(x.expand(R, V), tok.expand(R, -1).contiguous(), val.expand(R, -1).contiguous())
+    torch.cuda.synchronize()
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    compare(logits, token, value, None, 1.0, True, f(alone["loss"]), None, alone["status"].cpu().numpy())
+    compare(logits, token, value, None, 1.0, True, f(many["loss"][:1]), None, many["status"][:1].cpu().numpy())
+    assert torch.equal(many["loss"], many["loss"][:1].expand(R)) and not bool(many["status"].any())
