@@ -494,9 +494,9 @@ template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, c
   const bool small = row <= (GRAD ? 32768 : 131072);
   unsigned C = 1;
   if (GRAD)
-    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C < 456))) C *= 2;
+    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C * 2 <= 456))) C *= 2;
   else
-    C = row_ctas(row, a.R, 16384, small ? 1216 : 608);
+    C = row_ctas(row, a.R, small ? 456 : 304);
   while (C < kMaxRowCluster && row > C * (size_t)262144) C *= 2;  // a slice's bits: 16 KB, of the longest rows 128
   return small ? launch_loss<T, GRAD, 128>(a, C, st) : launch_loss<T, GRAD, 256>(a, C, st);
 }

@@ -36,12 +36,14 @@ namespace {
 
 typedef unsigned long long u64;
 constexpr int kMaxTop = 128;
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kMaxima = 256;   // of a CTA's elements, one or two to a thread: they give the threshold
 constexpr int kRing = 3;       // groups: one in work, two on their way
 constexpr int kRuns = 8;       // of a thread's elements
 constexpr int kList = 2048;    // keys, in the ring's place; a power of two
-constexpr int kSlowList = 512; // of them, where the list is cut back: at least kMaxTop + kRowThreads
-static_assert(kList * 8 + kRuns * kRowThreads * 2 <= kRing * kGroupBytes<kRowThreads> && kSlowList >= kMaxTop + kRowThreads, "lists");
+constexpr int kSlowList = 512; // of them, where the list is cut back: at least kMaxTop + THREADS
+template <int THREADS>
+constexpr bool kFits = kList * 8 + kRuns * THREADS * 2 <= kRing * kGroupBytes<THREADS> && kSlowList >= kMaxTop + THREADS;
+static_assert(kFits<128> && kFits<256> && kMaxTop <= kMaxima, "lists");
 
 struct LogArgs {
   const void *logits;
@@ -71,32 +73,50 @@ __device__ __forceinline__ int index_of(u64 key) { return (int)~(uint32_t)key; }
 // The min(n, K) largest of keys[0, n), all different, in descending order at the
 // front; keys has room for the next power of two.  Every thread of the CTA calls
 // it with the keys visible, and finds them in place.
-__device__ void keep_best(u64 *keys, int n, int K) {
-  if (n <= kRowThreads) {  // a thread counts what is above its key
+template <int THREADS> __device__ void keep_best(u64 *keys, int n, int K) {
+  constexpr int M = kMaxima / THREADS;
+  if (n <= kMaxima) {  // a thread counts what is above its keys
     const int i = threadIdx.x;
-    const u64 mine = i < n ? keys[i] : 0;
-    int above = 0;
-    if ((i & ~31) < n) {
-      const ulonglong2 *two = (const ulonglong2 *)keys;
+    u64 mine[M];
+    int above[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      mine[m] = i + m * THREADS < n ? keys[i + m * THREADS] : 0;
+      above[m] = 0;
+    }
+    const ulonglong2 *two = (const ulonglong2 *)keys;
+    auto count = [&](int of) {
 #pragma unroll 4
       for (int j = 0; j < n / 2; ++j) {
         const ulonglong2 o = two[j];
-        above += (o.x > mine) + (o.y > mine);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (m < of) above[m] += (o.x > mine[m]) + (o.y > mine[m]);
       }
-      if (n & 1) above += keys[n - 1] > mine;
-    }
+      if (n & 1) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (m < of) above[m] += keys[n - 1] > mine[m];
+      }
+    };
+    if (n > THREADS)
+      count(M);
+    else if ((i & ~31) < n)
+      count(1);
     __syncthreads();
-    if (i < n && above < K) keys[above] = mine;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      if (i + m * THREADS < n && above[m] < K) keys[above[m]] = mine[m];
     __syncthreads();
     return;
   }
-  int size = 2 * kRowThreads;
+  int size = 2 * kMaxima;
   while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kRowThreads) keys[i] = 0;
+  for (int i = n + threadIdx.x; i < size; i += THREADS) keys[i] = 0;
   for (int run = 2; run <= size; run *= 2)
     for (int step = run / 2; step; step /= 2) {
       __syncthreads();
-      for (int i = threadIdx.x; i < size / 2; i += kRowThreads) {
+      for (int i = threadIdx.x; i < size / 2; i += THREADS) {
         const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
         const u64 a = keys[lo], b = keys[hi];
         if ((a < b) == ((lo & run) == 0)) {  // descending where the run's bit is clear
@@ -151,7 +171,7 @@ template <typename T> __device__ __forceinline__ uint4 piece_at(const T *row, co
 // The K best of a slice by a list that is cut back as it fills, a group of pieces
 // after the other.  Every thread of the CTA calls it and finds the list's first
 // min(K, elements) in order; returns their number.  s_n: a counter.
-template <typename T>
+template <typename T, int THREADS>
 __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32_t rank, u64 *list, int K, int *s_n) {
   constexpr int VEC = RowElem<T>::VEC;
   float tau = -INFINITY;  // what an element has to reach, and its key to exceed
@@ -170,7 +190,7 @@ __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32
   };
   // after a barrier behind the last offer
   auto cut = [&](int n) {
-    keep_best(list, n, K);
+    keep_best<THREADS>(list, n, K);
     if (n >= K) {
       tau_key = list[K - 1];
       tau = value_of(tau_key);
@@ -183,9 +203,9 @@ __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32
     offer(RowElem<T>::load(row + i), i);
   }
   __syncthreads();
-  const int groups = row_groups<kRowThreads>(s);
+  const int groups = row_groups<THREADS>(s);
   for (int g = 0; g < groups; ++g) {
-    auto piece = [&](int j) { return s.v0 + g * kGroupVecs<kRowThreads> + j * kRowThreads + (int)threadIdx.x; };
+    auto piece = [&](int j) { return s.v0 + g * kGroupVecs<THREADS> + j * THREADS + (int)threadIdx.x; };
     const int before = *s_n;  // settled by the barriers that ended the last group
     float most[kPieces], top = -INFINITY;
 #pragma unroll
@@ -214,7 +234,7 @@ __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32
       n = before;
       for (int j = 0; j < kPieces; ++j) {
         for (int i = 0; i < VEC; ++i) {
-          if (n > kSlowList - kRowThreads) cut(n);
+          if (n > kSlowList - THREADS) cut(n);
           if (piece(j) < s.v1) {
             const int at = s.head + piece(j) * VEC + i;
             offer(RowElem<T>::load(row + at), at);
@@ -228,12 +248,13 @@ __device__ __noinline__ int best_by_list(const T *row, const RowSlice &s, uint32
     if (n >= 2 * K + 32) cut(n);
   }
   const int n = *s_n;
-  keep_best(list, n, K);
+  keep_best<THREADS>(list, n, K);
   return min(n, K);
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs a, unsigned C) {
+// THREADS: the CTA's, of which as many stay on an SM as registers allow.
+template <typename T, bool TOP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) token_logprobs_kernel(LogArgs a, unsigned C) {
   grid_dep_sync();
   constexpr int VEC = RowElem<T>::VEC;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -241,10 +262,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   extern __shared__ __align__(16) unsigned char smem[];
   u64 *list = (u64 *)smem;                                         // [kList], when the ring is free
-  uint16_t *hits = (uint16_t *)(list + kList);                     // [kRuns kRowThreads], as the list
-  uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes<kRowThreads>);       // [kRuns][kRowThreads]
-  u64 *all = (u64 *)(smem + kRing * kGroupBytes<kRowThreads> + (TOP ? kRuns * kRowThreads * 2 : 0));  // [C][K], the first CTA's
-  __shared__ RowPart s_part[kRowWarps];
+  uint16_t *hits = (uint16_t *)(list + kList);                     // [kRuns THREADS], as the list
+  uint16_t *runs = (uint16_t *)(smem + kRing * kGroupBytes<THREADS>);  // [kRuns][THREADS]
+  u64 *all = (u64 *)(smem + kRing * kGroupBytes<THREADS> + (TOP ? kRuns * THREADS * 2 : 0));  // [C][K], the first CTA's
+  __shared__ RowPart s_part[THREADS / 32];
   __shared__ RowPart s_all[kMaxRowCluster];
   __shared__ int s_n, s_hits;
   __shared__ __align__(16) uint32_t s_bins[2][256];
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
         a.entropy[item] = skip ? 0.0f : nan;
         a.status[item] = skip ? 0u : SV_ROW_BAD_ROW;
       }
-      for (int i = threadIdx.x; i < a.K; i += kRowThreads) {
+      for (int i = threadIdx.x; i < a.K; i += THREADS) {
         a.top_token[item * a.K + i] = -1;
         a.top_logprob[item * a.K + i] = skip ? -INFINITY : nan;
       }
@@ -272,10 +293,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   if (C > 1) cluster_arrive_relaxed();
   const T *row = (const T *)a.logits + b * a.seq_stride + r * a.row_stride;
   const RowSlice s = row_slice(row, a.V, rank, C);
-  const int groups = row_groups<kRowThreads>(s);
+  const int groups = row_groups<THREADS>(s);
 #pragma unroll
   for (int g = 0; g < kRing - 1; ++g) {
-    if (g < groups) load_group<kRowThreads>(row, s, g, g, smem);
+    if (g < groups) load_group<THREADS>(row, s, g, g, smem);
     group_commit();
   }
   const bool known = token >= 0 && token < a.V;
@@ -289,23 +310,26 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   if (has_single) add_single<true>(sums, single_x, k);
   if (TOP) {
     if (threadIdx.x == 0) s_n = s_hits = 0;
-    for (int i = threadIdx.x; i < 512; i += kRowThreads) s_bins[0][i] = 0;
+    for (int i = threadIdx.x; i < 512; i += THREADS) s_bins[0][i] = 0;
     __syncthreads();
   }
 
   // run i of a thread: its groups [i per, (i + 1) per)
   const int per = (groups + kRuns - 1) / kRuns;
-  float thread_top = single_x;
+  constexpr int M = kMaxima / THREADS;
+  float tops[M];  // of the runs i with i % M, the first with the single
+#pragma unroll
+  for (int m = 0; m < M; ++m) tops[m] = m ? -INFINITY : single_x;
   int run = 0, slot = 0, slot_load = kRing - 1;
   for (int g = 0; g < groups; ++run) {
     float run_top = -INFINITY;
     for (const int end = min(g + per, groups); g < end; ++g) {
-      if (g + kRing - 1 < groups) load_group<kRowThreads>(row, s, g + kRing - 1, slot_load, smem);
+      if (g + kRing - 1 < groups) load_group<THREADS>(row, s, g + kRing - 1, slot_load, smem);
       group_commit();
       group_wait<kRing - 1>();
       uint4 w[kPieces];
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j) w[j] = ring_piece<kRowThreads>(smem, slot, j);
+      for (int j = 0; j < kPieces; ++j) w[j] = ring_piece<THREADS>(smem, slot, j);
       const float top = RowElem<T>::most4(w);
       if (top > sums.lim) raise<true>(sums, top, k);
 #pragma unroll
@@ -315,26 +339,37 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
       slot_load = slot_load + 1 == kRing ? 0 : slot_load + 1;
     }
     if (TOP) {
-      runs[run * kRowThreads + threadIdx.x] = up16(run_top);
-      thread_top = fmaxf(thread_top, run_top);
+      runs[run * THREADS + threadIdx.x] = up16(run_top);
+      if (M == 1 || run % 2 == 0)
+        tops[0] = fmaxf(tops[0], run_top);
+      else
+        tops[M - 1] = fmaxf(tops[M - 1], run_top);
     }
   }
   group_wait<0>();
 
-  // the upper 16 bits of the thread's maximum, as an ordered number (0: none above -inf)
-  const uint32_t top_key = TOP && thread_top > -INFINITY ? order_of(thread_top) >> 16 : 0u;
-  if (top_key) atomicAdd(&s_bins[0][top_key >> 8], 1u);
+  // the upper 16 bits of the thread's maxima, as ordered numbers (0: none above -inf)
+  uint32_t top_key[M];
+  float thread_top = -INFINITY;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    thread_top = fmaxf(thread_top, tops[m]);
+    top_key[m] = TOP && tops[m] > -INFINITY ? order_of(tops[m]) >> 16 : 0u;
+    if (top_key[m]) atomicAdd(&s_bins[0][top_key[m] >> 8], 1u);
+  }
   const RowPart mine = warp_join(part_of(sums), k);
   if (lane == 0) s_part[warp] = mine;
   __syncthreads();  // the ring is free, too
   int n = 0;
   if (TOP) {
-    // tau: the K-th largest of the threads' maxima, to 16 bits (none: all above -inf), a
+    // tau: the K-th largest of the CTA's maxima, to 16 bits (none: all above -inf), a
     // byte of it at a time.  K elements reach it, and a few more: in any order 1.04 K of
     // 128256 at K = 20, 1.4 K at 128.
     int left = a.K;
     const int high = digit_of(s_bins[0], left);
-    if (high >= 0 && (int)(top_key >> 8) == high) atomicAdd(&s_bins[1][top_key & 255], 1u);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      if (high >= 0 && (int)(top_key[m] >> 8) == high) atomicAdd(&s_bins[1][top_key[m] & 255], 1u);
     __syncthreads();
     const float tau = high < 0 ? -INFINITY : value_of((uint32_t)(high << 8 | digit_of(s_bins[1], left)) << 16);
     auto offer = [&](float x, int index) {
@@ -348,16 +383,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     if (thread_top >= tau && thread_top > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < kRuns; ++i) {
-        const float top = __uint_as_float((uint32_t)runs[i * kRowThreads + threadIdx.x] << 16);
-        if (i < run && top >= tau) hits[atomicAdd(&s_hits, 1)] = (uint16_t)(i * kRowThreads + threadIdx.x);
+        const float top = __uint_as_float((uint32_t)runs[i * THREADS + threadIdx.x] << 16);
+        if (i < run && top >= tau) hits[atomicAdd(&s_hits, 1)] = (uint16_t)(i * THREADS + threadIdx.x);
       }
     }
     __syncthreads();
     const int of_run = per * kPieces, pieces = s_hits * of_run;
-    for (int i = threadIdx.x; i < pieces; i += kRowThreads) {
+    for (int i = threadIdx.x; i < pieces; i += THREADS) {
       const int hit = hits[i / of_run], q = i % of_run;
-      const int g = hit / kRowThreads * per + q / kPieces;
-      const int v = s.v0 + g * kGroupVecs<kRowThreads> + q % kPieces * kRowThreads + hit % kRowThreads;
+      const int g = hit / THREADS * per + q / kPieces;
+      const int v = s.v0 + g * kGroupVecs<THREADS> + q % kPieces * THREADS + hit % THREADS;
       if (g >= groups || v >= s.v1) continue;
       const uint4 w = piece_at(row, s, v);
       const float m = RowElem<T>::most(w);
@@ -370,16 +405,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     __syncthreads();
     n = s_n;
     if (n > kList) {
-      n = best_by_list(row, s, rank, list, a.K, &s_n);
+      n = best_by_list<T, THREADS>(row, s, rank, list, a.K, &s_n);
     } else {
-      keep_best(list, n, a.K);
+      keep_best<THREADS>(list, n, a.K);
       n = min(n, a.K);
     }
   }
   auto join = [&](const RowPart *parts, int count) {
     return warp_join(lane < count ? parts[lane] : RowPart{-INFINITY, 0.0f, 0.0f}, k);
   };
-  RowPart sum = join(s_part, kRowWarps);
+  RowPart sum = join(s_part, THREADS / 32);
   if (C > 1) {
     cluster_wait();
     if (threadIdx.x == 0) {
@@ -390,14 +425,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 8), "r"(__float_as_uint(sum.s)) : "memory");
     }
     if (TOP)
-      for (int i = threadIdx.x; i < a.K; i += kRowThreads) cluster_st_u64(all + rank * a.K + i, 0, i < n ? list[i] : 0);
+      for (int i = threadIdx.x; i < a.K; i += THREADS) cluster_st_u64(all + rank * a.K + i, 0, i < n ? list[i] : 0);
     cluster_sync();
     if (rank != 0) return;
     sum = join(s_all, (int)C);
     if (TOP) {
       // lists that are not full hold zeros behind their keys; where the keys are
       // fewer than K in all, so does the first list behind their number
-      keep_best(all, (int)C * a.K, a.K);
+      keep_best<THREADS>(all, (int)C * a.K, a.K);
       list = all;
       n = a.K;
     }
@@ -418,7 +453,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
     a.status[item] = flags;
   }
   if (TOP) {
-    for (int i = threadIdx.x; i < a.K; i += kRowThreads) {
+    for (int i = threadIdx.x; i < a.K; i += THREADS) {
       const u64 key = i < n ? list[i] : 0;
       a.top_token[item * a.K + i] = bad || !key ? -1 : index_of(key);
       a.top_logprob[item * a.K + i] = bad ? nan : key ? logprob(value_of(key)) : -INFINITY;
@@ -426,31 +461,42 @@ __global__ void __launch_bounds__(kRowThreads, 4) token_logprobs_kernel(LogArgs 
   }
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, int THREADS>
 cudaError_t launch(const LogArgs &a, unsigned items, unsigned C, cudaStream_t st) {
   // dynamic memory beyond 48 KB has to be asked for, once for each device
   size_t keys = 0;
   if (TOP && C > 1) {
     keys = ((size_t)C * a.K + 1) / 2 * 2;
-    if (keys > (size_t)kRowThreads) {  // more than that keep_best sorts in a power of two
-      keys = 2 * kRowThreads;
+    if (keys > (size_t)kMaxima) {  // more than that keep_best sorts in a power of two
+      keys = 2 * kMaxima;
       while (keys < (size_t)C * a.K) keys *= 2;
     }
   }
-  const size_t smem = (size_t)kRing * kGroupBytes<kRowThreads> + (TOP ? kRuns * kRowThreads * 2 : 0) + keys * 8;
+  const size_t smem = (size_t)kRing * kGroupBytes<THREADS> + (TOP ? kRuns * THREADS * 2 : 0) + keys * 8;
   static thread_local int set_dev = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
-    const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kRing * kGroupBytes<kRowThreads> + kRuns * kRowThreads * 2 + (int)kMaxRowCluster * kMaxTop * 8);
+    const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRing * kGroupBytes<THREADS> + kRuns * THREADS * 2 + (int)kMaxRowCluster * kMaxTop * 8);
     if (e != cudaSuccess) return e;
     set_dev = dev;
   }
-  return launch_pdl_cluster(token_logprobs_kernel<T, TOP>, dim3(items * C), dim3(kRowThreads), C, smem, st, a, C);
+  return launch_pdl_cluster(token_logprobs_kernel<T, TOP, THREADS>, dim3(items * C), dim3(THREADS), C, smem, st, a, C);
 }
-template <typename T> cudaError_t launch(const LogArgs &a, unsigned items, unsigned C, cudaStream_t st) {
-  return a.K ? launch<T, true>(a, items, C, st) : launch<T, false>(a, items, C, st);
+// CTAs of 128 threads where rows are short, or the few best are asked for: what a CTA
+// does behind its row lies apart from more others' (4000 rows, K = 20: V = 8192 bf16 35
+// us, by 256 threads 54; 50257 bf16 86 and 105; 50256 fp32 149 and 146; K = 5: 128256
+// bf16 171 and 186; K = 0: 50257 bf16 68 and 74, 128256 162 and 153).  Of many best a
+// thread's share of the elements that reach the threshold is too large (K = 128, 50256
+// fp32: 288 and 213).
+bool small_ctas(size_t row_bytes, int K) { return K <= 32 && row_bytes <= (K > 0 && K <= 8 ? 262144 : 131072); }
+template <typename T> cudaError_t launch(const LogArgs &a, unsigned items, cudaStream_t st) {
+  const size_t row = (size_t)a.V * sizeof(T);
+  const bool small = small_ctas(row, a.K);
+  const unsigned C = row_ctas(row, items, small ? 456 : 304);
+  if (small) return a.K ? launch<T, true, 128>(a, items, C, st) : launch<T, false, 128>(a, items, C, st);
+  return a.K ? launch<T, true, 256>(a, items, C, st) : launch<T, false, 256>(a, items, C, st);
 }
 
 }  // namespace
@@ -517,11 +563,10 @@ extern "C" sv_status sv_token_logprobs(const void *logits, int64_t seq_stride, i
   a.top_token = out_top_token;
   a.top_logprob = out_top_logprob;
   a.status = out_status;
-  const unsigned C = row_ctas((size_t)V * es, (long long)B * P, 16384, 608);
   cudaStream_t st = (cudaStream_t)stream;
   LaunchScope ls("token_logprobs", st);
   const unsigned items = (unsigned)(B * P);
-  return check_launch("token_logprobs", dt == SV_F32    ? launch<float>(a, items, C, st)
-                                        : dt == SV_BF16 ? launch<__nv_bfloat16>(a, items, C, st)
-                                                        : launch<__half>(a, items, C, st));
+  return check_launch("token_logprobs", dt == SV_F32    ? launch<float>(a, items, st)
+                                        : dt == SV_BF16 ? launch<__nv_bfloat16>(a, items, st)
+                                                        : launch<__half>(a, items, st));
 }

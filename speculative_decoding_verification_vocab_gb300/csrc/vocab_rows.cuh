@@ -266,13 +266,13 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// CTAs to a row: one for each `bytes` of it while the grid has room for `want`, as
-// many as run at once (more of them: each has its way to the first piece and its
-// joins; 1000 rows of 201 KB with 64 alternatives take 51 us by one CTA each, 67 by
-// two, 105 by four)
-inline unsigned row_ctas(size_t row_bytes, long long rows, size_t bytes, long long want) {
+// CTAs to a row: one for each 16 KB of it while there are no more than `most` in all.
+// More of them have each its way to the first piece and back, and clusters wait for room
+// together (120 rows of 128256 bf16 with 64 alternatives: 28 us by 4 CTAs each, 18 by 2;
+// 300 rows: 29 by 2, 25 by 1; 80 rows with 5: 13 by 4, 14 by 2; 300 rows: 27 by 2, 21 by 1).
+inline unsigned row_ctas(size_t row_bytes, long long rows, long long most) {
   unsigned c = 1;
-  while (c < kMaxRowCluster && row_bytes > c * bytes && rows * c < want) c *= 2;
+  while (c < kMaxRowCluster && row_bytes > c * (size_t)16384 && rows * c * 2 <= most) c *= 2;
   return c;
 }
 
