@@ -16,13 +16,13 @@
 // through a ring of shared memory; the cluster's sums are exchanged by one barrier.
 // With the gradient asked for, a CTA then goes back through its slice: the last
 // three groups are still in the ring, the others come from L2 (so that few rows are
-// under way at once, 128 KB of a row to a CTA), and the gradient is stored past the
+// under way at once, some 80 KB of a row to a CTA), and the gradient is stored past the
 // lines that are still to be read.  Listed elements are found by a bit for each
 // element, set before the first piece is summed; they are few, so their gradients
 // are written one by one over the others', after a barrier.
 //
-// 2048 rows of V = 128256 bf16, K = 64, loss and gradient: 200 us (5.25 TB/s, 0.77; 15 %
-// of the elements come from memory again), the loss alone 86 (0.90).  Slices kept in
+// 2048 rows of V = 128256 bf16, K = 64, loss and gradient: 195 us (5.4 TB/s, 0.79; some
+// 15 % of the elements come from memory again), the loss alone 86 (0.90).  Slices kept in
 // shared memory, 64 KB to a CTA: 236 us (a third of the CTAs' time stands at barriers);
 // clusters that go from row to row with the next row's slice on its way: 301.
 #include <math.h>
@@ -484,20 +484,25 @@ template <typename T, bool GRAD, int THREADS> cudaError_t launch_loss(DistillArg
                             a.ring + groups * kGroupVecs<THREADS>, st, a, C);
 }
 template <typename T, bool GRAD> cudaError_t launch_loss(const DistillArgs &a, cudaStream_t st) {
-  // CTAs to a row: with a gradient 128 KB of it to each (256 or 64 KB, C = 1 or 4 at V =
-  // 128256 bf16: 229 and 206 us where these take 200), less where a batch of few rows
-  // would leave SMs idle.  CTAs of 128 threads for short rows, whose time is the way
+  // CTAs to a row: with a gradient about 80 KB of it to each (2048 rows of 128256 bf16 by
+  // 1 to 5 CTAs each: 226, 198, 192, 203 and 230 us; 1500 of 75000 fp32: 212, 179, 163,
+  // 154 and 164), less of few rows, and more where that many run at once (200 rows by 2 and
+  // 3: 24 and 29 us).  CTAs of 128 threads for short rows, whose time is the way
   // there and back, of which more are under way (4000 rows of 1000 fp32, loss: 18.5 us,
   // by 256 threads 31.9; with the gradient 21 and 36; of 32000 bf16 48 and 59, with the
   // gradient 98 and 96; of 50256 fp32 128 and 121, with the gradient 339 and 278)
   const size_t row = (size_t)a.V * sizeof(T);
   const bool small = row <= (GRAD ? 32768 : 131072);
   unsigned C = 1;
-  if (GRAD)
-    while (C < kMaxRowCluster && (row > C * (size_t)131072 || (row > C * (size_t)16384 && (long long)a.R * C * 2 <= 456))) C *= 2;
-  else
+  if (GRAD) {
+    const size_t slices = (row + 40960) / 81920, most = (row + 16383) / 16384, once = 456 / (size_t)a.R;
+    size_t c = once < most ? once : most;
+    if (c * 131072 < row) c = slices;
+    C = c < 1 ? 1u : c > kMaxRowCluster ? kMaxRowCluster : (unsigned)c;
+  } else {
     C = row_ctas(row, a.R, small ? 456 : 304);
-  while (C < kMaxRowCluster && row > C * (size_t)262144) C *= 2;  // a slice's bits: 16 KB, of the longest rows 128
+  }
+  while (C * 2 <= kMaxRowCluster && row > C * (size_t)262144) C *= 2;  // a slice's bits: 16 KB, of the longest rows 128
   return small ? launch_loss<T, GRAD, 128>(a, C, st) : launch_loss<T, GRAD, 256>(a, C, st);
 }
 template <typename T> cudaError_t launch_grad(const DistillArgs &a, cudaStream_t st) {
