@@ -658,8 +658,11 @@ sv_status sv_token_logprobs(const void *logits, int64_t seq_stride, int64_t row_
  *   out_loss[r] = sum t_k (ln t_k - ln s(v_k)) + t_r (ln t_r - ln s_r)
  *   out_grad[r][v] = weight[r] / T (s_v - t_v) for a listed v, weight[r] / T
  *             s_v (1 - t_r / s_r) for the others: weight[r] dloss[r] / dlogits
- * Terms with t = 0 are 0; s = 0 under t > 0 gives a loss of +inf.  A row whose
- * list has no entries has loss 0 and a gradient of zeros.
+ * Terms with t = 0 are 0; s = 0 under t > 0 gives a loss of +inf.  Where the
+ * student's rest has no share (s_r below 2^-100: masked, or a list of the whole
+ * vocabulary), a t_r below 2^-16, which is what the rounding of the a_k leaves of
+ * 1, counts as 0.  A row whose list has no entries has loss 0 and a gradient of
+ * zeros.
  *
  * sv_distill_loss gives the loss, with out_grad the gradient too (from one read
  * of the logits), with out_stat what sv_distill_grad needs to give the gradient

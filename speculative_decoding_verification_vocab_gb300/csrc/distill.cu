@@ -34,6 +34,12 @@ namespace {
 
 constexpr int kMaxList = 128;
 constexpr int kRing = 3;          // groups of the ring that a slice streams through
+// What the teacher's values leave of 1 is rounding where it is less than kRounding: a
+// value in 32 bits is off by some 2^-24 of itself, of ln l and of the exponentials that
+// l comes from, all of a list's values together by up to (K + 48) 2^-24; below 2^-16 it
+// is next to nothing.  A student without a share (below kNoShare: the rest is masked)
+// there would have to pay for it with an infinite loss, or 10^-7 of a mask of -3e38.
+constexpr float kRounding = 0x1p-16f, kNoShare = 0x1p-100f;
 
 struct DistillArgs {
   const void *logits;
@@ -309,8 +315,7 @@ __device__ __forceinline__ Row row_of(const DistillArgs &a, const RowPart &rest,
   r.flags = flags | li.flags;
   if (!(r.l > 0.0f)) r.flags |= SV_ROW_NAN;
   if (r.skip) r.flags = 0;
-  // a list of the whole vocabulary leaves nothing, but for its rounding
-  r.t_rest = li.used == a.V ? 0.0f : li.rest;
+  r.t_rest = li.rest < kRounding && !(all.l >= r.l * kNoShare) ? 0.0f : li.rest;
   const float coef = r.has_rest ? (all.l / r.l - r.t_rest) / rest.l : 0.0f;
   r.st = r.skip || r.flags ? make_float4(__uint_as_float(r.flags), 0.0f, 0.0f, 0.0f)
                            : make_float4(r.has_rest ? rest.top : 0.0f, coef, r.ref, 1.0f / r.l);
