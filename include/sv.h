@@ -658,6 +658,7 @@ sv_status sv_token_logprobs(const void *logits, int64_t seq_stride, int64_t row_
  *   out_loss[r] = sum t_k (ln t_k - ln s(v_k)) + t_r (ln t_r - ln s_r)
  *   out_grad[r][v] = weight[r] / T (s_v - t_v) for a listed v, weight[r] / T
  *             s_v (1 - t_r / s_r) for the others: weight[r] dloss[r] / dlogits
+ *             (s_v sum t_k in place of s_v where the t_k add up to more than 1)
  * Terms with t = 0 are 0; s = 0 under t > 0 gives a loss of +inf.  Where the
  * student's rest has no share (s_r below 2^-100: masked, or a list of the whole
  * vocabulary), a t_r below 2^-16, which is what the rounding of the a_k leaves of

@@ -6,7 +6,8 @@
 // the rest of the vocabulary, t_r = 1 - sum t_k, s_r = sum of the unlisted s_v
 // (tail); or normalised over the list, t_r = 0.
 //   L = sum t_k (ln t_k - ln s_k) + t_r (ln t_r - ln s_r)
-//   dL/dz_v = s_v - t_v where v is listed, s_v (1 - t_r / s_r) elsewhere.
+//   dL/dz_v = s_v - t_v where v is listed, s_v (1 - t_r / s_r) elsewhere
+// (s_v times sum t_k, where a teacher's rounded weights add up to more than 1).
 // The unlisted elements are summed apart from the listed ones, against their own
 // reference m and sum l: s_r would be lost as 1 - sum s_k where the draft is sure
 // of its list, and with them their gradient is 2^((x - m) k) (s_r - t_r) / l.
@@ -96,6 +97,7 @@ struct List {
   float shift, inv;  // t_k = exp(a_k - ref) inv, ln t_k = a_k - shift
   float ref;
   float rest;        // t_r
+  float total;       // sum of t_k and t_r: 1, or what a teacher's rounded values are above it
   float top, sum;    // as ListPart
   int used;
   uint32_t flags;
@@ -152,6 +154,7 @@ __device__ __forceinline__ List list_of(const ListPart *parts, int tail, float k
   li.inv = tail ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
   li.shift = tail ? 0.0f : li.ref + (sum > 0.0f ? logf(sum) : 0.0f);
   li.rest = tail ? (li.used ? fmaxf(-expm1f(most) - others, 0.0f) : 1.0f) : 0.0f;
+  li.total = tail ? fmaxf(sum, 1.0f) : 1.0f;
   // a teacher's log probabilities are rounded numbers: their sum may pass 1
   if (tail && !(sum < 1.0f + 0x1p-8f)) li.flags |= SV_ROW_NAN;
   if (!tail && li.used && !(sum > 0.0f)) li.flags |= SV_ROW_NAN;  // nothing to normalise
@@ -160,7 +163,7 @@ __device__ __forceinline__ List list_of(const ListPart *parts, int tail, float k
 // an entry's gradient; st: the row's statistics
 __device__ __forceinline__ float listed_grad(const Entry &e, const List &li, const float4 &st, float k, float w) {
   const float share = ex2_approx((e.x - st.z) * k) * st.w;
-  return (share - expf(e.value - li.ref) * li.inv) * w;
+  return (share * li.total - expf(e.value - li.ref) * li.inv) * w;
 }
 
 // Gradient of the unlisted elements of piece w.
@@ -316,7 +319,7 @@ __device__ __forceinline__ Row row_of(const DistillArgs &a, const RowPart &rest,
   if (!(r.l > 0.0f)) r.flags |= SV_ROW_NAN;
   if (r.skip) r.flags = 0;
   r.t_rest = li.rest < kRounding && !(all.l >= r.l * kNoShare) ? 0.0f : li.rest;
-  const float coef = r.has_rest ? (all.l / r.l - r.t_rest) / rest.l : 0.0f;
+  const float coef = r.has_rest ? (all.l / r.l * li.total - r.t_rest) / rest.l : 0.0f;
   r.st = r.skip || r.flags ? make_float4(__uint_as_float(r.flags), 0.0f, 0.0f, 0.0f)
                            : make_float4(r.has_rest ? rest.top : 0.0f, coef, r.ref, 1.0f / r.l);
   return r;

@@ -158,3 +158,37 @@ def test_the_whole_vocabulary_listed(V, dtype):
     loss = sv.distill_loss(x, token, value)["loss"]
     assert loss.isinf().tolist() == [False, True, False]
     hold(x, token, value, tail=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,K", [(50, 4), (50, 50), (3001, 20), (128256, 128)])
+def test_weights_that_add_up_to_more_than_one(V, K, dtype):
+    """Up to 1 + 2^-8 is taken: the loss's gradient is s_v sum t - t_v then."""
+    g = torch.Generator(device=DEV).manual_seed(V + K)
+    totals = torch.tensor([1 + 2.0 ** -9, 1 + 2.0 ** -8.1, 1 + 2.0 ** -12, 1.0], dtype=torch.float64, device=DEV)
+    R = len(totals)
+    x = (torch.randn(R, V, generator=g, device=DEV) * 2).to(dtype)
+    top = (x.double() + torch.randn(R, V, generator=g, device=DEV)).topk(K, -1)
+    value = (torch.log_softmax(top.values, -1) + totals.log()[:, None]).float()
+    for T in (1.0, 0.7):
+        hold(x, top.indices.to(torch.int32), value, T)
+
+
+def test_the_gradient_of_more_than_one_against_differences():
+    """Central differences of the loss, per element: the loss is off by d = 1e-5 at most
+    here (V = 50, logs below 12), a step of h = 0.03 by h^2 / 6 of third derivatives,
+    which are below 1.  A student sure of a token has s_v = 0.8 there: 2^-8.1 of it is
+    five times what these leave."""
+    V, K, h = 50, 4, 0.03
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(1, V, generator=g)
+    x[0, 7] = 5.5
+    token = torch.tensor([[3, 7, 20, 41]], dtype=torch.int32)
+    value = (torch.log_softmax(torch.randn(1, K, generator=g, dtype=torch.float64), 1) + math.log(1 + 2.0 ** -8.1)).float()
+    grad = sv.distill_loss(x.to(DEV), token.to(DEV), value.to(DEV), grad=True)["grad"].double().cpu()[0]
+    rows = torch.cat([x + torch.eye(V) * h, x - torch.eye(V) * h]).to(DEV)
+    loss = sv.distill_loss(rows, token.expand(2 * V, K).contiguous().to(DEV),
+                           value.expand(2 * V, K).contiguous().to(DEV))["loss"].double().cpu()
+    # the steps as they were taken
+    step = (rows[:V].double() - rows[V:].double()).diagonal().cpu()
+    assert float(((loss[:V] - loss[V:]) / step - grad).abs().max()) <= 1e-5 / h + h * h / 6
