@@ -796,6 +796,36 @@ struct JoinArgs {
   float *lse;
   uint32_t *status;
 };
+// The status of up to 32 sequences of a prefix, by a warp of their own.  A wait runs
+// out in one CTA, which has parts of some KV heads and a column of query rows: a
+// sequence's bits are those of all its heads and of every column that it has rows in.
+// (Collected by the warp of a sequence's first row the join took 2 us longer.)
+__device__ __forceinline__ void put_status(const PrefixArgs &a, const JoinArgs &j, int unit) {
+  const int lane = threadIdx.x & 31, groups = (a.W + 31) / 32, p = unit / groups, s0 = unit % groups * 32;
+  const int s = min(s0 + lane, a.W - 1), last = min(s0 + 31, a.W - 1);
+  const longlong2 n = count_tiles(a, p);
+  const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
+  int per = 32;  // lanes to a head
+  while (per > 1 && per * a.Hkv > 32) per /= 2;
+  grid_dep_sync();
+  uint32_t flag = (len < 0 || len > a.cap ? SV_ROW_BAD_LEN : 0u) | j.own_flag[p * a.W + s];
+  const long long all = n.x * a.Hkv;
+  auto column_of = [&](int sequence, int row) { return (sequence * a.G + row) / (2 * kRows); };
+  for (int column = column_of(s0, 0); tiles > 0 && column <= column_of(last, a.G - 1); ++column) {
+    const long long shares = cut_into(2 * column + 1 < a.mtiles ? a.shares2 : a.shares1, all);
+    uint32_t bits = 0;
+    for (int head = lane / per; head < a.Hkv; head += 32 / per) {
+      const long long first = n.y * a.Hkv + (long long)tiles * head;
+      const int end = share_of(first + tiles - 1, shares, all);
+#pragma unroll 4
+      for (int c = share_of(first, shares, all) + lane % per; c <= end; c += per)
+        bits |= a.w_flag[part_at(a, column, (long long)p * a.Hkv + head + c)];
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (column >= column_of(s, 0) && column <= column_of(s, a.G - 1)) flag |= bits;
+  }
+  if (s0 + lane < a.W) j.status[p * a.W + s] = flag;
+}
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, JoinArgs j) {
   const unsigned FULL = 0xffffffffu;
@@ -803,9 +833,12 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   constexpr int kLanes = 32 / ROWS, E = D / 32, U = ROWS > 1 ? 4 : 8;  // U: places on their way together
   const int lane = threadIdx.x & 31, mine = lane / kLanes, sub = lane % kLanes;
   const int wg = a.W * a.G, fours = (wg + ROWS - 1) / ROWS;
-  const int unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // below 2^27
-  const bool live = unit < a.N * a.Hkv * fours;
-  const int seg = live ? unit / fours : 0, at0 = live ? (unit - seg * fours) * ROWS : 0;
+  const int unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), units = a.N * a.Hkv * fours;  // below 2^28
+  if (unit >= units) {
+    if (j.status && unit - units < a.N * ((a.W + 31) / 32)) put_status(a, j, unit - units);
+    return;
+  }
+  const int seg = unit / fours, at0 = (unit - seg * fours) * ROWS;
   const int p = seg / a.Hkv, head = seg - p * a.Hkv, count = min(ROWS, wg - at0);
   const int mt = at0 / kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
   // the row of the lane's eight; the last one's again behind it
@@ -826,7 +859,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   const size_t part0 = part_at(a, column, (long long)p * a.Hkv + head + c0);
   const size_t place0 = (part0 * 2 + (pair ? mt & 1 : 0)) * a.rows + at0 % kRows, step = (size_t)a.rows << (1 - two);
   grid_dep_sync();
-  if (!live) return;
   auto load = [&](const float *src, float *x) {
     if constexpr (E == 4) {
       const float4 v = *(const float4 *)(src + lane * 4);
@@ -916,7 +948,6 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   }
   if (sub == 0 && mine < count) {
     if (j.lse) j.lse[row] = flag ? nan : sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
-    if (h == 0 && j.status) j.status[b] = flag;
   }
 }
 
@@ -986,7 +1017,8 @@ sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j,
                  a.num_pages, scale, own_o, own_ml, own_flag, own_ws, st);
   if (s != SV_OK) return s;
   const bool few = (long long)a.B * a.Hq <= kFewRows;
-  const long long at_once = few ? 1 : kJoinRows, units = (long long)a.N * a.Hkv * (((long long)a.W * a.G + at_once - 1) / at_once);
+  const long long at_once = few ? 1 : kJoinRows, status = j.status ? (long long)a.N * ((a.W + 31) / 32) : 0;
+  const long long units = (long long)a.N * a.Hkv * (((long long)a.W * a.G + at_once - 1) / at_once) + status;
   constexpr int kUnits = kJoinThreads / 32;
   LaunchScope ls("prefix_join", st);
   return check_launch("prefix_join", launch_pdl(few ? prefix_join_kernel<T, D, 1> : prefix_join_kernel<T, D, kJoinRows>,
