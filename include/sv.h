@@ -547,9 +547,10 @@ sv_status sv_paged_attention(const void *q, const void *kv, int64_t kv_stride,
  * slot are never read, and what their table entries hold is not looked at.  A
  * length out of range (SV_ROW_BAD_LEN) or a needed page outside [0, num_pages)
  * (SV_ROW_BAD_PAGE) gives NaN rows: of the sequence, or of all that share the
- * prefix.  The outputs overlap no input.  Weights of a prefix are rounded to dt
- * where they multiply the values (2^-8 or 2^-11 of each weight); sums are held in
- * 32 bits, unnormalised as in sv_paged_attention.
+ * prefix.  The outputs overlap no input.  Where more than 128 query rows share a KV
+ * head's prefix (W Hq / Hkv), its weights are rounded to dt as they multiply the
+ * values (2^-8 or 2^-11 of each weight), otherwise to twice dt's bits, as
+ * sv_paged_attention's; sums are held in 32 bits, unnormalised as there.
  *
  * Work is split by the lengths found on the device: one captured launch serves
  * growing prefixes and sequences.  The workspace is written before it is read;

@@ -35,8 +35,9 @@
 //               other's products: S = Q K^T from shared memory, O += P V with P in
 //               tensor memory, in the place of the S it comes from;
 //   warps 4-11  softmax, four to a buffer, a row to a thread, 64 keys at a time: the
-//               running maximum with a lazy rescale of O, P as 16-bit values; at a
-//               segment's end O, m and l to the workspace.  The halves of a buffer
+//               running maximum with a lazy rescale of O, P as 16-bit values (two for
+//               each where there is one query tile); at a segment's end O, m and l to
+//               the workspace.  The halves of a buffer
 //               take turns too: one is multiplied and filled with the next tile's
 //               scores while the other is worked on.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
@@ -75,9 +76,16 @@ constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 // A score moves the reference only when it is more than kSlack above it (log2
 // units).  Weights go into the product as 16-bit numbers: in fp16 the reference
 // lies 2^kBias below the maximum it was set by, so that they fill the type's range
-// from the top (2^15 at most) and the small ones do not round to nothing.  One
-// 16-bit part (half a step, 2^-8 or 2^-11, of each weight, independent from key to
-// key): a second one would double the product of a bound that is the product.
+// from the top (2^15 at most) and the small ones do not round to nothing.
+// TWO: a weight is the sum of two 16-bit parts, so that it keeps twice the type's bits,
+// as in the paged attention; one part alone (half a step, 2^-8 or 2^-11, of each weight,
+// independent from key to key) adds a rounding as large as the output's own (bf16:
+// 2.2e-3 from 64 bits, where rounding the output leaves 1.65e-3).  For one query tile,
+// where the product is not the bound, it costs 4 % of the call (4 prefixes of 20000
+// slots, 64 heads on 8 of 128: 4 sequences each 70.2 and 73.0 us, 16 each 86.9 and 89.9;
+// 16 of 5000, 32 on 8 of 64, fp16, pages of 20: 59 and 65).  Beyond 128 rows the product
+// is the bound, which a second part makes half again as long (32 sequences each 103 and
+// 118 us; 128 behind 32600 slots 131 and 159): one part.
 template <typename T> constexpr float kSlack = 8.0f;
 template <typename T> constexpr float kBias = 0.0f;
 template <> constexpr float kSlack<__half> = 4.0f;
@@ -86,7 +94,13 @@ template <typename T> constexpr uint32_t kAbType = 1;  // of the instruction des
 template <> constexpr uint32_t kAbType<__half> = 0;
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <typename T> __device__ __forceinline__ unsigned long long unpack2(uint32_t v);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <> __device__ __forceinline__ unsigned long long unpack2<__nv_bfloat16>(uint32_t v) { return f2_pack(bf16_lo(v), bf16_hi(v)); }
+template <> __device__ __forceinline__ unsigned long long unpack2<__half>(uint32_t v) {
+  const float2 f = __half22float2(*(const __half2 *)&v);
+  return f2_pack(f.x, f.y);
+}
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *(const uint32_t *)&v;
@@ -264,7 +278,7 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&v)[16])
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <typename T, int D, bool TMA>
+template <typename T, int D, bool TMA, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
   using R = Ring<D>;
@@ -565,8 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-              if (ks < steps)
-                mma_ts(tO, tS + 64 * half + (ks - 4 * half) * 8, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
+              if (ks < steps) {
+                const uint32_t p = tS + 64 * half + (ks - 4 * half) * 8;
+                mma_ts(tO, p, dv + (uint64_t)(ks * 128), kIdescO, (i > 0 || ks > 0) ? 1u : 0u);
+                if (TWO) mma_ts(tO, p + 32, dv + (uint64_t)(ks * 128), kIdescO, 1u);
+              }
             mma_commit(bar(R::kPV + 2 * s + half));
             if (half) mma_commit(bar(R::kFreeV + v_at));
           }
@@ -685,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned long long sc2 = f2_splat(a.scale_log2), mn2 = f2_splat(m_ref == -INFINITY ? 0.0f : -m_ref);
 #pragma unroll
           for (int c = 2 * half; c < 2 * half + 2; ++c) {
-            uint32_t p[16];
+            uint32_t p[16], rest[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const unsigned long long y =
@@ -694,8 +711,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               float y0, y1;
               f2_unpack(y, y0, y1);
               p[e] = pack2<T>(y0, y1);
+              if (TWO) {
+                f2_unpack(f2_sub(y, unpack2<T>(p[e])), y0, y1);
+                rest[e] = pack2<T>(y0, y1);
+              }
             }
             tm_st16(tS + 64 * half + 16 * (c - 2 * half), p);  // in the place of keys that have been read
+            if (TWO) tm_st16(tS + 64 * half + 32 + 16 * (c - 2 * half), rest);
           }
           auto done = [&]() {
             tm_wait_st();
@@ -993,7 +1015,7 @@ bool bad_shape(int B, int N, int Hq, int Hkv, int D, int page, int max_prefix_pa
          max_pages < 1;
 }
 
-template <typename T, int D, bool TMA>
+template <typename T, int D, bool TMA, bool TWO>
 sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j, const Sizes &z, const int32_t *block_table,
                  const int32_t *seq_len, int max_pages, float scale, sv_dtype dt, float *own_o, float2 *own_ml,
                  uint32_t *own_flag, void *own_ws, cudaStream_t st) {
@@ -1001,7 +1023,7 @@ sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j,
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev != set_dev) {
-    const cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<T, D, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<T, D, TMA, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)Ring<D>::kSmem);
     if (e != cudaSuccess) return check_launch("prefix_attention", e);
     set_dev = dev;
@@ -1010,7 +1032,7 @@ sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j,
   {
     LaunchScope ls("prefix_attention", st);
     s = check_launch("prefix_attention",
-                     launch_pdl(prefix_attn_kernel<T, D, TMA>, dim3((unsigned)z.ctas), dim3(kThreads), Ring<D>::kSmem, st, map, a));
+                     launch_pdl(prefix_attn_kernel<T, D, TMA, TWO>, dim3((unsigned)z.ctas), dim3(kThreads), Ring<D>::kSmem, st, map, a));
     if (s != SV_OK) return s;
   }
   s = paged_sums(a.q, a.kv, a.kv_stride, a.page_stride, dt, block_table, seq_len, a.B, a.Hq, a.Hkv, D, a.page, max_pages,
@@ -1154,10 +1176,13 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   auto go = [&](auto kernel) {
     return kernel(map, a, j, z, block_table, seq_len, max_pages, scale, dt, own_o, own_ml, own_flag, own_ws, st);
   };
-  if (dt == SV_BF16) {
-    if (D == 64) return tma ? go(launch<__nv_bfloat16, 64, true>) : go(launch<__nv_bfloat16, 64, false>);
-    return tma ? go(launch<__nv_bfloat16, 128, true>) : go(launch<__nv_bfloat16, 128, false>);
-  }
-  if (D == 64) return tma ? go(launch<__half, 64, true>) : go(launch<__half, 64, false>);
-  return tma ? go(launch<__half, 128, true>) : go(launch<__half, 128, false>);
+  auto by_head = [&](auto type, auto two) {
+    typedef decltype(type) T;
+    constexpr bool kTwo = decltype(two)::value != 0;
+    if (D == 64) return tma ? go(launch<T, 64, true, kTwo>) : go(launch<T, 64, false, kTwo>);
+    return tma ? go(launch<T, 128, true, kTwo>) : go(launch<T, 128, false, kTwo>);
+  };
+  const bool two = z.mtiles == 1;
+  if (dt == SV_BF16) return two ? by_head(__nv_bfloat16(), Int<1>()) : by_head(__nv_bfloat16(), Int<0>());
+  return two ? by_head(__half(), Int<1>()) : by_head(__half(), Int<0>());
 }
