@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(kGradThreads, 8) distill_grad_kernel(DistillAr
   }
   __syncthreads();
   const List li = list_of(s_list, a.tail, a.k);
-  const uint32_t flags = li.flags | (li.used && st.w == 0.0f ? __float_as_uint(st.x) : 0u);
-  const bool none = st.w == 0.0f || flags || li.used == 0;
+  const bool skip = li.used == 0 && li.flags == 0;  // as in the forward pass
+  const uint32_t flags = skip ? 0u : li.flags | (st.w == 0.0f ? __float_as_uint(st.x) : 0u);
+  const bool none = st.w == 0.0f || flags || skip;
   write_grad<T, kGradThreads>(row, grad, s, rank, st.x, none ? 0.0f : st.y * w, a.k,
                 [&](int, int, int v) { return ((const uint4 *)(row + s.head))[v]; });
   __syncthreads();

@@ -1,0 +1,62 @@
+"""Faulty, listless and ordinary rows in one batch, each held to its own answer."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_distill_mass import calls
+
+pytestmark = pytest.mark.gpu
+
+sv = pytest.importorskip("speculative_decoding_verification_vocab_gb300")
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load_library()
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,V,K", [(1000, 130, 128), (20, 5003, 16), (600, 70001, 8)])
+def test_every_row_has_its_own_answer(R, V, K, dtype, tail):
+    """By every way (and the same ones in place): NaN and a gradient of zeros exactly
+    where the status is not 0, zeros exactly where there is no list."""
+    g = torch.Generator(device=DEV).manual_seed(R)
+    x = (torch.randn(R, V, generator=g, device=DEV) * 3).to(dtype)
+    top = torch.log_softmax(x.double() + torch.randn(R, V, generator=g, device=DEV), -1).topk(K, -1)
+    token, value = top.indices.to(torch.int32), top.values.float()
+    r = torch.arange(R, device=DEV)
+    token[r % 5 == 1] = -1                                # no list
+    token[r % 7 == 2, 1] = token[r % 7 == 2, 4]           # listed twice, or an entry not used
+    x[r % 9 == 3, V - 1] = math.nan
+    value[r % 11 == 4, 2] = math.nan
+    token[r % 13 == 6, 0] = V
+    listless = (token == -1).all(1)
+    twice = token.sort(1).values
+    twice = ((twice[:, 1:] == twice[:, :-1]) & (twice[:, 1:] != -1)).any(1)
+    want = torch.zeros(R, dtype=torch.int32, device=DEV)
+    want[x.isnan().any(1) | (value.isnan() & (token != -1)).any(1)] |= sv.SV_ROW_NAN
+    want[twice | (token == V).any(1)] |= sv.SV_ROW_BAD_TOKEN
+    want[listless] = 0
+    assert 0 < int(listless.sum()) < R and 0 < int((want != 0).sum()) < R
+    ways = list(calls(x, token, value, tail=tail))
+    for loss, grad, status in ways:
+        assert torch.equal(status, want)
+        assert torch.equal(loss.isnan(), want != 0)
+        assert bool((loss[listless] == 0).all()) and bool((loss[(want == 0) & ~listless] != 0).all())
+        assert torch.equal(grad.any(1), (want == 0) & ~listless)
+    # an ordinary row is not another's neighbour: alone it is what it is in the batch, but
+    # for the order of its sums (a clone: where a row lies on the 16-byte grid is part of
+    # that order)
+    rel = 2.0 ** -24 * (3 * 48 + 4 + V / 512 + 24 + 8 + K)
+    at = int(((want == 0) & ~listless).nonzero()[-1])
+    alone = list(calls(x[at:at + 1].clone(), token[at:at + 1], value[at:at + 1], tail=tail))
+    for (loss, grad, _), (one, g1, _) in zip(ways, alone):
+        assert abs(float(loss[at] - one[0])) <= 4 * rel * 40
+        off = (grad[at].double() - g1[0].double()).abs()
+        assert bool((off <= 4 * rel + torch.finfo(dtype).eps * g1[0].double().abs()).all())
