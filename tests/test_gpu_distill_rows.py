@@ -1,9 +1,11 @@
-"""Faulty, listless and ordinary rows in one batch, each held to its own answer."""
+"""Faulty, listless and ordinary rows in one batch, each held to its own answer; the
+later gradient of the longest rows element by element."""
 import math
 
 import pytest
 import torch
 
+import test_gpu_distill as distill
 from test_gpu_distill_mass import calls
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +62,20 @@ def test_every_row_has_its_own_answer(R, V, K, dtype, tail):
         assert abs(float(loss[at] - one[0])) <= 4 * rel * 40
         off = (grad[at].double() - g1[0].double()).abs()
         assert bool((off <= 4 * rel + torch.finfo(dtype).eps * g1[0].double().abs()).all())
+
+
+@pytest.mark.parametrize("V,dtype", [(1 << 21, torch.float32), (sv.SV_MAX_VOCAB, torch.bfloat16), (900001, torch.float16)])
+def test_later_gradient_of_the_longest_rows(V, dtype):
+    K = 128
+    g = torch.Generator(device=DEV).manual_seed(V % 1000)
+    x = (torch.randn(2, V, generator=g, device=DEV) * 2).to(dtype)
+    top = torch.log_softmax(x.double() + torch.randn(2, V, generator=g, device=DEV), -1).topk(K, -1)
+    token, value = top.indices.to(torch.int32), top.values.float()
+    weight = torch.tensor([1000.0, -3.0])                 # (fp16 begins at 6e-8)
+    one = sv.distill_loss(x, token, value, weight=weight.to(DEV))
+    later, status = sv.distill_grad(x, token, value, one["stat"], weight=weight.to(DEV))
+    torch.cuda.synchronize()
+    distill.compare(x.cpu(), token.cpu(), value.cpu(), weight, 1.0, True, one["loss"].cpu().numpy(),
+                    later.float().cpu().numpy(), status.cpu().numpy())
+    # some of its elements are far above what compare allows beside them
+    assert float(later.float().abs().max()) > 2.0 ** -7
