@@ -314,7 +314,8 @@ __device__ __forceinline__ Row row_of(const DistillArgs &a, const RowPart &rest,
   const float top = fmaxf(rest.top, li.top);
   r.ref = top == -INFINITY ? 0.0f : top;
   const RowPart all = moved(rest, r.ref, k);
-  r.l = all.l + (li.top == -INFINITY ? 0.0f : li.sum * ex2_approx((li.top - r.ref) * k));
+  // (a list without a number above -inf has 0, or NaN from the data)
+  r.l = all.l + (li.top == -INFINITY ? li.sum : li.sum * ex2_approx((li.top - r.ref) * k));
   r.flags = flags | li.flags;
   if (!(r.l > 0.0f)) r.flags |= SV_ROW_NAN;
   if (r.skip) r.flags = 0;

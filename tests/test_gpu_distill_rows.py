@@ -64,6 +64,37 @@ def test_every_row_has_its_own_answer(R, V, K, dtype, tail):
         assert bool((off <= 4 * rel + torch.finfo(dtype).eps * g1[0].double().abs()).all())
 
 
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [3, 130, 9001, 128256])
+def test_a_fault_wherever_it_stands(V, dtype, tail):
+    """NaN or +inf at a listed token, at all of them, beside them, beside a list of
+    logits of -inf: the row is faulty.  -inf alone is no fault."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    for K in (1, 2, min(V, 40)):
+        R = 8
+        x = (torch.randn(R, V, generator=g, device=DEV) * 2).to(dtype)
+        token = torch.rand(R, V, generator=g, device=DEV).argsort(1)[:, :K].to(torch.int32)
+        value = torch.log_softmax(torch.randn(R, K, generator=g, device=DEV), 1) - (0.1 if K < V else 0.0)
+        at = token.long()
+        x[0].scatter_(0, at[0, -1:], math.nan)
+        x[1].scatter_(0, at[1], math.nan)
+        x[2].scatter_(0, at[2, :1], math.inf)
+        x[3].scatter_(0, at[3], math.inf)
+        x[4].scatter_(0, at[4], -math.inf)
+        if K < V:
+            other = torch.tensor([sorted(set(range(V)) - set(row.tolist()))[-1] for row in at.cpu()], device=DEV)
+            x[4, other[4]] = math.nan
+            x[5, other[5]] = math.nan
+            x[6].scatter_(0, at[6], -math.inf)
+        faulty = [0, 1, 2, 3, 4, 5] if K < V else [0, 1, 2, 3, 4]
+        for loss, grad, status in calls(x, token, value, tail=tail):
+            assert status.tolist() == [sv.SV_ROW_NAN if r in faulty else 0 for r in range(R)]
+            assert bool(loss[faulty].isnan().all()) and not bool(grad[faulty].any())
+            assert not bool(loss.isnan()[[6, 7]].any()) and not bool(grad.isnan().any())
+            assert math.isinf(float(loss[6])) == (K < V)
+
+
 @pytest.mark.parametrize("V,dtype", [(1 << 21, torch.float32), (sv.SV_MAX_VOCAB, torch.bfloat16), (900001, torch.float16)])
 def test_later_gradient_of_the_longest_rows(V, dtype):
     K = 128
