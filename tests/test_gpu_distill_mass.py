@@ -69,8 +69,8 @@ def hold(x, token, value, T=1.0, tail=True):
                 continue
             t, tr = mass.masses(vals[r][live], tail)
             of = lp[toks[r][live]]
-            counts = (t > 2.0 ** -126) & np.isfinite(of)
-            big = (np.abs(of) + np.abs(vals[r][live]))[counts].max(initial=0.0)
+            weighty = (t > 2.0 ** -126) & np.isfinite(of)
+            big = (np.abs(of) + np.abs(vals[r][live]))[weighty].max(initial=0.0)
             s = np.exp(lp)
             weight = np.zeros(V)
             weight[toks[r][live]] = t
@@ -79,13 +79,14 @@ def hold(x, token, value, T=1.0, tail=True):
             top = lp[rest].max(initial=-np.inf)
             e = np.where(rest & (lp > -np.inf), np.exp(np.minimum(lp - (top if top > -np.inf else 0), 0)), 0)
             share = e / max(e.sum(), 1e-300)
+            # (t_r is off by rel_t even where it is 0, but not where it does not count)
+            lsr = top + math.log(e.sum()) if top > -np.inf else -np.inf
+            counts = tail and not (lsr < math.log(mass.NO_SHARE) and tr < mass.ROUNDING)
             if math.isfinite(wl):
-                logs = 0.0
-                if tr > 0 and top > -np.inf:
-                    logs = abs(top + math.log(e.sum())) + abs(math.log(tr)) + 1
+                logs = abs(lsr) + abs(math.log(max(tr, 2.0 ** -24))) + 1 if counts else 0.0
                 tol = (rel + 2 * rel_t) * (2 + big) + logs * rel_t + tr * rel + 2.0 ** -22 * abs(wl)
                 assert abs(loss[r] - wl) <= tol, (r, loss[r], wl, tol)
-            tol = (3 * s * rel + weight * rel_t + share * (tr * rel + rel_t * (tr > 0))) / T
+            tol = (3 * s * rel + weight * rel_t + share * (tr * rel + rel_t * counts)) / T
             off = np.abs(grad[r] - wg) - tol - (half + 2.0 ** -23) * np.abs(wg) - tiny
             assert (off <= 0).all(), (r, off.max(), int(off.argmax()))
 
