@@ -239,11 +239,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // 32 consecutive columns of this thread's tensor-memory lane; the values are there
 // after tm_wait_ld
 __device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -680,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
           const bool grow = mx > m_ref + (kSlack<T> + kBias<T>);
           const float m_new = grow ? mx - kBias<T> : m_ref;
-          const float factor = grow && m_ref != -INFINITY ? ex2(m_ref - m_new) : 1.0f;
+          const float factor = grow && m_ref != -INFINITY ? ex2_approx(m_ref - m_new) : 1.0f;
           m_ref = m_new;
           if (__any_sync(FULL, factor != 1.0f)) {
             // O covers the keys before: the product of the half before is waited for (a
@@ -921,7 +916,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   }
   // A sum without a finite reference is 0, or NaN from the data: it stays, and so do
   // its values.  A buffer without a tile has no sums: it is passed over.
-  auto factor = [&](float m) { return m == -INFINITY ? 1.0f : ex2(m - M); };
+  auto factor = [&](float m) { return m == -INFINITY ? 1.0f : ex2_approx(m - M); };
   const float f0 = factor(own.x);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {

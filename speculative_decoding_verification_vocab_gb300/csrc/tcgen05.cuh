@@ -215,17 +215,11 @@ __device__ __forceinline__ void tm_st32u(uint32_t taddr, const uint32_t *v) {
   tm_st32(taddr, reinterpret_cast<const float *>(v));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ex2 of a packed pair on the MUFU (ex2.approx.ftz: -inf gives +0).
 __device__ __forceinline__ unsigned long long ex2_2(unsigned long long x) {
   float a, b;
   f2_unpack(x, a, b);
-  return f2_pack(ex2(a), ex2(b));
+  return f2_pack(ex2_approx(a), ex2_approx(b));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           mx *= a.scale_log2;  // scale > 0: max commutes with it
           const bool grow = mx > m_ref[e] + kRescaleLog2;
           const float m_new = grow ? mx : m_ref[e];
-          factor[e] = (grow && m_ref[e] != NEG_INF) ? ex2(m_ref[e] - m_new) : 1.0f;
+          factor[e] = (grow && m_ref[e] != NEG_INF) ? ex2_approx(m_ref[e] - m_new) : 1.0f;
           any_grow |= factor[e] != 1.0f;
           l[e] *= factor[e];
           m_ref[e] = m_new;

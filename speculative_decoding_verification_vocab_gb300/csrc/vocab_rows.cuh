@@ -22,12 +22,6 @@ constexpr float kLog2eF = 1.4426950408889634f;
 // any does, and sums of 2^22 terms of 2^8 are far from the end of 32 bits.
 constexpr float kRefSlack = 8.0f;
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // ------------------------------------------------------------ element types
 // most, most4: the largest element of a piece, of a group's pieces (NaN ones passed
 // over)
