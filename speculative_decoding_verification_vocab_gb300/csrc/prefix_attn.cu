@@ -147,6 +147,7 @@ struct PrefixArgs {
   float *w_o;
   float2 *w_ml;
   uint32_t *w_flag;
+  uint32_t *status;  // [B], or null
 };
 
 __device__ __forceinline__ int tiles_of(const PrefixArgs &a, int len) {
@@ -331,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   grid_dep_sync();
+  if (a.status)  // for the join's bits
+    for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) a.status[b] = 0;
   if (warp == 0) {
     // this CTA's column and share, and the prefix it starts in
     Walk w;
@@ -811,38 +814,7 @@ struct JoinArgs {
   const uint32_t *own_flag;
   void *out;
   float *lse;
-  uint32_t *status;
 };
-// The status of up to 32 sequences of a prefix, by a warp of their own.  A wait runs
-// out in one CTA, which has parts of some KV heads and a column of query rows: a
-// sequence's bits are those of all its heads and of every column that it has rows in.
-// (Collected by the warp of a sequence's first row the join took 2 us longer.)
-__device__ __forceinline__ void put_status(const PrefixArgs &a, const JoinArgs &j, int unit) {
-  const int lane = threadIdx.x & 31, groups = (a.W + 31) / 32, p = unit / groups, s0 = unit % groups * 32;
-  const int s = min(s0 + lane, a.W - 1), last = min(s0 + 31, a.W - 1);
-  const longlong2 n = count_tiles(a, p);
-  const int len = __ldcg(a.len + p), tiles = tiles_of(a, len);
-  int per = 32;  // lanes to a head
-  while (per > 1 && per * a.Hkv > 32) per /= 2;
-  grid_dep_sync();
-  uint32_t flag = (len < 0 || len > a.cap ? SV_ROW_BAD_LEN : 0u) | j.own_flag[p * a.W + s];
-  const long long all = n.x * a.Hkv;
-  auto column_of = [&](int sequence, int row) { return (sequence * a.G + row) / (2 * kRows); };
-  for (int column = column_of(s0, 0); tiles > 0 && column <= column_of(last, a.G - 1); ++column) {
-    const long long shares = cut_into(2 * column + 1 < a.mtiles ? a.shares2 : a.shares1, all);
-    uint32_t bits = 0;
-    for (int head = lane / per; head < a.Hkv; head += 32 / per) {
-      const long long first = n.y * a.Hkv + (long long)tiles * head;
-      const int end = share_of(first + tiles - 1, shares, all);
-#pragma unroll 4
-      for (int c = share_of(first, shares, all) + lane % per; c <= end; c += per)
-        bits |= a.w_flag[part_at(a, column, (long long)p * a.Hkv + head + c)];
-    }
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if (column >= column_of(s, 0) && column <= column_of(s, a.G - 1)) flag |= bits;
-  }
-  if (s0 + lane < a.W) j.status[p * a.W + s] = flag;
-}
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a, JoinArgs j) {
   const unsigned FULL = 0xffffffffu;
@@ -850,11 +822,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
   constexpr int kLanes = 32 / ROWS, E = D / 32, U = ROWS > 1 ? 4 : 8;  // U: places on their way together
   const int lane = threadIdx.x & 31, mine = lane / kLanes, sub = lane % kLanes;
   const int wg = a.W * a.G, fours = (wg + ROWS - 1) / ROWS;
-  const int unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), units = a.N * a.Hkv * fours;  // below 2^28
-  if (unit >= units) {
-    if (j.status && unit - units < a.N * ((a.W + 31) / 32)) put_status(a, j, unit - units);
-    return;
-  }
+  const int unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // below 2^27
+  if (unit >= a.N * a.Hkv * fours) return;
   const int seg = unit / fours, at0 = (unit - seg * fours) * ROWS;
   const int p = seg / a.Hkv, head = seg - p * a.Hkv, count = min(ROWS, wg - at0);
   const int mt = at0 / kRows, column = mt / 2, pair = 2 * column + 1 < a.mtiles;
@@ -914,6 +883,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(PrefixArgs a,
     M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
     flag |= __shfl_xor_sync(FULL, flag, o);
   }
+  // a sequence's status (0 from the first launch) is that of all its rows: a wait runs out
+  // in one CTA, which has parts of some heads
+  if (flag && a.status) atomicOr(a.status + b, flag);
   // A sum without a finite reference is 0, or NaN from the data: it stays, and so do
   // its values.  A buffer without a tile has no sums: it is passed over.
   auto factor = [&](float m) { return m == -INFINITY ? 1.0f : ex2_approx(m - M); };
@@ -1034,8 +1006,7 @@ sv_status launch(const CUtensorMap &map, const PrefixArgs &a, const JoinArgs &j,
                  a.num_pages, scale, own_o, own_ml, own_flag, own_ws, st);
   if (s != SV_OK) return s;
   const bool few = (long long)a.B * a.Hq <= kFewRows;
-  const long long at_once = few ? 1 : kJoinRows, status = j.status ? (long long)a.N * ((a.W + 31) / 32) : 0;
-  const long long units = (long long)a.N * a.Hkv * (((long long)a.W * a.G + at_once - 1) / at_once) + status;
+  const long long at_once = few ? 1 : kJoinRows, units = (long long)a.N * a.Hkv * (((long long)a.W * a.G + at_once - 1) / at_once);
   constexpr int kUnits = kJoinThreads / 32;
   LaunchScope ls("prefix_join", st);
   return check_launch("prefix_join", launch_pdl(few ? prefix_join_kernel<T, D, 1> : prefix_join_kernel<T, D, kJoinRows>,
@@ -1134,10 +1105,11 @@ extern "C" sv_status sv_prefix_attention(const void *q, const void *kv, int64_t 
   a.w_o = (float *)(w + z.o);
   a.w_ml = (float2 *)(w + z.ml);
   a.w_flag = (uint32_t *)(w + z.flag);
+  a.status = out_status;
   float *own_o = (float *)(w + z.own_o);
   float2 *own_ml = (float2 *)(w + z.own_ml);
   uint32_t *own_flag = (uint32_t *)(w + z.own_flag);
-  const JoinArgs j{own_o, own_ml, own_flag, out, out_lse, out_status};
+  const JoinArgs j{own_o, own_ml, own_flag, out, out_lse};
   void *own_ws = z.own_bytes ? w + z.own : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
   // Boxes of as many rows as a power of two divides the page by, where that is 16 and

@@ -77,8 +77,8 @@ template <int ROWS> static int check(int N, int W, int Hkv, int G, const std::ve
   j.own_flag = upload(std::vector<uint32_t>(B, 0));
   j.out = upload(std::vector<uint16_t>((size_t)B * Hq * D, 0));
   j.lse = upload(std::vector<float>((size_t)B * Hq, 0.0f));
-  j.status = upload(std::vector<uint32_t>(B, 0));
-  const long long units = (long long)N * Hkv * (((long long)W * G + ROWS - 1) / ROWS) + N * ((W + 31) / 32);
+  a.status = upload(std::vector<uint32_t>(B, 0));
+  const long long units = (long long)N * Hkv * (((long long)W * G + ROWS - 1) / ROWS);
   const unsigned ctas = (unsigned)((units + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   std::vector<uint32_t> status(B);
   std::vector<float> lse((size_t)B * Hq);
@@ -87,8 +87,9 @@ template <int ROWS> static int check(int N, int W, int Hkv, int G, const std::ve
     std::vector<uint32_t> flags = clean;
     if (i < parts.size()) flags[parts[i].at] = SV_ROW_TIMEOUT;
     cudaMemcpy(a.w_flag, flags.data(), room * 4, cudaMemcpyHostToDevice);
+    cudaMemset(a.status, 0, B * 4);  // as the prefixes' launch leaves it
     prefix_join_kernel<__nv_bfloat16, D, ROWS><<<ctas, kJoinThreads>>>(a, j);
-    if (cudaMemcpy(status.data(), j.status, B * 4, cudaMemcpyDeviceToHost) != cudaSuccess) return 1;
+    if (cudaMemcpy(status.data(), a.status, B * 4, cudaMemcpyDeviceToHost) != cudaSuccess) return 1;
     cudaMemcpy(lse.data(), j.lse, lse.size() * 4, cudaMemcpyDeviceToHost);
     for (int b = 0; b < B; ++b) {
       bool hit = false;  // some row of the sequence has the part
