@@ -23,7 +23,7 @@
 // are written one by one over the others', after a barrier.
 //
 // 2048 rows of V = 128256 bf16, K = 64, loss and gradient: 195 us (5.4 TB/s, 0.79; some
-// 15 % of the elements come from memory again), the loss alone 86 (0.90).  Slices kept in
+// 8 % of the bytes read are read again), the loss alone 86 (0.90).  Slices kept in
 // shared memory, 64 KB to a CTA: 236 us (a third of the CTAs' time stands at barriers);
 // clusters that go from row to row with the next row's slice on its way: 301.
 #include <math.h>

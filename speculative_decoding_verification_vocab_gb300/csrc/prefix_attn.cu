@@ -37,9 +37,9 @@
 //   warps 4-11  softmax, four to a buffer, a row to a thread, 64 keys at a time: the
 //               running maximum with a lazy rescale of O, P as 16-bit values (two for
 //               each where there is one query tile); at a segment's end O, m and l to
-//               the workspace.  The halves of a buffer
-//               take turns too: one is multiplied and filled with the next tile's
-//               scores while the other is worked on.
+//               the workspace.  The halves of a buffer take turns too: one is
+//               multiplied and filled with the next tile's scores while the other is
+//               worked on.
 // Every wait on an mbarrier is bounded; one that runs out marks the CTA's parts
 // with SV_ROW_TIMEOUT.
 //
@@ -49,8 +49,9 @@
 // waits for the next scores, whose halves of 64 keys read Q twice from shared memory).
 // With whole tiles in turn, the scores of the next behind the product of the last: 114;
 // one S buffer: 367; two warps to a row of scores (16 of softmax): 142.  16 prefixes of
-// 1500 to 9000 slots, 8 samples each, 32 heads on 8 of 64: 50 us (4.6 TB/s; a quarter of
-// a query tile's rows are there, and a row's softmax takes as long for few).
+// 1500 to 9000 slots, 8 samples each, 32 heads on 8 of 64, weights in two parts: 57 us (3.9
+// TB/s; a quarter of a query tile's rows are there, and a row's softmax takes as long for
+// few).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -81,11 +82,11 @@ constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 // as in the paged attention; one part alone (half a step, 2^-8 or 2^-11, of each weight,
 // independent from key to key) adds a rounding as large as the output's own (bf16:
 // 2.2e-3 from 64 bits, where rounding the output leaves 1.65e-3).  For one query tile,
-// where the product is not the bound, it costs 4 % of the call (4 prefixes of 20000
-// slots, 64 heads on 8 of 128: 4 sequences each 70.2 and 73.0 us, 16 each 86.9 and 89.9;
-// 16 of 5000, 32 on 8 of 64, fp16, pages of 20: 59 and 65).  Beyond 128 rows the product
-// is the bound, which a second part makes half again as long (32 sequences each 103 and
-// 118 us; 128 behind 32600 slots 131 and 159): one part.
+// where the product is not the bound, it costs 4 to 10 % of the call (4 prefixes of 20000
+// slots, 64 heads on 8 of 128: 4 sequences each 71 and 74 us, 16 each 87 and 90; one of
+// them, from L2, 33 and 36; 16 of 5000, 32 on 8 of 64, fp16, pages of 20: 59 and 65).
+// Beyond 128 rows the product is the bound, and the call 15 to 22 % longer with a second
+// part (32 sequences each 103 and 118 us; 128 behind 32600 slots 131 and 159): one part.
 template <typename T> constexpr float kSlack = 8.0f;
 template <typename T> constexpr float kBias = 0.0f;
 template <> constexpr float kSlack<__half> = 4.0f;
